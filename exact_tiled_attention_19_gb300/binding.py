@@ -9,12 +9,14 @@ The functions ``attn_fwd``, ``attn_fwd_ex``, ``attn_bwd``, ``attn_bwd_workspace_
 ``attn_fwd_varlen_global``,
 ``attn_fwd_varlen``, ``attn_fwd_varlen_ex``, ``attn_fwd_host``, ``attn_fwd_varlen_host``,
 ``attn_fwd_varlen_host_plan``,
+``attn_qk_norm_rope``, ``attn_qk_norm_rope_bwd``, ``attn_qk_norm_rope_bwd_workspace_size``,
+``attn_paged_append``, ``attn_fwd_paged``, ``attn_fwd_paged_workspace_size``, ``attn_fwd_paged_plan``,
 ``etattn_status_string``, ``etattn_last_cuda_error``,
 ``etattn_read_device_status``, ``etattn_selftest_wait_timeout`` and
 ``etattn_version`` have the C names and
 arguments (pointers as ints).  The helpers ``attention`` and
-``attention_varlen`` marshal torch CUDA tensors (output allocation, strides,
-the current stream) and call them; every step of the computation runs in the
+``attention_varlen`` (and the others below) marshal torch CUDA tensors (output
+allocation, strides, the current stream) and call them; every step of the computation runs in the
 library's kernels.  There is no fallback: if the
 library is missing or cannot be loaded, an error is raised.
 """
@@ -35,7 +37,7 @@ STATUS_NAMES = {
     0: "ETATTN_OK", 1: "ETATTN_ERR_NULL_PTR", 2: "ETATTN_ERR_BAD_DTYPE", 3: "ETATTN_ERR_BAD_SHAPE",
     4: "ETATTN_ERR_BAD_HEADS", 5: "ETATTN_ERR_BAD_STRIDE", 6: "ETATTN_ERR_BAD_ALIGN", 7: "ETATTN_ERR_ALIAS",
     8: "ETATTN_ERR_BAD_SCALE", 9: "ETATTN_ERR_BAD_SEQLENS", 10: "ETATTN_ERR_LAUNCH", 11: "ETATTN_ERR_DEVICE",
-    12: "ETATTN_ERR_NO_DEVICE",
+    12: "ETATTN_ERR_NO_DEVICE", 13: "ETATTN_ERR_BAD_INDEX",
 }
 globals().update({name: code for code, name in STATUS_NAMES.items()})
 
@@ -111,6 +113,23 @@ def load_library(path: str | None = None):
         lib.attn_fwd_varlen_host.restype = _int
         lib.attn_fwd_varlen_host_plan.argtypes = [_vp, _int, _int, ctypes.POINTER(ctypes.c_int32)]
         lib.attn_fwd_varlen_host_plan.restype = _int
+        lib.attn_qk_norm_rope.argtypes = [_vp] * 9 + [_int] * 5 + [_i64p] + [_int] * 3 + [ctypes.c_float, _vp]
+        lib.attn_qk_norm_rope.restype = _int
+        lib.attn_qk_norm_rope_bwd.argtypes = ([_vp] * 13 + [_int] * 5 + [_i64p] + [_int] * 3 +
+                                              [ctypes.c_float, _vp, ctypes.c_size_t, _vp])
+        lib.attn_qk_norm_rope_bwd.restype = _int
+        lib.attn_qk_norm_rope_bwd_workspace_size.argtypes = [_int] * 4
+        lib.attn_qk_norm_rope_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.attn_paged_append.argtypes = ([_vp] * 13 + [_int] * 6 + [_i64p] + [_int] * 3 + [ctypes.c_int64] +
+                                          [_int] * 3 + [ctypes.c_float, _vp])
+        lib.attn_paged_append.restype = _int
+        lib.attn_fwd_paged.argtypes = ([_vp] * 8 + [_int] * 7 + [_i64p] + [_int] * 3 + [ctypes.c_int64] + [_int] * 3 +
+                                       [ctypes.c_float, _int, _vp, ctypes.c_size_t, _vp])
+        lib.attn_fwd_paged.restype = _int
+        lib.attn_fwd_paged_workspace_size.argtypes = [_int] * 5
+        lib.attn_fwd_paged_workspace_size.restype = ctypes.c_size_t
+        lib.attn_fwd_paged_plan.argtypes = [_int] * 6 + [ctypes.POINTER(_int)]
+        lib.attn_fwd_paged_plan.restype = _int
         lib.etattn_status_string.argtypes = [_int]
         lib.etattn_status_string.restype = ctypes.c_char_p
         lib.etattn_last_cuda_error.argtypes = []
@@ -249,6 +268,67 @@ def attn_fwd_varlen_host(q_host, k_host, v_host, o_host, lse_host, cu_seqlens_ho
                                     v_dev or None, o_dev or None, lse_dev or None, cu_seqlens_dev or None,
                                     num_seqs, max_seqlen, total_tokens, Hq, Hkv, D, dtype, causal, scale,
                                     stream or None)
+
+
+def attn_qk_norm_rope(q, k, q_weight, k_weight, rope_cos, rope_sin, positions, q_out, k_out, total_tokens, Hq, Hk, D,
+                      dtype, strides, rope_dim, interleaved, max_position, eps, stream):
+    """C ``attn_qk_norm_rope``: pointers as ints (0 for NULL), ``strides`` 12 ints."""
+    lib = load_library()
+    return lib.attn_qk_norm_rope(q or None, k or None, q_weight or None, k_weight or None, rope_cos or None,
+                                 rope_sin or None, positions or None, q_out or None, k_out or None, total_tokens, Hq,
+                                 Hk, D, dtype, _strides_arg(strides), rope_dim, interleaved, max_position, eps,
+                                 stream or None)
+
+
+def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope_cos, rope_sin, positions, dq, dk, dq_weight,
+                          dk_weight, total_tokens, Hq, Hk, D, dtype, strides, rope_dim, interleaved, max_position,
+                          eps, workspace, workspace_bytes, stream):
+    """C ``attn_qk_norm_rope_bwd``: pointers as ints (0 for NULL), ``strides`` 18 ints."""
+    lib = load_library()
+    return lib.attn_qk_norm_rope_bwd(q or None, k or None, dq_out or None, dk_out or None, q_weight or None,
+                                     k_weight or None, rope_cos or None, rope_sin or None, positions or None,
+                                     dq or None, dk or None, dq_weight or None, dk_weight or None, total_tokens, Hq,
+                                     Hk, D, dtype, _strides_arg(strides), rope_dim, interleaved, max_position, eps,
+                                     workspace or None, workspace_bytes, stream or None)
+
+
+def attn_qk_norm_rope_bwd_workspace_size(total_tokens, Hq, Hk, D) -> int:
+    return load_library().attn_qk_norm_rope_bwd_workspace_size(total_tokens, Hq, Hk, D)
+
+
+def attn_paged_append(q, k, v, q_weight, k_weight, rope_cos, rope_sin, q_out, k_pages, v_pages, block_table, seqlens_k,
+                      cu_seqlens_q, num_seqs, total_tokens, Hq, Hkv, D, dtype, strides, page_size, num_pages,
+                      max_pages, table_stride, rope_dim, interleaved, max_position, eps, stream):
+    """C ``attn_paged_append``: pointers as ints (0 for NULL), ``strides`` 20 ints."""
+    lib = load_library()
+    return lib.attn_paged_append(q or None, k or None, v or None, q_weight or None, k_weight or None,
+                                 rope_cos or None, rope_sin or None, q_out or None, k_pages or None, v_pages or None,
+                                 block_table or None, seqlens_k or None, cu_seqlens_q or None, num_seqs, total_tokens,
+                                 Hq, Hkv, D, dtype, _strides_arg(strides), page_size, num_pages, max_pages,
+                                 table_stride, rope_dim, interleaved, max_position, eps, stream or None)
+
+
+def attn_fwd_paged(q, k_pages, v_pages, o, lse, block_table, seqlens_k, cu_seqlens_q, num_seqs, max_seqlen_q, total_q,
+                   Hq, Hkv, D, dtype, strides, page_size, num_pages, max_pages, table_stride, causal, window_left,
+                   window_right, scale, num_shares, workspace, workspace_bytes, stream):
+    """C ``attn_fwd_paged``: pointers as ints (0 for NULL), ``strides`` 14 ints."""
+    lib = load_library()
+    return lib.attn_fwd_paged(q or None, k_pages or None, v_pages or None, o or None, lse or None, block_table or None,
+                              seqlens_k or None, cu_seqlens_q or None, num_seqs, max_seqlen_q, total_q, Hq, Hkv, D,
+                              dtype, _strides_arg(strides), page_size, num_pages, max_pages, table_stride, causal,
+                              window_left, window_right, scale, num_shares, workspace or None, workspace_bytes,
+                              stream or None)
+
+
+def attn_fwd_paged_workspace_size(Hq, Hkv, max_seqlen_q, D, num_shares) -> int:
+    return load_library().attn_fwd_paged_workspace_size(Hq, Hkv, max_seqlen_q, D, num_shares)
+
+
+def attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D):
+    """(status, num_shares) for the current device."""
+    out = _int(0)
+    rc = load_library().attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, ctypes.byref(out))
+    return rc, out.value
 
 
 def etattn_status_string(code: int) -> str:
@@ -551,4 +631,249 @@ def attention_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = Tru
         if num_global <= 0 and num_splits <= 1:
             name = "attn_fwd_varlen" if plain else "attn_fwd_varlen_ex"
         raise EtattnError(rc, name)
+    return out, lse
+
+
+def _address(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _like(name, t, shape, dtype, device):
+    """Checks an optional tensor argument."""
+    if t is None:
+        return
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _dense(name, t):
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rope_args(D, dtype, device, q_weight, k_weight, rope_cos, rope_sin):
+    """(rope_dim, max_position) of the rotation tables, after checking them and the weights."""
+    import torch
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _like(name, t, (D,), dtype, device)
+        _dense(name, t)
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin come together")
+    if rope_cos is None:
+        return 0, 0
+    if rope_cos.dim() != 2:
+        raise ValueError("rope_cos and rope_sin must be [max_position, rope_dim / 2]")
+    for name, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)):
+        _like(name, t, tuple(rope_cos.shape), torch.float32, device)
+        _dense(name, t)
+    return 2 * rope_cos.shape[1], rope_cos.shape[0]
+
+
+def rope_tables(max_position: int, rope_dim: int, *, theta: float = 10000.0, device=None):
+    """(rope_cos, rope_sin): FP32 [max_position, rope_dim / 2] tables of the angles
+    position * theta^(-2i / rope_dim), from angles in 64 bits (an angle of a far
+    position has no correct digit left in 32)."""
+    import torch
+    device = torch.device("cuda") if device is None else device
+    inv = theta ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64, device=device) / rope_dim)
+    angle = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * inv
+    return angle.cos().float(), angle.sin().float()
+
+
+def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, rope_cos=None, rope_sin=None, positions=None,
+                 interleaved: bool = False, eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head and rotation by position of q [T, Hq, D] and k
+    [T, Hk, D] in one pass; returns (q_out, k_out), new tensors when not given.
+
+    ``q_weight`` / ``k_weight`` ([D], q's dtype): the norm's weights, None for
+    no norm.  ``rope_cos`` / ``rope_sin`` (FP32 [max_position, rope_dim / 2],
+    see ``rope_tables``) and ``positions`` (int32 [T]): the rotation, None for
+    none.  Views of a fused projection serve as q and k."""
+    import torch
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    dtype, device = _dtype_code(q), q.device
+    _like("k", k, (T, Hk, D), q.dtype, device)
+    rope_dim, max_position = _rope_args(D, q.dtype, device, q_weight, k_weight, rope_cos, rope_sin)
+    if rope_dim:
+        if positions is None:
+            raise ValueError("positions are needed with rope_cos and rope_sin")
+        _like("positions", positions, (T,), torch.int32, device)
+        _dense("positions", positions)
+    _like("q_out", q_out, (T, Hq, D), q.dtype, device)
+    _like("k_out", k_out, (T, Hk, D), q.dtype, device)
+    with torch.cuda.device(device):
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=device)
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=device)
+        rc = attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), _address(q_weight), _address(k_weight), _address(rope_cos),
+                               _address(rope_sin), _address(positions), q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hk,
+                               D, dtype, (*q.stride(), *k.stride(), *q_out.stride(), *k_out.stride()), rope_dim,
+                               1 if interleaved else 0, max_position, float(eps), _stream_handle(stream))
+    if rc != 0:
+        raise EtattnError(rc, "attn_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, rope_cos=None, rope_sin=None,
+                          positions=None, interleaved: bool = False, eps: float = 1e-6, dq=None, dk=None,
+                          workspace=None, stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of ``qk_norm_rope`` for the
+    upstream gradients ``dq_out`` and ``dk_out``; the weights' are FP32 [D]
+    (None without the weight)."""
+    import torch
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    dtype, device = _dtype_code(q), q.device
+    _like("k", k, (T, Hk, D), q.dtype, device)
+    rope_dim, max_position = _rope_args(D, q.dtype, device, q_weight, k_weight, rope_cos, rope_sin)
+    if rope_dim:
+        if positions is None:
+            raise ValueError("positions are needed with rope_cos and rope_sin")
+        _like("positions", positions, (T,), torch.int32, device)
+        _dense("positions", positions)
+    for name, t, H in (("dq_out", dq_out, Hq), ("dk_out", dk_out, Hk), ("dq", dq, Hq), ("dk", dk, Hk)):
+        _like(name, t, (T, H, D), q.dtype, device)
+    with torch.cuda.device(device):
+        if dq is None:
+            dq = torch.empty((T, Hq, D), dtype=q.dtype, device=device)
+        if dk is None:
+            dk = torch.empty((T, Hk, D), dtype=q.dtype, device=device)
+        dwq = torch.empty(D, dtype=torch.float32, device=device) if q_weight is not None else None
+        dwk = torch.empty(D, dtype=torch.float32, device=device) if k_weight is not None else None
+        need = attn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D) if dwq is not None or dwk is not None else 0
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        rc = attn_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
+                                   _address(q_weight), _address(k_weight), _address(rope_cos), _address(rope_sin),
+                                   _address(positions), dq.data_ptr(), dk.data_ptr(), _address(dwq), _address(dwk), T,
+                                   Hq, Hk, D, dtype,
+                                   (*q.stride(), *k.stride(), *dq_out.stride(), *dk_out.stride(), *dq.stride(),
+                                    *dk.stride()), rope_dim, 1 if interleaved else 0, max_position, float(eps),
+                                   _address(workspace),
+                                   workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                   _stream_handle(stream))
+    if rc != 0:
+        raise EtattnError(rc, "attn_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+def _page_args(k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device):
+    """Checks the cache's tensors; returns (num_seqs, num_pages, Hkv, page_size)."""
+    import torch
+    num_pages, Hkv, page_size, D = k_pages.shape
+    _like("k_pages", k_pages, (num_pages, Hkv, page_size, D), dtype, device)
+    _like("v_pages", v_pages, (num_pages, Hkv, page_size, D), dtype, device)
+    S = block_table.shape[0]
+    _like("block_table", block_table, (S, block_table.shape[1]), torch.int32, device)
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table's rows must be contiguous")
+    _like("seqlens_k", seqlens_k, (S,), torch.int32, device)
+    _dense("seqlens_k", seqlens_k)
+    _like("cu_seqlens_q", cu_seqlens_q, (S + 1,), torch.int32, device)
+    _dense("cu_seqlens_q", cu_seqlens_q)
+    return S, num_pages, Hkv, page_size
+
+
+def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_weight=None, k_weight=None,
+                 rope_cos=None, rope_sin=None, interleaved: bool = False, eps: float = 1e-6, cu_seqlens_q=None,
+                 q_out=None, stream=None):
+    """Writes this step's keys and values k, v [T, Hkv, D] into the paged cache,
+    the keys normed and rotated at their positions on the way (as
+    ``qk_norm_rope``), and returns q [T, Hq, D] normed and rotated (None
+    without q).
+
+    k_pages, v_pages: logical [num_pages, Hkv, page_size, D] (any strides with d
+    contiguous); block_table: int32 [S, max_pages]; seqlens_k: int32 [S], the
+    keys of every sequence with the new ones; cu_seqlens_q: int32 [S + 1]
+    offsets of the new tokens, None when every sequence has T / S."""
+    import torch
+    T, Hk, D = k.shape
+    dtype, device = _dtype_code(k), k.device
+    S, num_pages, Hkv, page_size = _page_args(k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, k.dtype, device)
+    _like("k", k, (T, Hkv, k_pages.shape[3]), k.dtype, device)
+    _like("v", v, (T, Hkv, D), k.dtype, device)
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[1]
+        _like("q", q, (T, Hq, D), k.dtype, device)
+        _like("q_out", q_out, (T, Hq, D), k.dtype, device)
+    rope_dim, max_position = _rope_args(D, k.dtype, device, q_weight, k_weight, rope_cos, rope_sin)
+    with torch.cuda.device(device):
+        if q is None:
+            q_out = None
+        elif q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=k.dtype, device=device)
+        q_stride = (0, 0, 1) if q is None else q.stride()
+        o_stride = (0, 0, 1) if q is None else q_out.stride()
+        rc = attn_paged_append(_address(q), k.data_ptr(), v.data_ptr(), _address(q_weight), _address(k_weight),
+                               _address(rope_cos), _address(rope_sin), _address(q_out), k_pages.data_ptr(),
+                               v_pages.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(),
+                               _address(cu_seqlens_q), S, T, Hq, Hkv, D, dtype,
+                               (*q_stride, *k.stride(), *v.stride(), *o_stride, *k_pages.stride(),
+                                *v_pages.stride()), page_size, num_pages, block_table.shape[1], block_table.stride(0),
+                               rope_dim, 1 if interleaved else 0, max_position, float(eps), _stream_handle(stream))
+    if rc != 0:
+        raise EtattnError(rc, "attn_paged_append")
+    return q_out
+
+
+def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q=None, max_seqlen_q: int | None = None,
+                    max_seqlen_k: int | None = None, causal: bool = True, scale: float | None = None,
+                    window_left: int = -1, window_right: int = -1, num_shares: int | None = None, workspace=None,
+                    out=None, lse=None, return_lse: bool = True, stream=None):
+    """Attention of the new tokens q [T, Hq, D] over a paged cache; returns
+    (o [T, Hq, D], lse [Hq, T] FP32 or None).
+
+    k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q: as for
+    ``paged_append``; with cu_seqlens_q, ``max_seqlen_q`` (the most new tokens
+    of a sequence) is needed too.  ``max_seqlen_k`` (default: what the block
+    table can hold) only bounds the number of shares the work is cut into;
+    ``num_shares`` (default: the library's plan for the current device) and
+    ``workspace`` (a CUDA uint8 tensor of ``attn_fwd_paged_workspace_size``
+    bytes) may be given, as a captured graph's owner would."""
+    import torch
+    T, Hq, D = q.shape
+    dtype, device = _dtype_code(q), q.device
+    S, num_pages, Hkv, page_size = _page_args(k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, q.dtype, device)
+    if k_pages.shape[3] != D:
+        raise ValueError(f"k_pages has head dim {k_pages.shape[3]}, q has {D}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if cu_seqlens_q is None:
+        max_seqlen_q = T // S if S > 0 else 0
+    elif max_seqlen_q is None:
+        raise ValueError("max_seqlen_q is needed with cu_seqlens_q")
+    _like("out", out, (T, Hq, D), q.dtype, device)
+    _like("lse", lse, (Hq, T), torch.float32, device)
+    _dense("lse", lse)
+    _dense("workspace", workspace)
+    with torch.cuda.device(device):
+        if num_shares is None:
+            most = block_table.shape[1] * page_size if max_seqlen_k is None else int(max_seqlen_k)
+            rc, num_shares = attn_fwd_paged_plan(S, Hq, Hkv, int(max_seqlen_q), min(most, 1 << 30), D)
+            if rc != 0:
+                raise EtattnError(rc, "attn_fwd_paged_plan")
+        need = attn_fwd_paged_workspace_size(Hq, Hkv, int(max_seqlen_q), D, int(num_shares))
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=q.dtype, device=device)
+        if lse is None and return_lse:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
+        rc = attn_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _address(lse),
+                            block_table.data_ptr(), seqlens_k.data_ptr(), _address(cu_seqlens_q), S,
+                            int(max_seqlen_q), T, Hq, Hkv, D, dtype,
+                            (*q.stride(), *k_pages.stride(), *v_pages.stride(), *out.stride()), page_size, num_pages,
+                            block_table.shape[1], block_table.stride(0), 1 if causal else 0, int(window_left),
+                            int(window_right), float(scale), int(num_shares), _address(workspace),
+                            workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                            _stream_handle(stream))
+    if rc != 0:
+        raise EtattnError(rc, "attn_fwd_paged")
     return out, lse

@@ -73,9 +73,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
               os.path.join(BUILD_DIR, "attn_api.o")], "attn_api"),
             ([nvcc, *ARCH, *CFLAGS, "-c", os.path.join(CSRC, "attn_combine.cu"), "-o",
               os.path.join(BUILD_DIR, "attn_combine.o")], "attn_combine")]
-    jobs.append(([nvcc, *ARCH, *CFLAGS, "-c", os.path.join(CSRC, "attn_bwd_aux.cu"), "-o",
-                  os.path.join(BUILD_DIR, "attn_bwd_aux.o")], "attn_bwd_aux"))
-    for kind in ("fwd", "bwd"):
+    for name in ("attn_bwd_aux", "attn_rope"):
+        jobs.append(([nvcc, *ARCH, *CFLAGS, "-c", os.path.join(CSRC, f"{name}.cu"), "-o",
+                      os.path.join(BUILD_DIR, f"{name}.o")], name))
+    for kind in ("fwd", "bwd", "paged"):
         for d, bf in VARIANTS:
             obj = os.path.join(BUILD_DIR, f"attn_{kind}_d{d}_{bf}.o")
             jobs.append(([nvcc, *ARCH, *CFLAGS, f"-DETATTN_INST_D={d}", f"-DETATTN_INST_BF16={bf}", "-c",

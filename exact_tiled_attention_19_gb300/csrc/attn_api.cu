@@ -172,11 +172,12 @@ int current_device(int* dev_out, int** status_out, int* num_sms_out = nullptr) {
 
 // 4-D tensor map over (d, token, head, batch) with a box of one 128-row tile
 // of SW elements along d: 128 tokens of one head, or with box_heads = P > 1,
-// 128 / P tokens of P heads.  If the token stride exceeds the head stride
+// 128 / P tokens of P heads (box_rows: another number of rows than 128).  If the token stride exceeds the head stride
 // the two middle axes are exchanged so that strides grow outward; *swapped
 // says so.
 int encode_map(CUtensorMap* map, int dtype, const void* ptr, int D, int64_t n_tokens, int64_t n_heads,
-               int64_t n_batch, int64_t s_tok, int64_t s_head, int64_t s_batch, bool* swapped, int box_heads = 1) {
+               int64_t n_batch, int64_t s_tok, int64_t s_head, int64_t s_batch, bool* swapped, int box_heads = 1,
+               int box_rows = 128) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return fail_cuda(cudaErrorNotSupported);
   const uint64_t esz = 2;
@@ -194,7 +195,7 @@ int encode_map(CUtensorMap* map, int dtype, const void* ptr, int D, int64_t n_to
   cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(sw ? n_heads : n_tokens), (cuuint64_t)(sw ? n_tokens : n_heads),
                         (cuuint64_t)n_batch};
   cuuint64_t strides[3] = {sw ? bh : bt, sw ? bt : bh, bb};
-  const cuuint32_t box_tok = 128u / (cuuint32_t)box_heads, box_head = (cuuint32_t)box_heads;
+  const cuuint32_t box_tok = (cuuint32_t)(box_rows / box_heads), box_head = (cuuint32_t)box_heads;
   cuuint32_t box[4] = {(cuuint32_t)sw_elems, sw ? box_head : box_tok, sw ? box_tok : box_head, 1u};
   cuuint32_t estride[4] = {1, 1, 1, 1};
   CUresult r = enc(map, dtype == ETATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
@@ -933,6 +934,425 @@ int varlen_impl(const void* q, const void* k, const void* v, void* o, float* lse
   return ETATTN_OK;
 }
 
+// ---------------------------------------------------------------- queries and keys before attention
+// What the calls on norm, rotation and pages have in common.
+bool rope_dim_ok(int rope_dim, int D) { return rope_dim >= 0 && rope_dim <= D && rope_dim % 16 == 0; }
+bool page_size_ok(int n) { return n >= 8 && n <= 4096 && (n & (n - 1)) == 0; }
+int log2_of(int n) {
+  int k = 0;
+  while ((1 << k) < n) ++k;
+  return k;
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Rotation tables and norm weights: present where they are used, 16-byte aligned.
+int tables_ok(const float* cos, const float* sin, int rope_dim, int max_position, const void* wq, const void* wk,
+              float eps) {
+  if (rope_dim > 0) {
+    if (max_position < 1) return ETATTN_ERR_BAD_SHAPE;
+    if (!cos || !sin) return ETATTN_ERR_NULL_PTR;
+    if (!aligned16(cos) || !aligned16(sin)) return ETATTN_ERR_BAD_ALIGN;
+  }
+  if ((wq || wk) && !(std::isfinite(eps) && eps > 0.f)) return ETATTN_ERR_BAD_SCALE;
+  if (!aligned16(wq) || !aligned16(wk)) return ETATTN_ERR_BAD_ALIGN;
+  return ETATTN_OK;
+}
+
+View view3(const void* ptr, int64_t T, int64_t H, int D, const int64_t* st) {
+  return View{ptr, 3, {T, H, D, 0}, {st[0], st[1], st[2], 0}};
+}
+
+// overlaps for packed [T, H, D] views of 16-bit data, with views of different
+// heads of one fused [T, heads, D] buffer told apart: with one token stride,
+// they are disjoint when their parts of a token's row are.
+bool overlaps3(const View& a, const View& b) {
+  if (!overlaps(a, 2, b, 2)) return false;
+  const int64_t S = a.stride[0];
+  if (S != b.stride[0] || S <= 0) return true;
+  auto part = [](const View& v) { return (v.size[1] - 1) * v.stride[1] + v.size[2]; };
+  const int64_t pa = part(a), pb = part(b);
+  if (pa > S || pb > S) return true;
+  const int64_t off = (reinterpret_cast<intptr_t>(b.ptr) - reinterpret_cast<intptr_t>(a.ptr)) / 2;
+  const int64_t d = ((off % S) + S) % S;  // where b's part starts in a's period
+  return !(d >= pa && d + pb <= S);
+}
+
+// A pages tensor [num_pages, Hkv, page_size, D].
+View view_pages(const void* ptr, int num_pages, int Hkv, int page_size, int D, const int64_t* st) {
+  return View{ptr, 4, {num_pages, Hkv, page_size, D}, {st[0], st[1], st[2], st[3]}};
+}
+
+int rope_impl(const void* q, const void* k, const void* q_weight, const void* k_weight, const float* cos,
+              const float* sin, const int32_t* positions, void* q_out, void* k_out, int total_tokens, int Hq, int Hk,
+              int D, int dtype, const int64_t* st, int rope_dim, int interleaved, int max_position, float eps,
+              void* stream) {
+  if (dtype != ETATTN_F16 && dtype != ETATTN_BF16) return ETATTN_ERR_BAD_DTYPE;
+  if (total_tokens < 0 || total_tokens > kMaxTokens || Hq < 0 || Hk < 0 || Hq > kMaxGridYZ || Hk > kMaxGridYZ ||
+      !head_dim_ok(D) || !rope_dim_ok(rope_dim, D))
+    return ETATTN_ERR_BAD_SHAPE;
+  if (st == nullptr) return ETATTN_ERR_NULL_PTR;
+  if (total_tokens == 0 || Hq + Hk == 0) return ETATTN_OK;
+  if (int rc = tables_ok(cos, sin, rope_dim, max_position, q_weight, k_weight, eps)) return rc;
+  if ((Hq > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out)) || (rope_dim > 0 && !positions))
+    return ETATTN_ERR_NULL_PTR;
+  const View vq = view3(q, total_tokens, Hq, D, st), vk = view3(k, total_tokens, Hk, D, st + 3);
+  const View oq = view3(q_out, total_tokens, Hq, D, st + 6), ok = view3(k_out, total_tokens, Hk, D, st + 9);
+  for (const View* t : {&vq, &vk, &oq, &ok})
+    if (!strides_ok(*t, 2)) return ETATTN_ERR_BAD_STRIDE;
+  for (const View* t : {&vq, &oq})
+    if (Hq > 0 && !aligned16(t->ptr)) return ETATTN_ERR_BAD_ALIGN;
+  for (const View* t : {&vk, &ok})
+    if (Hk > 0 && !aligned16(t->ptr)) return ETATTN_ERR_BAD_ALIGN;
+  if (!aligned4(positions)) return ETATTN_ERR_BAD_ALIGN;
+  for (const View* o : {&oq, &ok})
+    if (overlaps3(*o, vq) || overlaps3(*o, vk)) return ETATTN_ERR_ALIAS;
+  if (overlaps3(oq, ok)) return ETATTN_ERR_ALIAS;
+
+  int dev = 0;
+  int* status = nullptr;
+  if (int rc = current_device(&dev, &status)) return rc;
+  RopeParams p{};
+  p.q = q;
+  p.k = k;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.cos = cos;
+  p.sin = sin;
+  p.positions = rope_dim > 0 ? positions : nullptr;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.q_st = st[0];
+  p.q_sh = st[1];
+  p.k_st = st[3];
+  p.k_sh = st[4];
+  p.qo_st = st[6];
+  p.qo_sh = st[7];
+  p.kp_st = st[9];
+  p.kp_sh = st[10];
+  p.total_tokens = total_tokens;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rope_dim = rope_dim;
+  p.interleaved = interleaved != 0;
+  p.max_position = max_position;
+  p.eps = eps;
+  p.status = status;
+  const cudaError_t e = launch_rope(D, dtype == ETATTN_BF16, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
+}
+
+// Blocks of the gradient launch, each with one partial sum per weight element:
+// at most kRopeBwdMaxBlocks, so that the workspace stays small.
+constexpr int kRopeBwdMaxBlocks = 608;
+int rope_bwd_blocks(int64_t total_tokens, int64_t Hq, int64_t Hk, int D) {
+  const int64_t items =
+      total_tokens * ((Hq + kRopeBwdHeads - 1) / kRopeBwdHeads + (Hk + kRopeBwdHeads - 1) / kRopeBwdHeads);
+  const int64_t per_block = 256 / (D / 8);
+  return (int)std::min<int64_t>((items + per_block - 1) / per_block, kRopeBwdMaxBlocks);
+}
+size_t rope_bwd_bytes(int64_t total_tokens, int64_t Hq, int64_t Hk, int D) {
+  return (size_t)rope_bwd_blocks(total_tokens, Hq, Hk, D) * 2 * D * 4;
+}
+
+int rope_bwd_impl(const void* q, const void* k, const void* dq_out, const void* dk_out, const void* q_weight,
+                  const void* k_weight, const float* cos, const float* sin, const int32_t* positions, void* dq,
+                  void* dk, float* dq_weight, float* dk_weight, int total_tokens, int Hq, int Hk, int D, int dtype,
+                  const int64_t* st, int rope_dim, int interleaved, int max_position, float eps, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  if (dtype != ETATTN_F16 && dtype != ETATTN_BF16) return ETATTN_ERR_BAD_DTYPE;
+  if (total_tokens < 0 || total_tokens > kMaxTokens || Hq < 0 || Hk < 0 || Hq > kMaxGridYZ || Hk > kMaxGridYZ ||
+      !head_dim_ok(D) || !rope_dim_ok(rope_dim, D))
+    return ETATTN_ERR_BAD_SHAPE;
+  if (st == nullptr) return ETATTN_ERR_NULL_PTR;
+  if ((q_weight && !dq_weight) || (k_weight && !dk_weight)) return ETATTN_ERR_NULL_PTR;
+  if (!aligned4(dq_weight) || !aligned4(dk_weight)) return ETATTN_ERR_BAD_ALIGN;
+  const bool work = total_tokens > 0 && Hq + Hk > 0;
+  const View vq = view3(q, total_tokens, Hq, D, st), vk = view3(k, total_tokens, Hk, D, st + 3);
+  const View gq = view3(dq_out, total_tokens, Hq, D, st + 6), gk = view3(dk_out, total_tokens, Hk, D, st + 9);
+  const View xq = view3(dq, total_tokens, Hq, D, st + 12), xk = view3(dk, total_tokens, Hk, D, st + 15);
+  const View wq{q_weight ? dq_weight : nullptr, 1, {q_weight ? D : 0, 0, 0, 0}, {1, 0, 0, 0}};
+  const View wk{k_weight ? dk_weight : nullptr, 1, {k_weight ? D : 0, 0, 0, 0}, {1, 0, 0, 0}};
+  const size_t need = work && (q_weight || k_weight) ? rope_bwd_bytes(total_tokens, Hq, Hk, D) : 0;
+  const View vw{workspace, 1, {(int64_t)need, 0, 0, 0}, {1, 0, 0, 0}};
+  if (work) {
+    if (int rc = tables_ok(cos, sin, rope_dim, max_position, q_weight, k_weight, eps)) return rc;
+    if ((Hq > 0 && (!q || !dq_out || !dq)) || (Hk > 0 && (!k || !dk_out || !dk)) || (rope_dim > 0 && !positions))
+      return ETATTN_ERR_NULL_PTR;
+    for (const View* t : {&vq, &vk, &gq, &gk, &xq, &xk})
+      if (!strides_ok(*t, 2)) return ETATTN_ERR_BAD_STRIDE;
+    for (const View* t : {&vq, &gq, &xq})
+      if (Hq > 0 && !aligned16(t->ptr)) return ETATTN_ERR_BAD_ALIGN;
+    for (const View* t : {&vk, &gk, &xk})
+      if (Hk > 0 && !aligned16(t->ptr)) return ETATTN_ERR_BAD_ALIGN;
+    if (!aligned4(positions)) return ETATTN_ERR_BAD_ALIGN;
+    if (need > 0) {
+      if (workspace == nullptr) return ETATTN_ERR_NULL_PTR;
+      if (reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign) return ETATTN_ERR_BAD_ALIGN;
+      if (workspace_bytes < need) return ETATTN_ERR_BAD_SHAPE;
+    }
+    for (const View* o : {&xq, &xk})
+      for (const View* in : {&vq, &vk, &gq, &gk})
+        if (overlaps3(*o, *in)) return ETATTN_ERR_ALIAS;
+    if (overlaps3(xq, xk)) return ETATTN_ERR_ALIAS;
+    const View* extra[] = {&wq, &wk, &vw};
+    const size_t esz[] = {4, 4, 1};
+    for (int i = 0; i < 3; ++i) {
+      for (const View* t : {&vq, &vk, &gq, &gk, &xq, &xk})
+        if (overlaps(*extra[i], esz[i], *t, 2)) return ETATTN_ERR_ALIAS;
+      for (int j = 0; j < i; ++j)
+        if (overlaps(*extra[i], esz[i], *extra[j], esz[j])) return ETATTN_ERR_ALIAS;
+    }
+  }
+  if (!work && !q_weight && !k_weight) return ETATTN_OK;
+
+  int dev = 0;
+  int* status = nullptr;
+  if (int rc = current_device(&dev, &status)) return rc;
+  RopeBwdParams p{};
+  p.q = q;
+  p.k = k;
+  p.dq_out = dq_out;
+  p.dk_out = dk_out;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.cos = cos;
+  p.sin = sin;
+  p.positions = positions;
+  p.dq = dq;
+  p.dk = dk;
+  p.dq_weight = q_weight ? dq_weight : nullptr;
+  p.dk_weight = k_weight ? dk_weight : nullptr;
+  p.partials = static_cast<float*>(workspace);
+  int64_t* dst[] = {&p.q_st,   &p.q_sh,   &p.k_st,  &p.k_sh,  &p.dqo_st, &p.dqo_sh,
+                    &p.dko_st, &p.dko_sh, &p.dq_st, &p.dq_sh, &p.dk_st,  &p.dk_sh};
+  for (int i = 0; i < 12; ++i) *dst[i] = st[3 * (i / 2) + i % 2];
+  p.total_tokens = total_tokens;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rope_dim = rope_dim;
+  p.interleaved = interleaved != 0;
+  p.max_position = max_position;
+  p.eps = eps;
+  p.blocks = work ? rope_bwd_blocks(total_tokens, Hq, Hk, D) : 0;
+  p.status = status;
+  const cudaError_t e = launch_rope_bwd(D, dtype == ETATTN_BF16, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
+}
+
+// Arguments that describe a paged cache and the new tokens' place in it.
+int pages_ok(int num_seqs, int page_size, int num_pages, int max_pages, int64_t table_stride) {
+  if (num_seqs < 0 || num_seqs > kMaxGridYZ || !page_size_ok(page_size) || num_pages < 0 || max_pages < 0 ||
+      table_stride < 0 || (num_seqs > 1 && table_stride < max_pages))
+    return ETATTN_ERR_BAD_SHAPE;
+  return ETATTN_OK;
+}
+
+int append_impl(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                const float* cos, const float* sin, void* q_out, void* k_pages, void* v_pages,
+                const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens, int num_seqs,
+                int total_tokens, int Hq, int Hkv, int D, int dtype, const int64_t* st, int page_size, int num_pages,
+                int max_pages, int64_t table_stride, int rope_dim, int interleaved, int max_position, float eps,
+                void* stream) {
+  if (dtype != ETATTN_F16 && dtype != ETATTN_BF16) return ETATTN_ERR_BAD_DTYPE;
+  if (total_tokens < 0 || total_tokens > kMaxTokens || Hq < 0 || Hq > kMaxGridYZ || Hkv > kMaxGridYZ ||
+      !head_dim_ok(D) || !rope_dim_ok(rope_dim, D))
+    return ETATTN_ERR_BAD_SHAPE;
+  if (int rc = pages_ok(num_seqs, page_size, num_pages, max_pages, table_stride)) return rc;
+  if (Hkv <= 0) return ETATTN_ERR_BAD_HEADS;
+  if (st == nullptr) return ETATTN_ERR_NULL_PTR;
+  if (total_tokens == 0 || num_seqs == 0) return ETATTN_OK;
+  if (cu_seqlens == nullptr && total_tokens % num_seqs != 0) return ETATTN_ERR_BAD_SHAPE;
+  if (num_pages < 1 || max_pages < 1) return ETATTN_ERR_BAD_SHAPE;
+  if (int rc = tables_ok(cos, sin, rope_dim, max_position, q_weight, k_weight, eps)) return rc;
+  if (!k || !v || !k_pages || !v_pages || !block_table || !seqlens_k || (Hq > 0 && (!q || !q_out)))
+    return ETATTN_ERR_NULL_PTR;
+  const View vq = view3(q, total_tokens, Hq, D, st), vk = view3(k, total_tokens, Hkv, D, st + 3);
+  const View vv = view3(v, total_tokens, Hkv, D, st + 6), oq = view3(q_out, total_tokens, Hq, D, st + 9);
+  const View pk = view_pages(k_pages, num_pages, Hkv, page_size, D, st + 12);
+  const View pv = view_pages(v_pages, num_pages, Hkv, page_size, D, st + 16);
+  for (const View* t : {&vq, &vk, &vv, &oq, &pk, &pv})
+    if (!strides_ok(*t, 2)) return ETATTN_ERR_BAD_STRIDE;
+  for (const View* t : {&vk, &vv, &pk, &pv})
+    if (!aligned16(t->ptr)) return ETATTN_ERR_BAD_ALIGN;
+  if (Hq > 0 && (!aligned16(q) || !aligned16(q_out))) return ETATTN_ERR_BAD_ALIGN;
+  if (!aligned4(block_table) || !aligned4(seqlens_k) || !aligned4(cu_seqlens)) return ETATTN_ERR_BAD_ALIGN;
+  for (const View* t : {&vq, &vk, &vv})
+    if (overlaps3(oq, *t) || overlaps(pk, 2, *t, 2) || overlaps(pv, 2, *t, 2)) return ETATTN_ERR_ALIAS;
+  // The pages of keys and values may interleave in one buffer.
+  if (overlaps(oq, 2, pk, 2) || overlaps(oq, 2, pv, 2) || k_pages == v_pages) return ETATTN_ERR_ALIAS;
+
+  int dev = 0;
+  int* status = nullptr;
+  if (int rc = current_device(&dev, &status)) return rc;
+  RopeParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.cos = cos;
+  p.sin = sin;
+  p.q_out = q_out;
+  p.k_out = k_pages;
+  p.v_out = v_pages;
+  p.q_st = st[0];
+  p.q_sh = st[1];
+  p.k_st = st[3];
+  p.k_sh = st[4];
+  p.v_st = st[6];
+  p.v_sh = st[7];
+  p.qo_st = st[9];
+  p.qo_sh = st[10];
+  p.kp_sp = st[12];
+  p.kp_sh = st[13];
+  p.kp_st = st[14];
+  p.vp_sp = st[16];
+  p.vp_sh = st[17];
+  p.vp_st = st[18];
+  p.total_tokens = total_tokens;
+  p.Hq = Hq;
+  p.Hk = Hkv;
+  p.rope_dim = rope_dim;
+  p.interleaved = interleaved != 0;
+  p.max_position = max_position;
+  p.eps = eps;
+  p.paged = 1;
+  p.block_table = block_table;
+  p.seqlens_k = seqlens_k;
+  p.cu_seqlens = cu_seqlens;
+  p.table_stride = table_stride;
+  p.num_seqs = num_seqs;
+  p.tokens_per_seq = cu_seqlens ? 0 : total_tokens / num_seqs;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.page_shift = log2_of(page_size);
+  p.status = status;
+  const cudaError_t e = launch_rope(D, dtype == ETATTN_BF16, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
+}
+
+// ---------------------------------------------------------------- attention over a paged cache
+constexpr int kMaxShares = 65535;
+
+// Rows of a unit: 16 hold a decode step of up to 16 query heads per KV head
+// in half the registers of 32.
+int paged_row_tile(int64_t rows) { return rows <= 16 ? 16 : 32; }
+int paged_tile_keys(int D) { return D == 128 ? 64 : 128; }
+
+// Workspace: the shares' join descriptors, then at 256-byte boundaries two
+// partial rows' lse and O per share and row of a tile.
+struct PagedLayout {
+  size_t lse_off, o_off, total;
+};
+PagedLayout paged_layout(int shares, int row_tile, int D) {
+  auto up = [](size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; };
+  PagedLayout L{};
+  L.lse_off = up((size_t)shares * sizeof(PagedShare));
+  L.o_off = L.lse_off + up((size_t)shares * 2 * row_tile * 4);
+  L.total = L.o_off + (size_t)shares * 2 * row_tile * D * 4;
+  return L;
+}
+
+int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+               const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
+               int max_seqlen_q, int total_q, int Hq, int Hkv, int D, int dtype, const int64_t* st, int page_size,
+               int num_pages, int max_pages, int64_t table_stride, int causal, int window_left, int window_right,
+               float scale, int num_shares, void* workspace, size_t workspace_bytes, void* stream) {
+  if (dtype != ETATTN_F16 && dtype != ETATTN_BF16) return ETATTN_ERR_BAD_DTYPE;
+  if (max_seqlen_q < 0 || max_seqlen_q > kMaxTokens || total_q < 0 || total_q > kMaxTokens || Hq < 0 ||
+      Hq > kMaxGridYZ || !head_dim_ok(D))
+    return ETATTN_ERR_BAD_SHAPE;
+  if (int rc = pages_ok(num_seqs, page_size, num_pages, max_pages, table_stride)) return rc;
+  if (Hkv <= 0 || Hq % Hkv != 0) return ETATTN_ERR_BAD_HEADS;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return ETATTN_ERR_BAD_SCALE;
+  if (st == nullptr) return ETATTN_ERR_NULL_PTR;
+  if (num_shares < 1 || num_shares > kMaxShares) return ETATTN_ERR_BAD_SHAPE;
+  if (num_seqs == 0 || Hq == 0 || total_q == 0 || max_seqlen_q == 0) return ETATTN_OK;
+  if (cu_seqlens_q == nullptr && (int64_t)num_seqs * max_seqlen_q != total_q) return ETATTN_ERR_BAD_SHAPE;
+  if (num_pages < 1 || max_pages < 1) return ETATTN_ERR_BAD_SHAPE;
+  if ((int64_t)max_seqlen_q * (Hq / Hkv) > kMaxTokens) return ETATTN_ERR_BAD_SHAPE;  // rows of one KV head
+  if (!q || !o || !k_pages || !v_pages || !block_table || !seqlens_k) return ETATTN_ERR_NULL_PTR;
+  const View vq = view3(q, total_q, Hq, D, st), vo = view3(o, total_q, Hq, D, st + 11);
+  const View pk = view_pages(k_pages, num_pages, Hkv, page_size, D, st + 3);
+  const View pv = view_pages(v_pages, num_pages, Hkv, page_size, D, st + 7);
+  const View vl{lse, 2, {Hq, total_q, 0, 0}, {total_q, 1, 0, 0}};
+  for (const View* t : {&vq, &vo, &pk, &pv})
+    if (!strides_ok(*t, 2)) return ETATTN_ERR_BAD_STRIDE;
+  for (const View* t : {&vq, &vo, &pk, &pv})
+    if (!aligned16(t->ptr)) return ETATTN_ERR_BAD_ALIGN;
+  if (!aligned4(lse) || !aligned4(block_table) || !aligned4(seqlens_k) || !aligned4(cu_seqlens_q))
+    return ETATTN_ERR_BAD_ALIGN;
+  for (const View* t : {&vq, &pk, &pv})
+    if (overlaps(vo, 2, *t, 2) || (lse && overlaps(vl, 4, *t, 2))) return ETATTN_ERR_ALIAS;
+  if (lse && overlaps(vl, 4, vo, 2)) return ETATTN_ERR_ALIAS;
+  const int group = Hq / Hkv;
+  const int row_tile = paged_row_tile((int64_t)max_seqlen_q * group);
+  const PagedLayout L = paged_layout(num_shares, row_tile, D);
+  if (num_shares > 1) {
+    if (workspace == nullptr) return ETATTN_ERR_NULL_PTR;
+    if (reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign) return ETATTN_ERR_BAD_ALIGN;
+    if (workspace_bytes < L.total) return ETATTN_ERR_BAD_SHAPE;
+    const View vw{workspace, 1, {(int64_t)L.total, 0, 0, 0}, {1, 0, 0, 0}};
+    for (const View* t : {&vq, &pk, &pv, &vo})
+      if (overlaps(vw, 1, *t, 2)) return ETATTN_ERR_ALIAS;
+    if (lse && overlaps(vw, 1, vl, 4)) return ETATTN_ERR_ALIAS;
+  }
+
+  int dev = 0;
+  int* status = nullptr;
+  if (int rc = current_device(&dev, &status)) return rc;
+  CUtensorMap mk, mv;
+  bool swk = false, swv = false;
+  const int box = std::min(page_size, paged_tile_keys(D));
+  if (int rc = encode_map(&mk, dtype, k_pages, D, page_size, Hkv, num_pages, st[5], st[4], st[3], &swk, 1, box))
+    return rc;
+  if (int rc = encode_map(&mv, dtype, v_pages, D, page_size, Hkv, num_pages, st[9], st[8], st[7], &swv, 1, box))
+    return rc;
+  PagedParams p{};
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.q_st = st[0];
+  p.q_sh = st[1];
+  p.o_st = st[11];
+  p.o_sh = st[12];
+  p.block_table = block_table;
+  p.seqlens_k = seqlens_k;
+  p.cu_seqlens_q = cu_seqlens_q;
+  p.table_stride = table_stride;
+  p.num_seqs = num_seqs;
+  p.tokens_per_seq = max_seqlen_q;
+  p.max_seqlen_q = max_seqlen_q;
+  p.total_q = total_q;
+  p.Hkv = Hkv;
+  p.group = group;
+  p.max_keys = (int)std::min<int64_t>((int64_t)max_pages * page_size, kMaxTokens);
+  p.num_pages = num_pages;
+  p.page_shift = log2_of(page_size);
+  p.win_left = window_left_of(window_left);
+  p.win_right = window_right_of(window_right, causal);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.hn_swapped = (swk ? 1 : 0) | (swv ? 2 : 0);
+  p.row_tile = row_tile;
+  p.shares = num_shares;
+  if (num_shares > 1) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.desc = reinterpret_cast<PagedShare*>(ws);
+    p.part_lse = reinterpret_cast<float*>(ws + L.lse_off);
+    p.part_o = reinterpret_cast<float*>(ws + L.o_off);
+  }
+  p.status = status;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf = dtype == ETATTN_BF16;
+  cudaError_t e;
+  switch (D) {
+    case 32: e = bf ? launch_paged_d32_1(mk, mv, p, s) : launch_paged_d32_0(mk, mv, p, s); break;
+    case 64: e = bf ? launch_paged_d64_1(mk, mv, p, s) : launch_paged_d64_0(mk, mv, p, s); break;
+    default: e = bf ? launch_paged_d128_1(mk, mv, p, s) : launch_paged_d128_0(mk, mv, p, s);
+  }
+  return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
+}
+
 // ---------------------------------------------------------------- host-buffer pipeline
 // The host-buffer calls cut the problem into chunks (whole sequences of a
 // packed batch, whole batches, or runs of KV heads) and pipeline them over
@@ -1162,6 +1582,74 @@ int attn_fwd_varlen_global(const void* q, const void* k, const void* v, void* o,
                      window_right, scale, stream, true, nullptr, window_is_everything ? 0 : num_global);
 }
 
+int attn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight, const float* rope_cos,
+                      const float* rope_sin, const int32_t* positions, void* q_out, void* k_out, int total_tokens,
+                      int Hq, int Hk, int D, int dtype, const int64_t* strides, int rope_dim, int interleaved,
+                      int max_position, float eps, void* stream) {
+  return rope_impl(q, k, q_weight, k_weight, rope_cos, rope_sin, positions, q_out, k_out, total_tokens, Hq, Hk, D,
+                   dtype, strides, rope_dim, interleaved, max_position, eps, stream);
+}
+
+int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, const void* q_weight,
+                          const void* k_weight, const float* rope_cos, const float* rope_sin, const int32_t* positions,
+                          void* dq, void* dk, float* dq_weight, float* dk_weight, int total_tokens, int Hq, int Hk,
+                          int D, int dtype, const int64_t* strides, int rope_dim, int interleaved, int max_position,
+                          float eps, void* workspace, size_t workspace_bytes, void* stream) {
+  return rope_bwd_impl(q, k, dq_out, dk_out, q_weight, k_weight, rope_cos, rope_sin, positions, dq, dk, dq_weight,
+                       dk_weight, total_tokens, Hq, Hk, D, dtype, strides, rope_dim, interleaved, max_position, eps,
+                       workspace, workspace_bytes, stream);
+}
+
+size_t attn_qk_norm_rope_bwd_workspace_size(int total_tokens, int Hq, int Hk, int D) {
+  if (total_tokens <= 0 || Hq < 0 || Hk < 0 || Hq > kMaxGridYZ || Hk > kMaxGridYZ || !head_dim_ok(D)) return 0;
+  return rope_bwd_bytes(total_tokens, Hq, Hk, D);
+}
+
+int attn_paged_append(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                      const float* rope_cos, const float* rope_sin, void* q_out, void* k_pages, void* v_pages,
+                      const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
+                      int total_tokens, int Hq, int Hkv, int D, int dtype, const int64_t* strides, int page_size,
+                      int num_pages, int max_pages, int64_t table_stride, int rope_dim, int interleaved,
+                      int max_position, float eps, void* stream) {
+  return append_impl(q, k, v, q_weight, k_weight, rope_cos, rope_sin, q_out, k_pages, v_pages, block_table, seqlens_k,
+                     cu_seqlens_q, num_seqs, total_tokens, Hq, Hkv, D, dtype, strides, page_size, num_pages, max_pages,
+                     table_stride, rope_dim, interleaved, max_position, eps, stream);
+}
+
+int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                   const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
+                   int max_seqlen_q, int total_q, int Hq, int Hkv, int D, int dtype, const int64_t* strides,
+                   int page_size, int num_pages, int max_pages, int64_t table_stride, int causal, int window_left,
+                   int window_right, float scale, int num_shares, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  return paged_impl(q, k_pages, v_pages, o, lse, block_table, seqlens_k, cu_seqlens_q, num_seqs, max_seqlen_q, total_q,
+                    Hq, Hkv, D, dtype, strides, page_size, num_pages, max_pages, table_stride, causal, window_left,
+                    window_right, scale, num_shares, workspace, workspace_bytes, stream);
+}
+
+size_t attn_fwd_paged_workspace_size(int Hq, int Hkv, int max_seqlen_q, int D, int num_shares) {
+  if (Hq < 0 || Hkv <= 0 || Hq % Hkv != 0 || max_seqlen_q < 0 || !head_dim_ok(D) || num_shares < 1 ||
+      num_shares > kMaxShares)
+    return 0;
+  if (num_shares == 1 || Hq == 0 || max_seqlen_q == 0) return 0;
+  return paged_layout(num_shares, paged_row_tile((int64_t)max_seqlen_q * (Hq / Hkv)), D).total;
+}
+
+int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int D, int* num_shares) {
+  if (num_shares == nullptr) return ETATTN_ERR_NULL_PTR;
+  if (num_seqs < 0 || Hq < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || !head_dim_ok(D)) return ETATTN_ERR_BAD_SHAPE;
+  if (Hkv <= 0 || Hq % Hkv != 0) return ETATTN_ERR_BAD_HEADS;
+  int dev = 0, num_sms = 0;
+  int* status = nullptr;
+  if (int rc = current_device(&dev, &status, &num_sms)) return rc;
+  // Two CTAs fit on an SM; no more shares than key tiles.
+  const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_row_tile(rows);
+  const int64_t tk = paged_tile_keys(D);
+  const double tiles = (double)num_seqs * Hkv * ((rows + mt - 1) / mt) * std::max<int64_t>(1, (max_seqlen_k + tk - 1) / tk);
+  *num_shares = (int)std::max(1.0, std::min(tiles, 2.0 * num_sms));
+  return ETATTN_OK;
+}
+
 int attn_fwd_varlen_host_plan(const int32_t* cu_seqlens_host, int num_seqs, int max_chunks,
                                          int32_t* seq_bounds) {
   if (cu_seqlens_host == nullptr || seq_bounds == nullptr) return -ETATTN_ERR_NULL_PTR;
@@ -1352,6 +1840,7 @@ const char* etattn_status_string(int code) {
     case ETATTN_ERR_LAUNCH: return "a CUDA runtime call failed";
     case ETATTN_ERR_DEVICE: return "the device reported a failure (a bounded wait ran out)";
     case ETATTN_ERR_NO_DEVICE: return "no sm_103 CUDA device is current";
+    case ETATTN_ERR_BAD_INDEX: return "a position or a page of the block table is out of range";
     default: return "unknown status";
   }
 }
@@ -1374,7 +1863,8 @@ int etattn_read_device_status(int* out, int clear, void* stream) {
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return fail_cuda(e);
   }
-  *out = word == kDevOk ? ETATTN_OK : word == kDevBadSeqlens ? ETATTN_ERR_BAD_SEQLENS : ETATTN_ERR_DEVICE;
+  *out = word == kDevOk ? ETATTN_OK : word == kDevBadSeqlens ? ETATTN_ERR_BAD_SEQLENS
+         : word == kDevBadIndex ? ETATTN_ERR_BAD_INDEX : ETATTN_ERR_DEVICE;
   return ETATTN_OK;
 }
 
@@ -1390,6 +1880,6 @@ int etattn_selftest_wait_timeout(int limit_us, void* stream) {
   return ETATTN_OK;
 }
 
-int etattn_version(void) { return 201; }
+int etattn_version(void) { return 300; }
 
 }  // extern "C"

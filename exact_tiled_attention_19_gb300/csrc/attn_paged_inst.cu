@@ -1,0 +1,139 @@
+// The paged attention kernel's instantiations for one (head dim, element
+// type), its launcher and the join of its partial states, compiled once per
+// variant with -DETATTN_INST_D=<32|64|128> -DETATTN_INST_BF16=<0|1> (like
+// attn_fwd_inst.cu).
+#include <atomic>
+#include <cuda_runtime.h>
+
+#include "attn_paged_kernel.cuh"
+#include "launchers.h"
+
+#ifndef ETATTN_INST_D
+#error "ETATTN_INST_D must be defined"
+#endif
+#ifndef ETATTN_INST_BF16
+#error "ETATTN_INST_BF16 must be defined"
+#endif
+
+#define ETATTN_PCAT2(a, b, c) a##b##_##c
+#define ETATTN_PCAT(a, b, c) ETATTN_PCAT2(a, b, c)
+#define ETATTN_PAGED_LAUNCHER ETATTN_PCAT(launch_paged_d, ETATTN_INST_D, ETATTN_INST_BF16)
+
+namespace etattn {
+
+namespace {
+
+// Joins the partial states of every unit that a share boundary cut: with
+// normalised partial rows O_s and their lse_s, M = max lse_s and
+// w_s = exp(lse_s - M):  O = sum w_s O_s / sum w_s,  lse = M + ln sum w_s.
+// Block c belongs to share c.  A unit over the shares first .. first + parts
+// - 1 has parts - 1 boundaries; the blocks of the shares after the first take
+// every (parts - 1)-th row of it, so that a unit cut into many parts is joined
+// by many blocks.  Warps take parts; their sums meet in shared memory.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p) {
+  pdl_wait();
+  const PagedShare u = p.desc[blockIdx.x];
+  if (u.parts == 0) return;
+  constexpr int PER = D / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = min(p.row_tile, u.n * p.group - u.row0);
+  __shared__ float s_acc[8][D];
+  __shared__ float s_sum[8];
+  __shared__ float s_max[8];
+  auto slot = [&](int part) { return ((int64_t)(u.first + part) * 2 + (part == 0 ? 1 : 0)) * p.row_tile; };
+  for (int r = (int)blockIdx.x - u.first - 1; r < rows; r += u.parts - 1) {
+    float mx = -INFINITY;
+    for (int s = tid; s < u.parts; s += 256) mx = fmaxf(mx, p.part_lse[slot(s) + r]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    if (lane == 0) s_max[warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, s_max[i]);
+    float acc[PER], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    if (mx == -INFINITY) mx = 0.f;  // no key at all, or only NaN sums
+    for (int s = warp; s < u.parts; s += 8) {
+      const float w = expf(p.part_lse[slot(s) + r] - mx);
+      if (w == 0.f) continue;  // no eligible key: the partial row is 0
+      sum += w;
+      const float* src = p.part_o + (slot(s) + r) * D + lane * PER;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] += w * src[i];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s_acc[warp][lane * PER + i] = acc[i];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    const int rr = u.row0 + r, i = rr / p.group;
+    const int head = u.head0 + rr - i * p.group;
+    float z = 0.f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) z += s_sum[x];
+    // A row without a key is 0; a NaN sum stays one.
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    if (tid < D / 2) {
+      float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        a0 += s_acc[x][2 * tid];
+        a1 += s_acc[x][2 * tid + 1];
+      }
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (int64_t)(u.t0 + i) * p.o_st +
+                                   (int64_t)head * p.o_sh + 2 * tid) =
+          BF16 ? pack_bf16x2(a0 * inv, a1 * inv) : pack_f16x2(a0 * inv, a1 * inv);
+    }
+    if (p.lse != nullptr && tid == 0)
+      p.lse[(int64_t)head * p.total_q + u.t0 + i] = z == 0.f ? -INFINITY : mx + logf(z);
+    __syncthreads();
+  }
+}
+
+// Programmatic stream serialisation (as for the forward kernel): the grid may
+// be scheduled while its predecessor on the stream ends; griddepcontrol.wait
+// in the kernel keeps its memory accesses behind the predecessor's completion.
+template <typename... A>
+cudaError_t launch_pdl(void (*kern)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int MT>
+cudaError_t launch_one(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, cudaStream_t stream) {
+  using C = PagedCfg<ETATTN_INST_D, MT>;
+  auto kern = attn_paged_kernel<ETATTN_INST_D, MT, ETATTN_INST_BF16 != 0>;
+  // The dynamic shared-memory opt-in is per device; set it once per device.
+  static std::atomic<unsigned long long> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  e = launch_pdl(kern, dim3(p.shares), C::THREADS, C::SMEM_BYTES, stream, k, v, p);
+  if (e != cudaSuccess || p.shares == 1) return e;
+  return launch_pdl(paged_join_kernel<ETATTN_INST_D, ETATTN_INST_BF16 != 0>, dim3(p.shares), 256, 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t ETATTN_PAGED_LAUNCHER(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p,
+                                  cudaStream_t stream) {
+  return p.row_tile == 16 ? launch_one<16>(k, v, p, stream) : launch_one<32>(k, v, p, stream);
+}
+
+}  // namespace etattn

@@ -84,4 +84,85 @@ ETATTN_DECLARE_BWD_LAUNCHER(launch_bwd_d128_1)
 
 #undef ETATTN_DECLARE_BWD_LAUNCHER
 
+// Query/key norm and rotation, plain or into a paged cache (attn_rope.cu).
+// Strides in elements: token, head (pages: page, head, token); d-stride 1.
+struct RopeParams {
+  const void *q, *k, *v;           // [T, Hq, D], [T, Hk, D]; v: paged form only
+  const void *q_weight, *k_weight; // [D] in the input type, or nullptr: no norm
+  const float *cos, *sin;          // [max_position, rope_dim / 2]
+  const int* positions;            // [T]: plain form
+  void *q_out, *k_out, *v_out;     // [T, H, D]; paged: k_out, v_out are the pages
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, qo_st, qo_sh;
+  int64_t kp_sp, kp_sh, kp_st, vp_sp, vp_sh, vp_st;  // plain form: kp_st, kp_sh of k_out
+  int total_tokens, Hq, Hk;
+  int rope_dim, interleaved, max_position;
+  float eps;
+  int paged;
+  const int *block_table, *seqlens_k, *cu_seqlens;   // cu_seqlens nullptr: tokens_per_seq each
+  int64_t table_stride;
+  int num_seqs, tokens_per_seq, max_pages, num_pages, page_shift;
+  int* status;
+};
+
+// Its gradients.
+struct RopeBwdParams {
+  const void *q, *k, *dq_out, *dk_out;
+  const void *q_weight, *k_weight;
+  const float *cos, *sin;
+  const int* positions;
+  void *dq, *dk;
+  float *dq_weight, *dk_weight;    // [D] or nullptr
+  float* partials;                 // [blocks][2][D]
+  int64_t q_st, q_sh, k_st, k_sh, dqo_st, dqo_sh, dko_st, dko_sh, dq_st, dq_sh, dk_st, dk_sh;
+  int total_tokens, Hq, Hk;
+  int rope_dim, interleaved, max_position;
+  float eps;
+  int blocks;
+  int* status;
+};
+constexpr int kRopeBwdHeads = 1;   // heads a group of threads takes at a time
+
+cudaError_t launch_rope(int D, bool bf16, const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_rope_bwd(int D, bool bf16, const RopeBwdParams& p, cudaStream_t stream);
+
+// Attention over a paged cache (attn_paged_inst.cu).
+// What a CTA whose piece begins inside a unit leaves for the join.
+struct PagedShare {
+  int t0, n, head0, row0;          // the unit: first q row, new tokens, first query head, first row of the tile
+  int first, parts;                // the shares it spans (parts = 0: nothing to join)
+  int pad[2];
+};
+
+struct PagedParams {
+  const void* q;                   // [total_q, Hq, D]
+  void* o;
+  float* lse;                      // [Hq, total_q] or nullptr
+  int64_t q_st, q_sh, o_st, o_sh;
+  const int *block_table, *seqlens_k, *cu_seqlens_q;  // cu_seqlens_q nullptr: tokens_per_seq each
+  int64_t table_stride;
+  int num_seqs, tokens_per_seq, max_seqlen_q, total_q;
+  int Hkv, group;
+  int max_keys;                    // block-table width * page size, at most 2^30
+  int num_pages, page_shift;
+  int win_left, win_right;
+  float scale_log2;
+  int hn_swapped;                  // bit 0 / 1: head and token axes exchanged in the K / V map
+  int row_tile, shares;
+  PagedShare* desc;                // [shares]
+  float *part_lse, *part_o;        // [shares][2][row_tile], [shares][2][row_tile][D]
+  int* status;
+};
+
+#define ETATTN_DECLARE_PAGED_LAUNCHER(name) \
+  cudaError_t name(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, cudaStream_t stream);
+
+ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d32_0)
+ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d32_1)
+ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d64_0)
+ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d64_1)
+ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d128_0)
+ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d128_1)
+
+#undef ETATTN_DECLARE_PAGED_LAUNCHER
+
 }  // namespace etattn

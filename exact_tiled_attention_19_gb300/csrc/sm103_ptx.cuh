@@ -17,6 +17,7 @@ enum DeviceStatus : int {
   kDevOk = 0,
   kDevWaitTimeout = 1,
   kDevBadSeqlens = 2,
+  kDevBadIndex = 3,
 };
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s of global time

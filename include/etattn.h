@@ -81,6 +81,7 @@ enum etattn_status {
   ETATTN_ERR_LAUNCH = 10,      /* a CUDA runtime call failed (the CUDA error is in etattn_last_cuda_error) */
   ETATTN_ERR_DEVICE = 11,      /* the device reported a failure (see etattn_read_device_status) */
   ETATTN_ERR_NO_DEVICE = 12,   /* no sm_103 device is current */
+  ETATTN_ERR_BAD_INDEX = 13,   /* a position or a page of the block table is out of range (found on the device) */
 };
 
 /*
@@ -327,6 +328,158 @@ int attn_fwd_varlen_ex(const void* q, const void* k, const void* v, void* o, flo
                        int window_left, int window_right, float scale, void* stream);
 
 /*
+ * ---- Queries and keys before attention, and the paged cache ----
+ *
+ * The calls below make the q and k that attention reads, store keys and
+ * values in a paged cache and attend over it.  Tokens are packed: [T, H, D]
+ * tensors with strides (t, h, d), as for attn_fwd_varlen, so that views of one
+ * fused projection [T, Hq + 2*Hkv, D] serve as q, k and v.
+ *
+ * Norm: with a weight vector w of D elements (the input type),
+ *     n_d = x_d * w_d / sqrt(mean_e(x_e^2) + eps)          for every head of
+ * every token; without one (NULL), n = x.
+ * Rotation: the first rope_dim elements (0, or a multiple of 16 up to D) are
+ * rotated in pairs (a, b) by the angle of the token's position p and the pair,
+ *     y_a = n_a*cos - n_b*sin,   y_b = n_b*cos + n_a*sin;
+ * pair i is (i, i + rope_dim/2), or (2i, 2i + 1) when interleaved != 0; its
+ * cosine and sine are rope_cos[p * rope_dim/2 + i] and rope_sin[...], FP32
+ * DEVICE tables [max_position, rope_dim/2] (16-byte aligned).  Everything is
+ * computed in FP32 and rounded once.
+ *
+ * Paged cache: k_pages and v_pages are logical [num_pages, Hkv, page_size, D]
+ * with strides (page, head, slot, d), so that [num_pages, page_size, Hkv, D]
+ * storage, or keys and values interleaved in one buffer, work too; page_size
+ * is a power of two from 8 to 4096.  Key position j of sequence s lives in
+ * page block_table[s * table_stride + j / page_size], slot j % page_size;
+ * block_table is DEVICE int32 [num_seqs, max_pages].
+ * seqlens_k: DEVICE int32 [num_seqs], the keys of every sequence, this step's
+ * new tokens included.  cu_seqlens_q: DEVICE int32 [num_seqs + 1], sequence s
+ * owning tokens cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1, or NULL when every
+ * sequence has the same number of new tokens (total / num_seqs).  Token i of
+ * the n new ones of a sequence with Lk keys stands at position i + Lk - n.
+ * Rows of q, k, v and of outputs behind cu_seqlens_q[num_seqs] are neither
+ * read nor written, and a sequence with seqlens_k = 0 is an unused slot of a
+ * padded batch.
+ * Found on the device, recorded in the status word (etattn_read_device_status):
+ * offsets or lengths that do not fit (ETATTN_ERR_BAD_SEQLENS), and positions
+ * past the rotation tables or pages outside 0 .. num_pages-1
+ * (ETATTN_ERR_BAD_INDEX).  Nothing is read or written out of range.
+ */
+
+/*
+ * attn_qk_norm_rope: norm and rotation of queries and keys in one pass.
+ *
+ *   q, q_out: logical [total_tokens, Hq, D];  k, k_out: [total_tokens, Hk, D]
+ *   q_weight, k_weight: [D] in the input type, or NULL (no norm for that one)
+ *   positions: DEVICE int32 [total_tokens], 0 <= position < max_position (may
+ *           be NULL when rope_dim is 0).  A token whose position is out of
+ *           range is skipped and recorded (ETATTN_ERR_BAD_INDEX).
+ *   strides: 12 int64 values, (t, h, d) for q, k, q_out, k_out.
+ *   eps   : finite and > 0 when there is a weight (ETATTN_ERR_BAD_SCALE).
+ * Hq or Hk may be 0 (its pointers may then be NULL).  Outputs must not
+ * overlap an input or each other; different heads of one fused buffer with one
+ * token stride do not.
+ */
+int attn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight, const float* rope_cos,
+                      const float* rope_sin, const int32_t* positions, void* q_out, void* k_out, int total_tokens,
+                      int Hq, int Hk, int D, int dtype, const int64_t* strides, int rope_dim, int interleaved,
+                      int max_position, float eps, void* stream);
+
+/*
+ * attn_qk_norm_rope_bwd: gradients of attn_qk_norm_rope.  With g the upstream
+ * gradient rotated by the negative angle, x the input and
+ * r = 1 / sqrt(mean(x^2) + eps),
+ *     dx_d = r * (g_d*w_d - x_d * r^2 * mean_e(g_e*w_e*x_e)),
+ *     dw_d = sum over tokens and heads of g_d * x_d * r.
+ *
+ *   dq_out, dk_out: upstream gradients, as q_out, k_out
+ *   dq, dk  : gradients of q and k;  dq_weight, dk_weight: FP32 [D], required
+ *             with the weight they belong to.  dw is summed in FP32 in an
+ *             order that depends on the sizes alone.
+ *   strides : 18 int64 values, (t, h, d) for q, k, dq_out, dk_out, dq, dk.
+ *   workspace: caller-owned DEVICE scratch, 256-byte aligned, at least
+ *             attn_qk_norm_rope_bwd_workspace_size bytes when there is a
+ *             weight, private to the call until its last launch has run.
+ * A token whose position is out of range is skipped, as in the forward call,
+ * and adds nothing to dw.  total_tokens = 0 gives dw = 0.
+ */
+int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, const void* q_weight,
+                          const void* k_weight, const float* rope_cos, const float* rope_sin, const int32_t* positions,
+                          void* dq, void* dk, float* dq_weight, float* dk_weight, int total_tokens, int Hq, int Hk,
+                          int D, int dtype, const int64_t* strides, int rope_dim, int interleaved, int max_position,
+                          float eps, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_qk_norm_rope_bwd needs (0 for empty or invalid sizes). */
+size_t attn_qk_norm_rope_bwd_workspace_size(int total_tokens, int Hq, int Hk, int D);
+
+/*
+ * attn_paged_append: this step's keys and values into the paged cache, keys
+ * (and queries) normed and rotated at their positions on the way.
+ *
+ *   q, q_out: [total_tokens, Hq, D]; Hq = 0 leaves them out (NULL)
+ *   k, v    : [total_tokens, Hkv, D];  k_pages, v_pages: the cache, written
+ *             only at the new tokens' slots
+ *   strides : 20 int64 values, (t, h, d) for q, k, v, q_out, then (page, head,
+ *             slot, d) for k_pages and v_pages.
+ *   weights, tables, eps: as for attn_qk_norm_rope; the position is the
+ *             token's place in the cache.
+ * A token whose position would be negative has no place: nothing of it is
+ * written, its q_out row neither.  A token of a bad sequence, past the block
+ * table or the rotation tables, or on a bad page is skipped and recorded.
+ * k_pages and v_pages must not overlap q, k, v or q_out; two sequences must
+ * not be given the same slot to write.
+ */
+int attn_paged_append(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                      const float* rope_cos, const float* rope_sin, void* q_out, void* k_pages, void* v_pages,
+                      const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
+                      int total_tokens, int Hq, int Hkv, int D, int dtype, const int64_t* strides, int page_size,
+                      int num_pages, int max_pages, int64_t table_stride, int rope_dim, int interleaved,
+                      int max_position, float eps, void* stream);
+
+/*
+ * attn_fwd_paged: attention of the new tokens over the paged cache, for few
+ * query rows per sequence (a decode step, or a few drafted tokens; a long
+ * prompt's own attention belongs to attn_fwd_varlen).  The eligibility rule
+ * is that of attn_fwd_ex, with the row of token i at key position i + Lk - n.
+ *
+ *   q, o: logical [total_q, Hq, D];  lse: [Hq, total_q] contiguous FP32 (or NULL)
+ *   strides: 14 int64 values, (t, h, d) for q, (page, head, slot, d) for
+ *           k_pages and v_pages, (t, h, d) for o.
+ *   max_seqlen_q: the most new tokens of a sequence; with cu_seqlens_q = NULL
+ *           the number of each (total_q = num_seqs * max_seqlen_q).
+ *   num_shares: 1 .. 65535.  The key tiles of all sequences and heads are cut
+ *           into that many equal shares that run side by side; a second launch
+ *           joins what a boundary cut (attn_fwd_paged_plan suggests a number).
+ *           The result is the same up to rounding order.
+ *   workspace: caller-owned DEVICE scratch, 256-byte aligned, at least
+ *           attn_fwd_paged_workspace_size bytes (none for one share), private
+ *           to the call until its last launch has run; it may hold anything.
+ * A row without an eligible key gives O = 0 and lse = -inf.  What the cache
+ * holds outside a row's eligible keys (the unused slots of a page, NaN or
+ * infinity among it) does not reach that row, and table entries of pages that
+ * no row of the sequence reads are not looked at.  A page out of range reads
+ * as zeros and is recorded; the rows of that sequence then mean nothing.  A
+ * sequence whose offsets or length do not fit is skipped and recorded.
+ */
+int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                   const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
+                   int max_seqlen_q, int total_q, int Hq, int Hkv, int D, int dtype, const int64_t* strides,
+                   int page_size, int num_pages, int max_pages, int64_t table_stride, int causal, int window_left,
+                   int window_right, float scale, int num_shares, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Bytes of workspace attn_fwd_paged needs (0 for one share, or for empty or
+ * invalid sizes): two FP32 partial rows per share and row of a unit (16 rows,
+ * or 32 when max_seqlen_q * Hq/Hkv > 16), and a descriptor per share. */
+size_t attn_fwd_paged_workspace_size(int Hq, int Hkv, int max_seqlen_q, int D, int num_shares);
+
+/* A number of shares for attn_fwd_paged on the current device: what the GPU
+ * runs at once, and no more than there are key tiles when every sequence has
+ * max_seqlen_k keys.  Returns ETATTN_OK, ETATTN_ERR_NULL_PTR,
+ * ETATTN_ERR_BAD_SHAPE, ETATTN_ERR_BAD_HEADS or ETATTN_ERR_NO_DEVICE. */
+int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int D, int* num_shares);
+
+/*
  * attn_fwd_host: attn_fwd for callers whose q, k, v live in HOST memory and
  * who want O (and lse) back in host memory, all in one call.
  *
@@ -394,8 +547,8 @@ int etattn_last_cuda_error(void);
 
 /*
  * Read the device status word of the current device that kernels set on a
- * failure they detect themselves (a bounded wait that ran out, or a bad
- * cu_seqlens entry).  Synchronises `stream`.  *out receives ETATTN_OK or the
+ * failure they detect themselves (a bounded wait that ran out, a bad cu_seqlens
+ * entry, or a position or page out of range).  Synchronises `stream`.  *out receives ETATTN_OK or the
  * ETATTN_ERR_* code; when clear != 0 the word is reset to 0 afterwards.
  * Returns ETATTN_OK or ETATTN_ERR_LAUNCH.
  */

@@ -16,6 +16,9 @@ Modules
 ``backward``     the gradients dQ, dK, dV of sum(dO * O), from probabilities
                  recomputed by the definition (dense, or sampled rows of a
                  large problem).
+``cache``        norm and rotation of queries and keys with their gradients, the
+                 append to a paged cache and attention over one (pinned in
+                 ``tests/test_oracle_cache.py``).
 
 Sources (web pages, cited by title and section):
   * "Intermediate and advanced extension" (triton-cuda-lab), workshop table row
