@@ -29,7 +29,9 @@ namespace {
 // Block c belongs to share c.  A unit over the shares first .. first + parts
 // - 1 has parts - 1 boundaries; the blocks of the shares after the first take
 // every (parts - 1)-th row of it, so that a unit cut into many parts is joined
-// by many blocks.  Warps take parts; their sums meet in shared memory.
+// by many blocks.  A block with several rows gives each to a warp; one with a
+// single row (many parts) gives its warps every eighth part of it and adds
+// their sums in shared memory.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p) {
   pdl_wait();
@@ -38,56 +40,59 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   constexpr int PER = D / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = min(p.row_tile, u.n * p.group - u.row0);
+  const int r0 = (int)blockIdx.x - u.first - 1, step = u.parts - 1;  // rows r0, r0 + step, ...
+  const bool by_warp = r0 + step < rows;
+  auto slot = [&](int part) { return ((int64_t)(u.first + part) * 2 + (part == 0 ? 1 : 0)) * p.row_tile; };
   __shared__ float s_acc[8][D];
   __shared__ float s_sum[8];
-  __shared__ float s_max[8];
-  auto slot = [&](int part) { return ((int64_t)(u.first + part) * 2 + (part == 0 ? 1 : 0)) * p.row_tile; };
-  for (int r = (int)blockIdx.x - u.first - 1; r < rows; r += u.parts - 1) {
+  for (int r = by_warp ? r0 + warp * step : r0; r < rows; r += by_warp ? 8 * step : rows) {
     float mx = -INFINITY;
-    for (int s = tid; s < u.parts; s += 256) mx = fmaxf(mx, p.part_lse[slot(s) + r]);
+    for (int s = lane; s < u.parts; s += 32) mx = fmaxf(mx, p.part_lse[slot(s) + r]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    if (lane == 0) s_max[warp] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, s_max[i]);
+    if (mx == -INFINITY) mx = 0.f;  // no key at all, or only NaN sums
     float acc[PER], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    if (mx == -INFINITY) mx = 0.f;  // no key at all, or only NaN sums
-    for (int s = warp; s < u.parts; s += 8) {
+#pragma unroll 4
+    for (int s = by_warp ? 0 : warp; s < u.parts; s += by_warp ? 1 : 8) {
       const float w = expf(p.part_lse[slot(s) + r] - mx);
-      if (w == 0.f) continue;  // no eligible key: the partial row is 0
-      sum += w;
       const float* src = p.part_o + (slot(s) + r) * D + lane * PER;
+      sum += w;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] += w * src[i];
+      for (int i = 0; i < PER; ++i) acc[i] += w * src[i];  // (a part without a key is a row of zeros)
     }
+    if (!by_warp) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s_acc[warp][lane * PER + i] = acc[i];
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-    const int rr = u.row0 + r, i = rr / p.group;
-    const int head = u.head0 + rr - i * p.group;
-    float z = 0.f;
+      for (int i = 0; i < PER; ++i) s_acc[warp][lane * PER + i] = acc[i];
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      if (warp != 0) return;
+      sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < 8; ++x) z += s_sum[x];
-    // A row without a key is 0; a NaN sum stays one.
-    const float inv = z == 0.f ? 0.f : 1.f / z;
-    if (tid < D / 2) {
-      float a0 = 0.f, a1 = 0.f;
+      for (int i = 0; i < PER; ++i) acc[i] = 0.f;
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        a0 += s_acc[x][2 * tid];
-        a1 += s_acc[x][2 * tid + 1];
+        sum += s_sum[x];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] += s_acc[x][lane * PER + i];
       }
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (int64_t)(u.t0 + i) * p.o_st +
-                                   (int64_t)head * p.o_sh + 2 * tid) =
-          BF16 ? pack_bf16x2(a0 * inv, a1 * inv) : pack_f16x2(a0 * inv, a1 * inv);
     }
-    if (p.lse != nullptr && tid == 0)
-      p.lse[(int64_t)head * p.total_q + u.t0 + i] = z == 0.f ? -INFINITY : mx + logf(z);
-    __syncthreads();
+    const int rr = u.row0 + r, i = rr / p.group;
+    const int head = u.head0 + rr - i * p.group;
+    // A row without a key is 0; a NaN sum stays one.
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t* dst = static_cast<uint16_t*>(p.o) + (int64_t)(u.t0 + i) * p.o_st + (int64_t)head * p.o_sh + lane * PER;
+    if constexpr (PER == 1) {
+      dst[0] = (uint16_t)(BF16 ? pack_bf16x2(acc[0] * inv, 0.f) : pack_f16x2(acc[0] * inv, 0.f));
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; j += 2)
+        *reinterpret_cast<uint32_t*>(dst + j) =
+            BF16 ? pack_bf16x2(acc[j] * inv, acc[j + 1] * inv) : pack_f16x2(acc[j] * inv, acc[j + 1] * inv);
+    }
+    if (p.lse != nullptr && lane == 0)
+      p.lse[(int64_t)head * p.total_q + u.t0 + i] = sum == 0.f ? -INFINITY : mx + logf(sum);
   }
 }
 

@@ -14,9 +14,13 @@
 //    line, in units order, and cut into `shares` equal pieces, one per CTA,
 //    whatever the sequences' lengths.  A unit cut by a boundary leaves
 //    partial states in the workspace and paged_join_kernel joins them.
-//  * One producer warp looks up the pages of a tile and issues one TMA box
-//    per page and 64 columns (the lanes work on different pages), STAGES
-//    tiles ahead.
+//    Entering a unit costs about a tile's time beside its tiles, so a unit is
+//    kUnitCost tiles longer on the line than it is.
+//  * One producer warp walks the line: it looks up the pages of a tile one
+//    tile ahead and issues one TMA box per page and 64 columns (the lanes work
+//    on different pages), STAGES tiles ahead; a unit's Q rows and its
+//    description go through slots of their own, so that the consumers
+//    find the next unit ready.
 //  * Four consumer warps take a quarter of a tile's keys each, with a private
 //    state, so that they never wait for one another inside a unit; the four
 //    states merge through shared memory at its end.  The products run on
@@ -49,20 +53,27 @@ struct PagedCfg {
   static constexpr int SUB_BYTES = TK * ROW_BYTES;    // one box column of a tile
   static constexpr int TILE_BYTES = HALVES * SUB_BYTES;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V
-  static constexpr int STAGES = D == 32 ? 6 : 3;
-  // Columns merged at a time: the four warps' rows fill 16 KB (MT = 16), or
-  // 8 KB (MT = 32, which also holds Q), so that two CTAs fit on an SM.
-  static constexpr int MERGE_COLS = MT == 16 ? (D < 64 ? D : 64) : 16;
+  // As many stages as let two CTAs share an SM (113 KB each).
+  static constexpr int STAGES = (D == 32 ? 2 : 1) * (MT == 16 ? 3 : 2);
+  static constexpr int MERGE_COLS = 32;               // columns merged at a time
   static constexpr int MERGE_BYTES = 4 * MT * MERGE_COLS * 4;
-  static constexpr int Q_BYTES = MT == 16 ? 0 : MT * D * 2;
+  static constexpr int Q_PITCH = 2 * D + 16;          // padded: no bank conflicts
+  static constexpr int Q_BYTES = MT * Q_PITCH;        // a slot
+  // Slots for a unit's description and Q rows.  16 rows' fragments fit in
+  // registers, and their slot is free again as soon as they are read; 32 rows
+  // are read again in every tile and keep theirs to the end of the unit.
+  static constexpr int SLOTS = MT == 16 ? 1 : 2;
   static constexpr int OFF_MERGE = STAGES * STAGE_BYTES;
   static constexpr int OFF_Q = OFF_MERGE + MERGE_BYTES;
-  static constexpr int OFF_STATE = OFF_Q + Q_BYTES;   // m and l: 2 x 4 warps x MT
-  static constexpr int OFF_SCAN = OFF_STATE + 2 * 4 * MT * 4;
-  static constexpr int OFF_BARS = OFF_SCAN + 64;
-  static constexpr int SMEM_BYTES = OFF_BARS + 2 * STAGES * 8;
+  static constexpr int OFF_STATE = OFF_Q + SLOTS * Q_BYTES;  // m and l: 2 x 4 warps x MT
+  static constexpr int OFF_UNITS = OFF_STATE + 2 * 4 * MT * 4;
+  static constexpr int OFF_BARS = OFF_UNITS + SLOTS * 48;
+  static constexpr int SMEM_BYTES = OFF_BARS + 2 * (STAGES + SLOTS) * 8;
+  static_assert(SMEM_BYTES <= 115712, "two CTAs per SM");
   static constexpr int CONSUMERS = 128, THREADS = 160;
 };
+
+constexpr int kUnitCost = 1;  // tiles that entering a unit costs
 
 // Everything of one sequence that the roles need.
 struct PagedSeq {
@@ -104,26 +115,40 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int s) {
   return q;
 }
 
-// A position on the line of tiles.
-struct PagedWalk {
-  PagedSeq q;
-  int s, unit, tile;
+// A stretch of one unit's tiles, as the producer hands it to the consumers.
+struct PagedUnit {
+  int t0, n, Lk;         // the sequence
+  int head0, row0;       // first query head, first row of the row tile
+  int tile, tiles;       // first tile (of the sequence) and how many; 0 tiles: no more units
+  int from_start, to_end;
+  int pad[3];
 };
+static_assert(sizeof(PagedUnit) == 48, "");
 
+// The sequences s_base .. s_base + 31, one per lane.
 template <class C>
-__device__ __forceinline__ void paged_next_unit(const PagedParams& p, PagedWalk& w) {
-  w.tile = 0;
-  if (++w.unit < w.q.units) return;
-  w.unit = 0;
-  do {
-    ++w.s;
-    if (w.s >= p.num_seqs) {
-      w.q.units = 0;
-      return;
-    }
-    w.q = paged_seq<C>(p, w.s);
-  } while (w.q.units == 0);
-}
+struct PagedWindow {
+  PagedSeq mine;
+  int base;
+  __device__ __forceinline__ void load(const PagedParams& p, int s0, int lane) {
+    base = s0;
+    mine.n = mine.t0 = mine.Lk = mine.tile0 = mine.nrt = mine.units = 0;
+    mine.tiles = 1;
+    if (s0 + lane < p.num_seqs) mine = paged_seq<C>(p, s0 + lane);
+  }
+  __device__ __forceinline__ PagedSeq at(int s) const {
+    const int src = s - base;
+    PagedSeq q;
+    q.n = __shfl_sync(0xffffffffu, mine.n, src);
+    q.t0 = __shfl_sync(0xffffffffu, mine.t0, src);
+    q.Lk = __shfl_sync(0xffffffffu, mine.Lk, src);
+    q.tile0 = __shfl_sync(0xffffffffu, mine.tile0, src);
+    q.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
+    q.nrt = __shfl_sync(0xffffffffu, mine.nrt, src);
+    q.units = __shfl_sync(0xffffffffu, mine.units, src);
+    return q;
+  }
+};
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -152,6 +177,20 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
   }
 }
 
+// One arrival of the warp on `bar`, giving back shared memory that it has read.
+// A read is issued before the arrival but need not have been served by then:
+// nothing makes the arrival wait for a register that is still on its way, and a
+// refill then overtakes the last reads (it did, where bank conflicts held them
+// up).  So the arrival's address takes in `seen`, a value made of everything
+// that was read, and with `zero` (a 0 that the compiler does not know) leaves
+// it where it is.
+__device__ __forceinline__ void release_after(uint64_t* bar, uint32_t seen, uint32_t zero, int lane) {
+  const uint32_t off = seen & zero;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(bar) + off));
+  __syncwarp();
+}
+
 // Byte offset of 16-byte column `c16` of row `row` in a tile as TMA writes it
 // (128-byte swizzle: bits 4-6 take bits 7-9; 64-byte: bits 4-5 take bits 7-8).
 template <class C>
@@ -163,16 +202,199 @@ __device__ __forceinline__ uint32_t tile_off(int row, int c16) {
   }
 }
 
-// Splits the line: where CTA `c` of `shares` starts, and its length.
-__device__ __forceinline__ int64_t share_start(int64_t total, int shares, int c) {
-  const int64_t each = total / shares, rest = total - each * shares;
-  return c * each + min((int64_t)c, rest);
+// a / b for a >= 0, b > 0, in 32 bits where they do (the 64-bit division is a
+// long call, several times on the way to a CTA's first load).
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
-// The CTA that owns tile x.
-__device__ __forceinline__ int share_of(int64_t total, int shares, int64_t x) {
-  const int64_t each = total / shares, rest = total - each * shares;
-  const int64_t big = rest * (each + 1);
-  return (int)(x < big ? x / (each + 1) : rest + (x - big) / each);
+
+// The line cut into shares: the first `rest` of them one longer than `each`.
+struct PagedCut {
+  int64_t each, rest;
+  __device__ __forceinline__ PagedCut(int64_t total, int shares) {
+    each = div_pos(total, shares);
+    rest = total - each * shares;
+  }
+  __device__ __forceinline__ int64_t start(int c) const { return c * each + min((int64_t)c, rest); }
+  __device__ __forceinline__ int holder(int64_t x) const {
+    const int64_t big = rest * (each + 1);
+    return (int)(x < big ? div_pos(x, each + 1) : rest + div_pos(x - big, each));
+  }
+};
+
+// The producer warp.
+template <class C>
+__device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedParams& p,
+                                               uint8_t* smem, int lane) {
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* ufull = empty + C::STAGES;
+  uint64_t* uempty = ufull + C::SLOTS;
+  PagedUnit* units = reinterpret_cast<PagedUnit*>(smem + C::OFF_UNITS);
+  uint32_t uphase = 1;
+  int uslot = 0;
+  // Hands over the end of the line.
+  auto finish = [&]() {
+    if (!mbar_wait(uempty + uslot, uphase, p.status)) return;
+    if (lane == 0) {
+      units[uslot].tiles = 0;
+      mbar_arrive(ufull + uslot);
+    }
+  };
+
+  // This CTA's piece of the line: lane i sums up its run of sequences; the
+  // lane whose run holds the piece's start finds the sequence.
+  const int per = (p.num_seqs + 31) / 32;
+  const int s_begin = min(p.num_seqs, lane * per), s_end = min(p.num_seqs, s_begin + per);
+  auto length = [](const PagedSeq& q) { return (int64_t)q.units * (q.tiles + kUnitCost); };
+  int64_t mine = 0;
+  for (int s = s_begin; s < s_end; ++s) mine += length(paged_seq<C>(p, s));
+  int64_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+  const int share = blockIdx.x;
+  const PagedCut cut(total, p.shares);
+  const int64_t begin = cut.start(share), end = cut.start(share + 1);
+  PagedShare* desc = p.desc + share;
+  if (begin >= end) {
+    if (lane == 0 && p.shares > 1) desc->parts = 0;
+    finish();
+    return;
+  }
+  int s = 0;
+  int64_t at = incl - mine;
+  const bool holds = begin >= at && begin < incl;
+  if (holds)
+    for (s = s_begin;; ++s) {
+      const int64_t len = length(paged_seq<C>(p, s));
+      if (begin < at + len) break;
+      at += len;
+    }
+  const int holder = __ffs(__ballot_sync(0xffffffffu, holds)) - 1;
+  s = __shfl_sync(0xffffffffu, s, holder);
+  at = __shfl_sync(0xffffffffu, at, holder);
+  PagedWindow<C> win;
+  win.load(p, s, lane);
+  PagedSeq q = win.at(s);
+  int unit = (int)div_pos(begin - at, q.tiles + kUnitCost);
+  int64_t u0 = at + (int64_t)unit * (q.tiles + kUnitCost);  // where the unit lies on the line
+  int tile = max(0, (int)(begin - u0) - kUnitCost);
+
+  PagedShare mark{};  // for the join, written at the end
+  int64_t mark_u0 = 0;
+  int mark_tiles = 0;
+  if (tile > 0) {
+    mark.t0 = q.t0;
+    mark.n = q.n;
+    mark.head0 = (unit / q.nrt) * p.group;
+    mark.row0 = (unit % q.nrt) * C::MT;
+    mark_u0 = u0 + kUnitCost;
+    mark_tiles = q.tiles;
+  }
+
+  const int page_keys = 1 << p.page_shift;
+  const int box_keys = min(page_keys, C::TK);
+  const int boxes = C::TK / box_keys;  // pages of a tile (1 when a page holds whole tiles); at most 16
+  const uint32_t box_bytes = (uint32_t)box_keys * C::ROW_BYTES;
+  const uint64_t policy = l2_policy_evict_first();
+  uint32_t phase = 1;
+  int stage = 0;
+
+  // Unit by unit; `stop` is the end of this share's tiles in the unit.
+  while (true) {
+    const int stop = (int)max((int64_t)0, min((int64_t)q.tiles, end - u0 - kUnitCost));
+    if (tile < stop) {
+      const int head = unit / q.nrt;
+      const int row0 = (unit - head * q.nrt) * C::MT, rows = min(C::MT, q.n * p.group - row0);
+      // Keys that some row of the sequence reads; a box beside them is not loaded.
+      const int lo = max(0, q.Lk - q.n - p.win_left);
+      const int hi = (int)min((int64_t)q.Lk - 1, (int64_t)q.Lk - 1 + p.win_right);
+      const int* table = p.block_table + (int64_t)s * p.table_stride;
+      auto wants = [&](int k0) { return lane < boxes && k0 <= hi && k0 + box_keys > lo; };
+      auto look_up = [&](int t) {
+        const int k0 = (q.tile0 + t) * C::TK + lane * box_keys;
+        return wants(k0) ? table[k0 >> p.page_shift] : 0;
+      };
+      int page = look_up(tile);
+
+      if (!mbar_wait(uempty + uslot, uphase, p.status)) return;
+      if (lane == 0) {
+        units[uslot] = PagedUnit{q.t0, q.n, q.Lk, head * p.group, row0, q.tile0 + tile, stop - tile, tile == 0,
+                                 stop == q.tiles, {0, 0, 0}};
+        mbar_arrive_expect_tx(ufull + uslot, (uint32_t)rows * 2 * C::D);
+      }
+      __syncwarp();
+      if (lane < rows) {
+        const int rr = row0 + lane, i = rr / p.group;
+        bulk_load(smem + C::OFF_Q + uslot * C::Q_BYTES + lane * C::Q_PITCH,
+                  static_cast<const uint16_t*>(p.q) + (int64_t)(q.t0 + i) * p.q_st +
+                      (int64_t)(head * p.group + rr - i * p.group) * p.q_sh,
+                  2 * C::D, ufull + uslot);
+      }
+      if (++uslot == C::SLOTS) {
+        uslot = 0;
+        uphase ^= 1;
+      }
+
+      for (; tile < stop; ++tile) {
+        const int k0 = (q.tile0 + tile) * C::TK + lane * box_keys;
+        const bool on = wants(k0);
+        int pg = page;
+        if (tile + 1 < stop) page = look_up(tile + 1);
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, on));
+        if (!mbar_wait(empty + stage, phase, p.status)) return;
+        uint8_t* base = smem + stage * C::STAGE_BYTES;
+        if (lane == 0) mbar_arrive_expect_tx(full + stage, loads * 2 * C::HALVES * box_bytes);
+        __syncwarp();
+        if (on) {
+          if (pg < 0 || pg >= p.num_pages) {
+            atomicCAS(p.status, 0, (int)kDevBadIndex);
+            pg = p.num_pages;  // past the map: the box is filled with zeros
+          }
+          const int slot = k0 & (page_keys - 1);
+#pragma unroll
+          for (int h = 0; h < C::HALVES; ++h) {
+            uint8_t* dst = base + h * C::SUB_BYTES + lane * box_bytes;
+            tma_load_4d_hint(dst, &kmap, full + stage, h * C::COLS, (p.hn_swapped & 1) ? head : slot,
+                             (p.hn_swapped & 1) ? slot : head, pg, policy);
+            tma_load_4d_hint(dst + C::TILE_BYTES, &vmap, full + stage, h * C::COLS, (p.hn_swapped & 2) ? head : slot,
+                             (p.hn_swapped & 2) ? slot : head, pg, policy);
+          }
+        }
+        __syncwarp();
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // The next unit of the line.
+    u0 += q.tiles + kUnitCost;
+    if (u0 >= end) break;
+    tile = 0;
+    if (++unit == q.units) {
+      unit = 0;
+      do {  // u0 < end <= total: some later sequence has units
+        if (++s == win.base + 32) win.load(p, s, lane);
+        q = win.at(s);
+      } while (q.units == 0);
+    }
+  }
+  // The join of a unit that began in an earlier share is shared by those that
+  // continue it: each leaves itself the unit and its shares.
+  if (lane == 0 && p.shares > 1) {
+    if (mark_tiles > 0) {
+      mark.first = cut.holder(mark_u0);
+      mark.parts = cut.holder(mark_u0 + mark_tiles - 1) - mark.first + 1;
+    }
+    *desc = mark;
+  }
+  finish();
 }
 
 template <int D, int MT, bool BF16>
@@ -185,7 +407,8 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
   uint64_t* empty = full + C::STAGES;
-  volatile int64_t* scan = reinterpret_cast<volatile int64_t*>(smem + C::OFF_SCAN);
+  uint64_t* ufull = empty + C::STAGES;
+  uint64_t* uempty = ufull + C::SLOTS;
 
   pdl_launch_dependents();
   if (tid == 0) {
@@ -193,133 +416,18 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
       mbar_init(full + i, 1);
       mbar_init(empty + i, 4);
     }
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(ufull + i, 1);
+      mbar_init(uempty + i, 4);
+    }
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
+  __syncthreads();
   pdl_wait();
-
-  // ------------------------------------------------ this CTA's piece of the line
-  // Thread i sums up the tiles of its run of sequences; the thread whose run
-  // holds the piece's first tile finds the place inside it.
-  const int per = (p.num_seqs + C::THREADS - 1) / C::THREADS;
-  const int s_begin = min(p.num_seqs, tid * per), s_end = min(p.num_seqs, s_begin + per);
-  int64_t mine = 0;
-  for (int s = s_begin; s < s_end; ++s) {
-    const PagedSeq q = paged_seq<C>(p, s);
-    mine += (int64_t)q.units * q.tiles;
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += o;
-  }
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  int64_t total = 0, before = incl - mine;
-#pragma unroll
-  for (int w = 0; w < 5; ++w) {
-    const int64_t v = scan[w];
-    if (w < warp) before += v;
-    total += v;
-  }
-  __syncthreads();
-  const int share = blockIdx.x;
-  const int64_t begin = share_start(total, p.shares, share), end = share_start(total, p.shares, share + 1);
-  PagedShare* desc = p.desc + share;
-  if (begin >= end) {
-    if (tid == 0 && p.shares > 1) desc->parts = 0;
-    return;
-  }
-  if (begin >= before && begin < before + mine) {
-    int64_t at = before;
-    for (int s = s_begin;; ++s) {
-      const PagedSeq q = paged_seq<C>(p, s);
-      const int64_t len = (int64_t)q.units * q.tiles;
-      if (begin < at + len) {
-        scan[0] = s;
-        scan[1] = (begin - at) / q.tiles;
-        scan[2] = (begin - at) % q.tiles;
-        break;
-      }
-      at += len;
-    }
-  }
-  __syncthreads();
-  PagedWalk w;
-  w.s = (int)scan[0];
-  w.unit = (int)scan[1];
-  w.tile = (int)scan[2];
-  w.q = paged_seq<C>(p, w.s);
-  const int count = (int)(end - begin);  // tiles of this CTA
-
-  // The join of a unit that began in an earlier CTA is shared by the CTAs
-  // that continue it: each leaves itself the unit and its CTAs.
-  if (tid == 0 && p.shares > 1) {
-    if (w.tile > 0) {
-      const int64_t u0 = begin - w.tile;
-      desc->t0 = w.q.t0;
-      desc->n = w.q.n;
-      desc->head0 = (w.unit / w.q.nrt) * p.group;
-      desc->row0 = (w.unit % w.q.nrt) * MT;
-      desc->first = share_of(total, p.shares, u0);
-      desc->parts = share_of(total, p.shares, u0 + w.q.tiles - 1) - desc->first + 1;
-    } else {
-      desc->parts = 0;
-    }
-  }
-
   if (warp == 4) {
-    // ---------------------------------------------- producer
-    const int page_keys = 1 << p.page_shift;
-    const int box_keys = min(page_keys, C::TK);
-    const int boxes = C::TK / box_keys;  // pages of a tile (1 when a page holds whole tiles)
-    const uint32_t box_bytes = (uint32_t)box_keys * C::ROW_BYTES;
-    const uint64_t policy = l2_policy_evict_first();
-    uint32_t phase = 1;
-    int stage = 0;
-    for (int i = 0; i < count; ++i) {
-      const int head = w.unit / w.q.nrt;
-      const int key0 = (w.q.tile0 + w.tile) * C::TK;
-      // Keys that some row of the sequence reads; a box past them is not loaded.
-      const int lo = max(0, w.q.Lk - w.q.n - p.win_left);
-      const int hi = (int)min((int64_t)w.q.Lk - 1, (int64_t)w.q.Lk - 1 + p.win_right);
-      if (!mbar_wait(empty + stage, phase, p.status)) return;
-      uint8_t* base = smem + stage * C::STAGE_BYTES;
-      uint32_t loads = 0;
-      for (int b0 = 0; b0 < boxes; b0 += 32) {
-        const int b = b0 + lane, k0 = key0 + b * box_keys;
-        const bool on = b < boxes && k0 <= hi && k0 + box_keys > lo;
-        loads += __popc(__ballot_sync(0xffffffffu, on));
-      }
-      if (lane == 0) mbar_arrive_expect_tx(full + stage, loads * 2 * C::HALVES * box_bytes);
-      __syncwarp();
-      for (int b = lane; b < boxes; b += 32) {
-        const int k0 = key0 + b * box_keys;
-        if (!(k0 <= hi && k0 + box_keys > lo)) continue;
-        int page = p.block_table[(int64_t)w.s * p.table_stride + (k0 >> p.page_shift)];
-        if (page < 0 || page >= p.num_pages) {
-          atomicCAS(p.status, 0, (int)kDevBadIndex);
-          page = p.num_pages;  // past the map: the box is filled with zeros
-        }
-        const int slot = k0 & (page_keys - 1);
-#pragma unroll
-        for (int h = 0; h < C::HALVES; ++h) {
-          uint8_t* dst = base + h * C::SUB_BYTES + b * box_bytes;
-          tma_load_4d_hint(dst, &kmap, full + stage, h * C::COLS, (p.hn_swapped & 1) ? head : slot,
-                           (p.hn_swapped & 1) ? slot : head, page, policy);
-          tma_load_4d_hint(dst + C::TILE_BYTES, &vmap, full + stage, h * C::COLS, (p.hn_swapped & 2) ? head : slot,
-                           (p.hn_swapped & 2) ? slot : head, page, policy);
-        }
-      }
-      __syncwarp();
-      if (++stage == C::STAGES) {
-        stage = 0;
-        phase ^= 1;
-      }
-      if (++w.tile == w.q.tiles) paged_next_unit<C>(p, w);
-    }
+    paged_producer<C>(kmap, vmap, p, smem, lane);
     return;
   }
 
@@ -328,13 +436,21 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
   float* st_m = reinterpret_cast<float*>(smem + C::OFF_STATE);
   float* st_l = st_m + 4 * MT;
   float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
-  uint32_t phase = 0;
-  int stage = 0, left = count;
+  const int share = blockIdx.x;
+  uint32_t phase = 0, uphase = 0;
+  int stage = 0, uslot = 0;
   bool alive = true;
-  while (left > 0) {
-    const int head0 = (w.unit / w.q.nrt) * p.group, row0 = (w.unit % w.q.nrt) * MT;
-    const int rows = min(MT, w.q.n * p.group - row0);
-    const int delta = w.q.Lk - w.q.n;
+  while (true) {
+    // A wait that ran out in one warp ends them all, here, where none of them
+    // waits in a barrier for another.
+    alive = alive && mbar_wait(ufull + uslot, uphase, p.status);
+    if (named_barrier_or(1, C::CONSUMERS, !alive)) return;
+    __syncwarp();
+    const PagedUnit w = reinterpret_cast<const PagedUnit*>(smem + C::OFF_UNITS)[uslot];
+    if (w.tiles == 0) return;
+    const int head0 = w.head0, row0 = w.row0;
+    const int rows = min(MT, w.n * p.group - row0);
+    const int delta = w.Lk - w.n;
     // The tokens of this row tile and the rows' key ranges (rows g, g + 8, ...).
     const int tok_first = row0 / p.group, tok_last = (row0 + rows - 1) / p.group;
     int tok[2 * NM], row_lo[2 * NM], row_hi[2 * NM];
@@ -344,39 +460,26 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
       tok[j] = min((row0 + r) / p.group, tok_last);
       const int c = tok[j] + delta;
       row_lo[j] = max(0, c - p.win_left);
-      row_hi[j] = (int)min((int64_t)w.q.Lk - 1, (int64_t)c + p.win_right);
+      row_hi[j] = (int)min((int64_t)w.Lk - 1, (int64_t)c + p.win_right);
     }
     // Keys in [in_lo, in_hi] are read by every row of the tile.
     const int in_lo = max(0, tok_last + delta - p.win_left);
-    const int in_hi = (int)min((int64_t)w.q.Lk - 1, (int64_t)tok_first + delta + p.win_right);
+    const int in_hi = (int)min((int64_t)w.Lk - 1, (int64_t)tok_first + delta + p.win_right);
 
-    // Q: fragments in registers (MT = 16), or rows in shared memory.
-    auto q_row = [&](int r) {
-      const int rr = row0 + r, i = rr / p.group;
-      return static_cast<const uint16_t*>(p.q) + (int64_t)(w.q.t0 + i) * p.q_st +
-             (int64_t)(head0 + rr - i * p.group) * p.q_sh;
+    // Q: fragments in registers (MT = 16), or read from its slot in every tile
+    // (MT = 32).  Rows past the last hold anything; nothing of them is written.
+    const uint32_t qbase = smem_u32(smem + C::OFF_Q + uslot * C::Q_BYTES);
+    auto load_q = [&](uint32_t (&f)[4], int a, int ks) {
+      ldsm4(f, qbase + (a * 16 + (lane & 15)) * C::Q_PITCH + (ks * 2 + (lane >> 4)) * 16);
     };
     uint32_t qf[NM == 1 ? D / 16 : 1][4];
     if constexpr (NM == 1) {
-      const uint16_t* r0 = g < rows ? q_row(g) : nullptr;
-      const uint16_t* r1 = g + 8 < rows ? q_row(g + 8) : nullptr;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const int d = ks * 16 + 2 * t4;
-        qf[ks][0] = r0 ? *reinterpret_cast<const uint32_t*>(r0 + d) : 0u;
-        qf[ks][1] = r1 ? *reinterpret_cast<const uint32_t*>(r1 + d) : 0u;
-        qf[ks][2] = r0 ? *reinterpret_cast<const uint32_t*>(r0 + d + 8) : 0u;
-        qf[ks][3] = r1 ? *reinterpret_cast<const uint32_t*>(r1 + d + 8) : 0u;
-      }
-    } else {
-      // 16-byte column c of row r at r * 2D + ((c ^ (r & 7 of the row's columns)) * 16).
-      constexpr int CH = D / 8, SWZ = CH < 8 ? CH - 1 : 7;
-      for (int x = tid; x < MT * CH; x += C::CONSUMERS) {
-        const int r = x / CH, c = x % CH;
-        const uint4 v = r < rows ? *reinterpret_cast<const uint4*>(q_row(r) + 8 * c) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(smem + C::OFF_Q + r * 2 * D + ((c ^ (r & SWZ)) << 4)) = v;
-      }
-      named_barrier(1, C::CONSUMERS);
+      for (int ks = 0; ks < D / 16; ++ks) load_q(qf[ks], 0, ks);
+      uint32_t seen = 0;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) seen |= qf[ks][0] | qf[ks][1] | qf[ks][2] | qf[ks][3];
+      release_after(uempty + uslot, seen, p.zero, lane);
     }
 
     float m[2 * NM], l[2 * NM], o[NM][D / 8][4];
@@ -389,12 +492,11 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[a][n][i] = 0.f;
 
-    const bool from_start = w.tile == 0;
-    const int here = min(left, w.q.tiles - w.tile);
-    const bool to_end = w.tile + here == w.q.tiles;
-    for (int x = 0; x < here; ++x) {
-      const int key0 = (w.q.tile0 + w.tile + x) * C::TK + warp * C::WK;
-      if (alive) alive = mbar_wait(full + stage, phase, p.status);
+    for (int x = 0; x < w.tiles; ++x) {
+      const int key0 = (w.tile + x) * C::TK + warp * C::WK;
+      alive = alive && mbar_wait(full + stage, phase, p.status);
+      alive = __all_sync(0xffffffffu, alive);  // and the lanes, which leave the wait one by one, are together
+      uint32_t seen = 0;  // everything read of V (what is read of K goes into the maxima)
       if (alive) {
         const uint32_t kbase = smem_u32(smem + stage * C::STAGE_BYTES), vbase = kbase + C::TILE_BYTES;
         constexpr int KB = C::WK / 16;
@@ -413,12 +515,8 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 4; ++i) qa[0][i] = qf[ks][i];
           } else {
-            constexpr int CH = D / 8, SWZ = CH < 8 ? CH - 1 : 7;
 #pragma unroll
-            for (int a = 0; a < NM; ++a) {
-              const int r = a * 16 + (lane & 15), c = ks * 2 + (lane >> 4);
-              ldsm4(qa[a], smem_u32(smem + C::OFF_Q) + r * 2 * D + ((c ^ (r & SWZ)) << 4));
-            }
+            for (int a = 0; a < NM; ++a) load_q(qa[a], a, ks);
           }
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
@@ -500,6 +598,7 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
             for (int n = 0; n < D / 16; ++n) {
               uint32_t b[4];
               ldsm4_trans(b, vbase + tile_off<C>(row, 2 * n + (lane >> 4)));
+              seen |= b[0] | b[1] | b[2] | b[3];
 #pragma unroll
               for (int a = 0; a < NM; ++a) {
                 mma16816<BF16>(o[a][2 * n], pf[a][kb], b[0], b[1]);
@@ -512,7 +611,7 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
             const int key = key0 + kb * 16 + 2 * t4;
             for (int tk = tok_first; tk <= tok_last; ++tk) {
               const int lo = max(0, tk + delta - p.win_left);
-              const int hi = (int)min((int64_t)w.q.Lk - 1, (int64_t)tk + delta + p.win_right);
+              const int hi = (int)min((int64_t)w.Lk - 1, (int64_t)tk + delta + p.win_right);
               auto keep = [&](int k) { return k >= lo && k <= hi; };
               const uint32_t m0 = (keep(key) ? 0xffffu : 0u) | (keep(key + 1) ? 0xffff0000u : 0u);
               const uint32_t m1 = (keep(key + 8) ? 0xffffu : 0u) | (keep(key + 9) ? 0xffff0000u : 0u);
@@ -521,6 +620,7 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
               for (int n = 0; n < D / 16; ++n) {
                 uint32_t b[4];
                 ldsm4_trans(b, vbase + tile_off<C>(row, 2 * n + (lane >> 4)));
+              seen |= b[0] | b[1] | b[2] | b[3];
 #pragma unroll
                 for (int a = 0; a < NM; ++a)
 #pragma unroll
@@ -536,14 +636,17 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + stage);
+      release_after(empty + stage, seen, p.zero, lane);
       if (++stage == C::STAGES) {
         stage = 0;
         phase ^= 1;
       }
     }
-    left -= here;
+    if constexpr (NM > 1) release_after(uempty + uslot, __float_as_uint(l[0]), p.zero, lane);
+    if (++uslot == C::SLOTS) {
+      uslot = 0;
+      uphase ^= 1;
+    }
 
     // Merge the four warps' states.
 #pragma unroll
@@ -568,10 +671,10 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
       for (int x = 0; x < 4; ++x) ll += st_l[x * MT + r] * ex2_approx(st_m[x * MT + r] - ref);
       inv[j] = ll == 0.f ? 0.f : ex2_approx(m[j] - ref) / ll;  // no key: 0; a NaN sum stays one
     }
-    const bool whole = from_start && to_end;
+    const bool whole = w.from_start && w.to_end;
     // Where this piece of the unit goes: the output, or the workspace (slot 0
     // for a unit that began earlier, slot 1 for one that begins here).
-    const int64_t part_row = ((int64_t)share * 2 + (from_start ? 1 : 0)) * MT;
+    const int64_t part_row = ((int64_t)share * 2 + (w.from_start ? 1 : 0)) * MT;
     if (tid < rows) {
       const int r = tid;
       float mm = -INFINITY, ll = 0.f;
@@ -584,14 +687,14 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
       if (whole) {
         if (p.lse != nullptr) {
           const int rr = row0 + r, i = rr / p.group;
-          p.lse[(int64_t)(head0 + rr - i * p.group) * p.total_q + w.q.t0 + i] = lse;
+          p.lse[(int64_t)(head0 + rr - i * p.group) * p.total_q + w.t0 + i] = lse;
         }
       } else {
         p.part_lse[part_row + r] = lse;
       }
     }
     constexpr int MC = C::MERGE_COLS;
-    auto swz = [](int r) { return MC >= 32 ? (r & 3) << 3 : ((r >> 1) & 1) << 3; };
+    auto swz = [](int r) { return (r & 3) << 3; };  // keeps a warp's eight rows out of one another's banks
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += MC) {
 #pragma unroll
@@ -626,7 +729,7 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             u[k] = BF16 ? pack_bf16x2(v[2 * k], v[2 * k + 1]) : pack_f16x2(v[2 * k], v[2 * k + 1]);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (int64_t)(w.q.t0 + i) * p.o_st +
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (int64_t)(w.t0 + i) * p.o_st +
                                     (int64_t)(head0 + rr - i * p.group) * p.o_sh + c0 + c) =
               make_uint4(u[0], u[1], u[2], u[3]);
         } else {
@@ -637,8 +740,6 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
       }
       named_barrier(1, C::CONSUMERS);
     }
-    w.tile += here;
-    if (left > 0) paged_next_unit<C>(p, w);
   }
 }
 

@@ -2,6 +2,7 @@
 // and element type), implemented in attn_fwd_inst.cu.
 #pragma once
 
+#include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -150,6 +151,7 @@ struct PagedParams {
   int row_tile, shares;
   PagedShare* desc;                // [shares]
   float *part_lse, *part_o;        // [shares][2][row_tile], [shares][2][row_tile][D]
+  uint32_t zero;                   // 0 (the kernel's release_after)
   int* status;
 };
 

@@ -126,6 +126,17 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void named_barrier(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
+// The same, telling every thread whether some thread's `x` is set.
+__device__ __forceinline__ bool named_barrier_or(int id, int count, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
 
 // Programmatic dependent launch: let the next grid on the stream be
 // scheduled now, and wait until the grids this one depends on have completed
