@@ -26,6 +26,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -113,17 +114,17 @@ def load_library(path: str | None = None):
         lib.attn_fwd_varlen_host.restype = _int
         lib.attn_fwd_varlen_host_plan.argtypes = [_vp, _int, _int, ctypes.POINTER(ctypes.c_int32)]
         lib.attn_fwd_varlen_host_plan.restype = _int
-        lib.attn_qk_norm_rope.argtypes = [_vp] * 9 + [_int] * 5 + [_i64p] + [_int] * 3 + [ctypes.c_float, _vp]
+        lib.attn_qk_norm_rope.argtypes = [_vp] * 9 + [_int] * 5 + [ctypes.c_char_p] + [_int] * 3 + [ctypes.c_float, _vp]
         lib.attn_qk_norm_rope.restype = _int
-        lib.attn_qk_norm_rope_bwd.argtypes = ([_vp] * 13 + [_int] * 5 + [_i64p] + [_int] * 3 +
+        lib.attn_qk_norm_rope_bwd.argtypes = ([_vp] * 13 + [_int] * 5 + [ctypes.c_char_p] + [_int] * 3 +
                                               [ctypes.c_float, _vp, ctypes.c_size_t, _vp])
         lib.attn_qk_norm_rope_bwd.restype = _int
         lib.attn_qk_norm_rope_bwd_workspace_size.argtypes = [_int] * 4
         lib.attn_qk_norm_rope_bwd_workspace_size.restype = ctypes.c_size_t
-        lib.attn_paged_append.argtypes = ([_vp] * 13 + [_int] * 6 + [_i64p] + [_int] * 3 + [ctypes.c_int64] +
+        lib.attn_paged_append.argtypes = ([_vp] * 13 + [_int] * 6 + [ctypes.c_char_p] + [_int] * 3 + [ctypes.c_int64] +
                                           [_int] * 3 + [ctypes.c_float, _vp])
         lib.attn_paged_append.restype = _int
-        lib.attn_fwd_paged.argtypes = ([_vp] * 8 + [_int] * 7 + [_i64p] + [_int] * 3 + [ctypes.c_int64] + [_int] * 3 +
+        lib.attn_fwd_paged.argtypes = ([_vp] * 8 + [_int] * 7 + [ctypes.c_char_p] + [_int] * 3 + [ctypes.c_int64] + [_int] * 3 +
                                        [ctypes.c_float, _int, _vp, ctypes.c_size_t, _vp])
         lib.attn_fwd_paged.restype = _int
         lib.attn_fwd_paged_workspace_size.argtypes = [_int] * 5
@@ -276,7 +277,7 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, rope_cos, rope_sin, positions, q
     lib = load_library()
     return lib.attn_qk_norm_rope(q or None, k or None, q_weight or None, k_weight or None, rope_cos or None,
                                  rope_sin or None, positions or None, q_out or None, k_out or None, total_tokens, Hq,
-                                 Hk, D, dtype, _strides_arg(strides), rope_dim, interleaved, max_position, eps,
+                                 Hk, D, dtype, _STRIDES[12](*strides), rope_dim, interleaved, max_position, eps,
                                  stream or None)
 
 
@@ -288,7 +289,7 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope_cos, ro
     return lib.attn_qk_norm_rope_bwd(q or None, k or None, dq_out or None, dk_out or None, q_weight or None,
                                      k_weight or None, rope_cos or None, rope_sin or None, positions or None,
                                      dq or None, dk or None, dq_weight or None, dk_weight or None, total_tokens, Hq,
-                                     Hk, D, dtype, _strides_arg(strides), rope_dim, interleaved, max_position, eps,
+                                     Hk, D, dtype, _STRIDES[18](*strides), rope_dim, interleaved, max_position, eps,
                                      workspace or None, workspace_bytes, stream or None)
 
 
@@ -304,7 +305,7 @@ def attn_paged_append(q, k, v, q_weight, k_weight, rope_cos, rope_sin, q_out, k_
     return lib.attn_paged_append(q or None, k or None, v or None, q_weight or None, k_weight or None,
                                  rope_cos or None, rope_sin or None, q_out or None, k_pages or None, v_pages or None,
                                  block_table or None, seqlens_k or None, cu_seqlens_q or None, num_seqs, total_tokens,
-                                 Hq, Hkv, D, dtype, _strides_arg(strides), page_size, num_pages, max_pages,
+                                 Hq, Hkv, D, dtype, _STRIDES[20](*strides), page_size, num_pages, max_pages,
                                  table_stride, rope_dim, interleaved, max_position, eps, stream or None)
 
 
@@ -315,7 +316,7 @@ def attn_fwd_paged(q, k_pages, v_pages, o, lse, block_table, seqlens_k, cu_seqle
     lib = load_library()
     return lib.attn_fwd_paged(q or None, k_pages or None, v_pages or None, o or None, lse or None, block_table or None,
                               seqlens_k or None, cu_seqlens_q or None, num_seqs, max_seqlen_q, total_q, Hq, Hkv, D,
-                              dtype, _strides_arg(strides), page_size, num_pages, max_pages, table_stride, causal,
+                              dtype, _STRIDES[14](*strides), page_size, num_pages, max_pages, table_stride, causal,
                               window_left, window_right, scale, num_shares, workspace or None, workspace_bytes,
                               stream or None)
 
@@ -634,43 +635,71 @@ def attention_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = Tru
     return out, lse
 
 
+# The calls of one decode step take a few microseconds on the device, so the
+# helpers below keep their own time down: one comparison per tensor on the way
+# through (the messages are made when it fails), strides packed into bytes, the
+# device made current only when it is not, and the C functions called directly.
+
+_STRIDES = {n: struct.Struct(f"{n}q").pack for n in (12, 14, 18, 20)}
+
+
+class _NoSwitch:
+    """Stands in for ``torch.cuda.device`` when the device is current already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SWITCH = _NoSwitch()
+
+
+def _on(torch, device):
+    """A context in which ``device`` is current."""
+    if device.type == "cuda" and torch.cuda.current_device() == device.index:
+        return _NO_SWITCH
+    return torch.cuda.device(device)
+
+
+def _raw_stream(torch, device, stream):
+    """The stream's handle: the given one's, or the device's current one's."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else int(stream.cuda_stream)
+
+
 def _address(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _like(name, t, shape, dtype, device):
-    """Checks an optional tensor argument."""
-    if t is None:
+def _like(name, t, shape, dtype, device, dense=False):
+    """Checks a tensor argument (None passes)."""
+    if t is None or (t.shape == shape and t.dtype == dtype and t.device == device
+                     and (not dense or t.is_contiguous())):
         return
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _dense(name, t):
-    if t is not None and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _rope_args(D, dtype, device, q_weight, k_weight, rope_cos, rope_sin):
+def _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos, rope_sin):
     """(rope_dim, max_position) of the rotation tables, after checking them and the weights."""
-    import torch
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _like(name, t, (D,), dtype, device)
-        _dense(name, t)
-    if (rope_cos is None) != (rope_sin is None):
-        raise ValueError("rope_cos and rope_sin come together")
-    if rope_cos is None:
+    _like("q_weight", q_weight, (D,), dtype, device, True)
+    _like("k_weight", k_weight, (D,), dtype, device, True)
+    if rope_cos is None and rope_sin is None:
         return 0, 0
-    if rope_cos.dim() != 2:
+    if rope_cos is None or rope_sin is None:
+        raise ValueError("rope_cos and rope_sin come together")
+    shape = rope_cos.shape
+    if len(shape) != 2:
         raise ValueError("rope_cos and rope_sin must be [max_position, rope_dim / 2]")
-    for name, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)):
-        _like(name, t, tuple(rope_cos.shape), torch.float32, device)
-        _dense(name, t)
-    return 2 * rope_cos.shape[1], rope_cos.shape[0]
+    _like("rope_cos", rope_cos, shape, torch.float32, device, True)
+    _like("rope_sin", rope_sin, shape, torch.float32, device, True)
+    return 2 * shape[1], shape[0]
 
 
 def rope_tables(max_position: int, rope_dim: int, *, theta: float = 10000.0, device=None):
@@ -695,26 +724,27 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, rope_cos=None, rope_sin=
     none.  Views of a fused projection serve as q and k."""
     import torch
     T, Hq, D = q.shape
-    Hk = k.shape[1]
-    dtype, device = _dtype_code(q), q.device
-    _like("k", k, (T, Hk, D), q.dtype, device)
-    rope_dim, max_position = _rope_args(D, q.dtype, device, q_weight, k_weight, rope_cos, rope_sin)
-    if rope_dim:
-        if positions is None:
-            raise ValueError("positions are needed with rope_cos and rope_sin")
-        _like("positions", positions, (T,), torch.int32, device)
-        _dense("positions", positions)
-    _like("q_out", q_out, (T, Hq, D), q.dtype, device)
-    _like("k_out", k_out, (T, Hk, D), q.dtype, device)
-    with torch.cuda.device(device):
+    Hk, dtype, device = k.shape[1], q.dtype, q.device
+    code = _dtype_code(q)
+    _like("k", k, (T, Hk, D), dtype, device)
+    rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos, rope_sin)
+    if rope_dim and positions is None:
+        raise ValueError("positions are needed with rope_cos and rope_sin")
+    _like("positions", positions, (T,), torch.int32, device, True)
+    with _on(torch, device):
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=device)
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        else:
+            _like("q_out", q_out, (T, Hq, D), dtype, device)
         if k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=device)
-        rc = attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), _address(q_weight), _address(k_weight), _address(rope_cos),
-                               _address(rope_sin), _address(positions), q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hk,
-                               D, dtype, (*q.stride(), *k.stride(), *q_out.stride(), *k_out.stride()), rope_dim,
-                               1 if interleaved else 0, max_position, float(eps), _stream_handle(stream))
+            k_out = torch.empty((T, Hk, D), dtype=dtype, device=device)
+        else:
+            _like("k_out", k_out, (T, Hk, D), dtype, device)
+        rc = (_lib or load_library()).attn_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), _address(q_weight), _address(k_weight), _address(rope_cos), _address(rope_sin),
+            _address(positions), q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hk, D, code,
+            _STRIDES[12](*q.stride(), *k.stride(), *q_out.stride(), *k_out.stride()), rope_dim,
+            1 if interleaved else 0, max_position, eps, _raw_stream(torch, device, stream))
     if rc != 0:
         raise EtattnError(rc, "attn_qk_norm_rope")
     return q_out, k_out
@@ -728,56 +758,67 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
     (None without the weight)."""
     import torch
     T, Hq, D = q.shape
-    Hk = k.shape[1]
-    dtype, device = _dtype_code(q), q.device
-    _like("k", k, (T, Hk, D), q.dtype, device)
-    rope_dim, max_position = _rope_args(D, q.dtype, device, q_weight, k_weight, rope_cos, rope_sin)
-    if rope_dim:
-        if positions is None:
-            raise ValueError("positions are needed with rope_cos and rope_sin")
-        _like("positions", positions, (T,), torch.int32, device)
-        _dense("positions", positions)
-    for name, t, H in (("dq_out", dq_out, Hq), ("dk_out", dk_out, Hk), ("dq", dq, Hq), ("dk", dk, Hk)):
-        _like(name, t, (T, H, D), q.dtype, device)
-    with torch.cuda.device(device):
+    Hk, dtype, device = k.shape[1], q.dtype, q.device
+    code = _dtype_code(q)
+    _like("k", k, (T, Hk, D), dtype, device)
+    _like("dq_out", dq_out, (T, Hq, D), dtype, device)
+    _like("dk_out", dk_out, (T, Hk, D), dtype, device)
+    rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos, rope_sin)
+    if rope_dim and positions is None:
+        raise ValueError("positions are needed with rope_cos and rope_sin")
+    _like("positions", positions, (T,), torch.int32, device, True)
+    lib = _lib or load_library()
+    with _on(torch, device):
         if dq is None:
-            dq = torch.empty((T, Hq, D), dtype=q.dtype, device=device)
+            dq = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        else:
+            _like("dq", dq, (T, Hq, D), dtype, device)
         if dk is None:
-            dk = torch.empty((T, Hk, D), dtype=q.dtype, device=device)
+            dk = torch.empty((T, Hk, D), dtype=dtype, device=device)
+        else:
+            _like("dk", dk, (T, Hk, D), dtype, device)
         dwq = torch.empty(D, dtype=torch.float32, device=device) if q_weight is not None else None
         dwk = torch.empty(D, dtype=torch.float32, device=device) if k_weight is not None else None
-        need = attn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D) if dwq is not None or dwk is not None else 0
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        rc = attn_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
-                                   _address(q_weight), _address(k_weight), _address(rope_cos), _address(rope_sin),
-                                   _address(positions), dq.data_ptr(), dk.data_ptr(), _address(dwq), _address(dwk), T,
-                                   Hq, Hk, D, dtype,
-                                   (*q.stride(), *k.stride(), *dq_out.stride(), *dk_out.stride(), *dq.stride(),
-                                    *dk.stride()), rope_dim, 1 if interleaved else 0, max_position, float(eps),
-                                   _address(workspace),
-                                   workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                   _stream_handle(stream))
+        if dwq is None and dwk is None:
+            ws_bytes = 0
+        elif workspace is None:
+            ws_bytes = lib.attn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D)
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        else:
+            _workspace(workspace, device)
+            ws_bytes = workspace.numel() * workspace.element_size()
+        rc = lib.attn_qk_norm_rope_bwd(
+            q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), _address(q_weight), _address(k_weight),
+            _address(rope_cos), _address(rope_sin), _address(positions), dq.data_ptr(), dk.data_ptr(), _address(dwq),
+            _address(dwk), T, Hq, Hk, D, code,
+            _STRIDES[18](*q.stride(), *k.stride(), *dq_out.stride(), *dk_out.stride(), *dq.stride(), *dk.stride()),
+            rope_dim, 1 if interleaved else 0, max_position, eps, _address(workspace), ws_bytes,
+            _raw_stream(torch, device, stream))
     if rc != 0:
         raise EtattnError(rc, "attn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
-def _page_args(k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device):
-    """Checks the cache's tensors; returns (num_seqs, num_pages, Hkv, page_size)."""
-    import torch
-    num_pages, Hkv, page_size, D = k_pages.shape
-    _like("k_pages", k_pages, (num_pages, Hkv, page_size, D), dtype, device)
-    _like("v_pages", v_pages, (num_pages, Hkv, page_size, D), dtype, device)
-    S = block_table.shape[0]
-    _like("block_table", block_table, (S, block_table.shape[1]), torch.int32, device)
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+def _workspace(t, device):
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+
+
+def _page_args(torch, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device):
+    """Checks the cache's tensors; returns (num_seqs, max_pages, table_stride)."""
+    shape = k_pages.shape
+    if len(shape) != 4:
+        raise ValueError("k_pages must be [num_pages, Hkv, page_size, D]")
+    _like("k_pages", k_pages, shape, dtype, device)
+    _like("v_pages", v_pages, shape, dtype, device)
+    S, width = block_table.shape
+    _like("block_table", block_table, (S, width), torch.int32, device)
+    row, col = block_table.stride()
+    if col != 1 and width > 1:
         raise ValueError("block_table's rows must be contiguous")
-    _like("seqlens_k", seqlens_k, (S,), torch.int32, device)
-    _dense("seqlens_k", seqlens_k)
-    _like("cu_seqlens_q", cu_seqlens_q, (S + 1,), torch.int32, device)
-    _dense("cu_seqlens_q", cu_seqlens_q)
-    return S, num_pages, Hkv, page_size
+    _like("seqlens_k", seqlens_k, (S,), torch.int32, device, True)
+    _like("cu_seqlens_q", cu_seqlens_q, (S + 1,), torch.int32, device, True)
+    return S, width, row
 
 
 def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_weight=None, k_weight=None,
@@ -793,31 +834,32 @@ def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_we
     keys of every sequence with the new ones; cu_seqlens_q: int32 [S + 1]
     offsets of the new tokens, None when every sequence has T / S."""
     import torch
-    T, Hk, D = k.shape
-    dtype, device = _dtype_code(k), k.device
-    S, num_pages, Hkv, page_size = _page_args(k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, k.dtype, device)
-    _like("k", k, (T, Hkv, k_pages.shape[3]), k.dtype, device)
-    _like("v", v, (T, Hkv, D), k.dtype, device)
-    Hq = 0
-    if q is not None:
-        Hq = q.shape[1]
-        _like("q", q, (T, Hq, D), k.dtype, device)
-        _like("q_out", q_out, (T, Hq, D), k.dtype, device)
-    rope_dim, max_position = _rope_args(D, k.dtype, device, q_weight, k_weight, rope_cos, rope_sin)
-    with torch.cuda.device(device):
+    T, _, D = k.shape
+    dtype, device = k.dtype, k.device
+    code = _dtype_code(k)
+    S, width, row = _page_args(torch, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device)
+    num_pages, Hkv, page_size, Dp = k_pages.shape
+    _like("k", k, (T, Hkv, Dp), dtype, device)
+    _like("v", v, (T, Hkv, Dp), dtype, device)
+    rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos, rope_sin)
+    with _on(torch, device):
         if q is None:
-            q_out = None
-        elif q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=k.dtype, device=device)
-        q_stride = (0, 0, 1) if q is None else q.stride()
-        o_stride = (0, 0, 1) if q is None else q_out.stride()
-        rc = attn_paged_append(_address(q), k.data_ptr(), v.data_ptr(), _address(q_weight), _address(k_weight),
-                               _address(rope_cos), _address(rope_sin), _address(q_out), k_pages.data_ptr(),
-                               v_pages.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(),
-                               _address(cu_seqlens_q), S, T, Hq, Hkv, D, dtype,
-                               (*q_stride, *k.stride(), *v.stride(), *o_stride, *k_pages.stride(),
-                                *v_pages.stride()), page_size, num_pages, block_table.shape[1], block_table.stride(0),
-                               rope_dim, 1 if interleaved else 0, max_position, float(eps), _stream_handle(stream))
+            Hq, q_out, q_stride, o_stride = 0, None, (0, 0, 1), (0, 0, 1)
+        else:
+            Hq = q.shape[1]
+            _like("q", q, (T, Hq, D), dtype, device)
+            if q_out is None:
+                q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+            else:
+                _like("q_out", q_out, (T, Hq, D), dtype, device)
+            q_stride, o_stride = q.stride(), q_out.stride()
+        rc = (_lib or load_library()).attn_paged_append(
+            _address(q), k.data_ptr(), v.data_ptr(), _address(q_weight), _address(k_weight), _address(rope_cos),
+            _address(rope_sin), _address(q_out), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+            seqlens_k.data_ptr(), _address(cu_seqlens_q), S, T, Hq, Hkv, D, code,
+            _STRIDES[20](*q_stride, *k.stride(), *v.stride(), *o_stride, *k_pages.stride(), *v_pages.stride()),
+            page_size, num_pages, width, row, rope_dim, 1 if interleaved else 0, max_position, eps,
+            _raw_stream(torch, device, stream))
     if rc != 0:
         raise EtattnError(rc, "attn_paged_append")
     return q_out
@@ -839,41 +881,48 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
     bytes) may be given, as a captured graph's owner would."""
     import torch
     T, Hq, D = q.shape
-    dtype, device = _dtype_code(q), q.device
-    S, num_pages, Hkv, page_size = _page_args(k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, q.dtype, device)
-    if k_pages.shape[3] != D:
-        raise ValueError(f"k_pages has head dim {k_pages.shape[3]}, q has {D}")
+    dtype, device = q.dtype, q.device
+    code = _dtype_code(q)
+    S, width, row = _page_args(torch, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device)
+    num_pages, Hkv, page_size, Dp = k_pages.shape
+    if Dp != D:
+        raise ValueError(f"k_pages has head dim {Dp}, q has {D}")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if cu_seqlens_q is None:
         max_seqlen_q = T // S if S > 0 else 0
     elif max_seqlen_q is None:
         raise ValueError("max_seqlen_q is needed with cu_seqlens_q")
-    _like("out", out, (T, Hq, D), q.dtype, device)
-    _like("lse", lse, (Hq, T), torch.float32, device)
-    _dense("lse", lse)
-    _dense("workspace", workspace)
-    with torch.cuda.device(device):
+    lib = _lib or load_library()
+    with _on(torch, device):
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        else:
+            _like("out", out, (T, Hq, D), dtype, device)
+        if lse is not None:
+            _like("lse", lse, (Hq, T), torch.float32, device, True)
+        elif return_lse:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
         if num_shares is None:
-            most = block_table.shape[1] * page_size if max_seqlen_k is None else int(max_seqlen_k)
-            rc, num_shares = attn_fwd_paged_plan(S, Hq, Hkv, int(max_seqlen_q), min(most, 1 << 30), D)
+            if max_seqlen_k is None:
+                max_seqlen_k = min(width * page_size, 1 << 30)
+            plan = _int(0)
+            rc = lib.attn_fwd_paged_plan(S, Hq, Hkv, int(max_seqlen_q), int(max_seqlen_k), D, plan)
             if rc != 0:
                 raise EtattnError(rc, "attn_fwd_paged_plan")
-        need = attn_fwd_paged_workspace_size(Hq, Hkv, int(max_seqlen_q), D, int(num_shares))
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if out is None:
-            out = torch.empty((T, Hq, D), dtype=q.dtype, device=device)
-        if lse is None and return_lse:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
-        rc = attn_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _address(lse),
-                            block_table.data_ptr(), seqlens_k.data_ptr(), _address(cu_seqlens_q), S,
-                            int(max_seqlen_q), T, Hq, Hkv, D, dtype,
-                            (*q.stride(), *k_pages.stride(), *v_pages.stride(), *out.stride()), page_size, num_pages,
-                            block_table.shape[1], block_table.stride(0), 1 if causal else 0, int(window_left),
-                            int(window_right), float(scale), int(num_shares), _address(workspace),
-                            workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                            _stream_handle(stream))
+            num_shares = plan.value
+        if workspace is None:
+            ws_bytes = lib.attn_fwd_paged_workspace_size(Hq, Hkv, int(max_seqlen_q), D, int(num_shares))
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes > 0 else None
+        else:
+            _workspace(workspace, device)
+            ws_bytes = workspace.numel() * workspace.element_size()
+        rc = lib.attn_fwd_paged(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _address(lse),
+            block_table.data_ptr(), seqlens_k.data_ptr(), _address(cu_seqlens_q), S, int(max_seqlen_q), T, Hq, Hkv, D, code,
+            _STRIDES[14](*q.stride(), *k_pages.stride(), *v_pages.stride(), *out.stride()), page_size, num_pages,
+            width, row, 1 if causal else 0, int(window_left), int(window_right), scale, int(num_shares), _address(workspace),
+            ws_bytes, _raw_stream(torch, device, stream))
     if rc != 0:
         raise EtattnError(rc, "attn_fwd_paged")
     return out, lse

@@ -202,13 +202,6 @@ __device__ __forceinline__ uint32_t tile_off(int row, int c16) {
   }
 }
 
-// a / b for a >= 0, b > 0, in 32 bits where they do (the 64-bit division is a
-// long call, several times on the way to a CTA's first load).
-__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
-
 // The line cut into shares: the first `rest` of them one longer than `each`.
 struct PagedCut {
   int64_t each, rest;

@@ -14,11 +14,15 @@
 //
 // Everything is computed in FP32 from the 16-bit inputs and rounded once, to
 // the type of the output.  Each row is read and written once, so memory
-// bounds these kernels.  D/8 threads hold a row, 16 bytes each.
+// bounds these kernels once the instructions per element are few.  D/16
+// threads hold a row, two 16-byte chunks each, chosen so that both elements of
+// every pair are in one thread: pair rotation needs no exchange, and a row's
+// two sums take log2(D/16) shuffles.  All heads of a group of threads share
+// the token and so the coefficients: with P = w cos and Q = -/+ w sin of the
+// partner folded together, an output is r (x P + x_partner Q), in paired FP32
+// arithmetic.
+#include <atomic>
 #include <cstdint>
-#include <cstring>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "launchers.h"
@@ -47,6 +51,35 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A thread's own 16-byte cells of shared memory, filled by asynchronous copies
+// that it alone waits for.
+__device__ __forceinline__ void copy_async(uint4* cell, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(cell)), "l"(src) : "memory");
+}
+// The same for what neighbouring groups read too: through L1.
+__device__ __forceinline__ void copy_async_shared(uint4* cell, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(cell)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+// copy_wait for a count that becomes a constant when its loop is unrolled.
+__device__ __forceinline__ void copy_wait_for(int pending) {
+  switch (pending) {
+    case 0: copy_wait<0>(); break;
+    case 1: copy_wait<1>(); break;
+    case 2: copy_wait<2>(); break;
+    case 3: copy_wait<3>(); break;
+    case 4: copy_wait<4>(); break;
+    case 5: copy_wait<5>(); break;
+    case 6: copy_wait<6>(); break;
+    default: copy_wait<7>(); break;
+  }
+}
+
+// The sum over the LANES threads that hold a row.
 template <int LANES>
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
@@ -54,64 +87,94 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// The thread's share of a token's angles: chunk c holds elements 8c .. 8c+7.
-// Paired with the other half, element j has cos[j], sin[j] of its own; side by
-// side, pair j of the chunk (elements 2j, 2j + 1) has cos[j], sin[j], j < 4.
-struct Angles {
-  float c[8], s[8];
+// A thread's two chunks of a row.  Rotated lanes hold the pairs (first + j,
+// second + j), or, interleaved, 16 neighbours; the others 16 neighbours past
+// rope_dim.
+struct Chunks {
+  int first, second;  // element offsets
+  bool rotated;
 };
+__device__ __forceinline__ Chunks chunks_of(int lane, int rope_dim, bool interleaved) {
+  if (interleaved) return {16 * lane, 16 * lane + 8, 16 * lane < rope_dim};
+  const int n = rope_dim / 16;
+  if (lane < n) return {8 * lane, rope_dim / 2 + 8 * lane, true};
+  return {16 * lane, 16 * lane + 8, false};
+}
 
-__device__ __forceinline__ void load_angles(Angles& a, const float* cos, const float* sin, int64_t pos, int rope_dim,
-                                            bool interleaved, int chunk) {
-  const int half = rope_dim / 2;
-  if (8 * chunk >= rope_dim) return;
-  const int first = interleaved ? 4 * chunk : (8 * chunk < half ? 8 * chunk : 8 * chunk - half);
-  const float* pc = cos + pos * half + first;
-  const float* ps = sin + pos * half + first;
+// cos and sin of the thread's eight pairs (1 and 0 where nothing rotates).
+__device__ __forceinline__ void load_angles(float (&c)[8], float (&s)[8], const float* cos, const float* sin,
+                                            int64_t pos, int rope_dim, int lane, bool rotated) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c[j] = 1.f, s[j] = 0.f;
+  if (!rotated) return;
+  const float* pc = cos + pos * (rope_dim / 2) + 8 * lane;  // half and interleaved pairs alike: 8 lane ..
+  const float* ps = sin + pos * (rope_dim / 2) + 8 * lane;
 #pragma unroll
   for (int j = 0; j < 8; j += 4) {
-    if (j == 4 && interleaved) break;
     const float4 c4 = *reinterpret_cast<const float4*>(pc + j), s4 = *reinterpret_cast<const float4*>(ps + j);
-    a.c[j] = c4.x, a.c[j + 1] = c4.y, a.c[j + 2] = c4.z, a.c[j + 3] = c4.w;
-    a.s[j] = s4.x, a.s[j + 1] = s4.y, a.s[j + 2] = s4.z, a.s[j + 3] = s4.w;
+    c[j] = c4.x, c[j + 1] = c4.y, c[j + 2] = c4.z, c[j + 3] = c4.w;
+    s[j] = s4.x, s[j + 1] = s4.y, s[j + 2] = s4.z, s[j + 3] = s4.w;
   }
 }
 
-// Rotates the thread's eight elements by sign * angle.  Every thread of the
-// warp takes part (the other half of a row is in its other threads).
-__device__ __forceinline__ void rotate(float (&n)[8], const Angles& a, int rope_dim, bool interleaved, int chunk,
-                                       float sign) {
-  if (rope_dim == 0) return;
-  if (interleaved) {
-    if (8 * chunk >= rope_dim) return;
+// Index of element i's partner among the thread's 16 (chunk first: 0-7,
+// second: 8-15) and of their pair.
+template <bool INTER>
+__device__ __forceinline__ constexpr int partner(int i) { return INTER ? (i ^ 1) : (i ^ 8); }
+template <bool INTER>
+__device__ __forceinline__ constexpr int pair_of(int i) { return INTER ? (i >> 1) : (i & 7); }
+template <bool INTER>
+__device__ __forceinline__ constexpr bool is_first(int i) { return INTER ? (i & 1) == 0 : i < 8; }
+
+template <bool BF16>
+__device__ __forceinline__ void load_weight(const void* w, const Chunks& ch, float (&f)[16]) {
+  if (w != nullptr) {
+    float lo[8], hi[8];
+    unpack8<BF16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + ch.first), lo);
+    unpack8<BF16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + ch.second), hi);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float c = a.c[j], s = sign * a.s[j], x = n[2 * j], y = n[2 * j + 1];
-      n[2 * j] = x * c - y * s;
-      n[2 * j + 1] = y * c + x * s;
-    }
-    return;
-  }
-  const int half_chunks = rope_dim / 16;
-  const bool first = chunk < half_chunks, second = !first && chunk < 2 * half_chunks;
-  const int lane = threadIdx.x & 31;
-  const int other = first ? lane + half_chunks : second ? lane - half_chunks : lane;
+    for (int j = 0; j < 8; ++j) f[j] = lo[j], f[8 + j] = hi[j];
+  } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float o = __shfl_sync(0xffffffffu, n[j], other);
-    // first half: x cos - y sin; second: y cos + x sin
-    if (first) n[j] = n[j] * a.c[j] - o * (sign * a.s[j]);
-    else if (second) n[j] = n[j] * a.c[j] + o * (sign * a.s[j]);
+    for (int j = 0; j < 16; ++j) f[j] = 1.f;
   }
 }
 
 template <bool BF16>
-__device__ __forceinline__ void load_weight(const void* w, int chunk, float (&f)[8]) {
-  if (w != nullptr) {
-    unpack8<BF16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + 8 * chunk), f);
-  } else {
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&x)[16]) {
+  float lo[8], hi[8];
+  unpack8<BF16>(a, lo);
+  unpack8<BF16>(b, hi);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = 1.f;
+  for (int j = 0; j < 8; ++j) x[j] = lo[j], x[8 + j] = hi[j];
+}
+template <bool BF16>
+__device__ __forceinline__ void store16(uint16_t* row, const Chunks& ch, const float (&y)[16]) {
+  float lo[8], hi[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) lo[j] = y[j], hi[j] = y[8 + j];
+  *reinterpret_cast<uint4*>(row + ch.first) = pack8<BF16>(lo);
+  *reinterpret_cast<uint4*>(row + ch.second) = pack8<BF16>(hi);
+}
+// sum of a[j] * b[j]
+__device__ __forceinline__ float dot16(const float (&a)[16], const float (&b)[16]) {
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) fma2(s0, s1, a[j], a[j + 1], b[j], b[j + 1], s0, s1);
+  return s0 + s1;
+}
+// y = x P + x_partner Q.  A lane that does not rotate must not meet its
+// "partner" (0 times infinity is not 0).
+template <bool INTER, bool FULL>
+__device__ __forceinline__ void turn16(const float (&x)[16], const float (&P)[16], const float (&Q)[16], bool rotated,
+                                       float (&y)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    const float o0 = FULL || rotated ? x[partner<INTER>(j)] : 0.f;
+    const float o1 = FULL || rotated ? x[partner<INTER>(j + 1)] : 0.f;
+    float t0, t1;
+    fma2(t0, t1, x[j], x[j + 1], P[j], P[j + 1], 0.f, 0.f);
+    fma2(y[j], y[j + 1], o0, o1, Q[j], Q[j + 1], t0, t1);
   }
 }
 
@@ -177,18 +240,19 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, int t) {
   return r;
 }
 
-// Group of D/8 threads: HP consecutive heads of one token, so that the
+// A group of D/16 threads takes HP consecutive heads of one token, so that the
 // position, its angles and the weights are read once for all of them.  The
 // heads of a token are numbered q, then k, then (paged) v; a group's heads are
-// all of one kind.
-template <int D, bool BF16, int HP>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p) {
-  constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
-  const int chunk = threadIdx.x % LANES;
+// all of one kind.  FULL: the whole head is rotated.
+template <int D, bool BF16, int HP, bool INTER, bool FULL>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int LANES = D / 16, GROUPS = kThreads / LANES;
+  const int lane = threadIdx.x % LANES;
+  const Chunks ch = chunks_of(lane, FULL ? D : p.rope_dim, INTER);
   const int cq = (p.Hq + HP - 1) / HP, ck = (p.Hk + HP - 1) / HP, per_token = cq + (p.paged ? 2 : 1) * ck;
   const int64_t item = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES;
   const bool live = item < (int64_t)p.total_tokens * per_token;
-  const int t = live ? (int)(item / per_token) : 0;
+  const int t = live ? (int)div_pos(item, per_token) : 0;
   int c = live ? (int)(item - (int64_t)t * per_token) : 0;
   const int kind = c < cq ? 0 : c < cq + ck ? 1 : 2;
   c -= kind == 0 ? 0 : kind == 1 ? cq : cq + ck;
@@ -196,12 +260,26 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p) {
   const void* src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
   const int64_t st = kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st;
   const int64_t sh = kind == 0 ? p.q_sh : kind == 1 ? p.k_sh : p.v_sh;
-  const uint16_t* in = static_cast<const uint16_t*>(src) + t * st + 8 * chunk;
+  const uint16_t* in = static_cast<const uint16_t*>(src) + t * st + h0 * sh;
 
-  uint4 raw[HP];
+  // One row a group (few rows: latency counts) waits in registers; several are
+  // all on their way at once into the thread's cells, [row][half][thread].
+  constexpr bool STAGED = HP > 1;
+  extern __shared__ uint4 cells[];
+  uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
 #pragma unroll
-  for (int i = 0; i < HP; ++i)
-    raw[i] = live && h0 + i < heads ? *reinterpret_cast<const uint4*>(in + (h0 + i) * sh) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < HP; ++i) {
+    if (live && h0 + i < heads) {
+      if constexpr (STAGED) {
+        copy_async(cells + (2 * i) * kThreads + threadIdx.x, in + i * sh + ch.first);
+        copy_async(cells + (2 * i + 1) * kThreads + threadIdx.x, in + i * sh + ch.second);
+      } else {
+        ra = *reinterpret_cast<const uint4*>(in + ch.first);
+        rb = *reinterpret_cast<const uint4*>(in + ch.second);
+      }
+    }
+    if constexpr (STAGED) copy_commit();
+  }
 
   Place at{false, 0, 0, 0};
   if (live) at = place_of(p, t);
@@ -218,180 +296,312 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p) {
     out = static_cast<uint16_t*>(p.v_out) + at.v_off;
     oh = p.vp_sh;
   }
-  out += 8 * chunk;
+  out += h0 * oh;
 
   const void* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-  float w[8];
-  load_weight<BF16>(weight, chunk, w);
-  Angles ang;
-  const int rope_dim = kind == 2 ? 0 : p.rope_dim;
-  if (ok && rope_dim > 0) load_angles(ang, p.cos, p.sin, at.pos, rope_dim, p.interleaved, chunk);
+  const bool rotated = kind != 2 && ch.rotated;
+  float P[16], Q[16];
+  {
+    float w[16], c8[8], s8[8];
+    load_weight<BF16>(weight, ch, w);
+    load_angles(c8, s8, p.cos, p.sin, ok ? at.pos : 0, FULL ? D : p.rope_dim, lane, ok && rotated);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      P[j] = w[j] * c8[pair_of<INTER>(j)];
+      Q[j] = (is_first<INTER>(j) ? -1.f : 1.f) * w[partner<INTER>(j)] * s8[pair_of<INTER>(j)];
+    }
+  }
 
 #pragma unroll
   for (int i = 0; i < HP; ++i) {
-    float x[8];
-    unpack8<BF16>(raw[i], x);
-    float ss = 0.f;
+    if constexpr (STAGED) {
+      copy_wait_for(HP - 1 - i);
+      ra = cells[(2 * i) * kThreads + threadIdx.x];
+      rb = cells[(2 * i + 1) * kThreads + threadIdx.x];
+    }
+    float x[16], y[16];
+    unpack16<BF16>(ra, rb, x);
+    const float ss = row_sum<LANES>(dot16(x, x));
+    turn16<INTER, FULL>(x, P, Q, rotated, y);
+    if (weight != nullptr) {
+      const float r = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-    ss = row_sum<LANES>(ss);
-    const float r = weight != nullptr ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
-    // A warp holds groups of different kinds: all of them shuffle.
-    rotate(x, ang, p.rope_dim, p.interleaved, rope_dim > 0 ? chunk : 1 << 20, 1.f);
-    if (ok && h0 + i < heads)
-      *reinterpret_cast<uint4*>(out + (h0 + i) * oh) = kind == 2 ? raw[i] : pack8<BF16>(x);
+      for (int j = 0; j < 16; j += 2) fma2(y[j], y[j + 1], y[j], y[j + 1], r, r, 0.f, 0.f);
+    }
+    if (ok && h0 + i < heads) {
+      if (kind == 2) {
+        *reinterpret_cast<uint4*>(out + i * oh + ch.first) = ra;
+        *reinterpret_cast<uint4*>(out + i * oh + ch.second) = rb;
+      } else {
+        store16<BF16>(out + i * oh, ch, y);
+      }
+    }
   }
 }
 
-// Gradients.  Each group strides over (token, HP heads) items and keeps the
-// weight gradients of its rows in registers; a block leaves one partial sum
-// per weight element, and rope_bwd_weights_kernel adds them in a fixed order.
-template <int D, bool BF16, int HP>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(RopeBwdParams p) {
-  constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
-  const int chunk = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-  const int cq = (p.Hq + HP - 1) / HP, ck = (p.Hk + HP - 1) / HP, per_token = cq + ck;
-  const int64_t items = (int64_t)p.total_tokens * per_token, stride = (int64_t)gridDim.x * GROUPS;
-  float accq[8], acck[8];
+// Gradients.  The first q_blocks blocks take q's rows and the others k's.  Each
+// group strides over (token, HP heads) items and keeps the weight gradient of
+// its rows in registers; a block leaves one partial sum per weight element,
+// and rope_bwd_weights_kernel adds them in a fixed order.
+template <int D, bool BF16, int HP, bool INTER, bool FULL>
+__global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
+  constexpr int LANES = D / 16, GROUPS = kThreads / LANES;
+  pdl_launch_dependents();
+  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  const Chunks ch = chunks_of(lane, FULL ? D : p.rope_dim, INTER);
+  const bool is_q = (int)blockIdx.x < p.q_blocks;
+  const int block = is_q ? blockIdx.x : blockIdx.x - p.q_blocks;
+  const int blocks = is_q ? p.q_blocks : p.blocks - p.q_blocks;
+  const int heads = is_q ? p.Hq : p.Hk;
+  const int64_t xh = is_q ? p.q_sh : p.k_sh, gh = is_q ? p.dqo_sh : p.dko_sh, oh = is_q ? p.dq_sh : p.dk_sh;
+  const int64_t xt = is_q ? p.q_st : p.k_st, gt = is_q ? p.dqo_st : p.dko_st, ot = is_q ? p.dq_st : p.dk_st;
+  const uint16_t* x0 = static_cast<const uint16_t*>(is_q ? p.q : p.k);
+  const uint16_t* g0 = static_cast<const uint16_t*>(is_q ? p.dq_out : p.dk_out);
+  uint16_t* d0 = static_cast<uint16_t*>(is_q ? p.dq : p.dk);
+  const void* weight = is_q ? p.q_weight : p.k_weight;
+  float w[16], acc[16];
+  load_weight<BF16>(weight, ch, w);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) accq[j] = acck[j] = 0.f;
+  for (int j = 0; j < 16; ++j) acc[j] = 0.f;
 
-  // Every warp makes the same number of rounds in all its groups (shuffles).
-  const int64_t first = (int64_t)blockIdx.x * GROUPS + grp;
-  const int64_t rounds = (items - (int64_t)blockIdx.x * GROUPS + stride - 1) / stride;
-  for (int64_t round = 0; round < rounds; ++round) {
-    const int64_t item = first + round * stride;
-    const bool live = item < items;
-    const int t = live ? (int)(item / per_token) : 0;
-    const int c = live ? (int)(item - (int64_t)t * per_token) : 0;
-    const bool is_q = c < cq;
-    const int h0 = (is_q ? c : c - cq) * HP, heads = is_q ? p.Hq : p.Hk;
-    const int64_t xh = is_q ? p.q_sh : p.k_sh, gh = is_q ? p.dqo_sh : p.dko_sh, oh = is_q ? p.dq_sh : p.dk_sh;
-    const uint16_t* in = static_cast<const uint16_t*>(is_q ? p.q : p.k) + t * (is_q ? p.q_st : p.k_st) + 8 * chunk;
-    const uint16_t* up =
-        static_cast<const uint16_t*>(is_q ? p.dq_out : p.dk_out) + t * (is_q ? p.dqo_st : p.dko_st) + 8 * chunk;
-    uint16_t* out = static_cast<uint16_t*>(is_q ? p.dq : p.dk) + t * (is_q ? p.dq_st : p.dk_st) + 8 * chunk;
+  // Items are (token, HP heads), the group's own `stride` apart; a step of the
+  // walk is step_t tokens and step_h heads, with a carry.
+  const int per_token = (heads + HP - 1) / HP, stride = blocks * GROUPS;
+  const int step_t = stride / per_token, step_h = (stride - step_t * per_token) * HP, all_h = per_token * HP;
+  struct Item {
+    int t, h;  // token (p.total_tokens or more: past the end) and first head
+  };
+  auto next = [&](Item x) {
+    x.t += step_t;
+    x.h += step_h;
+    if (x.h >= all_h) x.h -= all_h, ++x.t;
+    return x;
+  };
+  // While row i of an item is worked on, the item's later rows and the next
+  // item's earlier ones are on their way into the thread's cells ([row][x, x,
+  // dy, dy][thread]), and so are the next item's angles ([set][cos, cos, sin,
+  // sin][thread]); positions are read an item ahead of that.
+  extern __shared__ uint4 cells[];
+  uint4* const row_cells = cells + threadIdx.x;
+  uint4* const angle_cells = cells + HP * 4 * kThreads + threadIdx.x;
+  const bool turns = p.rope_dim > 0 && ch.rotated;
+  auto position = [&](Item x) { return x.t < p.total_tokens && p.rope_dim > 0 ? p.positions[x.t] : -1; };
+  auto fetch_row = [&](Item x, int i) {
+    if (x.t < p.total_tokens && x.h + i < heads) {
+      const uint16_t* in = x0 + x.t * xt + (x.h + i) * xh;
+      const uint16_t* up = g0 + x.t * gt + (x.h + i) * gh;
+      copy_async(row_cells + (4 * i) * kThreads, in + ch.first);
+      copy_async(row_cells + (4 * i + 1) * kThreads, in + ch.second);
+      copy_async(row_cells + (4 * i + 2) * kThreads, up + ch.first);
+      copy_async(row_cells + (4 * i + 3) * kThreads, up + ch.second);
+    }
+  };
+  auto fetch_angles = [&](int pos, int set) {
+    if (!turns || pos < 0 || pos >= p.max_position) return;
+    const int64_t off = (int64_t)pos * (p.rope_dim / 2) + 8 * lane;
+    uint4* dst = angle_cells + set * 4 * kThreads;
+    copy_async_shared(dst, p.cos + off);
+    copy_async_shared(dst + kThreads, p.cos + off + 4);
+    copy_async_shared(dst + 2 * kThreads, p.sin + off);
+    copy_async_shared(dst + 3 * kThreads, p.sin + off + 4);
+  };
+  const int start = block * GROUPS + grp;
+  Item item{start / per_token, (start % per_token) * HP};
+  Item after = next(item), second = next(after);
+  int pos = position(item), pos_next = position(after), set = 0;
+  fetch_angles(pos, 0);
+#pragma unroll
+  for (int i = 0; i < HP; ++i) {
+    fetch_row(item, i);
+    copy_commit();
+  }
+  // A warp's groups walk on until the last of them is past the end (they
+  // shuffle together).
+  for (; __any_sync(0xffffffffu, item.t < p.total_tokens); set ^= 1, item = after, after = second, second = next(second)) {
+    const bool live = item.t < p.total_tokens;
+    uint16_t* out = d0 + (live ? item.t * ot + item.h * oh : 0);
+    const int h0 = item.h;
+    const bool ok = live && (p.rope_dim == 0 || (pos >= 0 && pos < p.max_position));
+    if (live && !ok) atomicCAS(p.status, 0, (int)kDevBadIndex);
+    fetch_angles(pos_next, set ^ 1);  // part of the next group that is committed
+    pos = pos_next;
+    pos_next = position(second);
+    float c8[8], s8[8];
 
-    uint4 rx[HP], rg[HP];
 #pragma unroll
     for (int i = 0; i < HP; ++i) {
-      const bool on = live && h0 + i < heads;
-      rx[i] = on ? *reinterpret_cast<const uint4*>(in + (h0 + i) * xh) : make_uint4(0, 0, 0, 0);
-      rg[i] = on ? *reinterpret_cast<const uint4*>(up + (h0 + i) * gh) : make_uint4(0, 0, 0, 0);
-    }
-    int64_t pos = 0;
-    bool ok = live;
-    if (live && p.rope_dim > 0) {
-      pos = p.positions[t];
-      ok = pos >= 0 && pos < p.max_position;
-      if (!ok) atomicCAS(p.status, 0, (int)kDevBadIndex);
-    }
-    Angles ang;
-    if (ok && p.rope_dim > 0) load_angles(ang, p.cos, p.sin, pos, p.rope_dim, p.interleaved, chunk);
-    const void* weight = is_q ? p.q_weight : p.k_weight;
-    float w[8], dw[8];
-    load_weight<BF16>(weight, chunk, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[j] = 0.f;
-
-#pragma unroll
-    for (int i = 0; i < HP; ++i) {
-      float x[8], g[8];
-      unpack8<BF16>(rx[i], x);
-      unpack8<BF16>(rg[i], g);
-      rotate(g, ang, p.rope_dim, p.interleaved, chunk, -1.f);
-      float ss = 0.f, dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss = fmaf(x[j], x[j], ss);
-        dot = fmaf(g[j] * w[j], x[j], dot);
-      }
-      ss = row_sum<LANES>(ss);
-      dot = row_sum<LANES>(dot);
-      if (weight != nullptr) {
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        const float m = r * r * (dot * (1.f / D));
+      copy_wait<HP - 1>();
+      const bool on = ok && h0 + i < heads;
+      if (i == 0) {
+        const float* c4 = reinterpret_cast<const float*>(angle_cells + set * 4 * kThreads);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (ok) dw[j] = fmaf(g[j] * x[j], r, dw[j]);
-          g[j] = r * (g[j] * w[j] - x[j] * m);
+          const int at = (j >> 2) * kThreads * 4 + (j & 3);
+          c8[j] = turns ? c4[at] : 1.f;
+          s8[j] = turns ? c4[2 * kThreads * 4 + at] : 0.f;
         }
       }
-      if (ok && h0 + i < heads) *reinterpret_cast<uint4*>(out + (h0 + i) * oh) = pack8<BF16>(g);
-    }
+      float x[16], g[16];
+      unpack16<BF16>(row_cells[(4 * i) * kThreads], row_cells[(4 * i + 1) * kThreads], x);
+      {
+        float dy[16], P[16], Q[16];
+        unpack16<BF16>(row_cells[(4 * i + 2) * kThreads], row_cells[(4 * i + 3) * kThreads], dy);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      accq[j] += is_q ? dw[j] : 0.f;
-      acck[j] += is_q ? 0.f : dw[j];
+        for (int j = 0; j < 16; ++j) {
+          P[j] = c8[pair_of<INTER>(j)];
+          Q[j] = is_first<INTER>(j) ? s8[pair_of<INTER>(j)] : -s8[pair_of<INTER>(j)];
+        }
+        turn16<INTER, FULL>(dy, P, Q, ch.rotated, g);
+      }
+      if (weight != nullptr) {
+        float gw[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) fma2(gw[j], gw[j + 1], g[j], g[j + 1], w[j], w[j + 1], 0.f, 0.f);
+        const float ss = row_sum<LANES>(dot16(x, x));
+        const float dot = row_sum<LANES>(dot16(gw, x));
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        const float m = -r * (dot * (1.f / D)) * r;
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          float n0, n1;  // the normed row
+          fma2(n0, n1, x[j], x[j + 1], r, r, 0.f, 0.f);
+          if (on) fma2(acc[j], acc[j + 1], g[j], g[j + 1], n0, n1, acc[j], acc[j + 1]);
+          fma2(n0, n1, x[j], x[j + 1], m, m, gw[j], gw[j + 1]);
+          fma2(g[j], g[j + 1], n0, n1, r, r, 0.f, 0.f);
+        }
+      }
+      if (on) store16<BF16>(out + i * oh, ch, g);
+      fetch_row(after, i);  // x and dy of this row are in registers
+      copy_commit();
     }
   }
 
-  if (p.dq_weight == nullptr && p.dk_weight == nullptr) return;
-  __shared__ float sums[GROUPS][2 * D];
+  if (weight == nullptr) return;
+  // The block's sum, over its groups in order, through the cells (which no
+  // copy is on its way to any more).
+  float* sums = reinterpret_cast<float*>(cells);  // [GROUPS][D]
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    sums[grp][8 * chunk + j] = accq[j];
-    sums[grp][D + 8 * chunk + j] = acck[j];
+    sums[grp * D + ch.first + j] = acc[j];
+    sums[grp * D + ch.second + j] = acc[8 + j];
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * D; e += kThreads) {
+  for (int e = threadIdx.x; e < D; e += kThreads) {
     float v = 0.f;
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) v += sums[g][e];
-    p.partials[(int64_t)blockIdx.x * 2 * D + e] = v;
+#pragma unroll 8
+    for (int g = 0; g < GROUPS; ++g) v += sums[g * D + e];
+    p.partials[(int64_t)blockIdx.x * D + e] = v;
   }
 }
 
-// dw[e] = sum over the blocks' partials, 32 elements a block: 8 strided sums
-// in parallel, joined in order, so the result does not depend on timing.
-__global__ void __launch_bounds__(256) rope_bwd_weights_kernel(const float* partials, int blocks, int D, float* dqw,
-                                                               float* dkw) {
+// dw[e] = sum over the partials of q's blocks (blockIdx.y = 0) or k's, 32
+// elements a block: 32 strided sums in parallel, joined in order, so the
+// result does not depend on timing.
+__global__ void __launch_bounds__(1024) rope_bwd_weights_kernel(const float* partials, int q_blocks, int blocks, int D,
+                                                                float* dqw, float* dkw) {
+  pdl_wait();
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
   const int e = blockIdx.x * 32 + lane;
+  float* dst = blockIdx.y == 0 ? dqw : dkw;
+  if (dst == nullptr) return;
+  const int end = blockIdx.y == 0 ? q_blocks : blocks;
   float v = 0.f;
-  for (int b = part; b < blocks; b += 8) v += partials[(int64_t)b * 2 * D + e];
-  __shared__ float s[8][32];
-  s[part][lane] = v;
+#pragma unroll 8
+  for (int b = (blockIdx.y == 0 ? 0 : q_blocks) + part; b < end; b += 32) v += partials[(int64_t)b * D + e];
+  __shared__ float s[32][33];
+  s[lane][part] = v;
   __syncthreads();
-  if (part != 0) return;
-  v = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v += s[i][lane];
-  if (e < D) {
-    if (dqw != nullptr) dqw[e] = v;
-  } else if (dkw != nullptr) {
-    dkw[e - D] = v;
-  }
+  v = row_sum<32>(s[part][lane]);  // warp `part` adds up element `part`
+  if (lane == 0) dst[blockIdx.x * 32 + part] = v;
+}
+
+template <int D, bool BF16, int HP, bool INTER, bool FULL>
+cudaError_t launch_fwd(const RopeParams& p, unsigned blocks, cudaStream_t s) {
+  rope_kernel<D, BF16, HP, INTER, FULL><<<blocks, kThreads, HP > 1 ? HP * 2 * kThreads * 16 : 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// Blocks of `hp` heads a group over all items.
+template <int D>
+int64_t fwd_blocks(const RopeParams& p, int hp) {
+  constexpr int GROUPS = kThreads / (D / 16);
+  const int64_t cq = (p.Hq + hp - 1) / hp, ck = (p.Hk + hp - 1) / hp;
+  return ((cq + (p.paged ? 2 : 1) * ck) * p.total_tokens + GROUPS - 1) / GROUPS;
 }
 
 template <int D, bool BF16, int HP>
 cudaError_t fwd(const RopeParams& p, cudaStream_t s) {
-  constexpr int GROUPS = kThreads / (D / 8);
-  const int64_t cq = (p.Hq + HP - 1) / HP, ck = (p.Hk + HP - 1) / HP;
-  const int64_t blocks = ((cq + (p.paged ? 2 : 1) * ck) * p.total_tokens + GROUPS - 1) / GROUPS;
+  const int64_t blocks = fwd_blocks<D>(p, HP);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  rope_kernel<D, BF16, HP><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+  const bool full = p.rope_dim == D;
+  if (p.interleaved)
+    return full ? launch_fwd<D, BF16, HP, true, true>(p, (unsigned)blocks, s)
+                : launch_fwd<D, BF16, HP, true, false>(p, (unsigned)blocks, s);
+  return full ? launch_fwd<D, BF16, HP, false, true>(p, (unsigned)blocks, s)
+              : launch_fwd<D, BF16, HP, false, false>(p, (unsigned)blocks, s);
+}
+
+// One head a group while its blocks all run at once (four on each of a GB300's
+// 152 SMs), else four: measured with 32 + 8 heads of 128, 3.1 us against 4.3
+// at 8 tokens, 4.8 against 4.9 at 512, 6.8 against 5.8 at 1024 and 88 against
+// 60 at 16384 (heads of 64 and 32 cross at about the same number of blocks).
+// Two and eight heads a group are never the best by more than 5 %.
+constexpr int kOneHeadBlocks = 608, kHeads = 4;
+template <int D, bool BF16>
+cudaError_t fwd_any(const RopeParams& p, cudaStream_t s) {
+  return fwd_blocks<D>(p, 1) <= kOneHeadBlocks ? fwd<D, BF16, 1>(p, s) : fwd<D, BF16, kHeads>(p, s);
+}
+
+template <int D, bool BF16, bool INTER, bool FULL>
+cudaError_t launch_bwd(const RopeBwdParams& p, cudaStream_t s) {
+  auto kern = rope_bwd_kernel<D, BF16, kRopeBwdHeads, INTER, FULL>;
+  constexpr int SMEM = (kRopeBwdHeads + 2) * 4 * kThreads * 16;
+  // The dynamic shared-memory opt-in is per device; set it once per device.
+  static std::atomic<unsigned long long> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  kern<<<(unsigned)p.blocks, kThreads, SMEM, s>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, bool BF16>
 cudaError_t bwd(const RopeBwdParams& p, cudaStream_t s) {
-  if (p.blocks > 0) rope_bwd_kernel<D, BF16, kRopeBwdHeads><<<(unsigned)p.blocks, kThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  if (p.blocks > 0) {
+    const bool full = p.rope_dim == D;
+    if (p.interleaved) e = full ? launch_bwd<D, BF16, true, true>(p, s) : launch_bwd<D, BF16, true, false>(p, s);
+    else e = full ? launch_bwd<D, BF16, false, true>(p, s) : launch_bwd<D, BF16, false, false>(p, s);
+  }
   if (e != cudaSuccess || (p.dq_weight == nullptr && p.dk_weight == nullptr)) return e;
-  rope_bwd_weights_kernel<<<2 * D / 32, 256, 0, s>>>(p.partials, p.blocks, D, p.dq_weight, p.dk_weight);
-  return cudaGetLastError();
+  // Scheduled while the last blocks above still run; waits for them on the device.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(D / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_bwd_weights_kernel, (const float*)p.partials, p.q_blocks, p.blocks, D,
+                            p.dq_weight, p.dk_weight);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(int D, bool bf16, const RopeParams& p, cudaStream_t s) {
   switch (D) {
-    case 32: return bf16 ? fwd<32, true, 1>(p, s) : fwd<32, false, 1>(p, s);
-    case 64: return bf16 ? fwd<64, true, 1>(p, s) : fwd<64, false, 1>(p, s);
-    default: return bf16 ? fwd<128, true, 1>(p, s) : fwd<128, false, 1>(p, s);
+    case 32: return bf16 ? fwd_any<32, true>(p, s) : fwd_any<32, false>(p, s);
+    case 64: return bf16 ? fwd_any<64, true>(p, s) : fwd_any<64, false>(p, s);
+    default: return bf16 ? fwd_any<128, true>(p, s) : fwd_any<128, false>(p, s);
   }
 }
 

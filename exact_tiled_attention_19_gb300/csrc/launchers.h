@@ -113,15 +113,16 @@ struct RopeBwdParams {
   const int* positions;
   void *dq, *dk;
   float *dq_weight, *dk_weight;    // [D] or nullptr
-  float* partials;                 // [blocks][2][D]
+  float* partials;                 // [blocks][D]
   int64_t q_st, q_sh, k_st, k_sh, dqo_st, dqo_sh, dko_st, dko_sh, dq_st, dq_sh, dk_st, dk_sh;
   int total_tokens, Hq, Hk;
   int rope_dim, interleaved, max_position;
   float eps;
-  int blocks;
+  int q_blocks, blocks;            // blocks for q's rows, and all
   int* status;
 };
-constexpr int kRopeBwdHeads = 1;   // heads a group of threads takes at a time
+
+constexpr int kRopeBwdHeads = 2;   // heads a group of threads takes at a time
 
 cudaError_t launch_rope(int D, bool bf16, const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_rope_bwd(int D, bool bf16, const RopeBwdParams& p, cudaStream_t stream);

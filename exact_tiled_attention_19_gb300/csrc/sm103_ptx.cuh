@@ -302,6 +302,12 @@ __device__ __forceinline__ void regs_shrink() {
 }
 
 // ---------------------------------------------------------------- math
+// a / b for a >= 0, b > 0, in 32 bits where they do (the 64-bit division is a
+// long sequence of instructions).
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 // Three-input maximum (one instruction on sm_100+).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
