@@ -43,41 +43,63 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   const int r0 = (int)blockIdx.x - u.first - 1, step = u.parts - 1;  // rows r0, r0 + step, ...
   const bool by_warp = r0 + step < rows;
   auto slot = [&](int part) { return ((int64_t)(u.first + part) * 2 + (part == 0 ? 1 : 0)) * p.row_tile; };
-  __shared__ float s_acc[8][D];
-  __shared__ float s_sum[8];
+  __shared__ float s_acc[8][D], s_max[8], s_sum[8];
   for (int r = by_warp ? r0 + warp * step : r0; r < rows; r += by_warp ? 8 * step : rows) {
-    float mx = -INFINITY;
-    for (int s = lane; s < u.parts; s += 32) mx = fmaxf(mx, p.part_lse[slot(s) + r]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    if (mx == -INFINITY) mx = 0.f;  // no key at all, or only NaN sums
-    float acc[PER], sum = 0.f;
+    // A running state over the warp's parts, four at a time: their loads go
+    // out together.
+    float mx = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int s = by_warp ? 0 : warp; s < u.parts; s += by_warp ? 1 : 8) {
-      const float w = expf(p.part_lse[slot(s) + r] - mx);
-      const float* src = p.part_o + (slot(s) + r) * D + lane * PER;
-      sum += w;
+    const int hop = by_warp ? 1 : 8;
+    for (int s = by_warp ? 0 : warp; s < u.parts; s += 4 * hop) {
+      float lse[4], v[4][PER];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] += w * src[i];  // (a part without a key is a row of zeros)
+      for (int k = 0; k < 4; ++k) {
+        const bool on = s + k * hop < u.parts;
+        const int64_t at = slot(on ? s + k * hop : 0) + r;
+        lse[k] = on ? p.part_lse[at] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[k][i] = on ? p.part_o[at * D + lane * PER + i] : 0.f;
+      }
+      float top = mx;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, lse[k]);
+      const float ref = top == -INFINITY ? 0.f : top;  // no key yet, or only NaN sums
+      const float f = expf(mx - ref);                  // 0 while there was none
+      sum *= f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] *= f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float w = expf(lse[k] - ref);
+        sum += w;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] += w * v[k][i];  // (a part without a key is a row of zeros)
+      }
+      mx = top;
     }
     if (!by_warp) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) s_acc[warp][lane * PER + i] = acc[i];
-      if (lane == 0) s_sum[warp] = sum;
+      if (lane == 0) s_max[warp] = mx, s_sum[warp] = sum;
       __syncthreads();
       if (warp != 0) return;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) mx = fmaxf(mx, s_max[x]);
+      const float ref = mx == -INFINITY ? 0.f : mx;
       sum = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) acc[i] = 0.f;
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        sum += s_sum[x];
+        // A warp that saw only NaN sums has s_max -inf and a NaN s_sum.
+        const float w = s_max[x] == -INFINITY ? (s_sum[x] == 0.f ? 0.f : 1.f) : expf(s_max[x] - ref);
+        sum += w * s_sum[x];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] += s_acc[x][lane * PER + i];
+        for (int i = 0; i < PER; ++i) acc[i] += w * s_acc[x][lane * PER + i];
       }
     }
+    if (mx == -INFINITY) mx = 0.f;
     const int rr = u.row0 + r, i = rr / p.group;
     const int head = u.head0 + rr - i * p.group;
     // A row without a key is 0; a NaN sum stays one.

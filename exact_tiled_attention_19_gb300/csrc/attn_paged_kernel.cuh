@@ -55,8 +55,7 @@ struct PagedCfg {
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V
   // As many stages as let two CTAs share an SM (113 KB each).
   static constexpr int STAGES = (D == 32 ? 2 : 1) * (MT == 16 ? 3 : 2);
-  static constexpr int MERGE_COLS = 32;               // columns merged at a time
-  static constexpr int MERGE_BYTES = 4 * MT * MERGE_COLS * 4;
+  static constexpr int MERGE_BYTES = 4 * MT * 32 * 4;  // four warps' rows, 32 columns
   static constexpr int Q_PITCH = 2 * D + 16;          // padded: no bank conflicts
   static constexpr int Q_BYTES = MT * Q_PITCH;        // a slot
   // Slots for a unit's description and Q rows.  16 rows' fragments fit in
@@ -73,7 +72,9 @@ struct PagedCfg {
   static constexpr int CONSUMERS = 128, THREADS = 160;
 };
 
-constexpr int kUnitCost = 1;  // tiles that entering a unit costs
+// Tiles that entering a unit costs.  64 ragged sequences of up to 16384 keys, 8
+// KV heads of 128: 86.4 us with 1, 78.6 with 2, 78.9 with 3, 79.4 with 4.
+constexpr int kUnitCost = 2;
 
 // Everything of one sequence that the roles need.
 struct PagedSeq {
@@ -181,9 +182,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // A read is issued before the arrival but need not have been served by then:
 // nothing makes the arrival wait for a register that is still on its way, and a
 // refill then overtakes the last reads (it did, where bank conflicts held them
-// up).  So the arrival's address takes in `seen`, a value made of everything
-// that was read, and with `zero` (a 0 that the compiler does not know) leaves
-// it where it is.
+// up).  So the arrival's address takes in `seen`, a value made of a register of
+// every read (a read delivers its registers together), and with `zero` (a 0
+// that the compiler does not know) leaves it where it is.
 __device__ __forceinline__ void release_after(uint64_t* bar, uint32_t seen, uint32_t zero, int lane) {
   const uint32_t off = seen & zero;
   __syncwarp();
@@ -237,17 +238,33 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
   };
 
   // This CTA's piece of the line: lane i sums up its run of sequences; the
-  // lane whose run holds the piece's start finds the sequence.
+  // lane whose run holds the piece's start finds the sequence.  (With up to 32
+  // sequences a run is the lane's sequence of the window.)
+  PagedWindow<C> win;
+  win.load(p, 0, lane);
+  const bool one_each = p.num_seqs <= 32;
   const int per = (p.num_seqs + 31) / 32;
   const int s_begin = min(p.num_seqs, lane * per), s_end = min(p.num_seqs, s_begin + per);
   auto length = [](const PagedSeq& q) { return (int64_t)q.units * (q.tiles + kUnitCost); };
   int64_t mine = 0;
-  for (int s = s_begin; s < s_end; ++s) mine += length(paged_seq<C>(p, s));
+  if (one_each) mine = length(win.mine);
+  else
+    for (int s = s_begin; s < s_end; ++s) mine += length(paged_seq<C>(p, s));
   int64_t incl = mine;
+  if (__all_sync(0xffffffffu, mine < (1 << 26))) {  // every sum fits in 32 bits
+    int sum = (int)mine;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += o;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += o;
+    }
+    incl = sum;
+  } else {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
   }
   const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
   const int share = blockIdx.x;
@@ -259,10 +276,10 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
     finish();
     return;
   }
-  int s = 0;
+  int s = lane;
   int64_t at = incl - mine;
   const bool holds = begin >= at && begin < incl;
-  if (holds)
+  if (holds && !one_each)
     for (s = s_begin;; ++s) {
       const int64_t len = length(paged_seq<C>(p, s));
       if (begin < at + len) break;
@@ -271,8 +288,7 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
   const int holder = __ffs(__ballot_sync(0xffffffffu, holds)) - 1;
   s = __shfl_sync(0xffffffffu, s, holder);
   at = __shfl_sync(0xffffffffu, at, holder);
-  PagedWindow<C> win;
-  win.load(p, s, lane);
+  if (!one_each) win.load(p, s, lane);
   PagedSeq q = win.at(s);
   int unit = (int)div_pos(begin - at, q.tiles + kUnitCost);
   int64_t u0 = at + (int64_t)unit * (q.tiles + kUnitCost);  // where the unit lies on the line
@@ -390,6 +406,65 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
   finish();
 }
 
+// Adds up the four warps' scaled rows, MC columns at a time through shared
+// memory, and writes them: the output, or the unit's partial rows.  Rows from
+// ROWS on are nobody's.
+template <class C, bool BF16, int MC, int ROWS>
+__device__ __forceinline__ void paged_merge(const PagedParams& p, const PagedUnit& w, float* merge,
+                                            const float (&o)[C::MT / 16][C::D / 8][4],
+                                            const float (&inv)[C::MT / 8], bool whole, int64_t part_row) {
+  static_assert(4 * ROWS * MC * 4 <= C::MERGE_BYTES, "");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int rows = min(ROWS, w.n * p.group - w.row0);
+  auto swz = [](int r) { return (r & 3) << 3; };  // keeps a warp's eight rows out of one another's banks
+#pragma unroll
+  for (int c0 = 0; c0 < C::D; c0 += MC) {
+#pragma unroll
+    for (int a = 0; a < C::MT / 16; ++a)
+#pragma unroll
+      for (int n = 0; n < MC / 8; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = a * 16 + g + 8 * h;
+          if (ROWS < C::MT && r >= ROWS) continue;
+          const float f = inv[2 * a + h];
+          *reinterpret_cast<float2*>(merge + (warp * ROWS + r) * MC + ((n * 8) ^ swz(r)) + 2 * t4) =
+              make_float2(o[a][c0 / 8 + n][2 * h] * f, o[a][c0 / 8 + n][2 * h + 1] * f);
+        }
+    named_barrier(1, C::CONSUMERS);
+    for (int x = tid; x < rows * (MC / 8); x += C::CONSUMERS) {
+      const int r = x / (MC / 8), c = (x % (MC / 8)) * 8;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float4* src = reinterpret_cast<const float4*>(merge + (y * ROWS + r) * MC + (c ^ swz(r)));
+        const float4 u0 = src[0], u1 = src[1];
+        v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
+        v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
+      }
+      if (whole) {
+        const int rr = w.row0 + r, i = rr / p.group;
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          u[k] = BF16 ? pack_bf16x2(v[2 * k], v[2 * k + 1]) : pack_f16x2(v[2 * k], v[2 * k + 1]);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (int64_t)(w.t0 + i) * p.o_st +
+                                  (int64_t)(w.head0 + rr - i * p.group) * p.o_sh + c0 + c) =
+            make_uint4(u[0], u[1], u[2], u[3]);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + (part_row + r) * C::D + c0 + c);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+    // The next columns, or the next unit's (whose state the warps write first,
+    // and meet, before they come here again).
+    if (c0 + MC < C::D) named_barrier(1, C::CONSUMERS);
+  }
+}
+
 template <int D, int MT, bool BF16>
 __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constant__ CUtensorMap kmap,
                                                             const __grid_constant__ CUtensorMap vmap,
@@ -471,7 +546,7 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
       for (int ks = 0; ks < D / 16; ++ks) load_q(qf[ks], 0, ks);
       uint32_t seen = 0;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) seen |= qf[ks][0] | qf[ks][1] | qf[ks][2] | qf[ks][3];
+      for (int ks = 0; ks < D / 16; ++ks) seen |= qf[ks][0];
       release_after(uempty + uslot, seen, p.zero, lane);
     }
 
@@ -591,7 +666,7 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
             for (int n = 0; n < D / 16; ++n) {
               uint32_t b[4];
               ldsm4_trans(b, vbase + tile_off<C>(row, 2 * n + (lane >> 4)));
-              seen |= b[0] | b[1] | b[2] | b[3];
+              seen |= b[0];
 #pragma unroll
               for (int a = 0; a < NM; ++a) {
                 mma16816<BF16>(o[a][2 * n], pf[a][kb], b[0], b[1]);
@@ -613,7 +688,7 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
               for (int n = 0; n < D / 16; ++n) {
                 uint32_t b[4];
                 ldsm4_trans(b, vbase + tile_off<C>(row, 2 * n + (lane >> 4)));
-              seen |= b[0] | b[1] | b[2] | b[3];
+              seen |= b[0];
 #pragma unroll
                 for (int a = 0; a < NM; ++a)
 #pragma unroll
@@ -686,53 +761,11 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
         p.part_lse[part_row + r] = lse;
       }
     }
-    constexpr int MC = C::MERGE_COLS;
-    auto swz = [](int r) { return (r & 3) << 3; };  // keeps a warp's eight rows out of one another's banks
-#pragma unroll
-    for (int c0 = 0; c0 < D; c0 += MC) {
-#pragma unroll
-      for (int a = 0; a < NM; ++a)
-#pragma unroll
-        for (int n = 0; n < MC / 8; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = a * 16 + g + 8 * h;
-            const float f = inv[2 * a + h];
-            float2 v = make_float2(o[a][c0 / 8 + n][2 * h], o[a][c0 / 8 + n][2 * h + 1]);
-            v.x *= f;
-            v.y *= f;
-            *reinterpret_cast<float2*>(merge + (warp * MT + r) * MC + ((n * 8) ^ swz(r)) + 2 * t4) = v;
-          }
-      named_barrier(1, C::CONSUMERS);
-      for (int x = tid; x < rows * (MC / 8); x += C::CONSUMERS) {
-        const int r = x / (MC / 8), c = (x % (MC / 8)) * 8;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float4* src = reinterpret_cast<const float4*>(merge + (y * MT + r) * MC + (c ^ swz(r)));
-          const float4 u0 = src[0], u1 = src[1];
-          v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
-          v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
-        }
-        if (whole) {
-          const int rr = row0 + r, i = rr / p.group;
-          uint32_t u[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            u[k] = BF16 ? pack_bf16x2(v[2 * k], v[2 * k + 1]) : pack_f16x2(v[2 * k], v[2 * k + 1]);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (int64_t)(w.t0 + i) * p.o_st +
-                                    (int64_t)(head0 + rr - i * p.group) * p.o_sh + c0 + c) =
-              make_uint4(u[0], u[1], u[2], u[3]);
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (part_row + r) * D + c0 + c);
-          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-      }
-      named_barrier(1, C::CONSUMERS);
-    }
+    // The merge goes through 8 KB (MT = 16): all columns at once for up to
+    // four rows, half of 128 for eight, 32 for more.
+    if (MT == 16 && rows <= 4) paged_merge<C, BF16, (D < 128 ? D : 128), 4>(p, w, merge, o, inv, whole, part_row);
+    else if (MT == 16 && rows <= 8) paged_merge<C, BF16, (D < 64 ? D : 64), 8>(p, w, merge, o, inv, whole, part_row);
+    else paged_merge<C, BF16, 32, MT>(p, w, merge, o, inv, whole, part_row);
   }
 }
 
