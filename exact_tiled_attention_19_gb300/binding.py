@@ -129,7 +129,7 @@ def load_library(path: str | None = None):
         lib.attn_fwd_paged.restype = _int
         lib.attn_fwd_paged_workspace_size.argtypes = [_int] * 5
         lib.attn_fwd_paged_workspace_size.restype = ctypes.c_size_t
-        lib.attn_fwd_paged_plan.argtypes = [_int] * 6 + [ctypes.POINTER(_int)]
+        lib.attn_fwd_paged_plan.argtypes = [_int] * 6 + [ctypes.POINTER(_int), ctypes.POINTER(ctypes.c_size_t)]
         lib.attn_fwd_paged_plan.restype = _int
         lib.etattn_status_string.argtypes = [_int]
         lib.etattn_status_string.restype = ctypes.c_char_p
@@ -325,11 +325,12 @@ def attn_fwd_paged_workspace_size(Hq, Hkv, max_seqlen_q, D, num_shares) -> int:
     return load_library().attn_fwd_paged_workspace_size(Hq, Hkv, max_seqlen_q, D, num_shares)
 
 
-def attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D):
-    """(status, num_shares) for the current device."""
-    out = _int(0)
-    rc = load_library().attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, ctypes.byref(out))
-    return rc, out.value
+def attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_shares=0):
+    """(status, num_shares, workspace bytes) for the current device."""
+    shares, need = _int(num_shares), ctypes.c_size_t(0)
+    rc = load_library().attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, ctypes.byref(shares),
+                                            ctypes.byref(need))
+    return rc, shares.value, need.value
 
 
 def etattn_status_string(code: int) -> str:
@@ -638,29 +639,26 @@ def attention_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = Tru
 # The calls of one decode step take a few microseconds on the device, so the
 # helpers below keep their own time down: one comparison per tensor on the way
 # through (the messages are made when it fails), strides packed into bytes, the
-# device made current only when it is not, and the C functions called directly.
+# device made current (by a second call of the helper) only when it is not, and
+# the C functions called directly.
 
 _STRIDES = {n: struct.Struct(f"{n}q").pack for n in (12, 14, 18, 20)}
+_CODES: dict = {}  # torch dtype -> ETATTN_* code
 
 
-class _NoSwitch:
-    """Stands in for ``torch.cuda.device`` when the device is current already."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
+def _code_of(t):
+    """The element type's code; a TypeError for another type."""
+    code = _CODES.get(t.dtype)
+    if code is None:
+        code = _CODES[t.dtype] = _dtype_code(t)
+    return code
 
 
-_NO_SWITCH = _NoSwitch()
-
-
-def _on(torch, device):
-    """A context in which ``device`` is current."""
-    if device.type == "cuda" and torch.cuda.current_device() == device.index:
-        return _NO_SWITCH
-    return torch.cuda.device(device)
+def _elsewhere(torch, device):
+    """Whether ``device`` is not the current one; a ValueError for no CUDA device."""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got tensors on {device}")
+    return torch.cuda.current_device() != device.index
 
 
 def _raw_stream(torch, device, stream):
@@ -668,14 +666,9 @@ def _raw_stream(torch, device, stream):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else int(stream.cuda_stream)
 
 
-def _address(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _like(name, t, shape, dtype, device, dense=False):
-    """Checks a tensor argument (None passes)."""
-    if t is None or (t.shape == shape and t.dtype == dtype and t.device == device
-                     and (not dense or t.is_contiguous())):
+def _check(name, t, shape, dtype, device, dense=False):
+    """Raises for a tensor argument that is not as it must be (None passes)."""
+    if t is None:
         return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -683,23 +676,48 @@ def _like(name, t, shape, dtype, device, dense=False):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    raise ValueError(f"{name} must be contiguous")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos, rope_sin):
-    """(rope_dim, max_position) of the rotation tables, after checking them and the weights."""
-    _like("q_weight", q_weight, (D,), dtype, device, True)
-    _like("k_weight", k_weight, (D,), dtype, device, True)
-    if rope_cos is None and rope_sin is None:
-        return 0, 0
-    if rope_cos is None or rope_sin is None:
+    """(addresses of the weights and tables, rope_dim, max_position), after checking them."""
+    wq = wk = cos = sin = rope_dim = max_position = 0
+    if q_weight is not None:
+        if q_weight.shape != (D,) or q_weight.dtype != dtype or q_weight.device != device or q_weight.stride(0) != 1:
+            _check("q_weight", q_weight, (D,), dtype, device, True)
+        wq = q_weight.data_ptr()
+    if k_weight is not None:
+        if k_weight.shape != (D,) or k_weight.dtype != dtype or k_weight.device != device or k_weight.stride(0) != 1:
+            _check("k_weight", k_weight, (D,), dtype, device, True)
+        wk = k_weight.data_ptr()
+    if rope_cos is not None and rope_sin is not None:
+        shape = rope_cos.shape
+        if len(shape) != 2:
+            raise ValueError("rope_cos and rope_sin must be [max_position, rope_dim / 2]")
+        if (rope_cos.dtype != torch.float32 or rope_cos.device != device or not rope_cos.is_contiguous()
+                or rope_sin.shape != shape or rope_sin.dtype != torch.float32 or rope_sin.device != device
+                or not rope_sin.is_contiguous()):
+            _check("rope_cos", rope_cos, shape, torch.float32, device, True)
+            _check("rope_sin", rope_sin, shape, torch.float32, device, True)
+        max_position, rope_dim = shape
+        rope_dim *= 2
+        cos, sin = rope_cos.data_ptr(), rope_sin.data_ptr()
+    elif rope_cos is not rope_sin:
         raise ValueError("rope_cos and rope_sin come together")
-    shape = rope_cos.shape
-    if len(shape) != 2:
-        raise ValueError("rope_cos and rope_sin must be [max_position, rope_dim / 2]")
-    _like("rope_cos", rope_cos, shape, torch.float32, device, True)
-    _like("rope_sin", rope_sin, shape, torch.float32, device, True)
-    return 2 * shape[1], shape[0]
+    return wq, wk, cos, sin, rope_dim, max_position
+
+
+def _positions(torch, positions, T, rope_dim, device):
+    """The address of the tokens' positions, after checking them."""
+    if positions is None:
+        if rope_dim:
+            raise ValueError("positions are needed with rope_cos and rope_sin")
+        return 0
+    if positions.shape != (T,) or positions.dtype != torch.int32 or positions.device != device or (
+            T > 1 and positions.stride(0) != 1):
+        _check("positions", positions, (T,), torch.int32, device, True)
+    return positions.data_ptr()
 
 
 def rope_tables(max_position: int, rope_dim: int, *, theta: float = 10000.0, device=None):
@@ -724,27 +742,27 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, rope_cos=None, rope_sin=
     none.  Views of a fused projection serve as q and k."""
     import torch
     T, Hq, D = q.shape
-    Hk, dtype, device = k.shape[1], q.dtype, q.device
-    code = _dtype_code(q)
-    _like("k", k, (T, Hk, D), dtype, device)
-    rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos, rope_sin)
-    if rope_dim and positions is None:
-        raise ValueError("positions are needed with rope_cos and rope_sin")
-    _like("positions", positions, (T,), torch.int32, device, True)
-    with _on(torch, device):
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
-        else:
-            _like("q_out", q_out, (T, Hq, D), dtype, device)
-        if k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=dtype, device=device)
-        else:
-            _like("k_out", k_out, (T, Hk, D), dtype, device)
-        rc = (_lib or load_library()).attn_qk_norm_rope(
-            q.data_ptr(), k.data_ptr(), _address(q_weight), _address(k_weight), _address(rope_cos), _address(rope_sin),
-            _address(positions), q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hk, D, code,
-            _STRIDES[12](*q.stride(), *k.stride(), *q_out.stride(), *k_out.stride()), rope_dim,
-            1 if interleaved else 0, max_position, eps, _raw_stream(torch, device, stream))
+    Hk, dtype, device, code = k.shape[1], q.dtype, q.device, _code_of(q)
+    if k.shape != (T, Hk, D) or k.dtype != dtype or k.device != device:
+        _check("k", k, (T, Hk, D), dtype, device)
+    wq, wk, cos, sin, rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos,
+                                                          rope_sin)
+    pos = _positions(torch, positions, T, rope_dim, device)
+    _check("q_out", q_out, (T, Hq, D), dtype, device)
+    _check("k_out", k_out, (T, Hk, D), dtype, device)
+    if _elsewhere(torch, device):
+        with torch.cuda.device(device):
+            return qk_norm_rope(q, k, q_weight=q_weight, k_weight=k_weight, rope_cos=rope_cos, rope_sin=rope_sin,
+                                positions=positions, interleaved=interleaved, eps=eps, q_out=q_out, k_out=k_out,
+                                stream=stream)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=dtype, device=device)
+    rc = (_lib or load_library()).attn_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), wq, wk, cos, sin, pos, q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hk, D, code,
+        _STRIDES[12](*q.stride(), *k.stride(), *q_out.stride(), *k_out.stride()), rope_dim, interleaved,
+        max_position, eps, _raw_stream(torch, device, stream))
     if rc != 0:
         raise EtattnError(rc, "attn_qk_norm_rope")
     return q_out, k_out
@@ -758,67 +776,76 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
     (None without the weight)."""
     import torch
     T, Hq, D = q.shape
-    Hk, dtype, device = k.shape[1], q.dtype, q.device
-    code = _dtype_code(q)
-    _like("k", k, (T, Hk, D), dtype, device)
-    _like("dq_out", dq_out, (T, Hq, D), dtype, device)
-    _like("dk_out", dk_out, (T, Hk, D), dtype, device)
-    rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos, rope_sin)
-    if rope_dim and positions is None:
-        raise ValueError("positions are needed with rope_cos and rope_sin")
-    _like("positions", positions, (T,), torch.int32, device, True)
+    Hk, dtype, device, code = k.shape[1], q.dtype, q.device, _code_of(q)
+    if (k.shape != (T, Hk, D) or k.dtype != dtype or k.device != device or dq_out.shape != q.shape
+            or dq_out.dtype != dtype or dq_out.device != device or dk_out.shape != k.shape or dk_out.dtype != dtype
+            or dk_out.device != device):
+        _check("k", k, (T, Hk, D), dtype, device)
+        _check("dq_out", dq_out, (T, Hq, D), dtype, device)
+        _check("dk_out", dk_out, (T, Hk, D), dtype, device)
+    wq, wk, cos, sin, rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos,
+                                                          rope_sin)
+    pos = _positions(torch, positions, T, rope_dim, device)
+    _check("dq", dq, (T, Hq, D), dtype, device)
+    _check("dk", dk, (T, Hk, D), dtype, device)
+    if _elsewhere(torch, device):
+        with torch.cuda.device(device):
+            return qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=q_weight, k_weight=k_weight,
+                                         rope_cos=rope_cos, rope_sin=rope_sin, positions=positions,
+                                         interleaved=interleaved, eps=eps, dq=dq, dk=dk, workspace=workspace,
+                                         stream=stream)
     lib = _lib or load_library()
-    with _on(torch, device):
-        if dq is None:
-            dq = torch.empty((T, Hq, D), dtype=dtype, device=device)
-        else:
-            _like("dq", dq, (T, Hq, D), dtype, device)
-        if dk is None:
-            dk = torch.empty((T, Hk, D), dtype=dtype, device=device)
-        else:
-            _like("dk", dk, (T, Hk, D), dtype, device)
-        dwq = torch.empty(D, dtype=torch.float32, device=device) if q_weight is not None else None
-        dwk = torch.empty(D, dtype=torch.float32, device=device) if k_weight is not None else None
-        if dwq is None and dwk is None:
-            ws_bytes = 0
-        elif workspace is None:
-            ws_bytes = lib.attn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D)
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-        else:
-            _workspace(workspace, device)
-            ws_bytes = workspace.numel() * workspace.element_size()
-        rc = lib.attn_qk_norm_rope_bwd(
-            q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), _address(q_weight), _address(k_weight),
-            _address(rope_cos), _address(rope_sin), _address(positions), dq.data_ptr(), dk.data_ptr(), _address(dwq),
-            _address(dwk), T, Hq, Hk, D, code,
-            _STRIDES[18](*q.stride(), *k.stride(), *dq_out.stride(), *dk_out.stride(), *dq.stride(), *dk.stride()),
-            rope_dim, 1 if interleaved else 0, max_position, eps, _address(workspace), ws_bytes,
-            _raw_stream(torch, device, stream))
+    if dq is None:
+        dq = torch.empty((T, Hq, D), dtype=dtype, device=device)
+    if dk is None:
+        dk = torch.empty((T, Hk, D), dtype=dtype, device=device)
+    dwq = torch.empty(D, dtype=torch.float32, device=device) if wq else None
+    dwk = torch.empty(D, dtype=torch.float32, device=device) if wk else None
+    ws_bytes = 0
+    if workspace is not None:
+        ws_bytes = _workspace(workspace, device)
+    elif wq or wk:
+        ws_bytes = lib.attn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    rc = lib.attn_qk_norm_rope_bwd(
+        q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), wq, wk, cos, sin, pos, dq.data_ptr(),
+        dk.data_ptr(), dwq.data_ptr() if wq else 0, dwk.data_ptr() if wk else 0, T, Hq, Hk, D, code,
+        _STRIDES[18](*q.stride(), *k.stride(), *dq_out.stride(), *dk_out.stride(), *dq.stride(), *dk.stride()),
+        rope_dim, interleaved, max_position, eps, workspace.data_ptr() if ws_bytes else 0, ws_bytes,
+        _raw_stream(torch, device, stream))
     if rc != 0:
         raise EtattnError(rc, "attn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
 def _workspace(t, device):
+    """The bytes of a given workspace."""
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return t.numel() * t.element_size()
 
 
 def _page_args(torch, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device):
-    """Checks the cache's tensors; returns (num_seqs, max_pages, table_stride)."""
+    """(num_seqs, max_pages, table_stride, address of the offsets), after checking the cache's tensors."""
     shape = k_pages.shape
     if len(shape) != 4:
         raise ValueError("k_pages must be [num_pages, Hkv, page_size, D]")
-    _like("k_pages", k_pages, shape, dtype, device)
-    _like("v_pages", v_pages, shape, dtype, device)
     S, width = block_table.shape
-    _like("block_table", block_table, (S, width), torch.int32, device)
     row, col = block_table.stride()
+    if (k_pages.dtype != dtype or k_pages.device != device or v_pages.shape != shape or v_pages.dtype != dtype
+            or v_pages.device != device or block_table.dtype != torch.int32 or block_table.device != device
+            or seqlens_k.shape != (S,) or seqlens_k.dtype != torch.int32 or seqlens_k.device != device
+            or not seqlens_k.is_contiguous()):
+        _check("k_pages", k_pages, shape, dtype, device)
+        _check("v_pages", v_pages, shape, dtype, device)
+        _check("block_table", block_table, (S, width), torch.int32, device)
+        _check("seqlens_k", seqlens_k, (S,), torch.int32, device, True)
     if col != 1 and width > 1:
         raise ValueError("block_table's rows must be contiguous")
-    _like("seqlens_k", seqlens_k, (S,), torch.int32, device, True)
-    _like("cu_seqlens_q", cu_seqlens_q, (S + 1,), torch.int32, device, True)
-    return S, width, row
+    if cu_seqlens_q is None:
+        return S, width, row, 0
+    _check("cu_seqlens_q", cu_seqlens_q, (S + 1,), torch.int32, device, True)
+    return S, width, row, cu_seqlens_q.data_ptr()
 
 
 def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_weight=None, k_weight=None,
@@ -835,31 +862,37 @@ def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_we
     offsets of the new tokens, None when every sequence has T / S."""
     import torch
     T, _, D = k.shape
-    dtype, device = k.dtype, k.device
-    code = _dtype_code(k)
-    S, width, row = _page_args(torch, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device)
+    dtype, device, code = k.dtype, k.device, _code_of(k)
+    S, width, row, cu = _page_args(torch, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device)
     num_pages, Hkv, page_size, Dp = k_pages.shape
-    _like("k", k, (T, Hkv, Dp), dtype, device)
-    _like("v", v, (T, Hkv, Dp), dtype, device)
-    rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos, rope_sin)
-    with _on(torch, device):
-        if q is None:
-            Hq, q_out, q_stride, o_stride = 0, None, (0, 0, 1), (0, 0, 1)
-        else:
-            Hq = q.shape[1]
-            _like("q", q, (T, Hq, D), dtype, device)
-            if q_out is None:
-                q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
-            else:
-                _like("q_out", q_out, (T, Hq, D), dtype, device)
-            q_stride, o_stride = q.stride(), q_out.stride()
-        rc = (_lib or load_library()).attn_paged_append(
-            _address(q), k.data_ptr(), v.data_ptr(), _address(q_weight), _address(k_weight), _address(rope_cos),
-            _address(rope_sin), _address(q_out), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-            seqlens_k.data_ptr(), _address(cu_seqlens_q), S, T, Hq, Hkv, D, code,
-            _STRIDES[20](*q_stride, *k.stride(), *v.stride(), *o_stride, *k_pages.stride(), *v_pages.stride()),
-            page_size, num_pages, width, row, rope_dim, 1 if interleaved else 0, max_position, eps,
-            _raw_stream(torch, device, stream))
+    if k.shape != (T, Hkv, Dp) or v.shape != (T, Hkv, Dp) or v.dtype != dtype or v.device != device:
+        _check("k", k, (T, Hkv, Dp), dtype, device)
+        _check("v", v, (T, Hkv, Dp), dtype, device)
+    wq, wk, cos, sin, rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos,
+                                                          rope_sin)
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[1]
+        if q.shape != (T, Hq, D) or q.dtype != dtype or q.device != device:
+            _check("q", q, (T, Hq, D), dtype, device)
+        _check("q_out", q_out, (T, Hq, D), dtype, device)
+    if _elsewhere(torch, device):
+        with torch.cuda.device(device):
+            return paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, q=q, q_weight=q_weight,
+                                k_weight=k_weight, rope_cos=rope_cos, rope_sin=rope_sin, interleaved=interleaved,
+                                eps=eps, cu_seqlens_q=cu_seqlens_q, q_out=q_out, stream=stream)
+    if q is None:
+        q_out, qp, op, q_stride, o_stride = None, 0, 0, (0, 0, 1), (0, 0, 1)
+    else:
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        qp, op, q_stride, o_stride = q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
+    rc = (_lib or load_library()).attn_paged_append(
+        qp, k.data_ptr(), v.data_ptr(), wq, wk, cos, sin, op, k_pages.data_ptr(), v_pages.data_ptr(),
+        block_table.data_ptr(), seqlens_k.data_ptr(), cu, S, T, Hq, Hkv, D, code,
+        _STRIDES[20](*q_stride, *k.stride(), *v.stride(), *o_stride, *k_pages.stride(), *v_pages.stride()),
+        page_size, num_pages, width, row, rope_dim, interleaved, max_position, eps,
+        _raw_stream(torch, device, stream))
     if rc != 0:
         raise EtattnError(rc, "attn_paged_append")
     return q_out
@@ -881,48 +914,47 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
     bytes) may be given, as a captured graph's owner would."""
     import torch
     T, Hq, D = q.shape
-    dtype, device = q.dtype, q.device
-    code = _dtype_code(q)
-    S, width, row = _page_args(torch, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device)
+    dtype, device, code = q.dtype, q.device, _code_of(q)
+    S, width, row, cu = _page_args(torch, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q, dtype, device)
     num_pages, Hkv, page_size, Dp = k_pages.shape
     if Dp != D:
         raise ValueError(f"k_pages has head dim {Dp}, q has {D}")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    if cu_seqlens_q is None:
+    if not cu:
         max_seqlen_q = T // S if S > 0 else 0
     elif max_seqlen_q is None:
         raise ValueError("max_seqlen_q is needed with cu_seqlens_q")
+    _check("out", out, (T, Hq, D), dtype, device)
+    _check("lse", lse, (Hq, T), torch.float32, device, True)
+    if _elsewhere(torch, device):
+        with torch.cuda.device(device):
+            return attention_paged(q, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q=cu_seqlens_q,
+                                   max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, causal=causal, scale=scale,
+                                   window_left=window_left, window_right=window_right, num_shares=num_shares,
+                                   workspace=workspace, out=out, lse=lse, return_lse=return_lse, stream=stream)
     lib = _lib or load_library()
-    with _on(torch, device):
-        if out is None:
-            out = torch.empty((T, Hq, D), dtype=dtype, device=device)
-        else:
-            _like("out", out, (T, Hq, D), dtype, device)
-        if lse is not None:
-            _like("lse", lse, (Hq, T), torch.float32, device, True)
-        elif return_lse:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
-        if num_shares is None:
-            if max_seqlen_k is None:
-                max_seqlen_k = min(width * page_size, 1 << 30)
-            plan = _int(0)
-            rc = lib.attn_fwd_paged_plan(S, Hq, Hkv, int(max_seqlen_q), int(max_seqlen_k), D, plan)
-            if rc != 0:
-                raise EtattnError(rc, "attn_fwd_paged_plan")
-            num_shares = plan.value
-        if workspace is None:
-            ws_bytes = lib.attn_fwd_paged_workspace_size(Hq, Hkv, int(max_seqlen_q), D, int(num_shares))
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes > 0 else None
-        else:
-            _workspace(workspace, device)
-            ws_bytes = workspace.numel() * workspace.element_size()
-        rc = lib.attn_fwd_paged(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _address(lse),
-            block_table.data_ptr(), seqlens_k.data_ptr(), _address(cu_seqlens_q), S, int(max_seqlen_q), T, Hq, Hkv, D, code,
-            _STRIDES[14](*q.stride(), *k_pages.stride(), *v_pages.stride(), *out.stride()), page_size, num_pages,
-            width, row, 1 if causal else 0, int(window_left), int(window_right), scale, int(num_shares), _address(workspace),
-            ws_bytes, _raw_stream(torch, device, stream))
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+    if lse is None and return_lse:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
+    if num_shares is None or workspace is None:
+        shares, need = _int(0 if num_shares is None else num_shares), ctypes.c_size_t(0)
+        if max_seqlen_k is None:
+            max_seqlen_k = min(width * page_size, 1 << 30)
+        rc = lib.attn_fwd_paged_plan(S, Hq, Hkv, int(max_seqlen_q), int(max_seqlen_k), D, shares, need)
+        if rc != 0:
+            raise EtattnError(rc, "attn_fwd_paged_plan")
+        num_shares = shares.value
+    if workspace is None:
+        ws_bytes = need.value
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
+    else:
+        ws_bytes = _workspace(workspace, device)
+    rc = lib.attn_fwd_paged(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        block_table.data_ptr(), seqlens_k.data_ptr(), cu, S, int(max_seqlen_q), T, Hq, Hkv, D, code,
+        _STRIDES[14](*q.stride(), *k_pages.stride(), *v_pages.stride(), *out.stride()), page_size, num_pages, width,
+        row, causal, int(window_left), int(window_right), D ** -0.5 if scale is None else scale, int(num_shares),
+        0 if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(torch, device, stream))
     if rc != 0:
         raise EtattnError(rc, "attn_fwd_paged")
     return out, lse

@@ -1645,18 +1645,24 @@ size_t attn_fwd_paged_workspace_size(int Hq, int Hkv, int max_seqlen_q, int D, i
   return paged_layout(num_shares, paged_row_tile((int64_t)max_seqlen_q * (Hq / Hkv)), D).total;
 }
 
-int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int D, int* num_shares) {
+int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int D, int* num_shares,
+                        size_t* workspace_bytes) {
   if (num_shares == nullptr) return ETATTN_ERR_NULL_PTR;
-  if (num_seqs < 0 || Hq < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || !head_dim_ok(D)) return ETATTN_ERR_BAD_SHAPE;
+  if (num_seqs < 0 || Hq < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || !head_dim_ok(D) || *num_shares < 0 ||
+      *num_shares > kMaxShares)
+    return ETATTN_ERR_BAD_SHAPE;
   if (Hkv <= 0 || Hq % Hkv != 0) return ETATTN_ERR_BAD_HEADS;
-  int dev = 0, num_sms = 0;
-  int* status = nullptr;
-  if (int rc = current_device(&dev, &status, &num_sms)) return rc;
-  // Two CTAs fit on an SM; no more shares than key tiles.
-  const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_row_tile(rows);
-  const int64_t tk = paged_tile_keys(D);
-  const double tiles = (double)num_seqs * Hkv * ((rows + mt - 1) / mt) * std::max<int64_t>(1, (max_seqlen_k + tk - 1) / tk);
-  *num_shares = (int)std::max(1.0, std::min(tiles, 2.0 * num_sms));
+  if (*num_shares == 0) {
+    int dev = 0, num_sms = 0;
+    int* status = nullptr;
+    if (int rc = current_device(&dev, &status, &num_sms)) return rc;
+    // Two CTAs fit on an SM; no more shares than key tiles.
+    const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_row_tile(rows), tk = paged_tile_keys(D);
+    const double tiles = (double)num_seqs * Hkv * (double)((rows + mt - 1) / mt) *
+                         (double)std::max<int64_t>(1, (max_seqlen_k + tk - 1) / tk);
+    *num_shares = (int)std::max(1.0, std::min(tiles, 2.0 * num_sms));
+  }
+  if (workspace_bytes) *workspace_bytes = attn_fwd_paged_workspace_size(Hq, Hkv, max_seqlen_q, D, *num_shares);
   return ETATTN_OK;
 }
 

@@ -475,9 +475,13 @@ size_t attn_fwd_paged_workspace_size(int Hq, int Hkv, int max_seqlen_q, int D, i
 
 /* A number of shares for attn_fwd_paged on the current device: what the GPU
  * runs at once, and no more than there are key tiles when every sequence has
- * max_seqlen_k keys.  Returns ETATTN_OK, ETATTN_ERR_NULL_PTR,
- * ETATTN_ERR_BAD_SHAPE, ETATTN_ERR_BAD_HEADS or ETATTN_ERR_NO_DEVICE. */
-int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int D, int* num_shares);
+ * max_seqlen_k keys.  *num_shares is 0 on entry for a suggestion, or a number
+ * of the caller's that stays; *workspace_bytes (may be NULL) receives
+ * attn_fwd_paged_workspace_size for it.  Returns ETATTN_OK,
+ * ETATTN_ERR_NULL_PTR, ETATTN_ERR_BAD_SHAPE, ETATTN_ERR_BAD_HEADS or
+ * ETATTN_ERR_NO_DEVICE. */
+int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int D, int* num_shares,
+                        size_t* workspace_bytes);
 
 /*
  * attn_fwd_host: attn_fwd for callers whose q, k, v live in HOST memory and
