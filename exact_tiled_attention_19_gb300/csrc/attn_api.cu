@@ -172,12 +172,11 @@ int current_device(int* dev_out, int** status_out, int* num_sms_out = nullptr) {
 
 // 4-D tensor map over (d, token, head, batch) with a box of one 128-row tile
 // of SW elements along d: 128 tokens of one head, or with box_heads = P > 1,
-// 128 / P tokens of P heads (box_rows: another number of rows than 128).  If the token stride exceeds the head stride
+// 128 / P tokens of P heads.  If the token stride exceeds the head stride
 // the two middle axes are exchanged so that strides grow outward; *swapped
 // says so.
 int encode_map(CUtensorMap* map, int dtype, const void* ptr, int D, int64_t n_tokens, int64_t n_heads,
-               int64_t n_batch, int64_t s_tok, int64_t s_head, int64_t s_batch, bool* swapped, int box_heads = 1,
-               int box_rows = 128) {
+               int64_t n_batch, int64_t s_tok, int64_t s_head, int64_t s_batch, bool* swapped, int box_heads = 1) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return fail_cuda(cudaErrorNotSupported);
   const uint64_t esz = 2;
@@ -195,7 +194,7 @@ int encode_map(CUtensorMap* map, int dtype, const void* ptr, int D, int64_t n_to
   cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(sw ? n_heads : n_tokens), (cuuint64_t)(sw ? n_tokens : n_heads),
                         (cuuint64_t)n_batch};
   cuuint64_t strides[3] = {sw ? bh : bt, sw ? bt : bh, bb};
-  const cuuint32_t box_tok = (cuuint32_t)(box_rows / box_heads), box_head = (cuuint32_t)box_heads;
+  const cuuint32_t box_tok = 128u / (cuuint32_t)box_heads, box_head = (cuuint32_t)box_heads;
   cuuint32_t box[4] = {(cuuint32_t)sw_elems, sw ? box_head : box_tok, sw ? box_tok : box_head, 1u};
   cuuint32_t estride[4] = {1, 1, 1, 1};
   CUresult r = enc(map, dtype == ETATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
@@ -1244,10 +1243,11 @@ int append_impl(const void* q, const void* k, const void* v, const void* q_weigh
 // ---------------------------------------------------------------- attention over a paged cache
 constexpr int kMaxShares = 65535;
 
-// Rows of a unit: 16 hold a decode step of up to 16 query heads per KV head
-// in half the registers of 32.
+// Rows of a unit: 16 (two CTAs of four consumer warps on an SM) hold a decode
+// step of up to 16 query heads per KV head; more rows share the tiles among 32
+// (one CTA of eight).
 int paged_row_tile(int64_t rows) { return rows <= 16 ? 16 : 32; }
-int paged_tile_keys(int D) { return D == 128 ? 64 : 128; }
+int paged_tile_keys(int D) { return 8192 / D; }  // the kernel's PagedCfg::TK
 
 // Workspace: the shares' join descriptors, then at 256-byte boundaries two
 // partial rows' lse and O per share and row of a tile.
@@ -1261,6 +1261,26 @@ PagedLayout paged_layout(int shares, int row_tile, int D) {
   L.o_off = L.lse_off + up((size_t)shares * 2 * row_tile * 4);
   L.total = L.o_off + (size_t)shares * 2 * row_tile * D * 4;
   return L;
+}
+
+// 5-D tensor map over a cache's (d within 64, slot, d / 64, head, page) with a
+// box of `box` slots of one head and page, all of D: one copy per page.
+int encode_pages(CUtensorMap* map, int dtype, const void* ptr, int D, int page_size, int Hkv, int num_pages,
+                 const int64_t* st, int box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return fail_cuda(cudaErrorNotSupported);
+  const cuuint32_t cols = D >= 64 ? 64 : 32, halves = (cuuint32_t)D / cols;
+  // Strides of extent-1 axes are never used; give them a harmless value.
+  auto bytes = [](int64_t stride, int64_t extent) { return (cuuint64_t)(extent > 1 ? stride * 2 : 16); };
+  cuuint64_t dims[5] = {cols, (cuuint64_t)page_size, halves, (cuuint64_t)Hkv, (cuuint64_t)num_pages};
+  cuuint64_t strides[4] = {bytes(st[2], page_size), cols * 2, bytes(st[1], Hkv), bytes(st[0], num_pages)};
+  cuuint32_t boxes[5] = {cols, (cuuint32_t)box, halves, 1u, 1u};
+  cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+  const CUresult r = enc(map, dtype == ETATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         5, const_cast<void*>(ptr), dims, strides, boxes, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         D >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ETATTN_OK : fail_cuda(cudaErrorInvalidValue);
 }
 
 int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
@@ -1312,12 +1332,9 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
   int* status = nullptr;
   if (int rc = current_device(&dev, &status)) return rc;
   CUtensorMap mk, mv;
-  bool swk = false, swv = false;
   const int box = std::min(page_size, paged_tile_keys(D));
-  if (int rc = encode_map(&mk, dtype, k_pages, D, page_size, Hkv, num_pages, st[5], st[4], st[3], &swk, 1, box))
-    return rc;
-  if (int rc = encode_map(&mv, dtype, v_pages, D, page_size, Hkv, num_pages, st[9], st[8], st[7], &swv, 1, box))
-    return rc;
+  if (int rc = encode_pages(&mk, dtype, k_pages, D, page_size, Hkv, num_pages, st + 3, box)) return rc;
+  if (int rc = encode_pages(&mv, dtype, v_pages, D, page_size, Hkv, num_pages, st + 7, box)) return rc;
   PagedParams p{};
   p.q = q;
   p.o = o;
@@ -1342,7 +1359,6 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
   p.win_left = window_left_of(window_left);
   p.win_right = window_right_of(window_right, causal);
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.hn_swapped = (swk ? 1 : 0) | (swv ? 2 : 0);
   p.row_tile = row_tile;
   p.shares = num_shares;
   if (num_shares > 1) {
@@ -1656,11 +1672,11 @@ int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max
     int dev = 0, num_sms = 0;
     int* status = nullptr;
     if (int rc = current_device(&dev, &status, &num_sms)) return rc;
-    // Two CTAs fit on an SM; no more shares than key tiles.
+    // Two CTAs of 16 rows fit on an SM, or one of 32; no more shares than key tiles.
     const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_row_tile(rows), tk = paged_tile_keys(D);
     const double tiles = (double)num_seqs * Hkv * (double)((rows + mt - 1) / mt) *
                          (double)std::max<int64_t>(1, (max_seqlen_k + tk - 1) / tk);
-    *num_shares = (int)std::max(1.0, std::min(tiles, 2.0 * num_sms));
+    *num_shares = (int)std::max(1.0, std::min(tiles, (mt == 16 ? 2.0 : 1.0) * num_sms));
   }
   if (workspace_bytes) *workspace_bytes = attn_fwd_paged_workspace_size(Hq, Hkv, max_seqlen_q, D, *num_shares);
   return ETATTN_OK;

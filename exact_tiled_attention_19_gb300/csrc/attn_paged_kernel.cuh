@@ -17,15 +17,16 @@
 //    Entering a unit costs about a tile's time beside its tiles, so a unit is
 //    kUnitCost tiles longer on the line than it is.
 //  * One producer warp walks the line: it looks up the pages of a tile one
-//    tile ahead and issues one TMA box per page and 64 columns (the lanes work
-//    on different pages), STAGES tiles ahead; a unit's Q rows and its
-//    description go through slots of their own, so that the consumers
-//    find the next unit ready.
+//    tile ahead and issues one TMA box for K and one for V per page (the lanes
+//    work on different pages), STAGES tiles ahead; a unit's Q rows and its
+//    description go through a slot of their own, so that the consumers find
+//    the next unit ready.
 //  * Four consumer warps take a quarter of a tile's keys each, with a private
 //    state, so that they never wait for one another inside a unit; the four
 //    states merge through shared memory at its end.  The products run on
-//    m16n8k16 MMAs: 16 or 32 rows per unit would leave 7/8 or 3/4 of a
-//    128-row tcgen05 tile empty, and the products are no bound here.
+//    m16n8k16 MMAs: 16 rows would leave 7/8 of a 128-row tcgen05 tile empty,
+//    and the products are no bound here.  Units of up to 32 rows have a second
+//    group of four warps for rows 16 .. 31, on the same tiles.
 //
 // Masked keys: only tiles at the edge of some row's range are masked.  There
 // a score of a key outside the row's range becomes -inf whatever the key
@@ -45,31 +46,27 @@ namespace etattn {
 template <int D_, int MT_>
 struct PagedCfg {
   static constexpr int D = D_, MT = MT_;
-  static constexpr int TK = D == 128 ? 64 : 128;      // keys per tile
+  static constexpr int GROUPS = MT / 16;              // of four consumer warps, 16 rows each
+  static constexpr int TK = 8192 / D;                 // keys per tile: 16 KB each of K and V
   static constexpr int WK = TK / 4;                   // keys per consumer warp
-  static constexpr int COLS = D > 64 ? 64 : D;        // columns of one TMA box
+  static constexpr int COLS = D > 64 ? 64 : D;        // columns of a box row
   static constexpr int HALVES = D / COLS;
   static constexpr int ROW_BYTES = COLS * 2;          // 128, or 64 for D = 32
-  static constexpr int SUB_BYTES = TK * ROW_BYTES;    // one box column of a tile
-  static constexpr int TILE_BYTES = HALVES * SUB_BYTES;
+  static constexpr int TILE_BYTES = TK * D * 2;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V
-  // As many stages as let two CTAs share an SM (113 KB each).
-  static constexpr int STAGES = (D == 32 ? 2 : 1) * (MT == 16 ? 3 : 2);
-  static constexpr int MERGE_BYTES = 4 * MT * 32 * 4;  // four warps' rows, 32 columns
+  // As many stages as let two CTAs of 16 rows (113 KB each), or one of 32,
+  // share an SM.
+  static constexpr int STAGES = 3 * GROUPS;
+  static constexpr int MERGE_BYTES = 4 * 16 * 32 * 4; // a group's: four warps' 16 rows, 32 columns
   static constexpr int Q_PITCH = 2 * D + 16;          // padded: no bank conflicts
-  static constexpr int Q_BYTES = MT * Q_PITCH;        // a slot
-  // Slots for a unit's description and Q rows.  16 rows' fragments fit in
-  // registers, and their slot is free again as soon as they are read; 32 rows
-  // are read again in every tile and keep theirs to the end of the unit.
-  static constexpr int SLOTS = MT == 16 ? 1 : 2;
   static constexpr int OFF_MERGE = STAGES * STAGE_BYTES;
-  static constexpr int OFF_Q = OFF_MERGE + MERGE_BYTES;
-  static constexpr int OFF_STATE = OFF_Q + SLOTS * Q_BYTES;  // m and l: 2 x 4 warps x MT
-  static constexpr int OFF_UNITS = OFF_STATE + 2 * 4 * MT * 4;
-  static constexpr int OFF_BARS = OFF_UNITS + SLOTS * 48;
-  static constexpr int SMEM_BYTES = OFF_BARS + 2 * (STAGES + SLOTS) * 8;
-  static_assert(SMEM_BYTES <= 115712, "two CTAs per SM");
-  static constexpr int CONSUMERS = 128, THREADS = 160;
+  static constexpr int OFF_Q = OFF_MERGE + GROUPS * MERGE_BYTES;
+  static constexpr int OFF_STATE = OFF_Q + MT * Q_PITCH;  // a group's m and l: 2 x 4 warps x 16
+  static constexpr int OFF_UNIT = OFF_STATE + GROUPS * 2 * 4 * 16 * 4;
+  static constexpr int OFF_BARS = OFF_UNIT + 48;
+  static constexpr int SMEM_BYTES = OFF_BARS + 2 * (STAGES + 1) * 8;
+  static_assert(GROUPS == 1 ? SMEM_BYTES <= 115712 : SMEM_BYTES <= 232448, "two CTAs per SM, or one");
+  static constexpr int CONSUMER_WARPS = 4 * GROUPS, THREADS = 32 * (CONSUMER_WARPS + 1);
 };
 
 // Tiles that entering a unit costs.  64 ragged sequences of up to 16384 keys, 8
@@ -192,14 +189,15 @@ __device__ __forceinline__ void release_after(uint64_t* bar, uint32_t seen, uint
   __syncwarp();
 }
 
-// Byte offset of 16-byte column `c16` of row `row` in a tile as TMA writes it
-// (128-byte swizzle: bits 4-6 take bits 7-9; 64-byte: bits 4-5 take bits 7-8).
+// Byte offset of 16-byte column `c16` in row `row` of a tile, beside where the
+// row starts: TMA's 128-byte swizzle (bits 4-6 take bits 7-9), or its 64-byte
+// one (bits 4-5 take bits 7-8).  `half` is the distance of columns 64 .. 127.
 template <class C>
-__device__ __forceinline__ uint32_t tile_off(int row, int c16) {
+__device__ __forceinline__ uint32_t col_off(int row, int c16, uint32_t half) {
   if constexpr (C::ROW_BYTES == 128) {
-    return (uint32_t)((c16 >> 3) * C::SUB_BYTES + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
+    return (c16 >= 8 ? half : 0u) + (uint32_t)(((c16 & 7) ^ (row & 7)) << 4);
   } else {
-    return (uint32_t)(row * 64 + ((c16 ^ ((row >> 1) & 3)) << 4));
+    return (uint32_t)((c16 ^ ((row >> 1) & 3)) << 4);
   }
 }
 
@@ -224,16 +222,15 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
   uint64_t* empty = full + C::STAGES;
   uint64_t* ufull = empty + C::STAGES;
-  uint64_t* uempty = ufull + C::SLOTS;
-  PagedUnit* units = reinterpret_cast<PagedUnit*>(smem + C::OFF_UNITS);
+  uint64_t* uempty = ufull + 1;
+  PagedUnit* handed = reinterpret_cast<PagedUnit*>(smem + C::OFF_UNIT);
   uint32_t uphase = 1;
-  int uslot = 0;
   // Hands over the end of the line.
   auto finish = [&]() {
-    if (!mbar_wait(uempty + uslot, uphase, p.status)) return;
+    if (!mbar_wait(uempty, uphase, p.status)) return;
     if (lane == 0) {
-      units[uslot].tiles = 0;
-      mbar_arrive(ufull + uslot);
+      handed->tiles = 0;
+      mbar_arrive(ufull);
     }
   };
 
@@ -308,8 +305,8 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
 
   const int page_keys = 1 << p.page_shift;
   const int box_keys = min(page_keys, C::TK);
-  const int boxes = C::TK / box_keys;  // pages of a tile (1 when a page holds whole tiles); at most 16
-  const uint32_t box_bytes = (uint32_t)box_keys * C::ROW_BYTES;
+  const int boxes = C::TK / box_keys;  // pages of a tile (1 when a page holds whole tiles); at most 32
+  const uint32_t box_bytes = (uint32_t)box_keys * 2 * C::D;
   const uint64_t policy = l2_policy_evict_first();
   uint32_t phase = 1;
   int stage = 0;
@@ -331,23 +328,20 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
       };
       int page = look_up(tile);
 
-      if (!mbar_wait(uempty + uslot, uphase, p.status)) return;
+      if (!mbar_wait(uempty, uphase, p.status)) return;
+      uphase ^= 1;
       if (lane == 0) {
-        units[uslot] = PagedUnit{q.t0, q.n, q.Lk, head * p.group, row0, q.tile0 + tile, stop - tile, tile == 0,
-                                 stop == q.tiles, {0, 0, 0}};
-        mbar_arrive_expect_tx(ufull + uslot, (uint32_t)rows * 2 * C::D);
+        *handed = PagedUnit{q.t0, q.n, q.Lk, head * p.group, row0, q.tile0 + tile, stop - tile, tile == 0,
+                            stop == q.tiles, {0, 0, 0}};
+        mbar_arrive_expect_tx(ufull, (uint32_t)rows * 2 * C::D);
       }
       __syncwarp();
       if (lane < rows) {
         const int rr = row0 + lane, i = rr / p.group;
-        bulk_load(smem + C::OFF_Q + uslot * C::Q_BYTES + lane * C::Q_PITCH,
+        bulk_load(smem + C::OFF_Q + lane * C::Q_PITCH,
                   static_cast<const uint16_t*>(p.q) + (int64_t)(q.t0 + i) * p.q_st +
                       (int64_t)(head * p.group + rr - i * p.group) * p.q_sh,
-                  2 * C::D, ufull + uslot);
-      }
-      if (++uslot == C::SLOTS) {
-        uslot = 0;
-        uphase ^= 1;
+                  2 * C::D, ufull);
       }
 
       for (; tile < stop; ++tile) {
@@ -358,7 +352,7 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
         const uint32_t loads = __popc(__ballot_sync(0xffffffffu, on));
         if (!mbar_wait(empty + stage, phase, p.status)) return;
         uint8_t* base = smem + stage * C::STAGE_BYTES;
-        if (lane == 0) mbar_arrive_expect_tx(full + stage, loads * 2 * C::HALVES * box_bytes);
+        if (lane == 0) mbar_arrive_expect_tx(full + stage, loads * 2 * box_bytes);
         __syncwarp();
         if (on) {
           if (pg < 0 || pg >= p.num_pages) {
@@ -366,14 +360,9 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
             pg = p.num_pages;  // past the map: the box is filled with zeros
           }
           const int slot = k0 & (page_keys - 1);
-#pragma unroll
-          for (int h = 0; h < C::HALVES; ++h) {
-            uint8_t* dst = base + h * C::SUB_BYTES + lane * box_bytes;
-            tma_load_4d_hint(dst, &kmap, full + stage, h * C::COLS, (p.hn_swapped & 1) ? head : slot,
-                             (p.hn_swapped & 1) ? slot : head, pg, policy);
-            tma_load_4d_hint(dst + C::TILE_BYTES, &vmap, full + stage, h * C::COLS, (p.hn_swapped & 2) ? head : slot,
-                             (p.hn_swapped & 2) ? slot : head, pg, policy);
-          }
+          uint8_t* dst = base + lane * box_bytes;
+          tma_load_5d_hint(dst, &kmap, full + stage, 0, slot, 0, head, pg, policy);
+          tma_load_5d_hint(dst + C::TILE_BYTES, &vmap, full + stage, 0, slot, 0, head, pg, policy);
         }
         __syncwarp();
         if (++stage == C::STAGES) {
@@ -406,33 +395,43 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
   finish();
 }
 
-// Adds up the four warps' scaled rows, MC columns at a time through shared
-// memory, and writes them: the output, or the unit's partial rows.  Rows from
-// ROWS on are nobody's.
+// Barriers among a group's four warps.  For the only group the id is a
+// constant: in a register it made entering and leaving a unit 0.5 us longer
+// (16000 units of two tiles, 232 us against 202); a branch between two
+// constants made the two-group kernel's loop slower (203 us against 189).
+template <class C>
+__device__ __forceinline__ void group_barrier(int grp) {
+  named_barrier(C::GROUPS == 1 ? 1 : 1 + grp, 128);
+}
+template <class C>
+__device__ __forceinline__ bool group_any(int grp, bool x) {
+  return named_barrier_or(C::GROUPS == 1 ? 1 : 1 + grp, 128, x);
+}
+
+// Adds up a group's four warps' scaled rows, MC columns at a time through its
+// 8 KB of shared memory, and writes them: the output, or the unit's partial
+// rows.  Rows from ROWS on are nobody's.
 template <class C, bool BF16, int MC, int ROWS>
-__device__ __forceinline__ void paged_merge(const PagedParams& p, const PagedUnit& w, float* merge,
-                                            const float (&o)[C::MT / 16][C::D / 8][4],
-                                            const float (&inv)[C::MT / 8], bool whole, int64_t part_row) {
+__device__ __forceinline__ void paged_merge(const PagedParams& p, const PagedUnit& w, int grp, int rows, float* merge,
+                                            const float (&o)[C::D / 8][4], const float (&inv)[2], bool whole,
+                                            int64_t part_row) {
   static_assert(4 * ROWS * MC * 4 <= C::MERGE_BYTES, "");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int rows = min(ROWS, w.n * p.group - w.row0);
+  const int tid = C::GROUPS == 1 ? threadIdx.x : threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3, row0 = w.row0 + 16 * grp;
   auto swz = [](int r) { return (r & 3) << 3; };  // keeps a warp's eight rows out of one another's banks
 #pragma unroll
   for (int c0 = 0; c0 < C::D; c0 += MC) {
 #pragma unroll
-    for (int a = 0; a < C::MT / 16; ++a)
+    for (int n = 0; n < MC / 8; ++n)
 #pragma unroll
-      for (int n = 0; n < MC / 8; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = a * 16 + g + 8 * h;
-          if (ROWS < C::MT && r >= ROWS) continue;
-          const float f = inv[2 * a + h];
-          *reinterpret_cast<float2*>(merge + (warp * ROWS + r) * MC + ((n * 8) ^ swz(r)) + 2 * t4) =
-              make_float2(o[a][c0 / 8 + n][2 * h] * f, o[a][c0 / 8 + n][2 * h + 1] * f);
-        }
-    named_barrier(1, C::CONSUMERS);
-    for (int x = tid; x < rows * (MC / 8); x += C::CONSUMERS) {
+      for (int h = 0; h < 2; ++h) {
+        const int r = g + 8 * h;
+        if (ROWS < 16 && r >= ROWS) continue;
+        *reinterpret_cast<float2*>(merge + (warp * ROWS + r) * MC + ((n * 8) ^ swz(r)) + 2 * t4) =
+            make_float2(o[c0 / 8 + n][2 * h] * inv[h], o[c0 / 8 + n][2 * h + 1] * inv[h]);
+      }
+    group_barrier<C>(grp);
+    for (int x = tid; x < rows * (MC / 8); x += 128) {
       const int r = x / (MC / 8), c = (x % (MC / 8)) * 8;
       float v[8];
 #pragma unroll
@@ -445,7 +444,7 @@ __device__ __forceinline__ void paged_merge(const PagedParams& p, const PagedUni
         v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
       }
       if (whole) {
-        const int rr = w.row0 + r, i = rr / p.group;
+        const int rr = row0 + r, i = rr / p.group;
         uint32_t u[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -461,217 +460,199 @@ __device__ __forceinline__ void paged_merge(const PagedParams& p, const PagedUni
     }
     // The next columns, or the next unit's (whose state the warps write first,
     // and meet, before they come here again).
-    if (c0 + MC < C::D) named_barrier(1, C::CONSUMERS);
+    if (c0 + MC < C::D) group_barrier<C>(grp);
   }
 }
 
 template <int D, int MT, bool BF16>
-__global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constant__ CUtensorMap kmap,
-                                                            const __grid_constant__ CUtensorMap vmap,
-                                                            const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
+    attn_paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ PagedParams p) {
   using C = PagedCfg<D, MT>;
-  constexpr int NM = MT / 16;  // 16-row MMA tiles
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
   uint64_t* empty = full + C::STAGES;
   uint64_t* ufull = empty + C::STAGES;
-  uint64_t* uempty = ufull + C::SLOTS;
+  uint64_t* uempty = ufull + 1;
 
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, 4);
+      mbar_init(empty + i, C::CONSUMER_WARPS);
     }
-    for (int i = 0; i < C::SLOTS; ++i) {
-      mbar_init(ufull + i, 1);
-      mbar_init(uempty + i, 4);
-    }
+    mbar_init(ufull, 1);
+    mbar_init(uempty, C::CONSUMER_WARPS);
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
   __syncthreads();
   pdl_wait();
-  if (warp == 4) {
+  if (warp == C::CONSUMER_WARPS) {
     paged_producer<C>(kmap, vmap, p, smem, lane);
     return;
   }
 
   // ------------------------------------------------ consumers
+  // The warp's 16 rows, and its quarter of a tile's keys.
+  const int grp = C::GROUPS == 1 ? 0 : warp >> 2, quarter = C::GROUPS == 1 ? warp : warp & 3;
   const int g = lane >> 2, t4 = lane & 3;
-  float* st_m = reinterpret_cast<float*>(smem + C::OFF_STATE);
-  float* st_l = st_m + 4 * MT;
-  float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
+  float* st_m = reinterpret_cast<float*>(smem + C::OFF_STATE) + grp * 128;
+  float* st_l = st_m + 64;
+  float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE + grp * C::MERGE_BYTES);
   const int share = blockIdx.x;
+  // A tile is laid out box by box, [box][half][key][64 columns].  ldmatrix
+  // takes an address per lane: for K (two 8-key blocks of two 8-column blocks
+  // each) and, transposed, V the lane's key within 16 keys and its column.
+  constexpr int KB = C::WK / 16;
+  const int box_keys = min(1 << p.page_shift, C::TK);
+  const uint32_t half = (uint32_t)box_keys * C::ROW_BYTES;
+  const int krow = ((lane >> 4) << 3) + (lane & 7), kcol = (lane >> 3) & 1;
+  const int vrow = (((lane >> 3) & 1) << 3) + (lane & 7), vcol = lane >> 4;
+  uint32_t kstart[KB], vstart[KB];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    auto start = [&](int row) {
+      return (uint32_t)(row + (C::HALVES - 1) * (row & ~(box_keys - 1))) * C::ROW_BYTES;
+    };
+    kstart[kb] = start(quarter * C::WK + kb * 16 + krow);
+    vstart[kb] = start(quarter * C::WK + kb * 16 + vrow);
+  }
+
   uint32_t phase = 0, uphase = 0;
-  int stage = 0, uslot = 0;
+  int stage = 0;
   bool alive = true;
   while (true) {
-    // A wait that ran out in one warp ends them all, here, where none of them
+    // A wait that ran out in one warp ends its group, here, where none of them
     // waits in a barrier for another.
-    alive = alive && mbar_wait(ufull + uslot, uphase, p.status);
-    if (named_barrier_or(1, C::CONSUMERS, !alive)) return;
+    alive = alive && mbar_wait(ufull, uphase, p.status);
+    uphase ^= 1;
+    if (group_any<C>(grp, !alive)) return;
     __syncwarp();
-    const PagedUnit w = reinterpret_cast<const PagedUnit*>(smem + C::OFF_UNITS)[uslot];
+    const PagedUnit w = *reinterpret_cast<const PagedUnit*>(smem + C::OFF_UNIT);
     if (w.tiles == 0) return;
-    const int head0 = w.head0, row0 = w.row0;
-    const int rows = min(MT, w.n * p.group - row0);
+    const int row0 = w.row0 + 16 * grp;
+    const int rows = min(16, w.n * p.group - row0);  // none (or fewer) for the second group of a short unit
+    const bool upper = rows > 8;                     // rows 8 .. 15 are somebody's
     const int delta = w.Lk - w.n;
-    // The tokens of this row tile and the rows' key ranges (rows g, g + 8, ...).
-    const int tok_first = row0 / p.group, tok_last = (row0 + rows - 1) / p.group;
-    int tok[2 * NM], row_lo[2 * NM], row_hi[2 * NM];
+    // The tokens of the group's rows and the key ranges of rows g and g + 8.
+    const int tok_first = row0 / p.group, tok_last = (row0 + max(rows, 1) - 1) / p.group;
+    int tok[2], row_lo[2], row_hi[2];
 #pragma unroll
-    for (int j = 0; j < 2 * NM; ++j) {
-      const int r = g + 8 * j;
-      tok[j] = min((row0 + r) / p.group, tok_last);
-      const int c = tok[j] + delta;
-      row_lo[j] = max(0, c - p.win_left);
-      row_hi[j] = (int)min((int64_t)w.Lk - 1, (int64_t)c + p.win_right);
+    for (int h = 0; h < 2; ++h) {
+      tok[h] = min((row0 + g + 8 * h) / p.group, tok_last);
+      const int c = tok[h] + delta;
+      row_lo[h] = max(0, c - p.win_left);
+      row_hi[h] = (int)min((int64_t)w.Lk - 1, (int64_t)c + p.win_right);
     }
-    // Keys in [in_lo, in_hi] are read by every row of the tile.
+    // Keys in [in_lo, in_hi] are read by every row of the group.
     const int in_lo = max(0, tok_last + delta - p.win_left);
     const int in_hi = (int)min((int64_t)w.Lk - 1, (int64_t)tok_first + delta + p.win_right);
 
-    // Q: fragments in registers (MT = 16), or read from its slot in every tile
-    // (MT = 32).  Rows past the last hold anything; nothing of them is written.
-    const uint32_t qbase = smem_u32(smem + C::OFF_Q + uslot * C::Q_BYTES);
-    auto load_q = [&](uint32_t (&f)[4], int a, int ks) {
-      ldsm4(f, qbase + (a * 16 + (lane & 15)) * C::Q_PITCH + (ks * 2 + (lane >> 4)) * 16);
-    };
-    uint32_t qf[NM == 1 ? D / 16 : 1][4];
-    if constexpr (NM == 1) {
+    // Q's fragments; rows past the last hold anything, and nothing of them is
+    // written.
+    uint32_t qf[D / 16][4], qseen = (uint32_t)(w.t0 | w.row0 | w.to_end);
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) load_q(qf[ks], 0, ks);
-      uint32_t seen = 0;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) seen |= qf[ks][0];
-      release_after(uempty + uslot, seen, p.zero, lane);
+    for (int ks = 0; ks < D / 16; ++ks) {
+      ldsm4(qf[ks], smem_u32(smem + C::OFF_Q) + (16 * grp + (lane & 15)) * C::Q_PITCH + (ks * 2 + (lane >> 4)) * 16);
+      qseen |= qf[ks][0];
     }
+    release_after(uempty, qseen, p.zero, lane);
 
-    float m[2 * NM], l[2 * NM], o[NM][D / 8][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
 #pragma unroll
-    for (int j = 0; j < 2 * NM; ++j) m[j] = -INFINITY, l[j] = 0.f;
+    for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-    for (int a = 0; a < NM; ++a)
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[a][n][i] = 0.f;
+      for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
 
     for (int x = 0; x < w.tiles; ++x) {
-      const int key0 = (w.tile + x) * C::TK + warp * C::WK;
+      const int key0 = (w.tile + x) * C::TK + quarter * C::WK;
       alive = alive && mbar_wait(full + stage, phase, p.status);
       alive = __all_sync(0xffffffffu, alive);  // and the lanes, which leave the wait one by one, are together
       uint32_t seen = 0;  // everything read of V (what is read of K goes into the maxima)
-      if (alive) {
+      if (alive && rows > 0) {
         const uint32_t kbase = smem_u32(smem + stage * C::STAGE_BYTES), vbase = kbase + C::TILE_BYTES;
-        constexpr int KB = C::WK / 16;
         // S = Q K^T for the warp's keys.
-        float sc[NM][2 * KB][4];
+        float sc[2 * KB][4];
 #pragma unroll
-        for (int a = 0; a < NM; ++a)
+        for (int n = 0; n < 2 * KB; ++n)
 #pragma unroll
-          for (int n = 0; n < 2 * KB; ++n)
+          for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sc[a][n][i] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t qa[NM][4];
-          if constexpr (NM == 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) qa[0][i] = qf[ks][i];
-          } else {
-#pragma unroll
-            for (int a = 0; a < NM; ++a) load_q(qa[a], a, ks);
-          }
+        for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
             uint32_t b[4];
             // matrices: keys 0-7 / d 0-7, keys 0-7 / d 8-15, keys 8-15 / d 0-7, keys 8-15 / d 8-15
-            const int row = warp * C::WK + kb * 16 + ((lane >> 4) << 3) + (lane & 7);
-            ldsm4(b, kbase + tile_off<C>(row, ks * 2 + ((lane >> 3) & 1)));
-#pragma unroll
-            for (int a = 0; a < NM; ++a) {
-              mma16816<BF16>(sc[a][2 * kb], qa[a], b[0], b[1]);
-              mma16816<BF16>(sc[a][2 * kb + 1], qa[a], b[2], b[3]);
-            }
+            ldsm4(b, kbase + kstart[kb] + col_off<C>(krow, ks * 2 + kcol, half));
+            mma16816<BF16>(sc[2 * kb], qf[ks], b[0], b[1]);
+            mma16816<BF16>(sc[2 * kb + 1], qf[ks], b[2], b[3]);
           }
-        }
         const bool edge = key0 < in_lo || key0 + C::WK - 1 > in_hi;
-        float mx[2 * NM];
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 2 * NM; ++j) mx[j] = -INFINITY;
+        for (int n = 0; n < 2 * KB; ++n)
 #pragma unroll
-        for (int a = 0; a < NM; ++a)
-#pragma unroll
-          for (int n = 0; n < 2 * KB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int j = 2 * a + (i >> 1);
-              float s = sc[a][n][i] * p.scale_log2;
-              if (edge) {
-                const int key = key0 + n * 8 + 2 * t4 + (i & 1);
-                if (key < row_lo[j] || key > row_hi[j]) s = -INFINITY;
-              }
-              sc[a][n][i] = s;
-              mx[j] = fmaxf(mx[j], s);
+          for (int i = 0; i < 4; ++i) {
+            const int h = i >> 1;
+            float s = sc[n][i] * p.scale_log2;
+            if (edge) {
+              const int key = key0 + n * 8 + 2 * t4 + (i & 1);
+              if (key < row_lo[h] || key > row_hi[h]) s = -INFINITY;
             }
+            sc[n][i] = s;
+            mx[h] = fmaxf(mx[h], s);
+          }
         bool grew = false;
 #pragma unroll
-        for (int j = 0; j < 2 * NM; ++j) {
-          mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 1));
-          mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 2));
-          grew = grew || mx[j] > m[j];
+        for (int h = 0; h < 2; ++h) {
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+          grew = grew || ((h == 0 || upper) && mx[h] > m[h]);
         }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-          for (int j = 0; j < 2 * NM; ++j) {
-            const float mn = fmaxf(m[j], mx[j]);
-            const float f = mn == -INFINITY ? 1.f : ex2_approx(m[j] - mn);
-            m[j] = mn;
-            l[j] *= f;
+          for (int h = 0; h < 2; ++h) {
+            const float mn = fmaxf(m[h], mx[h]);
+            const float f = mn == -INFINITY ? 1.f : ex2_approx(m[h] - mn);
+            m[h] = mn;
+            l[h] *= f;
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
-              o[j >> 1][n][2 * (j & 1)] *= f;
-              o[j >> 1][n][2 * (j & 1) + 1] *= f;
+              o[n][2 * h] *= f;
+              o[n][2 * h + 1] *= f;
             }
           }
         }
         // P = 2^(S - m), rounded to the input type for the product with V (a
         // relative half step per weight); l sums the unrounded values.
-        uint32_t pf[NM][KB][4];
+        uint32_t pf[KB][4];
 #pragma unroll
-        for (int a = 0; a < NM; ++a)
+        for (int n = 0; n < 2 * KB; ++n) {
+          float e[4];
 #pragma unroll
-          for (int n = 0; n < 2 * KB; ++n) {
-            float e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int j = 2 * a + (i >> 1);
-              e[i] = ex2_approx(sc[a][n][i] - (m[j] == -INFINITY ? 0.f : m[j]));
-              l[j] += e[i];
-            }
-            pf[a][n >> 1][(n & 1) * 2] = BF16 ? pack_bf16x2(e[0], e[1]) : pack_f16x2(e[0], e[1]);
-            pf[a][n >> 1][(n & 1) * 2 + 1] = BF16 ? pack_bf16x2(e[2], e[3]) : pack_f16x2(e[2], e[3]);
+          for (int i = 0; i < 4; ++i) {
+            const int h = i >> 1;
+            e[i] = ex2_approx(sc[n][i] - (m[h] == -INFINITY ? 0.f : m[h]));
+            l[h] += e[i];
           }
+          pf[n >> 1][(n & 1) * 2] = BF16 ? pack_bf16x2(e[0], e[1]) : pack_f16x2(e[0], e[1]);
+          pf[n >> 1][(n & 1) * 2 + 1] = BF16 ? pack_bf16x2(e[2], e[3]) : pack_f16x2(e[2], e[3]);
+        }
         // O += P V.
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
           // matrices (transposed): keys 0-7 / d 0-7, keys 8-15 / d 0-7, keys 0-7 / d 8-15, keys 8-15 / d 8-15
-          const int row = warp * C::WK + kb * 16 + (((lane >> 3) & 1) << 3) + (lane & 7);
           if (!edge) {
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {
               uint32_t b[4];
-              ldsm4_trans(b, vbase + tile_off<C>(row, 2 * n + (lane >> 4)));
+              ldsm4_trans(b, vbase + vstart[kb] + col_off<C>(vrow, 2 * n + vcol, half));
               seen |= b[0];
-#pragma unroll
-              for (int a = 0; a < NM; ++a) {
-                mma16816<BF16>(o[a][2 * n], pf[a][kb], b[0], b[1]);
-                mma16816<BF16>(o[a][2 * n + 1], pf[a][kb], b[2], b[3]);
-              }
+              mma16816<BF16>(o[2 * n], pf[kb], b[0], b[1]);
+              mma16816<BF16>(o[2 * n + 1], pf[kb], b[2], b[3]);
             }
           } else {
             // One pass per token: its range alone survives in V, and only its
@@ -687,18 +668,16 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
 #pragma unroll
               for (int n = 0; n < D / 16; ++n) {
                 uint32_t b[4];
-                ldsm4_trans(b, vbase + tile_off<C>(row, 2 * n + (lane >> 4)));
-              seen |= b[0];
+                ldsm4_trans(b, vbase + vstart[kb] + col_off<C>(vrow, 2 * n + vcol, half));
+                seen |= b[0];
 #pragma unroll
-                for (int a = 0; a < NM; ++a)
+                for (int h = 0; h < 2; ++h) {
+                  float d[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816<BF16>(d, pf[kb], b[2 * h] & m0, b[2 * h + 1] & m1);
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16816<BF16>(d, pf[a][kb], b[2 * h] & m0, b[2 * h + 1] & m1);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                      if (tok[2 * a + (i >> 1)] == tk) o[a][2 * n + h][i] += d[i];
-                  }
+                  for (int i = 0; i < 4; ++i)
+                    if (tok[i >> 1] == tk) o[2 * n + h][i] += d[i];
+                }
               }
             }
           }
@@ -710,62 +689,57 @@ __global__ void __launch_bounds__(160, 2) attn_paged_kernel(const __grid_constan
         phase ^= 1;
       }
     }
-    if constexpr (NM > 1) release_after(uempty + uslot, __float_as_uint(l[0]), p.zero, lane);
-    if (++uslot == C::SLOTS) {
-      uslot = 0;
-      uphase ^= 1;
-    }
+    if (rows <= 0) continue;  // (the whole group)
 
     // Merge the four warps' states.
 #pragma unroll
-    for (int j = 0; j < 2 * NM; ++j) {
-      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
-      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       if (t4 == 0) {
-        st_m[warp * MT + g + 8 * j] = m[j];
-        st_l[warp * MT + g + 8 * j] = l[j];
+        st_m[quarter * 16 + g + 8 * h] = m[h];
+        st_l[quarter * 16 + g + 8 * h] = l[h];
       }
     }
-    named_barrier(1, C::CONSUMERS);
-    float inv[2 * NM];
+    group_barrier<C>(grp);
+    // Row r's largest maximum (0 for none) and its sum.
+    auto state_of = [&](int r, float& ref, float& sum) {
+      float mm = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 2 * NM; ++j) {
-      const int r = g + 8 * j;
-      float mm = -INFINITY, ll = 0.f;
+      for (int x = 0; x < 4; ++x) mm = fmaxf(mm, st_m[x * 16 + r]);
+      ref = mm == -INFINITY ? 0.f : mm;
+      sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) mm = fmaxf(mm, st_m[x * MT + r]);
-      const float ref = mm == -INFINITY ? 0.f : mm;
+      for (int x = 0; x < 4; ++x) sum += st_l[x * 16 + r] * ex2_approx(st_m[x * 16 + r] - ref);
+    };
+    float inv[2];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) ll += st_l[x * MT + r] * ex2_approx(st_m[x * MT + r] - ref);
-      inv[j] = ll == 0.f ? 0.f : ex2_approx(m[j] - ref) / ll;  // no key: 0; a NaN sum stays one
+    for (int h = 0; h < 2; ++h) {
+      float ref, sum;
+      state_of(g + 8 * h, ref, sum);
+      inv[h] = sum == 0.f ? 0.f : ex2_approx(m[h] - ref) / sum;  // no key: 0; a NaN sum stays one
     }
     const bool whole = w.from_start && w.to_end;
     // Where this piece of the unit goes: the output, or the workspace (slot 0
     // for a unit that began earlier, slot 1 for one that begins here).
-    const int64_t part_row = ((int64_t)share * 2 + (w.from_start ? 1 : 0)) * MT;
-    if (tid < rows) {
-      const int r = tid;
-      float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) mm = fmaxf(mm, st_m[x * MT + r]);
-      const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) ll += st_l[x * MT + r] * ex2_approx(st_m[x * MT + r] - ref);
-      const float lse = ll == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(ll);
-      if (whole) {
-        if (p.lse != nullptr) {
-          const int rr = row0 + r, i = rr / p.group;
-          p.lse[(int64_t)(head0 + rr - i * p.group) * p.total_q + w.t0 + i] = lse;
-        }
-      } else {
+    const int64_t part_row = ((int64_t)share * 2 + (w.from_start ? 1 : 0)) * MT + 16 * grp;
+    const int r = C::GROUPS == 1 ? tid : tid & 127;
+    if (r < rows) {
+      float ref, sum;
+      state_of(r, ref, sum);
+      const float lse = sum == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(sum);
+      if (!whole) {
         p.part_lse[part_row + r] = lse;
+      } else if (p.lse != nullptr) {
+        const int rr = row0 + r, i = rr / p.group;
+        p.lse[(int64_t)(w.head0 + rr - i * p.group) * p.total_q + w.t0 + i] = lse;
       }
     }
-    // The merge goes through 8 KB (MT = 16): all columns at once for up to
-    // four rows, half of 128 for eight, 32 for more.
-    if (MT == 16 && rows <= 4) paged_merge<C, BF16, (D < 128 ? D : 128), 4>(p, w, merge, o, inv, whole, part_row);
-    else if (MT == 16 && rows <= 8) paged_merge<C, BF16, (D < 64 ? D : 64), 8>(p, w, merge, o, inv, whole, part_row);
-    else paged_merge<C, BF16, 32, MT>(p, w, merge, o, inv, whole, part_row);
+    __syncwarp();
+    // All columns at once for up to four rows, half of 128 for eight, 32 for more.
+    if (rows <= 4) paged_merge<C, BF16, D, 4>(p, w, grp, rows, merge, o, inv, whole, part_row);
+    else if (rows <= 8) paged_merge<C, BF16, (D < 64 ? D : 64), 8>(p, w, grp, rows, merge, o, inv, whole, part_row);
+    else paged_merge<C, BF16, 32, 16>(p, w, grp, rows, merge, o, inv, whole, part_row);
   }
 }
 

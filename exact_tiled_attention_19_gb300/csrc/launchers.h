@@ -148,7 +148,6 @@ struct PagedParams {
   int num_pages, page_shift;
   int win_left, win_right;
   float scale_log2;
-  int hn_swapped;                  // bit 0 / 1: head and token axes exchanged in the K / V map
   int row_tile, shares;
   PagedShare* desc;                // [shares]
   float *part_lse, *part_o;        // [shares][2][row_tile], [shares][2][row_tile][D]
