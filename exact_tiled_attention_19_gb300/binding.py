@@ -654,16 +654,17 @@ def _code_of(t):
     return code
 
 
-def _elsewhere(torch, device):
-    """Whether ``device`` is not the current one; a ValueError for no CUDA device."""
+def _elsewhere(torch, device, stream):
+    """The context in which a helper has to call itself again, so that what it
+    allocates and launches belongs to ``stream`` and ``device``; None when it
+    is there already.  A ValueError for tensors or a stream of another kind."""
     if device.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got tensors on {device}")
-    return torch.cuda.current_device() != device.index
-
-
-def _raw_stream(torch, device, stream):
-    """The stream's handle: the given one's, or the device's current one's."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else int(stream.cuda_stream)
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _check(name, t, shape, dtype, device, dense=False):
@@ -750,11 +751,11 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, rope_cos=None, rope_sin=
     pos = _positions(torch, positions, T, rope_dim, device)
     _check("q_out", q_out, (T, Hq, D), dtype, device)
     _check("k_out", k_out, (T, Hk, D), dtype, device)
-    if _elsewhere(torch, device):
-        with torch.cuda.device(device):
+    there = _elsewhere(torch, device, stream)
+    if there is not None:
+        with there:
             return qk_norm_rope(q, k, q_weight=q_weight, k_weight=k_weight, rope_cos=rope_cos, rope_sin=rope_sin,
-                                positions=positions, interleaved=interleaved, eps=eps, q_out=q_out, k_out=k_out,
-                                stream=stream)
+                                positions=positions, interleaved=interleaved, eps=eps, q_out=q_out, k_out=k_out)
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
     if k_out is None:
@@ -762,7 +763,7 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, rope_cos=None, rope_sin=
     rc = (_lib or load_library()).attn_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), wq, wk, cos, sin, pos, q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hk, D, code,
         _STRIDES[12](*q.stride(), *k.stride(), *q_out.stride(), *k_out.stride()), rope_dim, interleaved,
-        max_position, eps, _raw_stream(torch, device, stream))
+        max_position, eps, torch._C._cuda_getCurrentRawStream(device.index))
     if rc != 0:
         raise EtattnError(rc, "attn_qk_norm_rope")
     return q_out, k_out
@@ -788,12 +789,12 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
     pos = _positions(torch, positions, T, rope_dim, device)
     _check("dq", dq, (T, Hq, D), dtype, device)
     _check("dk", dk, (T, Hk, D), dtype, device)
-    if _elsewhere(torch, device):
-        with torch.cuda.device(device):
+    there = _elsewhere(torch, device, stream)
+    if there is not None:
+        with there:
             return qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=q_weight, k_weight=k_weight,
                                          rope_cos=rope_cos, rope_sin=rope_sin, positions=positions,
-                                         interleaved=interleaved, eps=eps, dq=dq, dk=dk, workspace=workspace,
-                                         stream=stream)
+                                         interleaved=interleaved, eps=eps, dq=dq, dk=dk, workspace=workspace)
     lib = _lib or load_library()
     if dq is None:
         dq = torch.empty((T, Hq, D), dtype=dtype, device=device)
@@ -812,7 +813,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
         dk.data_ptr(), dwq.data_ptr() if wq else 0, dwk.data_ptr() if wk else 0, T, Hq, Hk, D, code,
         _STRIDES[18](*q.stride(), *k.stride(), *dq_out.stride(), *dk_out.stride(), *dq.stride(), *dk.stride()),
         rope_dim, interleaved, max_position, eps, workspace.data_ptr() if ws_bytes else 0, ws_bytes,
-        _raw_stream(torch, device, stream))
+        torch._C._cuda_getCurrentRawStream(device.index))
     if rc != 0:
         raise EtattnError(rc, "attn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
@@ -876,11 +877,12 @@ def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_we
         if q.shape != (T, Hq, D) or q.dtype != dtype or q.device != device:
             _check("q", q, (T, Hq, D), dtype, device)
         _check("q_out", q_out, (T, Hq, D), dtype, device)
-    if _elsewhere(torch, device):
-        with torch.cuda.device(device):
+    there = _elsewhere(torch, device, stream)
+    if there is not None:
+        with there:
             return paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, q=q, q_weight=q_weight,
                                 k_weight=k_weight, rope_cos=rope_cos, rope_sin=rope_sin, interleaved=interleaved,
-                                eps=eps, cu_seqlens_q=cu_seqlens_q, q_out=q_out, stream=stream)
+                                eps=eps, cu_seqlens_q=cu_seqlens_q, q_out=q_out)
     if q is None:
         q_out, qp, op, q_stride, o_stride = None, 0, 0, (0, 0, 1), (0, 0, 1)
     else:
@@ -892,7 +894,7 @@ def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_we
         block_table.data_ptr(), seqlens_k.data_ptr(), cu, S, T, Hq, Hkv, D, code,
         _STRIDES[20](*q_stride, *k.stride(), *v.stride(), *o_stride, *k_pages.stride(), *v_pages.stride()),
         page_size, num_pages, width, row, rope_dim, interleaved, max_position, eps,
-        _raw_stream(torch, device, stream))
+        torch._C._cuda_getCurrentRawStream(device.index))
     if rc != 0:
         raise EtattnError(rc, "attn_paged_append")
     return q_out
@@ -925,12 +927,13 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
         raise ValueError("max_seqlen_q is needed with cu_seqlens_q")
     _check("out", out, (T, Hq, D), dtype, device)
     _check("lse", lse, (Hq, T), torch.float32, device, True)
-    if _elsewhere(torch, device):
-        with torch.cuda.device(device):
+    there = _elsewhere(torch, device, stream)
+    if there is not None:
+        with there:
             return attention_paged(q, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q=cu_seqlens_q,
                                    max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, causal=causal, scale=scale,
                                    window_left=window_left, window_right=window_right, num_shares=num_shares,
-                                   workspace=workspace, out=out, lse=lse, return_lse=return_lse, stream=stream)
+                                   workspace=workspace, out=out, lse=lse, return_lse=return_lse)
     lib = _lib or load_library()
     if out is None:
         out = torch.empty((T, Hq, D), dtype=dtype, device=device)
@@ -954,7 +957,7 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
         block_table.data_ptr(), seqlens_k.data_ptr(), cu, S, int(max_seqlen_q), T, Hq, Hkv, D, code,
         _STRIDES[14](*q.stride(), *k_pages.stride(), *v_pages.stride(), *out.stride()), page_size, num_pages, width,
         row, causal, int(window_left), int(window_right), D ** -0.5 if scale is None else scale, int(num_shares),
-        0 if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(torch, device, stream))
+        0 if workspace is None else workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
     if rc != 0:
         raise EtattnError(rc, "attn_fwd_paged")
     return out, lse

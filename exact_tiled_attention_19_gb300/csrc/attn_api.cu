@@ -1300,7 +1300,7 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
   if (num_seqs == 0 || Hq == 0 || total_q == 0 || max_seqlen_q == 0) return ETATTN_OK;
   if (cu_seqlens_q == nullptr && (int64_t)num_seqs * max_seqlen_q != total_q) return ETATTN_ERR_BAD_SHAPE;
   if (num_pages < 1 || max_pages < 1) return ETATTN_ERR_BAD_SHAPE;
-  if ((int64_t)max_seqlen_q * (Hq / Hkv) > kMaxTokens) return ETATTN_ERR_BAD_SHAPE;  // rows of one KV head
+  if ((int64_t)max_seqlen_q * Hq > kMaxTokens) return ETATTN_ERR_BAD_SHAPE;  // a sequence's rows
   if (!q || !o || !k_pages || !v_pages || !block_table || !seqlens_k) return ETATTN_ERR_NULL_PTR;
   const View vq = view3(q, total_q, Hq, D, st), vo = view3(o, total_q, Hq, D, st + 11);
   const View pk = view_pages(k_pages, num_pages, Hkv, page_size, D, st + 3);

@@ -234,6 +234,12 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
     }
   };
 
+  // Nothing to join, until the end says otherwise: whatever the workspace held
+  // must not be taken for a unit if a wait of this CTA runs out.
+  const int share = blockIdx.x;
+  PagedShare* desc = p.desc + share;
+  if (lane == 0 && p.shares > 1) desc->parts = 0;
+
   // This CTA's piece of the line: lane i sums up its run of sequences; the
   // lane whose run holds the piece's start finds the sequence.  (With up to 32
   // sequences a run is the lane's sequence of the window.)
@@ -264,12 +270,9 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
     }
   }
   const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
-  const int share = blockIdx.x;
   const PagedCut cut(total, p.shares);
   const int64_t begin = cut.start(share), end = cut.start(share + 1);
-  PagedShare* desc = p.desc + share;
   if (begin >= end) {
-    if (lane == 0 && p.shares > 1) desc->parts = 0;
     finish();
     return;
   }
@@ -385,11 +388,9 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
   }
   // The join of a unit that began in an earlier share is shared by those that
   // continue it: each leaves itself the unit and its shares.
-  if (lane == 0 && p.shares > 1) {
-    if (mark_tiles > 0) {
-      mark.first = cut.holder(mark_u0);
-      mark.parts = cut.holder(mark_u0 + mark_tiles - 1) - mark.first + 1;
-    }
+  if (lane == 0 && mark_tiles > 0) {
+    mark.first = cut.holder(mark_u0);
+    mark.parts = cut.holder(mark_u0 + mark_tiles - 1) - mark.first + 1;
     *desc = mark;
   }
   finish();
@@ -553,7 +554,8 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
 
     // Q's fragments; rows past the last hold anything, and nothing of them is
     // written.
-    uint32_t qf[D / 16][4], qseen = (uint32_t)(w.t0 | w.row0 | w.to_end);
+    uint32_t qf[D / 16][4];
+    uint32_t qseen = (uint32_t)(w.t0 | w.n | w.Lk | w.head0 | w.row0 | w.tile | w.tiles | w.from_start | w.to_end);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       ldsm4(qf[ks], smem_u32(smem + C::OFF_Q) + (16 * grp + (lane & 15)) * C::Q_PITCH + (ks * 2 + (lane >> 4)) * 16);

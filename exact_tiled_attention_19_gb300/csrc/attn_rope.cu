@@ -216,10 +216,11 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, int t) {
       return r;
     }
   }
-  const int64_t pos = (int64_t)p.seqlens_k[s] - n + (t - first);
-  if (pos < 0) return r;  // the token has no place in the cache
+  const int keys = p.seqlens_k[s];
+  const int64_t pos = (int64_t)keys - n + (t - first);
+  if (keys >= 0 && pos < 0) return r;  // the token has no place in the cache
   const int64_t col = pos >> p.page_shift;
-  if (col >= p.max_pages) {
+  if (keys < 0 || col >= p.max_pages) {
     atomicCAS(p.status, 0, (int)kDevBadSeqlens);
     return r;
   }

@@ -364,6 +364,9 @@ int attn_fwd_varlen_ex(const void* q, const void* k, const void* v, void* o, flo
  * offsets or lengths that do not fit (ETATTN_ERR_BAD_SEQLENS), and positions
  * past the rotation tables or pages outside 0 .. num_pages-1
  * (ETATTN_ERR_BAD_INDEX).  Nothing is read or written out of range.
+ * The first of these calls on a device sets kernel attributes; make it before
+ * any stream capture begins.  A captured call reads lengths, tables and
+ * positions when it is replayed.
  */
 
 /*
@@ -445,8 +448,9 @@ int attn_paged_append(const void* q, const void* k, const void* v, const void* q
  *   q, o: logical [total_q, Hq, D];  lse: [Hq, total_q] contiguous FP32 (or NULL)
  *   strides: 14 int64 values, (t, h, d) for q, (page, head, slot, d) for
  *           k_pages and v_pages, (t, h, d) for o.
- *   max_seqlen_q: the most new tokens of a sequence; with cu_seqlens_q = NULL
- *           the number of each (total_q = num_seqs * max_seqlen_q).
+ *   max_seqlen_q: the most new tokens of a sequence (max_seqlen_q * Hq <=
+ *           2^30); with cu_seqlens_q = NULL the number of each (total_q =
+ *           num_seqs * max_seqlen_q).
  *   num_shares: 1 .. 65535.  The key tiles of all sequences and heads are cut
  *           into that many equal shares that run side by side; a second launch
  *           joins what a boundary cut (attn_fwd_paged_plan suggests a number).

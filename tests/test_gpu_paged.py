@@ -276,6 +276,82 @@ def test_another_stream_and_a_replayed_graph():
     check_attention(o, lse, q, k_pages, v_pages, table, lens, [0, 1, 2, 3])
 
 
+def test_calls_on_two_streams_at_once():
+    """Two problems in flight on two streams, given as the helpers' stream,
+    many times over: each gives its own result every time."""
+    jobs = []
+    for seed, lens, Hq in ((1, [900, 40, 333], 8), (2, [64, 1200], 6)):
+        k_pages, v_pages, table, seqlens = make_cache(lens, 16, 2, 64, torch.bfloat16, seed=seed)
+        q = torch.randn(len(lens), Hq, 64).bfloat16().cuda()
+        ref = binding.attention_paged(q, k_pages, v_pages, table, seqlens, num_shares=50)
+        jobs.append((q, k_pages, v_pages, table, seqlens, torch.cuda.Stream(), ref))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (q, k_pages, v_pages, table, seqlens, stream, _) in enumerate(jobs):
+            got[i].append(binding.attention_paged(q, k_pages, v_pages, table, seqlens, num_shares=50, stream=stream))
+    torch.cuda.synchronize()
+    for i, job in enumerate(jobs):
+        for o, lse in got[i]:
+            assert torch.equal(o, job[6][0]) and torch.equal(lse, job[6][1])
+
+
+def test_two_graphs_replayed_in_turn():
+    """Two captured graphs, each with a workspace of its own from its pool."""
+    graphs = []
+    for seed, lens in ((3, [500, 77]), (4, [1000, 9])):
+        k_pages, v_pages, table, seqlens = make_cache(lens, 16, 2, 128, torch.float16, seed=seed)
+        q = torch.randn(2, 8, 128).half().cuda()
+        ref = binding.attention_paged(q, k_pages, v_pages, table, seqlens, num_shares=30)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = binding.attention_paged(q, k_pages, v_pages, table, seqlens, num_shares=30)
+        graphs.append((graph, out, ref, q, k_pages, v_pages, table, seqlens))
+    for _ in range(3):
+        for graph, *_ in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, out, ref, *_ in graphs:
+        assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+
+
+def test_a_stream_of_another_kind_is_refused():
+    class Elsewhere:
+        device = torch.device("cuda", 7)
+        cuda_stream = 0
+
+    k_pages, v_pages, table, seqlens = make_cache([20], 16, 1, 32, torch.float16)
+    q = torch.zeros(1, 1, 32, dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError):
+        binding.attention_paged(q, k_pages, v_pages, table, seqlens, stream=Elsewhere())
+
+
+@pytest.mark.parametrize("layout", ["hnd", "nhd"])
+def test_caches_past_32_bit_offsets(layout):
+    """Pages at the end of a cache of more than 2^31 elements (and so bytes):
+    what is appended there is what attention reads back."""
+    page, Hkv, D = 128, 8, 128
+    pool = (1 << 31) // (page * Hkv * D) + 9
+    shape = (pool, Hkv, page, D) if layout == "hnd" else (pool, page, Hkv, D)
+    k_pages, v_pages = (torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    if layout == "nhd":
+        k_pages, v_pages = k_pages.permute(0, 2, 1, 3), v_pages.permute(0, 2, 1, 3)
+    lens = [300, 129]
+    table = torch.tensor([[pool - 1, pool - 4, pool - 2], [pool - 3, 0, -1]], dtype=torch.int32).cuda()
+    seqlens = torch.tensor(lens, dtype=torch.int32).cuda()
+    cu = [0, 300, 429]
+    k, v = (torch.randn(429, Hkv, D).bfloat16().cuda() for _ in range(2))
+    binding.paged_append(k, v, k_pages, v_pages, table, seqlens,
+                         cu_seqlens_q=torch.tensor(cu, dtype=torch.int32).cuda())
+    q = torch.randn(2, Hkv, D).bfloat16().cuda()
+    o, lse = binding.attention_paged(q, k_pages, v_pages, table, seqlens)
+    used = torch.tensor([pool - 1, pool - 4, pool - 2, pool - 3, 0], device="cuda")  # alone, for the oracle
+    kp, vp = k_pages[used].contiguous(), v_pages[used].contiguous()
+    at = torch.tensor([[0, 1, 2], [3, 4, -1]], dtype=torch.int32)
+    check_attention(o, lse, q, kp, vp, at, lens, [0, 1, 2])
+    assert torch.equal(kp[0, :, 5], k[5]) and torch.equal(vp[4, :, 0], v[300 + 128])
+
+
 def test_bad_lengths_offsets_and_pages_are_recorded():
     k_pages, v_pages, table, seqlens = make_cache([60, 50, 40], 16, 2, 64, torch.bfloat16, seed=13)
     q = torch.randn(3, 4, 64).bfloat16().cuda()
@@ -396,6 +472,8 @@ def test_append_bad_places_are_recorded_and_skipped():
         assert run(binding.ETATTN_ERR_BAD_INDEX, table=t) == 2
     lens = seqlens.clone()
     lens[0] = 33  # two pages of 16 hold 32
+    assert run(binding.ETATTN_ERR_BAD_SEQLENS, seqlens=lens) == 2
+    lens[0] = -5
     assert run(binding.ETATTN_ERR_BAD_SEQLENS, seqlens=lens) == 2
     for cu in ([0, 1, 5, 3], [2, 2, 2, 3], [0, -1, 2, 3]):
         run(binding.ETATTN_ERR_BAD_SEQLENS, cu=torch.tensor(cu, dtype=torch.int32).cuda())

@@ -247,6 +247,20 @@ def test_results_repeat_bit_for_bit_and_on_another_stream():
         assert torch.equal(x, y)
 
 
+def test_a_given_stream_is_the_one_that_runs():
+    q, k, kw = make(700, 8, 2, 128, torch.bfloat16, 128, seed=14)
+    ref = binding.qk_norm_rope(q, k, **kw)
+    ref_g = binding.qk_norm_rope_backward(q, k, q, k, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = binding.qk_norm_rope(q, k, stream=side, **kw)
+        got_g = binding.qk_norm_rope_backward(q, k, q, k, stream=side, **kw)
+    side.synchronize()
+    for x, y in zip(ref + ref_g, got + got_g):
+        assert torch.equal(x, y)
+
+
 def test_captured_and_replayed_with_new_inputs():
     q, k, kw = make(40, 8, 2, 64, torch.bfloat16, 64, seed=12, fused=False)
     qo, ko = binding.qk_norm_rope(q, k, **kw)  # attributes set before the capture
