@@ -24,6 +24,7 @@ library is missing or cannot be loaded, an error is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -646,6 +647,20 @@ _STRIDES = {n: struct.Struct(f"{n}q").pack for n in (12, 14, 18, 20)}
 _CODES: dict = {}  # torch dtype -> ETATTN_* code
 
 
+@functools.lru_cache(maxsize=512)
+def _paged_plan(device_index, num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_shares):
+    """attn_fwd_paged_plan on the current device (``device_index``): a function of the sizes alone."""
+    rc, shares, need = attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_shares)
+    if rc != 0:
+        raise EtattnError(rc, "attn_fwd_paged_plan")
+    return shares, need
+
+
+@functools.lru_cache(maxsize=512)
+def _rope_bwd_bytes(T, Hq, Hk, D):
+    return attn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D)
+
+
 def _code_of(t):
     """The element type's code; a TypeError for another type."""
     code = _CODES.get(t.dtype)
@@ -665,6 +680,11 @@ def _elsewhere(torch, device, stream):
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
     return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _new_like(torch, t):
+    """A new contiguous tensor of t's shape (``empty_like``, the cheaper call, keeps a dense t's strides)."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _check(name, t, shape, dtype, device, dense=False):
@@ -757,9 +777,9 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, rope_cos=None, rope_sin=
             return qk_norm_rope(q, k, q_weight=q_weight, k_weight=k_weight, rope_cos=rope_cos, rope_sin=rope_sin,
                                 positions=positions, interleaved=interleaved, eps=eps, q_out=q_out, k_out=k_out)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        q_out = _new_like(torch, q)
     if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=dtype, device=device)
+        k_out = _new_like(torch, k)
     rc = (_lib or load_library()).attn_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), wq, wk, cos, sin, pos, q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hk, D, code,
         _STRIDES[12](*q.stride(), *k.stride(), *q_out.stride(), *k_out.stride()), rope_dim, interleaved,
@@ -797,16 +817,16 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
                                          interleaved=interleaved, eps=eps, dq=dq, dk=dk, workspace=workspace)
     lib = _lib or load_library()
     if dq is None:
-        dq = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        dq = _new_like(torch, q)
     if dk is None:
-        dk = torch.empty((T, Hk, D), dtype=dtype, device=device)
+        dk = _new_like(torch, k)
     dwq = torch.empty(D, dtype=torch.float32, device=device) if wq else None
     dwk = torch.empty(D, dtype=torch.float32, device=device) if wk else None
     ws_bytes = 0
     if workspace is not None:
         ws_bytes = _workspace(workspace, device)
     elif wq or wk:
-        ws_bytes = lib.attn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D)
+        ws_bytes = _rope_bwd_bytes(T, Hq, Hk, D)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
     rc = lib.attn_qk_norm_rope_bwd(
         q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), wq, wk, cos, sin, pos, dq.data_ptr(),
@@ -887,7 +907,7 @@ def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_we
         q_out, qp, op, q_stride, o_stride = None, 0, 0, (0, 0, 1), (0, 0, 1)
     else:
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+            q_out = _new_like(torch, q)
         qp, op, q_stride, o_stride = q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
     rc = (_lib or load_library()).attn_paged_append(
         qp, k.data_ptr(), v.data_ptr(), wq, wk, cos, sin, op, k_pages.data_ptr(), v_pages.data_ptr(),
@@ -936,27 +956,22 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
                                    workspace=workspace, out=out, lse=lse, return_lse=return_lse)
     lib = _lib or load_library()
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        out = _new_like(torch, q)
     if lse is None and return_lse:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
     if num_shares is None or workspace is None:
-        shares, need = _int(0 if num_shares is None else num_shares), ctypes.c_size_t(0)
         if max_seqlen_k is None:
             max_seqlen_k = min(width * page_size, 1 << 30)
-        rc = lib.attn_fwd_paged_plan(S, Hq, Hkv, int(max_seqlen_q), int(max_seqlen_k), D, shares, need)
-        if rc != 0:
-            raise EtattnError(rc, "attn_fwd_paged_plan")
-        num_shares = shares.value
-    if workspace is None:
-        ws_bytes = need.value
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
-    else:
+        num_shares, ws_bytes = _paged_plan(device.index, S, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_shares or 0)
+    if workspace is not None:
         ws_bytes = _workspace(workspace, device)
+    elif ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
     rc = lib.attn_fwd_paged(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-        block_table.data_ptr(), seqlens_k.data_ptr(), cu, S, int(max_seqlen_q), T, Hq, Hkv, D, code,
+        block_table.data_ptr(), seqlens_k.data_ptr(), cu, S, max_seqlen_q, T, Hq, Hkv, D, code,
         _STRIDES[14](*q.stride(), *k_pages.stride(), *v_pages.stride(), *out.stride()), page_size, num_pages, width,
-        row, causal, int(window_left), int(window_right), D ** -0.5 if scale is None else scale, int(num_shares),
+        row, causal, window_left, window_right, D ** -0.5 if scale is None else scale, num_shares,
         0 if workspace is None else workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
     if rc != 0:
         raise EtattnError(rc, "attn_fwd_paged")
