@@ -87,31 +87,40 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// A thread's two chunks of a row.  Rotated lanes hold the pairs (first + j,
-// second + j), or, interleaved, 16 neighbours; the others 16 neighbours past
-// rope_dim.
+// A thread's two chunks of a row: element offsets, whether they are rotated
+// and where the angles of the thread's pairs 0-3 and 4-7 start in a table row.
+// Neighbouring lanes hold neighbouring chunks, so that a warp's access covers
+// whole sectors.  Pairs of halves: (first + j, second + j), the elements past
+// rope_dim in two runs of their own; side by side: a chunk's own neighbours.
 struct Chunks {
-  int first, second;  // element offsets
-  bool rotated;
+  int first, second;
+  bool turn_first, turn_second;
+  int angle_first, angle_second;
 };
-__device__ __forceinline__ Chunks chunks_of(int lane, int rope_dim, bool interleaved) {
-  if (interleaved) return {16 * lane, 16 * lane + 8, 16 * lane < rope_dim};
+__device__ __forceinline__ Chunks chunks_of(int D, int lane, int rope_dim, bool interleaved) {
+  if (interleaved) {
+    const int a = 8 * lane, b = D / 2 + 8 * lane;
+    return {a, b, a < rope_dim, b < rope_dim, a / 2, b / 2};
+  }
   const int n = rope_dim / 16;
-  if (lane < n) return {8 * lane, rope_dim / 2 + 8 * lane, true};
-  return {16 * lane, 16 * lane + 8, false};
+  if (lane < n) return {8 * lane, rope_dim / 2 + 8 * lane, true, true, 8 * lane, 8 * lane + 4};
+  const int a = rope_dim + 8 * (lane - n);
+  return {a, a + (D - rope_dim) / 2, false, false, 0, 0};
 }
 
 // cos and sin of the thread's eight pairs (1 and 0 where nothing rotates).
 __device__ __forceinline__ void load_angles(float (&c)[8], float (&s)[8], const float* cos, const float* sin,
-                                            int64_t pos, int rope_dim, int lane, bool rotated) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) c[j] = 1.f, s[j] = 0.f;
-  if (!rotated) return;
-  const float* pc = cos + pos * (rope_dim / 2) + 8 * lane;  // half and interleaved pairs alike: 8 lane ..
-  const float* ps = sin + pos * (rope_dim / 2) + 8 * lane;
+                                            int64_t pos, int rope_dim, const Chunks& ch, bool on) {
+  const float* pc = cos + pos * (rope_dim / 2);
+  const float* ps = sin + pos * (rope_dim / 2);
 #pragma unroll
   for (int j = 0; j < 8; j += 4) {
-    const float4 c4 = *reinterpret_cast<const float4*>(pc + j), s4 = *reinterpret_cast<const float4*>(ps + j);
+    float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on && (j == 0 ? ch.turn_first : ch.turn_second)) {
+      const int at = j == 0 ? ch.angle_first : ch.angle_second;
+      c4 = *reinterpret_cast<const float4*>(pc + at);
+      s4 = *reinterpret_cast<const float4*>(ps + at);
+    }
     c[j] = c4.x, c[j + 1] = c4.y, c[j + 2] = c4.z, c[j + 3] = c4.w;
     s[j] = s4.x, s[j + 1] = s4.y, s[j + 2] = s4.z, s[j + 3] = s4.w;
   }
@@ -163,15 +172,15 @@ __device__ __forceinline__ float dot16(const float (&a)[16], const float (&b)[16
   for (int j = 0; j < 16; j += 2) fma2(s0, s1, a[j], a[j + 1], b[j], b[j + 1], s0, s1);
   return s0 + s1;
 }
-// y = x P + x_partner Q.  A lane that does not rotate must not meet its
+// y = x P + x_partner Q.  An element that does not rotate must not meet its
 // "partner" (0 times infinity is not 0).
 template <bool INTER, bool FULL>
-__device__ __forceinline__ void turn16(const float (&x)[16], const float (&P)[16], const float (&Q)[16], bool rotated,
-                                       float (&y)[16]) {
+__device__ __forceinline__ void turn16(const float (&x)[16], const float (&P)[16], const float (&Q)[16],
+                                       const Chunks& ch, float (&y)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
-    const float o0 = FULL || rotated ? x[partner<INTER>(j)] : 0.f;
-    const float o1 = FULL || rotated ? x[partner<INTER>(j + 1)] : 0.f;
+    const bool turn = FULL || (j < 8 ? ch.turn_first : ch.turn_second);
+    const float o0 = turn ? x[partner<INTER>(j)] : 0.f, o1 = turn ? x[partner<INTER>(j + 1)] : 0.f;
     float t0, t1;
     fma2(t0, t1, x[j], x[j + 1], P[j], P[j + 1], 0.f, 0.f);
     fma2(y[j], y[j + 1], o0, o1, Q[j], Q[j + 1], t0, t1);
@@ -246,10 +255,10 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, int t) {
 // heads of a token are numbered q, then k, then (paged) v; a group's heads are
 // all of one kind.  FULL: the whole head is rotated.
 template <int D, bool BF16, int HP, bool INTER, bool FULL>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, HP > 1 ? 3 : 4) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = D / 16, GROUPS = kThreads / LANES;
   const int lane = threadIdx.x % LANES;
-  const Chunks ch = chunks_of(lane, FULL ? D : p.rope_dim, INTER);
+  const Chunks ch = chunks_of(D, lane, FULL ? D : p.rope_dim, INTER);
   const int cq = (p.Hq + HP - 1) / HP, ck = (p.Hk + HP - 1) / HP, per_token = cq + (p.paged ? 2 : 1) * ck;
   const int64_t item = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES;
   const bool live = item < (int64_t)p.total_tokens * per_token;
@@ -300,12 +309,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   out += h0 * oh;
 
   const void* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-  const bool rotated = kind != 2 && ch.rotated;
   float P[16], Q[16];
   {
     float w[16], c8[8], s8[8];
     load_weight<BF16>(weight, ch, w);
-    load_angles(c8, s8, p.cos, p.sin, ok ? at.pos : 0, FULL ? D : p.rope_dim, lane, ok && rotated);
+    load_angles(c8, s8, p.cos, p.sin, ok ? at.pos : 0, FULL ? D : p.rope_dim, ch, ok && kind != 2);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       P[j] = w[j] * c8[pair_of<INTER>(j)];
@@ -323,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     float x[16], y[16];
     unpack16<BF16>(ra, rb, x);
     const float ss = row_sum<LANES>(dot16(x, x));
-    turn16<INTER, FULL>(x, P, Q, rotated, y);
+    turn16<INTER, FULL>(x, P, Q, ch, y);
     if (weight != nullptr) {
       const float r = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_cons
   constexpr int LANES = D / 16, GROUPS = kThreads / LANES;
   pdl_launch_dependents();
   const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-  const Chunks ch = chunks_of(lane, FULL ? D : p.rope_dim, INTER);
+  const Chunks ch = chunks_of(D, lane, FULL ? D : p.rope_dim, INTER);
   const bool is_q = (int)blockIdx.x < p.q_blocks;
   const int block = is_q ? blockIdx.x : blockIdx.x - p.q_blocks;
   const int blocks = is_q ? p.q_blocks : p.blocks - p.q_blocks;
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_cons
   extern __shared__ uint4 cells[];
   uint4* const row_cells = cells + threadIdx.x;
   uint4* const angle_cells = cells + HP * 4 * kThreads + threadIdx.x;
-  const bool turns = p.rope_dim > 0 && ch.rotated;
+  const bool turn_first = p.rope_dim > 0 && ch.turn_first, turn_second = p.rope_dim > 0 && ch.turn_second;
   auto position = [&](Item x) { return x.t < p.total_tokens && p.rope_dim > 0 ? p.positions[x.t] : -1; };
   auto fetch_row = [&](Item x, int i) {
     if (x.t < p.total_tokens && x.h + i < heads) {
@@ -398,13 +406,17 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_cons
     }
   };
   auto fetch_angles = [&](int pos, int set) {
-    if (!turns || pos < 0 || pos >= p.max_position) return;
-    const int64_t off = (int64_t)pos * (p.rope_dim / 2) + 8 * lane;
+    if (pos < 0 || pos >= p.max_position) return;
+    const int64_t row = (int64_t)pos * (p.rope_dim / 2);
     uint4* dst = angle_cells + set * 4 * kThreads;
-    copy_async_shared(dst, p.cos + off);
-    copy_async_shared(dst + kThreads, p.cos + off + 4);
-    copy_async_shared(dst + 2 * kThreads, p.sin + off);
-    copy_async_shared(dst + 3 * kThreads, p.sin + off + 4);
+    if (turn_first) {
+      copy_async_shared(dst, p.cos + row + ch.angle_first);
+      copy_async_shared(dst + 2 * kThreads, p.sin + row + ch.angle_first);
+    }
+    if (turn_second) {
+      copy_async_shared(dst + kThreads, p.cos + row + ch.angle_second);
+      copy_async_shared(dst + 3 * kThreads, p.sin + row + ch.angle_second);
+    }
   };
   const int start = block * GROUPS + grp;
   Item item{start / per_token, (start % per_token) * HP};
@@ -438,8 +450,9 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int at = (j >> 2) * kThreads * 4 + (j & 3);
-          c8[j] = turns ? c4[at] : 1.f;
-          s8[j] = turns ? c4[2 * kThreads * 4 + at] : 0.f;
+          const bool turn = j < 4 ? turn_first : turn_second;
+          c8[j] = turn ? c4[at] : 1.f;
+          s8[j] = turn ? c4[2 * kThreads * 4 + at] : 0.f;
         }
       }
       float x[16], g[16];
@@ -452,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_cons
           P[j] = c8[pair_of<INTER>(j)];
           Q[j] = is_first<INTER>(j) ? s8[pair_of<INTER>(j)] : -s8[pair_of<INTER>(j)];
         }
-        turn16<INTER, FULL>(dy, P, Q, ch.rotated, g);
+        turn16<INTER, FULL>(dy, P, Q, ch, g);
       }
       if (weight != nullptr) {
         float gw[16];
@@ -517,9 +530,30 @@ __global__ void __launch_bounds__(1024) rope_bwd_weights_kernel(const float* par
   if (lane == 0) dst[blockIdx.x * 32 + part] = v;
 }
 
+// The dynamic shared-memory opt-in is per device; set once per device.
+template <typename P>
+cudaError_t opt_in(void (*kern)(P), int smem, std::atomic<unsigned long long>& configured) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) configured.fetch_or(bit);
+  }
+  return e;
+}
+
 template <int D, bool BF16, int HP, bool INTER, bool FULL>
 cudaError_t launch_fwd(const RopeParams& p, unsigned blocks, cudaStream_t s) {
-  rope_kernel<D, BF16, HP, INTER, FULL><<<blocks, kThreads, HP > 1 ? HP * 2 * kThreads * 16 : 0, s>>>(p);
+  auto kern = rope_kernel<D, BF16, HP, INTER, FULL>;
+  constexpr int SMEM = HP > 1 ? HP * 2 * kThreads * 16 : 0;
+  if (SMEM > 48 * 1024) {
+    static std::atomic<unsigned long long> configured{0};
+    const cudaError_t e = opt_in(kern, SMEM, configured);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<blocks, kThreads, SMEM, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -544,31 +578,28 @@ cudaError_t fwd(const RopeParams& p, cudaStream_t s) {
 }
 
 // One head a group while its blocks all run at once (four on each of a GB300's
-// 152 SMs), else four: measured with 32 + 8 heads of 128, 3.1 us against 4.3
-// at 8 tokens, 4.8 against 4.9 at 512, 6.8 against 5.8 at 1024 and 88 against
-// 60 at 16384 (heads of 64 and 32 cross at about the same number of blocks).
-// Two and eight heads a group are never the best by more than 5 %.
-constexpr int kOneHeadBlocks = 608, kHeads = 4;
+// 152 SMs), else four, and eight (which read the angles and weights half as
+// often) when more moves than the 126 MB L2 holds.  Measured with 32 + 8 heads
+// of 128, us with 1 / 4 / 8 heads a group: 3.1 / 4.0 / 5.1 at 128 tokens, 4.8 /
+// 4.5 / 5.1 at 512, 6.7 / 5.6 / 6.3 at 1024, 19 / 12.3 / 12.4 at 4096 (84 MB),
+// 46 / 33.6 / 31.3 at 8192 and 87 / 59 / 55 at 16384; heads of 64: 4.8 / 4.8 /
+// 5.5 at 1024, 20 / 13.0 / 13.5 at 8192 (84 MB), 46 / 33.9 / 32.1 at 16384.
+constexpr int kOneHeadBlocks = 608;
+constexpr int64_t kL2Bytes = 126 << 20;
 template <int D, bool BF16>
 cudaError_t fwd_any(const RopeParams& p, cudaStream_t s) {
-  return fwd_blocks<D>(p, 1) <= kOneHeadBlocks ? fwd<D, BF16, 1>(p, s) : fwd<D, BF16, kHeads>(p, s);
+  if (fwd_blocks<D>(p, 1) <= kOneHeadBlocks) return fwd<D, BF16, 1>(p, s);
+  const int64_t heads = (int64_t)p.Hq + (p.paged ? 2 : 1) * p.Hk;
+  return 4 * D * heads * p.total_tokens > kL2Bytes ? fwd<D, BF16, 8>(p, s) : fwd<D, BF16, 4>(p, s);
 }
 
 template <int D, bool BF16, bool INTER, bool FULL>
 cudaError_t launch_bwd(const RopeBwdParams& p, cudaStream_t s) {
   auto kern = rope_bwd_kernel<D, BF16, kRopeBwdHeads, INTER, FULL>;
   constexpr int SMEM = (kRopeBwdHeads + 2) * 4 * kThreads * 16;
-  // The dynamic shared-memory opt-in is per device; set it once per device.
   static std::atomic<unsigned long long> configured{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = opt_in(kern, SMEM, configured);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(bit);
-  }
   kern<<<(unsigned)p.blocks, kThreads, SMEM, s>>>(p);
   return cudaGetLastError();
 }

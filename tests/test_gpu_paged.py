@@ -442,6 +442,32 @@ def test_append_ragged_tokens(weighted, Hq, Hkv):
                 weighted, 3)
 
 
+def test_append_of_more_than_the_l2_holds_equals_pieces_of_it():
+    """140 MB of prompts at once (eight heads a group) leave the bits that the
+    same tokens leave when they come 60 at a time (one head a group)."""
+    S, Hq, Hkv, D, page = 4, 24, 8, 128, 32
+    n = (140 << 20) // (4 * D * (Hq + 2 * Hkv)) // S // 60 * 60 + 60
+    k_pages, v_pages, table, _ = make_cache([n] * S, page, Hkv, D, torch.bfloat16, "nhd", seed=3)
+    k2, v2 = k_pages.clone(), v_pages.clone()
+    x = torch.randn(S, n, Hq + 2 * Hkv, D).bfloat16().cuda()
+    cos, sin = binding.rope_tables(n, D)
+    w = (1 + 0.2 * torch.randn(D)).bfloat16().cuda()
+    kw = dict(q_weight=w, k_weight=w, rope_cos=cos, rope_sin=sin)
+
+    def append(rows, keys, kp, vp):
+        q, k, v = rows[..., :Hq, :], rows[..., Hq:Hq + Hkv, :], rows[..., Hq + Hkv:, :]
+        flat = lambda t: t.reshape(-1, t.shape[-2], D)  # noqa: E731
+        lens = torch.full((S,), keys, dtype=torch.int32, device="cuda")
+        return binding.paged_append(flat(k), flat(v), kp, vp, table, lens, q=flat(q), **kw).view(S, -1, Hq, D)
+
+    whole = append(x, n, k_pages, v_pages)
+    for a in list(range(0, n, 60)):
+        part = append(x[:, a:a + 60], a + 60, k2, v2)
+        if a in (0, 600, n - 60):
+            assert torch.equal(part, whole[:, a:a + 60])
+    assert torch.equal(k_pages, k2) and torch.equal(v_pages, v2)
+
+
 def test_append_rows_behind_the_last_sequence_stay():
     k_pages, v_pages, table, seqlens = make_cache([20, 10], 16, 2, 64, torch.bfloat16)
     before = k_pages.clone()

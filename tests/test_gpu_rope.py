@@ -148,6 +148,21 @@ def test_many_tokens(T):
     check_backward(dk, dwk, k, kw["k_weight"], ko, kw, False, 1e-6, torch.bfloat16)
 
 
+@pytest.mark.parametrize("Hq,Hk,D,rope_dim,interleaved", [(32, 8, 128, 128, False), (33, 7, 128, 64, True),
+                                                            (61, 12, 64, 64, False)])
+def test_more_than_the_l2_holds_equals_pieces_of_it(Hq, Hk, D, rope_dim, interleaved):
+    """Every row is computed by itself, so a large call (whose groups take eight
+    heads) gives the bits of small ones (one head a group)."""
+    T = (140 << 20) // (4 * D * (Hq + Hk)) + 5
+    q, k, kw = make(T, Hq, Hk, D, torch.bfloat16, rope_dim, seed=1)
+    qo, ko = binding.qk_norm_rope(q, k, interleaved=interleaved, **kw)
+    for a, b in ((0, 97), (T // 2, T // 2 + 130), (T - 101, T)):
+        part = dict(kw, positions=kw["positions"][a:b])
+        qp, kp = binding.qk_norm_rope(q[a:b], k[a:b], interleaved=interleaved, **part)
+        assert torch.equal(qp, qo[a:b]) and torch.equal(kp, ko[a:b])
+        check_forward(qp, q[a:b], kw["q_weight"], part, interleaved, 1e-6, torch.bfloat16)
+
+
 def test_gradients_equal_differences_of_the_forward_pass():
     """Directional differences of sum(dy * y) in the oracle's own forward pass
     (64 bits) against the kernel's gradients: the gradients' rounding to FP16
