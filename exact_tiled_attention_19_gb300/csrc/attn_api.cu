@@ -19,6 +19,7 @@
 
 #include "attn_bwd_kernel.cuh"
 #include "attn_fwd_kernel.cuh"
+#include "cache_ptx.cuh"
 #include "etattn.h"
 #include "launchers.h"
 

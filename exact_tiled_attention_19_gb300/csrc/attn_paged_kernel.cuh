@@ -39,7 +39,7 @@
 #include <cuda.h>
 
 #include "launchers.h"
-#include "sm103_ptx.cuh"
+#include "cache_ptx.cuh"
 
 namespace etattn {
 
@@ -359,7 +359,7 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
         __syncwarp();
         if (on) {
           if (pg < 0 || pg >= p.num_pages) {
-            atomicCAS(p.status, 0, (int)kDevBadIndex);
+            atomicCAS(p.status, 0, kDevBadIndex);
             pg = p.num_pages;  // past the map: the box is filled with zeros
           }
           const int slot = k0 & (page_keys - 1);

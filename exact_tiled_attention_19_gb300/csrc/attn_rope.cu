@@ -26,7 +26,7 @@
 #include <cuda_runtime.h>
 
 #include "launchers.h"
-#include "sm103_ptx.cuh"
+#include "cache_ptx.cuh"
 
 namespace etattn {
 
@@ -199,7 +199,7 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, int t) {
   if (!p.paged) {
     r.pos = p.positions != nullptr ? p.positions[t] : 0;
     r.ok = p.rope_dim == 0 || (r.pos >= 0 && r.pos < p.max_position);
-    if (!r.ok) atomicCAS(p.status, 0, (int)kDevBadIndex);
+    if (!r.ok) atomicCAS(p.status, 0, kDevBadIndex);
     return r;
   }
   // The sequence of token t: equal shares, or the last s with cu[s] <= t.
@@ -234,12 +234,12 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, int t) {
     return r;
   }
   if (p.rope_dim > 0 && pos >= p.max_position) {
-    atomicCAS(p.status, 0, (int)kDevBadIndex);
+    atomicCAS(p.status, 0, kDevBadIndex);
     return r;
   }
   const int page = p.block_table[(int64_t)s * p.table_stride + col];
   if (page < 0 || page >= p.num_pages) {
-    atomicCAS(p.status, 0, (int)kDevBadIndex);
+    atomicCAS(p.status, 0, kDevBadIndex);
     return r;
   }
   const int64_t slot = pos & ((1 << p.page_shift) - 1);
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_cons
     uint16_t* out = d0 + (live ? item.t * ot + item.h * oh : 0);
     const int h0 = item.h;
     const bool ok = live && (p.rope_dim == 0 || (pos >= 0 && pos < p.max_position));
-    if (live && !ok) atomicCAS(p.status, 0, (int)kDevBadIndex);
+    if (live && !ok) atomicCAS(p.status, 0, kDevBadIndex);
     fetch_angles(pos_next, set ^ 1);  // part of the next group that is committed
     pos = pos_next;
     pos_next = position(second);

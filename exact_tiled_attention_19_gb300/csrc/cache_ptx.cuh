@@ -1,0 +1,39 @@
+// What the kernels on norm, rotation and paged caches use beside sm103_ptx.cuh.
+#pragma once
+
+#include "sm103_ptx.cuh"
+
+namespace etattn {
+
+// Device status: a position or a page out of range (after DeviceStatus).
+constexpr int kDevBadIndex = 3;
+
+__device__ __forceinline__ void tma_load_5d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                                 int c2, int c3, int c4, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(policy)
+      : "memory");
+}
+
+// named_barrier, telling every thread whether some thread's `x` is set.
+__device__ __forceinline__ bool named_barrier_or(int id, int count, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
+// a / b for a >= 0, b > 0, in 32 bits where they do (the 64-bit division is a
+// long sequence of instructions).
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+}  // namespace etattn

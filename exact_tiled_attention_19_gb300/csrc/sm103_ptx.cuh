@@ -17,7 +17,6 @@ enum DeviceStatus : int {
   kDevOk = 0,
   kDevWaitTimeout = 1,
   kDevBadSeqlens = 2,
-  kDevBadIndex = 3,
 };
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s of global time
@@ -99,14 +98,6 @@ __device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_5d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
-                                                 int c2, int c3, int c4, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(policy)
-      : "memory");
-}
 // 1-D bulk copy of `bytes` (a multiple of 16; both addresses 16-byte
 // aligned) from global to shared memory, completion signalled on `bar`.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -133,17 +124,6 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 // Barrier among `count` threads (a multiple of 32) on named barrier `id`.
 __device__ __forceinline__ void named_barrier(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-// The same, telling every thread whether some thread's `x` is set.
-__device__ __forceinline__ bool named_barrier_or(int id, int count, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)x), "r"(id), "r"(count)
-      : "memory");
-  return r != 0;
 }
 
 // Programmatic dependent launch: let the next grid on the stream be
@@ -310,12 +290,6 @@ __device__ __forceinline__ void regs_shrink() {
 }
 
 // ---------------------------------------------------------------- math
-// a / b for a >= 0, b > 0, in 32 bits where they do (the 64-bit division is a
-// long sequence of instructions).
-__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
 // Three-input maximum (one instruction on sm_100+).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
