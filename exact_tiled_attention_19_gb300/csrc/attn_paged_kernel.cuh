@@ -33,6 +33,13 @@
 // holds, and the product with V runs once per token of the tile with the
 // values outside that token's range replaced by 0, so that nothing stored
 // outside a row's range (a NaN in a page's unused slots, say) reaches it.
+//
+// Measured (GB300, D = 128, 32 query and 8 KV heads, BF16, one new token, CUDA
+// graph): 8 sequences of 32768 keys 161 us, 6.68 TB/s of the 6.80 that a plain
+// copy reaches; one of 524288 keys 316 us, 6.80 TB/s; 64 of 1 .. 16384 keys 79
+// us, 6.04 TB/s (the units of short sequences cost their entry); one of 1000
+// keys 9 us (two launches, three dependent loads, the join).  32 rows (8 new
+// tokens) over 8 x 32768 keys: 189 us.
 #pragma once
 
 #include <cstdint>
