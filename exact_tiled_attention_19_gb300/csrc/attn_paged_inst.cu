@@ -118,24 +118,6 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   }
 }
 
-// Programmatic stream serialisation (as for the forward kernel): the grid may
-// be scheduled while its predecessor on the stream ends; griddepcontrol.wait
-// in the kernel keeps its memory accesses behind the predecessor's completion.
-template <typename... A>
-cudaError_t launch_pdl(void (*kern)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int MT>
 cudaError_t launch_one(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, cudaStream_t stream) {
   using C = PagedCfg<ETATTN_INST_D, MT>;

@@ -261,6 +261,8 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, int t) {
 // all of one kind.  FULL: the whole head is rotated.
 template <int D, bool BF16, int HP, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, HP > 1 ? 3 : 4) rope_kernel(const __grid_constant__ RopeParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr int LANES = D / 16, GROUPS = kThreads / LANES;
   const int lane = threadIdx.x % LANES;
   const Chunks ch = chunks_of(D, lane, FULL ? D : p.rope_dim, INTER);
@@ -361,6 +363,7 @@ template <int D, bool BF16, int HP, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
   constexpr int LANES = D / 16, GROUPS = kThreads / LANES;
   pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
   const Chunks ch = chunks_of(D, lane, FULL ? D : p.rope_dim, INTER);
   const bool is_q = (int)blockIdx.x < p.q_blocks;
@@ -558,8 +561,7 @@ cudaError_t launch_fwd(const RopeParams& p, unsigned blocks, cudaStream_t s) {
     const cudaError_t e = opt_in(kern, SMEM, configured);
     if (e != cudaSuccess) return e;
   }
-  kern<<<blocks, kThreads, SMEM, s>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(kern, dim3(blocks), kThreads, SMEM, s, p);
 }
 
 // Blocks of `hp` heads a group over all items.
@@ -605,8 +607,7 @@ cudaError_t launch_bwd(const RopeBwdParams& p, cudaStream_t s) {
   static std::atomic<unsigned long long> configured{0};
   const cudaError_t e = opt_in(kern, SMEM, configured);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)p.blocks, kThreads, SMEM, s>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(kern, dim3(p.blocks), kThreads, SMEM, s, p);
 }
 
 template <int D, bool BF16>
@@ -618,18 +619,8 @@ cudaError_t bwd(const RopeBwdParams& p, cudaStream_t s) {
     else e = full ? launch_bwd<D, BF16, false, true>(p, s) : launch_bwd<D, BF16, false, false>(p, s);
   }
   if (e != cudaSuccess || (p.dq_weight == nullptr && p.dk_weight == nullptr)) return e;
-  // Scheduled while the last blocks above still run; waits for them on the device.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(D / 32, 2);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_bwd_weights_kernel, (const float*)p.partials, p.q_blocks, p.blocks, D,
-                            p.dq_weight, p.dk_weight);
+  return launch_pdl(rope_bwd_weights_kernel, dim3(D / 32, 2), 1024, 0, s, (const float*)p.partials, p.q_blocks, p.blocks,
+                    D, p.dq_weight, p.dk_weight);
 }
 
 }  // namespace

@@ -85,6 +85,24 @@ ETATTN_DECLARE_BWD_LAUNCHER(launch_bwd_d128_1)
 
 #undef ETATTN_DECLARE_BWD_LAUNCHER
 
+// Programmatic stream serialisation (as for the forward kernel): the grid may
+// be scheduled while its predecessor on the stream ends; griddepcontrol.wait
+// in the kernel keeps its memory accesses behind the predecessor's completion.
+template <typename... A>
+cudaError_t launch_pdl(void (*kern)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Query/key norm and rotation, plain or into a paged cache (attn_rope.cu).
 // Strides in elements: token, head (pages: page, head, token); d-stride 1.
 struct RopeParams {
