@@ -793,8 +793,8 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
                           positions=None, interleaved: bool = False, eps: float = 1e-6, dq=None, dk=None,
                           workspace=None, stream=None):
     """Gradients (dq, dk, dq_weight, dk_weight) of ``qk_norm_rope`` for the
-    upstream gradients ``dq_out`` and ``dk_out``; the weights' are FP32 [D]
-    (None without the weight)."""
+    upstream gradients ``dq_out`` and ``dk_out`` (not broadcast ones: a stride of
+    0 is refused); the weights' are FP32 [D] (None without the weight)."""
     import torch
     T, Hq, D = q.shape
     Hk, dtype, device, code = k.shape[1], q.dtype, q.device, _code_of(q)
@@ -962,7 +962,8 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
     if num_shares is None or workspace is None:
         if max_seqlen_k is None:
             max_seqlen_k = min(width * page_size, 1 << 30)
-        num_shares, ws_bytes = _paged_plan(device.index, S, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_shares or 0)
+        num_shares, ws_bytes = _paged_plan(device.index, S, Hq, Hkv, int(max_seqlen_q), int(max_seqlen_k), D,
+                                           int(num_shares or 0))
     if workspace is not None:
         ws_bytes = _workspace(workspace, device)
     elif ws_bytes:

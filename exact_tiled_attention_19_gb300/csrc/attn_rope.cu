@@ -23,9 +23,9 @@
 // arithmetic.
 //
 // Measured (GB300, 16384 tokens, 32 + 8 heads of 128, BF16, CUDA graph; the
-// plain copy reaches 6.80 TB/s): norm and rotation 54.5 us, 6.31 TB/s (51.4
+// plain copy reaches 6.80 TB/s): norm and rotation 54.2 us, 6.35 TB/s (51.4
 // without the rotation, whose angles each group reads again); gradients 80 us,
-// 6.38 TB/s; 16000 tokens into a cache 64.5 us, 6.22 TB/s; 8 tokens 2.5 us.
+// 6.39 TB/s; 16000 tokens into a cache 64.1 us, 6.26 TB/s; 8 tokens 2.3 us.
 #include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
