@@ -641,7 +641,8 @@ def attention_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = Tru
 # helpers below keep their own time down: one comparison per tensor on the way
 # through (the messages are made when it fails), strides packed into bytes, the
 # device made current (by a second call of the helper) only when it is not, and
-# the C functions called directly.
+# the C functions called directly.  (``empty_like`` and ``empty`` with its sizes
+# as arguments take half the time of ``empty`` with a tuple.)
 
 _STRIDES = {n: struct.Struct(f"{n}q").pack for n in (12, 14, 18, 20)}
 _CODES: dict = {}  # torch dtype -> ETATTN_* code
@@ -682,15 +683,8 @@ def _elsewhere(torch, device, stream):
     return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
-def _new_like(torch, t):
-    """A new contiguous tensor of t's shape (``empty_like``, the cheaper call, keeps a dense t's strides)."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-
-
 def _check(name, t, shape, dtype, device, dense=False):
-    """Raises for a tensor argument that is not as it must be (None passes)."""
-    if t is None:
-        return
+    """Raises for a tensor argument that is not as it must be."""
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
@@ -705,11 +699,11 @@ def _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos, rope_sin):
     """(addresses of the weights and tables, rope_dim, max_position), after checking them."""
     wq = wk = cos = sin = rope_dim = max_position = 0
     if q_weight is not None:
-        if q_weight.shape != (D,) or q_weight.dtype != dtype or q_weight.device != device or q_weight.stride(0) != 1:
+        if q_weight.shape != (D,) or q_weight.dtype != dtype or q_weight.device != device or not q_weight.is_contiguous():
             _check("q_weight", q_weight, (D,), dtype, device, True)
         wq = q_weight.data_ptr()
     if k_weight is not None:
-        if k_weight.shape != (D,) or k_weight.dtype != dtype or k_weight.device != device or k_weight.stride(0) != 1:
+        if k_weight.shape != (D,) or k_weight.dtype != dtype or k_weight.device != device or not k_weight.is_contiguous():
             _check("k_weight", k_weight, (D,), dtype, device, True)
         wk = k_weight.data_ptr()
     if rope_cos is not None and rope_sin is not None:
@@ -735,8 +729,8 @@ def _positions(torch, positions, T, rope_dim, device):
         if rope_dim:
             raise ValueError("positions are needed with rope_cos and rope_sin")
         return 0
-    if positions.shape != (T,) or positions.dtype != torch.int32 or positions.device != device or (
-            T > 1 and positions.stride(0) != 1):
+    if (positions.shape != (T,) or positions.dtype != torch.int32 or positions.device != device
+            or not positions.is_contiguous()):
         _check("positions", positions, (T,), torch.int32, device, True)
     return positions.data_ptr()
 
@@ -769,17 +763,19 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, rope_cos=None, rope_sin=
     wq, wk, cos, sin, rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos,
                                                           rope_sin)
     pos = _positions(torch, positions, T, rope_dim, device)
-    _check("q_out", q_out, (T, Hq, D), dtype, device)
-    _check("k_out", k_out, (T, Hk, D), dtype, device)
+    if q_out is not None:
+        _check("q_out", q_out, (T, Hq, D), dtype, device)
+    if k_out is not None:
+        _check("k_out", k_out, (T, Hk, D), dtype, device)
     there = _elsewhere(torch, device, stream)
     if there is not None:
         with there:
             return qk_norm_rope(q, k, q_weight=q_weight, k_weight=k_weight, rope_cos=rope_cos, rope_sin=rope_sin,
                                 positions=positions, interleaved=interleaved, eps=eps, q_out=q_out, k_out=k_out)
     if q_out is None:
-        q_out = _new_like(torch, q)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if k_out is None:
-        k_out = _new_like(torch, k)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     rc = (_lib or load_library()).attn_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), wq, wk, cos, sin, pos, q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hk, D, code,
         _STRIDES[12](*q.stride(), *k.stride(), *q_out.stride(), *k_out.stride()), rope_dim, interleaved,
@@ -807,8 +803,10 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
     wq, wk, cos, sin, rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos,
                                                           rope_sin)
     pos = _positions(torch, positions, T, rope_dim, device)
-    _check("dq", dq, (T, Hq, D), dtype, device)
-    _check("dk", dk, (T, Hk, D), dtype, device)
+    if dq is not None:
+        _check("dq", dq, (T, Hq, D), dtype, device)
+    if dk is not None:
+        _check("dk", dk, (T, Hk, D), dtype, device)
     there = _elsewhere(torch, device, stream)
     if there is not None:
         with there:
@@ -817,9 +815,9 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
                                          interleaved=interleaved, eps=eps, dq=dq, dk=dk, workspace=workspace)
     lib = _lib or load_library()
     if dq is None:
-        dq = _new_like(torch, q)
+        dq = torch.empty_like(q, memory_format=torch.contiguous_format)
     if dk is None:
-        dk = _new_like(torch, k)
+        dk = torch.empty_like(k, memory_format=torch.contiguous_format)
     dwq = torch.empty(D, dtype=torch.float32, device=device) if wq else None
     dwk = torch.empty(D, dtype=torch.float32, device=device) if wk else None
     ws_bytes = 0
@@ -896,7 +894,8 @@ def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_we
         Hq = q.shape[1]
         if q.shape != (T, Hq, D) or q.dtype != dtype or q.device != device:
             _check("q", q, (T, Hq, D), dtype, device)
-        _check("q_out", q_out, (T, Hq, D), dtype, device)
+        if q_out is not None:
+            _check("q_out", q_out, (T, Hq, D), dtype, device)
     there = _elsewhere(torch, device, stream)
     if there is not None:
         with there:
@@ -907,7 +906,7 @@ def paged_append(k, v, k_pages, v_pages, block_table, seqlens_k, *, q=None, q_we
         q_out, qp, op, q_stride, o_stride = None, 0, 0, (0, 0, 1), (0, 0, 1)
     else:
         if q_out is None:
-            q_out = _new_like(torch, q)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         qp, op, q_stride, o_stride = q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
     rc = (_lib or load_library()).attn_paged_append(
         qp, k.data_ptr(), v.data_ptr(), wq, wk, cos, sin, op, k_pages.data_ptr(), v_pages.data_ptr(),
@@ -945,8 +944,10 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
         max_seqlen_q = T // S if S > 0 else 0
     elif max_seqlen_q is None:
         raise ValueError("max_seqlen_q is needed with cu_seqlens_q")
-    _check("out", out, (T, Hq, D), dtype, device)
-    _check("lse", lse, (Hq, T), torch.float32, device, True)
+    if out is not None:
+        _check("out", out, (T, Hq, D), dtype, device)
+    if lse is not None:
+        _check("lse", lse, (Hq, T), torch.float32, device, True)
     there = _elsewhere(torch, device, stream)
     if there is not None:
         with there:
@@ -956,9 +957,9 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
                                    workspace=workspace, out=out, lse=lse, return_lse=return_lse)
     lib = _lib or load_library()
     if out is None:
-        out = _new_like(torch, q)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if lse is None and return_lse:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
+        lse = torch.empty(Hq, T, dtype=torch.float32, device=device)
     if num_shares is None or workspace is None:
         if max_seqlen_k is None:
             max_seqlen_k = min(width * page_size, 1 << 30)
