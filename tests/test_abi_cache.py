@@ -228,6 +228,17 @@ def test_helpers_refuse_mismatched_tensors():
         B.attention_paged(q[..., :32], pages, pages, table, lens)
 
 
+def test_helpers_refuse_tensors_outside_the_gpu():
+    q, k = torch.zeros(6, 4, 64, dtype=torch.bfloat16), torch.zeros(6, 2, 64, dtype=torch.bfloat16)
+    pages = torch.zeros(9, 2, 16, 64, dtype=torch.bfloat16)
+    table, lens = torch.zeros(6, 2, dtype=torch.int32), torch.ones(6, dtype=torch.int32)
+    for call in (lambda: B.qk_norm_rope(q, k), lambda: B.qk_norm_rope_backward(q, k, q, k),
+                 lambda: B.paged_append(k, k, pages, pages.clone(), table, lens),
+                 lambda: B.attention_paged(q, pages, pages, table, lens)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
 def test_rope_tables_are_exact_far_out():
     cos, sin = B.rope_tables(200000, 32, device="cpu")
     import math
