@@ -1170,8 +1170,10 @@ int append_impl(const void* q, const void* k, const void* v, const void* q_weigh
   if (int rc = pages_ok(num_seqs, page_size, num_pages, max_pages, table_stride)) return rc;
   if (Hkv <= 0) return ETATTN_ERR_BAD_HEADS;
   if (st == nullptr) return ETATTN_ERR_NULL_PTR;
-  if (total_tokens == 0 || num_seqs == 0) return ETATTN_OK;
-  if (cu_seqlens == nullptr && total_tokens % num_seqs != 0) return ETATTN_ERR_BAD_SHAPE;
+  if (total_tokens == 0) return ETATTN_OK;
+  // Without offsets every token belongs to a sequence; with them the rows of no sequence are left alone.
+  if (cu_seqlens == nullptr && (num_seqs == 0 || total_tokens % num_seqs != 0)) return ETATTN_ERR_BAD_SHAPE;
+  if (num_seqs == 0) return ETATTN_OK;
   if (num_pages < 1 || max_pages < 1) return ETATTN_ERR_BAD_SHAPE;
   if (int rc = tables_ok(cos, sin, rope_dim, max_position, q_weight, k_weight, eps)) return rc;
   if (!k || !v || !k_pages || !v_pages || !block_table || !seqlens_k || (Hq > 0 && (!q || !q_out)))
@@ -1298,8 +1300,12 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
   if (!std::isfinite(scale) || !(scale > 0.f)) return ETATTN_ERR_BAD_SCALE;
   if (st == nullptr) return ETATTN_ERR_NULL_PTR;
   if (num_shares < 1 || num_shares > kMaxShares) return ETATTN_ERR_BAD_SHAPE;
-  if (num_seqs == 0 || Hq == 0 || total_q == 0 || max_seqlen_q == 0) return ETATTN_OK;
+  if (Hq == 0 || total_q == 0) return ETATTN_OK;
+  // Without offsets every row belongs to a sequence and has to be written.
   if (cu_seqlens_q == nullptr && (int64_t)num_seqs * max_seqlen_q != total_q) return ETATTN_ERR_BAD_SHAPE;
+  if (num_seqs == 0) return ETATTN_OK;
+  // A bound of 0 new tokens leaves nothing to share; whether the offsets keep it shows on the device.
+  if (max_seqlen_q == 0) num_shares = 1;
   if (num_pages < 1 || max_pages < 1) return ETATTN_ERR_BAD_SHAPE;
   if ((int64_t)max_seqlen_q * Hq > kMaxTokens) return ETATTN_ERR_BAD_SHAPE;  // a sequence's rows
   if (!q || !o || !k_pages || !v_pages || !block_table || !seqlens_k) return ETATTN_ERR_NULL_PTR;

@@ -429,6 +429,8 @@ size_t attn_qk_norm_rope_bwd_workspace_size(int total_tokens, int Hq, int Hk, in
  * A token whose position would be negative has no place: nothing of it is
  * written, its q_out row neither.  A token of a bad sequence, past the block
  * table or the rotation tables, or on a bad page is skipped and recorded.
+ * With cu_seqlens_q = NULL total_tokens is a multiple of num_seqs, and 0 when
+ * that is 0 (ETATTN_ERR_BAD_SHAPE).
  * k_pages and v_pages must not overlap q, k, v or q_out; two sequences must
  * not be given the same slot to write.
  */
@@ -449,8 +451,10 @@ int attn_paged_append(const void* q, const void* k, const void* v, const void* q
  *   strides: 14 int64 values, (t, h, d) for q, (page, head, slot, d) for
  *           k_pages and v_pages, (t, h, d) for o.
  *   max_seqlen_q: the most new tokens of a sequence (max_seqlen_q * Hq <=
- *           2^30); with cu_seqlens_q = NULL the number of each (total_q =
- *           num_seqs * max_seqlen_q).
+ *           2^30); with cu_seqlens_q = NULL the number of each: total_q =
+ *           num_seqs * max_seqlen_q, anything else but no rows at all is
+ *           ETATTN_ERR_BAD_SHAPE.  A sequence with more is skipped and
+ *           recorded, also when max_seqlen_q is 0.
  *   num_shares: 1 .. 65535.  The key tiles of all sequences and heads are cut
  *           into that many equal shares that run side by side; a second launch
  *           joins what a boundary cut (attn_fwd_paged_plan suggests a number).
