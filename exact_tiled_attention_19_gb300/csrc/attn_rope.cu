@@ -323,8 +323,10 @@ __global__ void __launch_bounds__(kThreads, HP > 1 ? 3 : 4) rope_kernel(const __
     load_angles(c8, s8, p.cos, p.sin, ok ? at.pos : 0, FULL ? D : p.rope_dim, ch, ok && kind != 2);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
+      // Nothing of the "partner" of an element that does not rotate: its weight may not be finite.
+      const bool turn = FULL || (j < 8 ? ch.turn_first : ch.turn_second);
       P[j] = w[j] * c8[pair_of<INTER>(j)];
-      Q[j] = (is_first<INTER>(j) ? -1.f : 1.f) * w[partner<INTER>(j)] * s8[pair_of<INTER>(j)];
+      Q[j] = turn ? (is_first<INTER>(j) ? -1.f : 1.f) * w[partner<INTER>(j)] * s8[pair_of<INTER>(j)] : 0.f;
     }
   }
 
