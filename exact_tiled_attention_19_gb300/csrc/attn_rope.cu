@@ -174,21 +174,23 @@ __device__ __forceinline__ void store16(uint16_t* row, const Chunks& ch, const f
 __device__ __forceinline__ float dot16(const float (&a)[16], const float (&b)[16]) {
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-  for (int j = 0; j < 16; j += 2) fma2(s0, s1, a[j], a[j + 1], b[j], b[j + 1], s0, s1);
+  for (int j = 0; j < 16; j += 2) fma2_keep(s0, s1, a[j], a[j + 1], b[j], b[j + 1], s0, s1);
   return s0 + s1;
 }
-// y = x P + x_partner Q.  An element that does not rotate must not meet its
-// "partner" (0 times infinity is not 0).
+// y = x P + x_partner Q, and x P alone for an element that does not rotate: its
+// "partner" and that one's weight may be infinite, and 0 times infinity is not
+// 0.  Adding -0 to x P changes no value, so P = 1 passes x through as it is.
 template <bool INTER, bool FULL>
 __device__ __forceinline__ void turn16(const float (&x)[16], const float (&P)[16], const float (&Q)[16],
                                        const Chunks& ch, float (&y)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
     const bool turn = FULL || (j < 8 ? ch.turn_first : ch.turn_second);
-    const float o0 = turn ? x[partner<INTER>(j)] : 0.f, o1 = turn ? x[partner<INTER>(j + 1)] : 0.f;
-    float t0, t1;
-    fma2(t0, t1, x[j], x[j + 1], P[j], P[j + 1], 0.f, 0.f);
-    fma2(y[j], y[j + 1], o0, o1, Q[j], Q[j + 1], t0, t1);
+    float t0, t1, u0, u1;
+    fma2_keep(t0, t1, x[j], x[j + 1], P[j], P[j + 1], -0.f, -0.f);
+    fma2_keep(u0, u1, x[partner<INTER>(j)], x[partner<INTER>(j + 1)], Q[j], Q[j + 1], t0, t1);
+    y[j] = turn ? u0 : t0;
+    y[j + 1] = turn ? u1 : t1;
   }
 }
 
@@ -323,10 +325,8 @@ __global__ void __launch_bounds__(kThreads, HP > 1 ? 3 : 4) rope_kernel(const __
     load_angles(c8, s8, p.cos, p.sin, ok ? at.pos : 0, FULL ? D : p.rope_dim, ch, ok && kind != 2);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      // Nothing of the "partner" of an element that does not rotate: its weight may not be finite.
-      const bool turn = FULL || (j < 8 ? ch.turn_first : ch.turn_second);
       P[j] = w[j] * c8[pair_of<INTER>(j)];
-      Q[j] = turn ? (is_first<INTER>(j) ? -1.f : 1.f) * w[partner<INTER>(j)] * s8[pair_of<INTER>(j)] : 0.f;
+      Q[j] = (is_first<INTER>(j) ? -1.f : 1.f) * w[partner<INTER>(j)] * s8[pair_of<INTER>(j)];
     }
   }
 
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, HP > 1 ? 3 : 4) rope_kernel(const __
     if (weight != nullptr) {
       const float r = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-      for (int j = 0; j < 16; j += 2) fma2(y[j], y[j + 1], y[j], y[j + 1], r, r, 0.f, 0.f);
+      for (int j = 0; j < 16; j += 2) fma2_keep(y[j], y[j + 1], y[j], y[j + 1], r, r, -0.f, -0.f);
     }
     if (ok && h0 + i < heads) {
       if (kind == 2) {
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_cons
       if (weight != nullptr) {
         float gw[16];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) fma2(gw[j], gw[j + 1], g[j], g[j + 1], w[j], w[j + 1], 0.f, 0.f);
+        for (int j = 0; j < 16; j += 2) fma2_keep(gw[j], gw[j + 1], g[j], g[j + 1], w[j], w[j + 1], 0.f, 0.f);
         const float ss = row_sum<LANES>(dot16(x, x));
         const float dot = row_sum<LANES>(dot16(gw, x));
         const float r = rsqrtf(ss * (1.f / D) + p.eps);
@@ -488,10 +488,10 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           float n0, n1;  // the normed row
-          fma2(n0, n1, x[j], x[j + 1], r, r, 0.f, 0.f);
-          if (on) fma2(acc[j], acc[j + 1], g[j], g[j + 1], n0, n1, acc[j], acc[j + 1]);
-          fma2(n0, n1, x[j], x[j + 1], m, m, gw[j], gw[j + 1]);
-          fma2(g[j], g[j + 1], n0, n1, r, r, 0.f, 0.f);
+          fma2_keep(n0, n1, x[j], x[j + 1], r, r, 0.f, 0.f);
+          if (on) fma2_keep(acc[j], acc[j + 1], g[j], g[j + 1], n0, n1, acc[j], acc[j + 1]);
+          fma2_keep(n0, n1, x[j], x[j + 1], m, m, gw[j], gw[j + 1]);
+          fma2_keep(g[j], g[j + 1], n0, n1, r, r, 0.f, 0.f);
         }
       }
       if (on) store16<BF16>(out + i * oh, ch, g);

@@ -29,6 +29,16 @@ __device__ __forceinline__ bool named_barrier_or(int id, int count, bool x) {
   return r != 0;
 }
 
+// fma2 that keeps denormals: a BF16 input below 2^-126 is one in FP32, too.
+__device__ __forceinline__ void fma2_keep(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0,
+                                          float c1) {
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
 // a / b for a >= 0, b > 0, in 32 bits where they do (the 64-bit division is a
 // long sequence of instructions).
 __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
