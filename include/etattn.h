@@ -357,9 +357,9 @@ int attn_fwd_varlen_ex(const void* q, const void* k, const void* v, void* o, flo
  * owning tokens cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1, or NULL when every
  * sequence has the same number of new tokens (total / num_seqs).  Token i of
  * the n new ones of a sequence with Lk keys stands at position i + Lk - n.
- * Rows of q, k, v and of outputs behind cu_seqlens_q[num_seqs] are neither
- * read nor written, and a sequence with seqlens_k = 0 is an unused slot of a
- * padded batch.
+ * Rows of outputs behind cu_seqlens_q[num_seqs] are not written, and what rows
+ * of q, k and v hold there reaches nothing (they may be read); a sequence with
+ * seqlens_k = 0 is an unused slot of a padded batch.
  * Found on the device, recorded in the status word (etattn_read_device_status):
  * offsets or lengths that do not fit (ETATTN_ERR_BAD_SEQLENS), and positions
  * past the rotation tables or pages outside 0 .. num_pages-1
