@@ -977,6 +977,23 @@ bool overlaps3(const View& a, const View& b) {
   return !(d >= pa && d + pb <= S);
 }
 
+// Whether `out` overlaps one of the arrays a call reads (absent ones: nullptr).
+struct Flat {
+  const void* ptr;
+  int64_t bytes;
+};
+template <size_t N>
+bool overlaps_any(const View& out, size_t esz, const Flat (&arrays)[N]) {
+  for (const Flat& a : arrays) {
+    const View v{a.ptr, 1, {a.bytes, 0, 0, 0}, {1, 0, 0, 0}};
+    if (a.ptr != nullptr && overlaps(out, esz, v, 1)) return true;
+  }
+  return false;
+}
+int64_t table_bytes(int num_seqs, int max_pages, int64_t table_stride) {
+  return 4 * ((num_seqs - 1) * table_stride + max_pages);
+}
+
 // A pages tensor [num_pages, Hkv, page_size, D].
 View view_pages(const void* ptr, int num_pages, int Hkv, int page_size, int D, const int64_t* st) {
   return View{ptr, 4, {num_pages, Hkv, page_size, D}, {st[0], st[1], st[2], st[3]}};
@@ -1007,6 +1024,10 @@ int rope_impl(const void* q, const void* k, const void* q_weight, const void* k_
   for (const View* o : {&oq, &ok})
     if (overlaps3(*o, vq) || overlaps3(*o, vk)) return ETATTN_ERR_ALIAS;
   if (overlaps3(oq, ok)) return ETATTN_ERR_ALIAS;
+  const int64_t table = rope_dim > 0 ? 2LL * max_position * rope_dim : 0;
+  const Flat reads[] = {{q_weight, 2 * D}, {k_weight, 2 * D}, {cos, table}, {sin, table},
+                        {positions, rope_dim > 0 ? 4LL * total_tokens : 0}};
+  if (overlaps_any(oq, 2, reads) || overlaps_any(ok, 2, reads)) return ETATTN_ERR_ALIAS;
 
   int dev = 0;
   int* status = nullptr;
@@ -1110,6 +1131,13 @@ int rope_bwd_impl(const void* q, const void* k, const void* dq_out, const void* 
       for (int j = 0; j < i; ++j)
         if (overlaps(*extra[i], esz[i], *extra[j], esz[j])) return ETATTN_ERR_ALIAS;
     }
+    const int64_t table = rope_dim > 0 ? 2LL * max_position * rope_dim : 0;
+    const Flat reads[] = {{q_weight, 2 * D}, {k_weight, 2 * D}, {cos, table}, {sin, table},
+                          {positions, rope_dim > 0 ? 4LL * total_tokens : 0}};
+    for (const View* t : {&xq, &xk})
+      if (overlaps_any(*t, 2, reads)) return ETATTN_ERR_ALIAS;
+    for (int i = 0; i < 3; ++i)
+      if (overlaps_any(*extra[i], esz[i], reads)) return ETATTN_ERR_ALIAS;
   }
   if (!work && !q_weight && !k_weight) return ETATTN_OK;
 
@@ -1192,6 +1220,16 @@ int append_impl(const void* q, const void* k, const void* v, const void* q_weigh
     if (overlaps3(oq, *t) || overlaps(pk, 2, *t, 2) || overlaps(pv, 2, *t, 2)) return ETATTN_ERR_ALIAS;
   // The pages of keys and values may interleave in one buffer.
   if (overlaps(oq, 2, pk, 2) || overlaps(oq, 2, pv, 2) || k_pages == v_pages) return ETATTN_ERR_ALIAS;
+  const int64_t table = rope_dim > 0 ? 2LL * max_position * rope_dim : 0;
+  const Flat reads[] = {{q_weight, 2 * D},
+                        {k_weight, 2 * D},
+                        {cos, table},
+                        {sin, table},
+                        {block_table, table_bytes(num_seqs, max_pages, table_stride)},
+                        {seqlens_k, 4LL * num_seqs},
+                        {cu_seqlens, 4LL * (num_seqs + 1)}};
+  for (const View* t : {&oq, &pk, &pv})
+    if (overlaps_any(*t, 2, reads)) return ETATTN_ERR_ALIAS;
 
   int dev = 0;
   int* status = nullptr;
@@ -1322,6 +1360,10 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
   for (const View* t : {&vq, &pk, &pv})
     if (overlaps(vo, 2, *t, 2) || (lse && overlaps(vl, 4, *t, 2))) return ETATTN_ERR_ALIAS;
   if (lse && overlaps(vl, 4, vo, 2)) return ETATTN_ERR_ALIAS;
+  const Flat reads[] = {{block_table, table_bytes(num_seqs, max_pages, table_stride)},
+                        {seqlens_k, 4LL * num_seqs},
+                        {cu_seqlens_q, 4LL * (num_seqs + 1)}};
+  if (overlaps_any(vo, 2, reads) || (lse && overlaps_any(vl, 4, reads))) return ETATTN_ERR_ALIAS;
   const int group = Hq / Hkv;
   const int row_tile = paged_row_tile((int64_t)max_seqlen_q * group);
   const PagedLayout L = paged_layout(num_shares, row_tile, D);
@@ -1333,6 +1375,7 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
     for (const View* t : {&vq, &pk, &pv, &vo})
       if (overlaps(vw, 1, *t, 2)) return ETATTN_ERR_ALIAS;
     if (lse && overlaps(vw, 1, vl, 4)) return ETATTN_ERR_ALIAS;
+    if (overlaps_any(vw, 1, reads)) return ETATTN_ERR_ALIAS;
   }
 
   int dev = 0;

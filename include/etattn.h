@@ -380,8 +380,9 @@ int attn_fwd_varlen_ex(const void* q, const void* k, const void* v, void* o, flo
  *   strides: 12 int64 values, (t, h, d) for q, k, q_out, k_out.
  *   eps   : finite and > 0 when there is a weight (ETATTN_ERR_BAD_SCALE).
  * Hq or Hk may be 0 (its pointers may then be NULL).  Outputs must not
- * overlap an input or each other; different heads of one fused buffer with one
- * token stride do not.
+ * overlap anything that the call reads (weights, tables and positions among
+ * it) or each other (ETATTN_ERR_ALIAS); different heads of one fused buffer
+ * with one token stride do not.
  */
 int attn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight, const float* rope_cos,
                       const float* rope_sin, const int32_t* positions, void* q_out, void* k_out, int total_tokens,
@@ -431,8 +432,9 @@ size_t attn_qk_norm_rope_bwd_workspace_size(int total_tokens, int Hq, int Hk, in
  * table or the rotation tables, or on a bad page is skipped and recorded.
  * With cu_seqlens_q = NULL total_tokens is a multiple of num_seqs, and 0 when
  * that is 0 (ETATTN_ERR_BAD_SHAPE).
- * k_pages and v_pages must not overlap q, k, v or q_out; two sequences must
- * not be given the same slot to write.
+ * k_pages, v_pages and q_out must not overlap anything that the call reads, or
+ * each other (ETATTN_ERR_ALIAS; pages of keys and values may interleave in one
+ * buffer).  Two sequences must not be given the same slot to write.
  */
 int attn_paged_append(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
                       const float* rope_cos, const float* rope_sin, void* q_out, void* k_pages, void* v_pages,
@@ -462,6 +464,8 @@ int attn_paged_append(const void* q, const void* k, const void* v, const void* q
  *   workspace: caller-owned DEVICE scratch, 256-byte aligned, at least
  *           attn_fwd_paged_workspace_size bytes (none for one share), private
  *           to the call until its last launch has run; it may hold anything.
+ * o, lse and the workspace must not overlap anything that the call reads, or
+ * each other (ETATTN_ERR_ALIAS).
  * A row without an eligible key gives O = 0 and lse = -inf.  What the cache
  * holds outside a row's eligible keys (the unused slots of a page, NaN or
  * infinity among it) does not reach that row, and table entries of pages that
