@@ -999,6 +999,55 @@ View view_pages(const void* ptr, int num_pages, int Hkv, int page_size, int D, c
   return View{ptr, 4, {num_pages, Hkv, page_size, D}, {st[0], st[1], st[2], st[3]}};
 }
 
+// overlaps for two pages tensors, with those that interleave in one buffer told
+// apart.  With equal strides an element is shared when the distance of the two
+// is a sum of d_i stride_i over the axes and of e, |d_i| < extent_i, |e| < D:
+// axis by axis, the longest stride first, each has a few candidates d_i (two at
+// most when an axis spans less than the next stride; past 4096 in all the two
+// count as overlapping).  Otherwise they are disjoint when their parts of a
+// page are.
+bool pages_overlap(const View& a, const View& b) {
+  if (!overlaps(a, 2, b, 2)) return false;
+  struct Axis {
+    int64_t n, stride;
+  } axes[3];
+  int count = 0;
+  bool equal = true;
+  int64_t part_a = a.size[3], part_b = b.size[3];
+  for (int i = 0; i < 3; ++i) {
+    if (a.size[i] <= 1) continue;
+    equal = equal && a.stride[i] == b.stride[i];
+    axes[count++] = {a.size[i], a.stride[i]};
+    if (i > 0) part_a += (a.size[i] - 1) * a.stride[i], part_b += (b.size[i] - 1) * b.stride[i];
+  }
+  const int64_t off = (reinterpret_cast<intptr_t>(b.ptr) - reinterpret_cast<intptr_t>(a.ptr)) / 2;
+  if (!equal) {
+    const int64_t S = a.stride[0];
+    if (a.size[0] <= 1 || S != b.stride[0] || part_a > S || part_b > S) return true;
+    const int64_t d = ((off % S) + S) % S;  // where b's part starts in a's page
+    return !(d >= part_a && d + part_b <= S);
+  }
+  std::sort(axes, axes + count, [](const Axis& x, const Axis& y) { return x.stride > y.stride; });
+  int64_t reach[4];  // of the axes behind the i-th, and of d
+  reach[count] = a.size[3] - 1;
+  for (int i = count - 1; i >= 0; --i) reach[i] = reach[i + 1] + (axes[i].n - 1) * axes[i].stride;
+  int budget = 4096;
+  auto shared = [&](auto&& self, int i, int64_t rest) -> bool {
+    if (--budget < 0) return true;
+    if (std::abs(rest) > reach[i]) return false;
+    if (i == count) return true;
+    const int64_t s = axes[i].stride, last = axes[i].n - 1;
+    // rest - d s has to lie within what the axes behind reach (1 more on each
+    // side: the divisions round towards zero).
+    const int64_t from = std::max(-last, (rest - reach[i + 1]) / s - 1);
+    const int64_t to = std::min(last, (rest + reach[i + 1]) / s + 1);
+    for (int64_t d = from; d <= to; ++d)
+      if (self(self, i + 1, rest - d * s)) return true;
+    return false;
+  };
+  return shared(shared, 0, off);
+}
+
 int rope_impl(const void* q, const void* k, const void* q_weight, const void* k_weight, const float* cos,
               const float* sin, const int32_t* positions, void* q_out, void* k_out, int total_tokens, int Hq, int Hk,
               int D, int dtype, const int64_t* st, int rope_dim, int interleaved, int max_position, float eps,
@@ -1219,7 +1268,7 @@ int append_impl(const void* q, const void* k, const void* v, const void* q_weigh
   for (const View* t : {&vq, &vk, &vv})
     if (overlaps3(oq, *t) || overlaps(pk, 2, *t, 2) || overlaps(pv, 2, *t, 2)) return ETATTN_ERR_ALIAS;
   // The pages of keys and values may interleave in one buffer.
-  if (overlaps(oq, 2, pk, 2) || overlaps(oq, 2, pv, 2) || k_pages == v_pages) return ETATTN_ERR_ALIAS;
+  if (overlaps(oq, 2, pk, 2) || overlaps(oq, 2, pv, 2) || pages_overlap(pk, pv)) return ETATTN_ERR_ALIAS;
   const int64_t table = rope_dim > 0 ? 2LL * max_position * rope_dim : 0;
   const Flat reads[] = {{q_weight, 2 * D},
                         {k_weight, 2 * D},

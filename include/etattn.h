@@ -433,8 +433,10 @@ size_t attn_qk_norm_rope_bwd_workspace_size(int total_tokens, int Hq, int Hk, in
  * With cu_seqlens_q = NULL total_tokens is a multiple of num_seqs, and 0 when
  * that is 0 (ETATTN_ERR_BAD_SHAPE).
  * k_pages, v_pages and q_out must not overlap anything that the call reads, or
- * each other (ETATTN_ERR_ALIAS; pages of keys and values may interleave in one
- * buffer).  Two sequences must not be given the same slot to write.
+ * each other (ETATTN_ERR_ALIAS).  Pages of keys and values may interleave in
+ * one buffer: with equal strides they are told apart element by element, else
+ * by the parts of a page that they take.  Two sequences must not be given the
+ * same slot to write.
  */
 int attn_paged_append(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
                       const float* rope_cos, const float* rope_sin, void* q_out, void* k_pages, void* v_pages,
