@@ -182,17 +182,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
   }
 }
 
-// One arrival of the warp on `bar`, giving back shared memory that it has read.
+// One arrival of the warp (by the lane that `arrives`) on `bar`, giving back shared memory that it has read.
 // A read is issued before the arrival but need not have been served by then:
 // nothing makes the arrival wait for a register that is still on its way, and a
 // refill then overtakes the last reads (it did, where bank conflicts held them
 // up).  So the arrival's address takes in `seen`, a value made of a register of
 // every read (a read delivers its registers together), and with `zero` (a 0
 // that the compiler does not know) leaves it where it is.
-__device__ __forceinline__ void release_after(uint64_t* bar, uint32_t seen, uint32_t zero, int lane) {
+__device__ __forceinline__ void release_after(uint64_t* bar, uint32_t seen, uint32_t zero, bool arrives) {
   const uint32_t off = seen & zero;
   __syncwarp();
-  if (lane == 0) mbar_arrive(reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(bar) + off));
+  if (arrives) mbar_arrive(reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(bar) + off));
   __syncwarp();
 }
 
@@ -222,24 +222,27 @@ struct PagedCut {
   }
 };
 
-// The producer warp.
+// What the producer warp knows of the ring: the stage to fill next, the parity
+// to wait for on its `empty`, and on Q's.
+struct PagedRing {
+  int stage = 0;
+  uint32_t phase = 1, uphase = 1;
+};
+
+// A wait that the whole warp takes the same way.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status)) != 0;
+}
+
+// The producer warp's walk along its piece of the line.  False: a wait ran out.
 template <class C>
-__device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedParams& p,
-                                               uint8_t* smem, int lane) {
+__device__ __forceinline__ bool paged_walk(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedParams& p,
+                                           uint8_t* smem, int lane, PagedRing& ring) {
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
   uint64_t* empty = full + C::STAGES;
   uint64_t* ufull = empty + C::STAGES;
   uint64_t* uempty = ufull + 1;
   PagedUnit* handed = reinterpret_cast<PagedUnit*>(smem + C::OFF_UNIT);
-  uint32_t uphase = 1;
-  // Hands over the end of the line.
-  auto finish = [&]() {
-    if (!mbar_wait(uempty, uphase, p.status)) return;
-    if (lane == 0) {
-      handed->tiles = 0;
-      mbar_arrive(ufull);
-    }
-  };
 
   // Nothing to join, until the end says otherwise: whatever the workspace held
   // must not be taken for a unit if a wait of this CTA runs out.
@@ -279,10 +282,7 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
   const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
   const PagedCut cut(total, p.shares);
   const int64_t begin = cut.start(share), end = cut.start(share + 1);
-  if (begin >= end) {
-    finish();
-    return;
-  }
+  if (begin >= end) return true;
   int s = lane;
   int64_t at = incl - mine;
   const bool holds = begin >= at && begin < incl;
@@ -318,8 +318,6 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
   const int boxes = C::TK / box_keys;  // pages of a tile (1 when a page holds whole tiles); at most 32
   const uint32_t box_bytes = (uint32_t)box_keys * 2 * C::D;
   const uint64_t policy = l2_policy_evict_first();
-  uint32_t phase = 1;
-  int stage = 0;
 
   // Unit by unit; `stop` is the end of this share's tiles in the unit.
   while (true) {
@@ -338,8 +336,8 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
       };
       int page = look_up(tile);
 
-      if (!mbar_wait(uempty, uphase, p.status)) return;
-      uphase ^= 1;
+      if (!warp_wait(uempty, ring.uphase, p.status)) return false;
+      ring.uphase ^= 1;
       if (lane == 0) {
         *handed = PagedUnit{q.t0, q.n, q.Lk, head * p.group, row0, q.tile0 + tile, stop - tile, tile == 0,
                             stop == q.tiles, {0, 0, 0}};
@@ -360,9 +358,9 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
         int pg = page;
         if (tile + 1 < stop) page = look_up(tile + 1);
         const uint32_t loads = __popc(__ballot_sync(0xffffffffu, on));
-        if (!mbar_wait(empty + stage, phase, p.status)) return;
-        uint8_t* base = smem + stage * C::STAGE_BYTES;
-        if (lane == 0) mbar_arrive_expect_tx(full + stage, loads * 2 * box_bytes);
+        if (!warp_wait(empty + ring.stage, ring.phase, p.status)) return false;
+        uint8_t* base = smem + ring.stage * C::STAGE_BYTES;
+        if (lane == 0) mbar_arrive_expect_tx(full + ring.stage, loads * 2 * box_bytes);
         __syncwarp();
         if (on) {
           if (pg < 0 || pg >= p.num_pages) {
@@ -371,13 +369,13 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
           }
           const int slot = k0 & (page_keys - 1);
           uint8_t* dst = base + lane * box_bytes;
-          tma_load_5d_hint(dst, &kmap, full + stage, 0, slot, 0, head, pg, policy);
-          tma_load_5d_hint(dst + C::TILE_BYTES, &vmap, full + stage, 0, slot, 0, head, pg, policy);
+          tma_load_5d_hint(dst, &kmap, full + ring.stage, 0, slot, 0, head, pg, policy);
+          tma_load_5d_hint(dst + C::TILE_BYTES, &vmap, full + ring.stage, 0, slot, 0, head, pg, policy);
         }
         __syncwarp();
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1;
+        if (++ring.stage == C::STAGES) {
+          ring.stage = 0;
+          ring.phase ^= 1;
         }
       }
     }
@@ -400,7 +398,30 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
     mark.parts = cut.holder(mark_u0 + mark_tiles - 1) - mark.first + 1;
     *desc = mark;
   }
-  finish();
+  return true;
+}
+
+// The producer warp: the walk, the end of the line, and its copies seen home.
+template <class C>
+__device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedParams& p,
+                                               uint8_t* smem, int lane) {
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+  uint64_t* ufull = full + 2 * C::STAGES;
+  uint64_t* uempty = ufull + 1;
+  PagedRing ring;
+  const bool ended = paged_walk<C>(kmap, vmap, p, smem, lane, ring) && warp_wait(uempty, ring.uphase, p.status);
+  if (ended && lane == 0) {
+    reinterpret_cast<PagedUnit*>(smem + C::OFF_UNIT)->tiles = 0;
+    mbar_arrive(ufull);
+  }
+  // Wait (bounded) until the last load into every stage has landed, and Q's, so
+  // that no copy writes shared memory after the CTA has ended.  After a normal
+  // run they have, or do soon, and Q's slot was free, after which ufull went on;
+  // where a wait ran out some may not.
+#pragma unroll 1
+  for (int i = 0; i < C::STAGES; ++i)
+    mbar_wait(full + i, i < ring.stage ? ring.phase ^ 1 : ring.phase, nullptr, 2 * kWaitLimitNs);
+  if (!ended) mbar_wait(ufull, ring.uphase, nullptr, 2 * kWaitLimitNs);
 }
 
 // Barriers among a group's four warps.  For the only group the id is a
@@ -568,7 +589,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
       ldsm4(qf[ks], smem_u32(smem + C::OFF_Q) + (16 * grp + (lane & 15)) * C::Q_PITCH + (ks * 2 + (lane >> 4)) * 16);
       qseen |= qf[ks][0];
     }
-    release_after(uempty, qseen, p.zero, lane);
+    release_after(uempty, qseen, p.zero, lane == 0);
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
 #pragma unroll
@@ -692,7 +713,8 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
           }
         }
       }
-      release_after(empty + stage, seen, p.zero, lane);
+      // (Without having waited the warp gives nothing back: the stage's load may be on its way.)
+      release_after(empty + stage, seen, p.zero, lane == 0 && alive);
       if (++stage == C::STAGES) {
         stage = 0;
         phase ^= 1;
