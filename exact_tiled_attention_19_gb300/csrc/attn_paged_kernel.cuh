@@ -80,6 +80,9 @@ struct PagedCfg {
 // KV heads of 128: 86.4 us with 1, 78.6 with 2, 78.9 with 3, 79.4 with 4.
 constexpr int kUnitCost = 2;
 
+// What FP16 weights, and the accumulators with them, are multiplied by.
+constexpr float kF16Weight = 32768.f;
+
 // Everything of one sequence that the roles need.
 struct PagedSeq {
   int n;        // new tokens (0: nothing to do)
@@ -657,7 +660,11 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
           }
         }
         // P = 2^(S - m), rounded to the input type for the product with V (a
-        // relative half step per weight); l sums the unrounded values.
+        // relative half step per weight, as in the forward kernel); l sums the
+        // unrounded values.  FP16 holds P times 2^15, so that weights keep
+        // their bits down to 2^-29 of the largest and count down to 2^-40: in
+        // a long cache very many small ones add up.  (A reference 15 below the
+        // maximum instead would round either itself or the largest weight.)
         uint32_t pf[KB][4];
 #pragma unroll
         for (int n = 0; n < 2 * KB; ++n) {
@@ -667,6 +674,10 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
             const int h = i >> 1;
             e[i] = ex2_approx(sc[n][i] - (m[h] == -INFINITY ? 0.f : m[h]));
             l[h] += e[i];
+          }
+          if (!BF16) {
+            fma2(e[0], e[1], e[0], e[1], kF16Weight, kF16Weight, 0.f, 0.f);
+            fma2(e[2], e[3], e[2], e[3], kF16Weight, kF16Weight, 0.f, 0.f);
           }
           pf[n >> 1][(n & 1) * 2] = BF16 ? pack_bf16x2(e[0], e[1]) : pack_f16x2(e[0], e[1]);
           pf[n >> 1][(n & 1) * 2 + 1] = BF16 ? pack_bf16x2(e[2], e[3]) : pack_f16x2(e[2], e[3]);
@@ -749,6 +760,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
       float ref, sum;
       state_of(g + 8 * h, ref, sum);
       inv[h] = sum == 0.f ? 0.f : ex2_approx(m[h] - ref) / sum;  // no key: 0; a NaN sum stays one
+      if (!BF16) inv[h] *= 1.f / kF16Weight;
     }
     const bool whole = w.from_start && w.to_end;
     // Where this piece of the unit goes: the output, or the workspace (slot 0
