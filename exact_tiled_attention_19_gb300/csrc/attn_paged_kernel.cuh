@@ -30,9 +30,21 @@
 //
 // Masked keys: only tiles at the edge of some row's range are masked.  There
 // a score of a key outside the row's range becomes -inf whatever the key
-// holds, and the product with V runs once per token of the tile with the
-// values outside that token's range replaced by 0, so that nothing stored
-// outside a row's range (a NaN in a page's unused slots, say) reaches it.
+// holds, and the values that no row of the group reads are replaced by 0.  A
+// value that some of them read and others do not meets weights of 0 in the
+// latter; where such a value is not finite, the product runs once per token
+// instead, with the values outside that token's range replaced by 0.  So
+// nothing stored outside a row's range (a NaN in a page's unused slots, say)
+// reaches it.
+//
+// Precision: scores, maxima, sums, accumulators and partial rows are FP32.  P
+// meets V in two parts of the input type, P = hi + lo, so that a weight is off
+// by 2^-16 of itself (BF16) and not by 2^-9: with P in one part the outputs
+// were off from 64 bits by up to 12 % more than a rounding of the exact ones.
+// The second product costs 0 to 2 % where the cache bounds (8 x 32768 keys 164.3
+// us against 163.2, 64 ragged sequences 80.6 against 81.0), 8 to 13 % for units
+// of 32 rows (200 against 185, heads of 64 131 against 116), 5 % for units of
+// two tiles (219 against 209).
 //
 // Measured (GB300, D = 128, 32 query and 8 KV heads, BF16, one new token, CUDA
 // graph): 8 sequences of 32768 keys 161 us, 6.68 TB/s of the 6.80 that a plain
@@ -183,6 +195,31 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
+}
+
+// x, y >= 0 as hi + lo, each a pair of 16-bit values: hi by cutting bits off (no
+// rounding to wait for), lo the rest, rounded.  Together they are off by 2^-16 of
+// x (BF16: 8 bits and a rest below 2^-7 x, rounded by at most 2^-9 of it) or
+// 2^-22 (FP16).
+template <bool BF16>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+  constexpr uint32_t kKept = BF16 ? 0xffff0000u : 0xffffe000u;
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  const float ha = __uint_as_float(a & kKept), hb = __uint_as_float(b & kKept);
+  hi = BF16 ? __byte_perm(a, b, 0x7632) : pack_f16x2(ha, hb);
+  lo = BF16 ? pack_bf16x2(x - ha, y - hb) : pack_f16x2(x - ha, y - hb);
+}
+
+// The halves of a register that hold keys k and k + 1 within [lo, hi], as a mask.
+__device__ __forceinline__ uint32_t half_mask(int k, int lo, int hi) {
+  return (k >= lo && k <= hi ? 0xffffu : 0u) | (k + 1 >= lo && k + 1 <= hi ? 0xffff0000u : 0u);
+}
+
+// Bits 15 and 31: whether the low and the high half are infinite or NaN (their
+// exponent carries over when it is all ones).
+template <bool BF16>
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) {
+  return ((w & (BF16 ? 0x7f807f80u : 0x7c007c00u)) + (BF16 ? 0x00800080u : 0x04000400u)) & 0x80008000u;
 }
 
 // One arrival of the warp (by the lane that `arrives`) on `bar`, giving back shared memory that it has read.
@@ -659,13 +696,12 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
             }
           }
         }
-        // P = 2^(S - m), rounded to the input type for the product with V (a
-        // relative half step per weight, as in the forward kernel); l sums the
-        // unrounded values.  FP16 holds P times 2^15, so that weights keep
-        // their bits down to 2^-29 of the largest and count down to 2^-40: in
-        // a long cache very many small ones add up.  (A reference 15 below the
-        // maximum instead would round either itself or the largest weight.)
-        uint32_t pf[KB][4];
+        // P = 2^(S - m) in two parts of the input type for the products with V;
+        // l sums the same values.  FP16 holds P times 2^15, so that weights
+        // keep their bits down to 2^-29 of the largest and count down to 2^-40:
+        // in a long cache very many small ones add up.  (A reference 15 below
+        // the maximum instead would round either itself or the largest weight.)
+        uint32_t pf[KB][4], pl[KB][4];
 #pragma unroll
         for (int n = 0; n < 2 * KB; ++n) {
           float e[4];
@@ -679,42 +715,82 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
             fma2(e[0], e[1], e[0], e[1], kF16Weight, kF16Weight, 0.f, 0.f);
             fma2(e[2], e[3], e[2], e[3], kF16Weight, kF16Weight, 0.f, 0.f);
           }
-          pf[n >> 1][(n & 1) * 2] = BF16 ? pack_bf16x2(e[0], e[1]) : pack_f16x2(e[0], e[1]);
-          pf[n >> 1][(n & 1) * 2 + 1] = BF16 ? pack_bf16x2(e[2], e[3]) : pack_f16x2(e[2], e[3]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int x = (n & 1) * 2 + i;
+            split_pair<BF16>(e[2 * i], e[2 * i + 1], pf[n >> 1][x], pl[n >> 1][x]);
+          }
         }
         // O += P V.
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
           // matrices (transposed): keys 0-7 / d 0-7, keys 8-15 / d 0-7, keys 0-7 / d 8-15, keys 8-15 / d 8-15
+          auto load = [&](uint32_t(&b)[4], int n) {
+            ldsm4_trans(b, vbase + vstart[kb] + col_off<C>(vrow, 2 * n + vcol, half));
+            seen |= b[0];
+          };
+          auto products = [&](int n, const uint32_t(&b)[4]) {
+            mma16816<BF16>(o[2 * n], pf[kb], b[0], b[1]);
+            mma16816<BF16>(o[2 * n + 1], pf[kb], b[2], b[3]);
+            mma16816<BF16>(o[2 * n], pl[kb], b[0], b[1]);
+            mma16816<BF16>(o[2 * n + 1], pl[kb], b[2], b[3]);
+          };
           if (!edge) {
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {
               uint32_t b[4];
-              ldsm4_trans(b, vbase + vstart[kb] + col_off<C>(vrow, 2 * n + vcol, half));
-              seen |= b[0];
-              mma16816<BF16>(o[2 * n], pf[kb], b[0], b[1]);
-              mma16816<BF16>(o[2 * n + 1], pf[kb], b[2], b[3]);
+              load(b, n);
+              products(n, b);
             }
-          } else {
-            // One pass per token: its range alone survives in V, and only its
-            // rows take the product.
-            const int key = key0 + kb * 16 + 2 * t4;
-            for (int tk = tok_first; tk <= tok_last; ++tk) {
-              const int lo = max(0, tk + delta - p.win_left);
-              const int hi = (int)min((int64_t)w.Lk - 1, (int64_t)tk + delta + p.win_right);
-              auto keep = [&](int k) { return k >= lo && k <= hi; };
-              const uint32_t m0 = (keep(key) ? 0xffffu : 0u) | (keep(key + 1) ? 0xffff0000u : 0u);
-              const uint32_t m1 = (keep(key + 8) ? 0xffffu : 0u) | (keep(key + 9) ? 0xffff0000u : 0u);
-              if (__all_sync(0xffffffffu, (m0 | m1) == 0u)) continue;
+            continue;
+          }
+          // V outside the range of all rows is taken as 0.  A key that some rows
+          // read and others do not has weight 0 in the latter, which is enough
+          // if its V is finite.  If not: one pass per token, in which its range
+          // alone survives in V and its rows alone take the products.
+          const int key = key0 + kb * 16 + 2 * t4;
+          bool apart = false;
+          if (tok_first != tok_last) {
+            const int lo = max(0, tok_first + delta - p.win_left);
+            const int hi = (int)min((int64_t)w.Lk - 1, (int64_t)tok_last + delta + p.win_right);
+            const uint32_t m0 = half_mask(key, lo, hi), m1 = half_mask(key + 8, lo, hi);
+            uint32_t bad = 0;
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+              uint32_t b[4];
+              load(b, n);
+              bad |= non_finite<BF16>(b[0] & m0) | non_finite<BF16>(b[1] & m1) | non_finite<BF16>(b[2] & m0) |
+                     non_finite<BF16>(b[3] & m1);
+            }
+            apart = __any_sync(0xffffffffu, bad != 0u);
+          }
+          if (!apart) {
+            const int lo = max(0, tok_first + delta - p.win_left);
+            const int hi = (int)min((int64_t)w.Lk - 1, (int64_t)tok_last + delta + p.win_right);
+            const uint32_t m0 = half_mask(key, lo, hi), m1 = half_mask(key + 8, lo, hi);
+            if (__any_sync(0xffffffffu, (m0 | m1) != 0u)) {
 #pragma unroll
               for (int n = 0; n < D / 16; ++n) {
                 uint32_t b[4];
-                ldsm4_trans(b, vbase + vstart[kb] + col_off<C>(vrow, 2 * n + vcol, half));
-                seen |= b[0];
+                load(b, n);
+                b[0] &= m0, b[1] &= m1, b[2] &= m0, b[3] &= m1;
+                products(n, b);
+              }
+            }
+          } else {
+            for (int tk = tok_first; tk <= tok_last; ++tk) {
+              const int lo = max(0, tk + delta - p.win_left);
+              const int hi = (int)min((int64_t)w.Lk - 1, (int64_t)tk + delta + p.win_right);
+              const uint32_t m0 = half_mask(key, lo, hi), m1 = half_mask(key + 8, lo, hi);
+#pragma unroll
+              for (int n = 0; n < D / 16; ++n) {
+                uint32_t b[4];
+                load(b, n);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   float d[4] = {0.f, 0.f, 0.f, 0.f};
                   mma16816<BF16>(d, pf[kb], b[2 * h] & m0, b[2 * h + 1] & m1);
+                  mma16816<BF16>(d, pl[kb], b[2 * h] & m0, b[2 * h + 1] & m1);
 #pragma unroll
                   for (int i = 0; i < 4; ++i)
                     if (tok[i >> 1] == tk) o[2 * n + h][i] += d[i];

@@ -1,12 +1,17 @@
-"""GPU tests of the weights in attention over a paged cache where one key has
-nearly all of the weight and very many others share the rest."""
+"""GPU tests of the weights in attention over a paged cache: their precision, very
+many small ones beside a large one, logits of any size, and rows of one unit of
+which some read keys that are not finite."""
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
 from exact_tiled_attention_19_gb300 import binding
+from oracle import cache
+from tests.test_gpu_paged import make_cache
+from tests.test_gpu_rope import f64, half_step
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +80,66 @@ def test_logits_of_any_size(dtype, sign, shares):
         assert bool((o == 1).all()), scale
         want = q[0, :, 0].double() * (sign * 4096 * scale)
         assert bool(((lse[:, 0].double() - want - math.log(L)).abs() <= 2.0 ** -22 * want.abs() + 2.0 ** -18).all()), scale
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("n,Hq,Hkv", [(1, 8, 2), (4, 8, 2), (5, 8, 2), (9, 8, 1)])  # 16, 32 and several times 32 rows
+@pytest.mark.parametrize("kw", [dict(), dict(num_shares=7), dict(window_left=40), dict(causal=False)])
+def test_weights_are_not_rounded_to_16_bits(dtype, D, n, Hq, Hkv, kw):
+    """One-hot queries make every score one exact product, so that the weights'
+    own errors show.  They are 2^-20 (the exponential, in a weight and in the
+    sum), 2^-22 of a score of at most 10 for its scaling by log2(e) (counted
+    four times), and that of the two 16-bit parts that meet V: 2^-16 relative
+    in BF16, 2^-22 in FP16 (and 2^-40 of the largest).  FP32 sums: at
+    most L / 16 additions in l and 2 L / 64 of 16 keys each in O per running
+    part, the joins of at most 8 parts and of four warps, 2^-23 each: under
+    (L / 8 + 64) 2^-23.  Rounding O adds u |O|, and 2^-25 where FP16 has no
+    normal value.  (One rounding of the weights to BF16 is 2^-8 of them.)"""
+    lens, page = [n + 4, 90, 700], 16
+    k_pages, v_pages, table, seqlens = make_cache(lens, page, Hkv, D, dtype, seed=D + n)
+    g = torch.Generator().manual_seed(n)
+    q = torch.zeros(3 * n, Hq, D)
+    q.scatter_(2, torch.randint(0, D, (3 * n, Hq, 1), generator=g), 2.0)
+    q = q.to(dtype).cuda()
+    o, lse = binding.attention_paged(q, k_pages, v_pages, table, seqlens, scale=1.0, **kw)
+    cu = [0, n, 2 * n, 3 * n]
+    where = dict(causal=kw.get("causal", True), window_left=kw.get("window_left", -1), scale=1.0)
+    args = table.cpu().numpy(), lens, cu
+    ro, rl = cache.attention_paged(f64(q), f64(k_pages), f64(v_pages), *args, **where)
+    ra, _ = cache.attention_paged(f64(q), f64(k_pages), np.abs(f64(v_pages)), *args, **where)
+    bf16 = dtype == torch.bfloat16
+    for s, L in enumerate(lens):
+        rows = slice(cu[s], cu[s + 1])
+        part = (2.0 ** -16 if bf16 else 2.0 ** -22) + 2.0 ** -20 + 4 * 2.0 ** -22 * 10 + (L / 8 + 64) * 2.0 ** -23
+        bound = part * ra[rows] + half_step(dtype) * np.abs(ro[rows])
+        bound += 1e-30 if bf16 else 2.0 ** -25 + L * 2.0 ** -39 * float(v_pages.abs().max())
+        err = np.abs(f64(o)[rows] - ro[rows])
+        assert np.all(err <= bound), f"sequence {s}: {np.max(err / bound):.2f} of the bound"
+        assert np.all(np.abs(f64(lse)[:, rows] - rl[:, rows]) <= 2.0 ** -18 + (L / 16 + 8) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("where", ["key", "value"])
+def test_each_row_meets_its_own_non_finite_keys_alone(dtype, D, bad, where):
+    """Eight new tokens, a window of 20: keys with an infinite or NaN value that
+    some rows of a unit read and others do not, before and after the rows'
+    ranges.  Rows that read none of them are those of the call without, bit for
+    bit; the others are not finite."""
+    n, Hq, Hkv, L = 8, 8, 2, 333
+    k_pages, v_pages, table, seqlens = make_cache([L], 16, Hkv, D, dtype, seed=D)
+    q = torch.randn(n, Hq, D, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    ref, lref = binding.attention_paged(q, k_pages, v_pages, table, seqlens, window_left=20)
+    for at in ([L - 1], [L - 3], [L - 27], [L - 24, L - 2], [L - 60], [L - 8 - 10]):
+        pages = [k_pages.clone(), v_pages.clone()]
+        for j in at:
+            pages[where == "value"][int(table[0, j // 16]), :, j % 16] = bad
+        o, lse = binding.attention_paged(q, *pages, table, seqlens, window_left=20)
+        for i in range(n):
+            pos = L - n + i
+            if any(pos - 20 <= j <= pos for j in at):
+                assert not bool(torch.isfinite(o[i]).all(-1).any()) or where == "key"
+            else:
+                assert torch.equal(o[i], ref[i]) and torch.equal(lse[:, i], lref[:, i]), (at, i)
