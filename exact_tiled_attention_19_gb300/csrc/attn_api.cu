@@ -1774,11 +1774,11 @@ int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max
     // Two CTAs of 16 rows fit on an SM, or one of 32; no more shares than key tiles.
     // 5/3 per SM reads long caches faster and short units slower, us at 304 and
     // 253 shares on 152 SMs, timed in turn (D = 128, 32 query and 8 KV heads):
-    //   1 x 524288 keys       323.4  316.3      64 x 512         26.0   27.7
-    //   8 x 32768             162.9  159.1      512 x 1..2048   101.8  115.0
-    //   64 x 4096             164.9  159.5      2000 x 100      206.0  242.1
+    //   1 x 131072 keys        86.0   84.5      64 x 512         25.7   27.6
+    //   64 x 4096             167.3  159.7      512 x 1..2048   102.9  117.9
+    //   8 x 8192, 32 KV heads 163.4  156.3      2000 x 100      219.2  258.5
     // The lengths are not known here, only their bound, which may be a graph's
-    // capacity: 2 per SM, the rule that loses 4 % at most against 18 %.  A caller
+    // capacity: 2 per SM, the rule that loses 5 % at most against 18 %.  A caller
     // that knows its lengths to be long can pass num_shares.
     const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_row_tile(rows), tk = paged_tile_keys(D);
     const double tiles = (double)num_seqs * Hkv * (double)((rows + mt - 1) / mt) *

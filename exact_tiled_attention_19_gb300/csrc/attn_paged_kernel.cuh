@@ -6,9 +6,9 @@
 // logits, rescaled whenever m grows; partial states of disjoint key sets
 // merge by M = max m_s, l = sum l_s 2^(m_s - M), acc likewise.
 //
-// What bounds it: every key and value is read once and meets few query rows
-// (the query heads of its KV head times the new tokens), far below the tensor
-// core's ridge point, so the HBM does.  The kernel therefore keeps as many
+// What bounds it: every key and value is read once for each row tile of up to
+// 32 query rows (the query heads of its KV head times the new tokens: one tile
+// in a decode step), far below the tensor core's ridge point, so the HBM does.  The kernel therefore keeps as many
 // bytes in flight as shared memory holds and keeps the CTAs equally long:
 //  * The key tiles of all (sequence, KV head, row tile) units are laid on one
 //    line, in units order, and cut into `shares` equal pieces, one per CTA,
@@ -47,11 +47,12 @@
 // two tiles (219 against 209).
 //
 // Measured (GB300, D = 128, 32 query and 8 KV heads, BF16, one new token, CUDA
-// graph): 8 sequences of 32768 keys 161 us, 6.68 TB/s of the 6.80 that a plain
-// copy reaches; one of 524288 keys 316 us, 6.80 TB/s; 64 of 1 .. 16384 keys 79
-// us, 6.04 TB/s (the units of short sequences cost their entry); one of 1000
-// keys 9 us (two launches, three dependent loads, the join).  32 rows (8 new
-// tokens) over 8 x 32768 keys: 189 us.
+// graph, over several boxes): 8 sequences of 32768 keys 162 to 165 us, 6.5 to
+// 6.6 TB/s of the 6.80 that a plain copy reaches; one of 524288 keys 320 to 326
+// us, 6.6 to 6.7 TB/s; 64 of 1 .. 16384 keys 79 to 81 us, 5.9 to 6.05 TB/s (the
+// units of short sequences cost their entry); one of 1000 keys 9 us (two
+// launches, three dependent loads, the join).  32 rows (8 new tokens) over 8 x
+// 32768 keys: 200 us, 64 rows 386.
 #pragma once
 
 #include <cstdint>
@@ -88,8 +89,9 @@ struct PagedCfg {
   static constexpr int CONSUMER_WARPS = 4 * GROUPS, THREADS = 32 * (CONSUMER_WARPS + 1);
 };
 
-// Tiles that entering a unit costs.  64 ragged sequences of up to 16384 keys, 8
-// KV heads of 128: 86.4 us with 1, 78.6 with 2, 78.9 with 3, 79.4 with 4.
+// Tiles that entering a unit costs.  8 KV heads of 128, us with 1 / 2 / 3 / 4: 64
+// ragged sequences of up to 16384 keys 86.6 / 79.6 / 79.4 / 79.9, 512 of up to
+// 2048 keys 121 / 103 / 108 / 115.
 constexpr int kUnitCost = 2;
 
 // What FP16 weights, and the accumulators with them, are multiplied by.
@@ -466,8 +468,8 @@ __device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CU
 
 // Barriers among a group's four warps.  For the only group the id is a
 // constant: in a register it made entering and leaving a unit 0.5 us longer
-// (16000 units of two tiles, 232 us against 202); a branch between two
-// constants made the two-group kernel's loop slower (203 us against 189).
+// (15 % at 16000 units of two tiles); a branch between two constants made the
+// two-group kernel's loop 7 % slower.
 template <class C>
 __device__ __forceinline__ void group_barrier(int grp) {
   named_barrier(C::GROUPS == 1 ? 1 : 1 + grp, 128);
