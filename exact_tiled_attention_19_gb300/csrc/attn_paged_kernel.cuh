@@ -42,9 +42,9 @@
 // by 2^-16 of itself (BF16) and not by 2^-9: with P in one part the outputs
 // were off from 64 bits by up to 12 % more than a rounding of the exact ones.
 // The second product costs 0 to 2 % where the cache bounds (8 x 32768 keys 164.3
-// us against 163.2, 64 ragged sequences 80.6 against 81.0), 8 to 13 % for units
-// of 32 rows (200 against 185, heads of 64 131 against 116), 5 % for units of
-// two tiles (219 against 209).
+// us against 163.2, 64 ragged sequences 80.7 against 81.0), 9 to 15 % for units
+// of 32 rows (202 against 185, heads of 64 134 against 116), 5 % for units of
+// two tiles (220 against 209).
 //
 // Measured (GB300, D = 128, 32 query and 8 KV heads, BF16, one new token, CUDA
 // graph, over several boxes): 8 sequences of 32768 keys 162 to 165 us, 6.5 to
@@ -52,7 +52,7 @@
 // us, 6.6 to 6.7 TB/s; 64 of 1 .. 16384 keys 79 to 81 us, 5.9 to 6.05 TB/s (the
 // units of short sequences cost their entry); one of 1000 keys 9 us (two
 // launches, three dependent loads, the join).  32 rows (8 new tokens) over 8 x
-// 32768 keys: 200 us, 64 rows 386.
+// 32768 keys: 202 us, 64 rows 388.
 #pragma once
 
 #include <cstdint>
@@ -200,13 +200,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // x, y >= 0 as hi + lo, each a pair of 16-bit values: hi by cutting bits off (no
-// rounding to wait for), lo the rest, rounded.  Together they are off by 2^-16 of
-// x (BF16: 8 bits and a rest below 2^-7 x, rounded by at most 2^-9 of it) or
-// 2^-22 (FP16).
+// rounding to wait for), lo the rest, rounded.  hi is cut from a little less
+// than x, so that lo is not 0 unless x is (or is 2^-28 of the largest weight in
+// FP16): an infinite value must not meet 0.  Together they are off by 2^-16 of x
+// (BF16: a rest of at most 2^-7 x, rounded by 2^-9 of it) or 2^-21 (FP16: cut
+// from one step less, a rest of at most 2^-9 x, rounded by 2^-12 of it).
 template <bool BF16>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
   constexpr uint32_t kKept = BF16 ? 0xffff0000u : 0xffffe000u;
-  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  const uint32_t a = __viaddmax_s32(__float_as_int(x), BF16 ? -1 : -0x2000, 0);
+  const uint32_t b = __viaddmax_s32(__float_as_int(y), BF16 ? -1 : -0x2000, 0);
   const float ha = __uint_as_float(a & kKept), hb = __uint_as_float(b & kKept);
   hi = BF16 ? __byte_perm(a, b, 0x7632) : pack_f16x2(ha, hb);
   lo = BF16 ? pack_bf16x2(x - ha, y - hb) : pack_f16x2(x - ha, y - hb);
@@ -790,12 +793,12 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
                 load(b, n);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  float d[4] = {0.f, 0.f, 0.f, 0.f};
+                  float d[4] = {o[2 * n + h][0], o[2 * n + h][1], o[2 * n + h][2], o[2 * n + h][3]};
                   mma16816<BF16>(d, pf[kb], b[2 * h] & m0, b[2 * h + 1] & m1);
                   mma16816<BF16>(d, pl[kb], b[2 * h] & m0, b[2 * h + 1] & m1);
 #pragma unroll
                   for (int i = 0; i < 4; ++i)
-                    if (tok[i >> 1] == tk) o[2 * n + h][i] += d[i];
+                    if (tok[i >> 1] == tk) o[2 * n + h][i] = d[i];
                 }
               }
             }

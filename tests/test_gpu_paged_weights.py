@@ -143,3 +143,29 @@ def test_each_row_meets_its_own_non_finite_keys_alone(dtype, D, bad, where):
                 assert not bool(torch.isfinite(o[i]).all(-1).any()) or where == "key"
             else:
                 assert torch.equal(o[i], ref[i]) and torch.equal(lse[:, i], lref[:, i]), (at, i)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("n,Hq", [(1, 4), (3, 4), (5, 8)])
+@pytest.mark.parametrize("shares", [1, 9])
+def test_an_infinite_value_that_a_row_reads_is_its_result(dtype, D, n, Hq, shares):
+    """Infinite values of one sign with weights above 0 make infinity in their
+    column, whatever the weights (one key, equal keys, random ones); of both
+    signs, or NaN, NaN.  Other columns are not touched."""
+    lens, page = [n, 40, 300], 16
+    k_pages, v_pages, table, seqlens = make_cache(lens, page, 1, D, dtype, seed=D)
+    k_pages[table[1, :3].long()] = 0.25  # the second sequence's keys are equal
+    q = torch.randn(3 * n, Hq, D, generator=torch.Generator().manual_seed(2)).to(dtype).cuda() * 0.5
+    ref, _ = binding.attention_paged(q, k_pages, v_pages, table, seqlens, num_shares=shares)
+    inf, nan = float("inf"), float("nan")
+    for L, s in zip(lens, range(3)):
+        for j in (0, L - n):  # every row reads both
+            v = v_pages[int(table[s, j // page]), 0, j % page]
+            v[1], v[3], v[D - 1] = inf, -inf, nan
+            v[5] = inf if j else -inf  # both signs where j differs
+    o, lse = binding.attention_paged(q, k_pages, v_pages, table, seqlens, num_shares=shares)
+    finite = [d for d in range(D) if d not in (1, 3, 5, D - 1)]
+    assert torch.equal(o[..., finite], ref[..., finite])
+    assert bool((o[..., 1] == inf).all()) and bool((o[..., 3] == -inf).all()) and bool(torch.isnan(o[..., D - 1]).all())
+    assert bool(torch.isnan(o[n:, :, 5]).all()) and bool((o[:n, :, 5] == -inf).all())
