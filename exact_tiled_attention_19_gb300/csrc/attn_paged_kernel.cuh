@@ -47,7 +47,7 @@
 // two tiles (220 against 209).
 //
 // Measured (GB300, D = 128, 32 query and 8 KV heads, BF16, one new token, CUDA
-// graph, over several boxes): 8 sequences of 32768 keys 162 to 165 us, 6.5 to
+// graph, over several boxes): 8 sequences of 32768 keys 162 to 166 us, 6.5 to
 // 6.6 TB/s of the 6.80 that a plain copy reaches; one of 524288 keys 320 to 326
 // us, 6.6 to 6.7 TB/s; 64 of 1 .. 16384 keys 79 to 81 us, 5.9 to 6.05 TB/s (the
 // units of short sequences cost their entry); one of 1000 keys 9 us (two

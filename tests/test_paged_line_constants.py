@@ -1,4 +1,5 @@
-"""The CPU models of paged attention use the kernel's own numbers."""
+"""The CPU models of paged attention use the kernel's own numbers, and sizes that
+no test can run are shown by the source."""
 
 import os
 import re
@@ -22,3 +23,15 @@ def test_the_protocol_model_has_the_kernels_stages_and_warps():
     warps = int(re.search(r"static constexpr int CONSUMER_WARPS = (\d+) \* GROUPS", text).group(1))
     assert warps == 4
     assert {(s, g) for _, s, g in test_paged_protocol_model.CASES} == {(stages, 1), (2 * stages, 2)}
+
+
+def test_the_appends_check_of_offsets_counts_threads_in_64_bits():
+    """2^30 tokens of one head of 32 (keys and values) make 2^24 blocks of 256
+    threads: a stride of 2^32, which is 0 in 32 bits and would never end."""
+    with open(os.path.join(CSRC, "attn_rope.cu")) as f:
+        text = f.read()
+    threads = int(re.search(r"constexpr int kThreads = (\d+);", text).group(1))
+    rows_a_block = threads // (32 // 16)
+    assert 2 * 2 ** 30 // rows_a_block * threads == 2 ** 32
+    loop = re.search(r"for \((.*); s < num_seqs; s \+= (.*)\) \{", text)
+    assert loop.group(1).startswith("int64_t s = (int64_t)blockIdx.x") and loop.group(2).startswith("(int64_t)gridDim.x")
