@@ -11,6 +11,9 @@ The functions ``attn_fwd``, ``attn_fwd_ex``, ``attn_bwd``, ``attn_bwd_workspace_
 ``attn_fwd_varlen_host_plan``,
 ``attn_qk_norm_rope``, ``attn_qk_norm_rope_bwd``, ``attn_qk_norm_rope_bwd_workspace_size``,
 ``attn_paged_append``, ``attn_fwd_paged``, ``attn_fwd_paged_workspace_size``, ``attn_fwd_paged_plan``,
+``attn_paged_append_q4``, ``attn_paged_unpack_q4``, ``attn_paged_q4_block_bytes``, ``attn_fwd_paged_q4``,
+``attn_fwd_paged_q4_workspace_size``, ``attn_fwd_paged_q4_plan``, ``attn_paged_extend``, ``attn_paged_truncate``,
+``attn_paged_tables_workspace_size``,
 ``etattn_status_string``, ``etattn_last_cuda_error``,
 ``etattn_read_device_status``, ``etattn_selftest_wait_timeout`` and
 ``etattn_version`` have the C names and
@@ -39,7 +42,7 @@ STATUS_NAMES = {
     0: "ETATTN_OK", 1: "ETATTN_ERR_NULL_PTR", 2: "ETATTN_ERR_BAD_DTYPE", 3: "ETATTN_ERR_BAD_SHAPE",
     4: "ETATTN_ERR_BAD_HEADS", 5: "ETATTN_ERR_BAD_STRIDE", 6: "ETATTN_ERR_BAD_ALIGN", 7: "ETATTN_ERR_ALIAS",
     8: "ETATTN_ERR_BAD_SCALE", 9: "ETATTN_ERR_BAD_SEQLENS", 10: "ETATTN_ERR_LAUNCH", 11: "ETATTN_ERR_DEVICE",
-    12: "ETATTN_ERR_NO_DEVICE", 13: "ETATTN_ERR_BAD_INDEX",
+    12: "ETATTN_ERR_NO_DEVICE", 13: "ETATTN_ERR_BAD_INDEX", 14: "ETATTN_ERR_NO_PAGES",
 }
 globals().update({name: code for code, name in STATUS_NAMES.items()})
 
@@ -132,6 +135,25 @@ def load_library(path: str | None = None):
         lib.attn_fwd_paged_workspace_size.restype = ctypes.c_size_t
         lib.attn_fwd_paged_plan.argtypes = [_int] * 6 + [ctypes.POINTER(_int), ctypes.POINTER(ctypes.c_size_t)]
         lib.attn_fwd_paged_plan.restype = _int
+        lib.attn_paged_append_q4.argtypes = ([_vp] * 12 + [_int] * 5 + [ctypes.c_char_p] + [_int] * 5 +
+                                             [ctypes.c_float, _vp])
+        lib.attn_paged_append_q4.restype = _int
+        lib.attn_paged_unpack_q4.argtypes = [_vp] * 2 + [_int] * 3 + [ctypes.c_char_p] + [_int] * 2 + [_vp]
+        lib.attn_paged_unpack_q4.restype = _int
+        lib.attn_paged_q4_block_bytes.argtypes = [_int] * 2
+        lib.attn_paged_q4_block_bytes.restype = ctypes.c_size_t
+        lib.attn_fwd_paged_q4.argtypes = lib.attn_fwd_paged.argtypes
+        lib.attn_fwd_paged_q4.restype = _int
+        lib.attn_fwd_paged_q4_workspace_size.argtypes = [_int] * 5
+        lib.attn_fwd_paged_q4_workspace_size.restype = ctypes.c_size_t
+        lib.attn_fwd_paged_q4_plan.argtypes = lib.attn_fwd_paged_plan.argtypes
+        lib.attn_fwd_paged_q4_plan.restype = _int
+        lib.attn_paged_extend.argtypes = ([_vp] * 10 + [_int] * 4 + [ctypes.c_int64, _int, _vp, ctypes.c_size_t, _vp])
+        lib.attn_paged_extend.restype = _int
+        lib.attn_paged_truncate.argtypes = ([_vp] * 7 + [_int] * 3 + [ctypes.c_int64, _int, _vp, ctypes.c_size_t, _vp])
+        lib.attn_paged_truncate.restype = _int
+        lib.attn_paged_tables_workspace_size.argtypes = [_int]
+        lib.attn_paged_tables_workspace_size.restype = ctypes.c_size_t
         lib.etattn_status_string.argtypes = [_int]
         lib.etattn_status_string.restype = ctypes.c_char_p
         lib.etattn_last_cuda_error.argtypes = []
@@ -332,6 +354,79 @@ def attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_sh
     rc = load_library().attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, ctypes.byref(shares),
                                             ctypes.byref(need))
     return rc, shares.value, need.value
+
+
+def attn_paged_append_q4(q, k, v, q_weight, k_weight, rope_cos, rope_sin, positions, slots, q_out, k_pages, v_pages,
+                         total_tokens, Hq, Hkv, D, dtype, strides, page_size, num_pages, rope_dim, interleaved,
+                         max_position, eps, stream):
+    """C ``attn_paged_append_q4``: pointers as ints (0 for NULL), ``strides`` 16 ints."""
+    lib = load_library()
+    return lib.attn_paged_append_q4(q or None, k or None, v or None, q_weight or None, k_weight or None,
+                                    rope_cos or None, rope_sin or None, positions or None, slots or None,
+                                    q_out or None, k_pages or None, v_pages or None, total_tokens, Hq, Hkv, D, dtype,
+                                    _STRIDES[16](*strides), page_size, num_pages, rope_dim, interleaved, max_position,
+                                    eps, stream or None)
+
+
+def attn_paged_unpack_q4(pages, out, Hkv, D, dtype, strides, page_size, num_pages, stream):
+    """C ``attn_paged_unpack_q4``: pointers as ints (0 for NULL), ``strides`` 6 ints."""
+    lib = load_library()
+    return lib.attn_paged_unpack_q4(pages or None, out or None, Hkv, D, dtype, _STRIDES[6](*strides), page_size,
+                                    num_pages, stream or None)
+
+
+def attn_paged_q4_block_bytes(page_size, D) -> int:
+    return load_library().attn_paged_q4_block_bytes(page_size, D)
+
+
+def attn_fwd_paged_q4(q, k_pages, v_pages, o, lse, block_table, seqlens_k, cu_seqlens_q, num_seqs, max_seqlen_q,
+                      total_q, Hq, Hkv, D, dtype, strides, page_size, num_pages, max_pages, table_stride, causal,
+                      window_left, window_right, scale, num_shares, workspace, workspace_bytes, stream):
+    """C ``attn_fwd_paged_q4``: pointers as ints (0 for NULL), ``strides`` 10 ints."""
+    lib = load_library()
+    return lib.attn_fwd_paged_q4(q or None, k_pages or None, v_pages or None, o or None, lse or None,
+                                 block_table or None, seqlens_k or None, cu_seqlens_q or None, num_seqs, max_seqlen_q,
+                                 total_q, Hq, Hkv, D, dtype, _STRIDES[10](*strides), page_size, num_pages, max_pages,
+                                 table_stride, causal, window_left, window_right, scale, num_shares, workspace or None,
+                                 workspace_bytes, stream or None)
+
+
+def attn_fwd_paged_q4_workspace_size(Hq, Hkv, max_seqlen_q, D, num_shares) -> int:
+    return load_library().attn_fwd_paged_q4_workspace_size(Hq, Hkv, max_seqlen_q, D, num_shares)
+
+
+def attn_fwd_paged_q4_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_shares=0):
+    """(status, num_shares, workspace bytes) for the current device."""
+    shares, need = _int(num_shares), ctypes.c_size_t(0)
+    rc = load_library().attn_fwd_paged_q4_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, ctypes.byref(shares),
+                                               ctypes.byref(need))
+    return rc, shares.value, need.value
+
+
+def attn_paged_extend(new_tokens, seqlens_k, block_table, free_pages, free_count, seqlens_out, free_count_out,
+                      cu_seqlens_q, positions, slots, num_seqs, total_tokens, page_size, max_pages, table_stride,
+                      capacity, workspace, workspace_bytes, stream):
+    """C ``attn_paged_extend``: pointers as ints (0 for NULL)."""
+    lib = load_library()
+    return lib.attn_paged_extend(new_tokens or None, seqlens_k or None, block_table or None, free_pages or None,
+                                 free_count or None, seqlens_out or None, free_count_out or None,
+                                 cu_seqlens_q or None, positions or None, slots or None, num_seqs, total_tokens,
+                                 page_size, max_pages, table_stride, capacity, workspace or None, workspace_bytes,
+                                 stream or None)
+
+
+def attn_paged_truncate(keep, seqlens_k, block_table, free_pages, free_count, seqlens_out, free_count_out, num_seqs,
+                        page_size, max_pages, table_stride, capacity, workspace, workspace_bytes, stream):
+    """C ``attn_paged_truncate``: pointers as ints (0 for NULL)."""
+    lib = load_library()
+    return lib.attn_paged_truncate(keep or None, seqlens_k or None, block_table or None, free_pages or None,
+                                   free_count or None, seqlens_out or None, free_count_out or None, num_seqs,
+                                   page_size, max_pages, table_stride, capacity, workspace or None, workspace_bytes,
+                                   stream or None)
+
+
+def attn_paged_tables_workspace_size(num_seqs) -> int:
+    return load_library().attn_paged_tables_workspace_size(num_seqs)
 
 
 def etattn_status_string(code: int) -> str:
@@ -644,7 +739,7 @@ def attention_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool = Tru
 # the C functions called directly.  (``empty_like`` and ``empty`` with its sizes
 # as arguments take half the time of ``empty`` with a tuple.)
 
-_STRIDES = {n: struct.Struct(f"{n}q").pack for n in (12, 14, 18, 20)}
+_STRIDES = {n: struct.Struct(f"{n}q").pack for n in (6, 10, 12, 14, 16, 18, 20)}
 _CODES: dict = {}  # torch dtype -> ETATTN_* code
 
 
@@ -654,6 +749,15 @@ def _paged_plan(device_index, num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, 
     rc, shares, need = attn_fwd_paged_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_shares)
     if rc != 0:
         raise EtattnError(rc, "attn_fwd_paged_plan")
+    return shares, need
+
+
+@functools.lru_cache(maxsize=512)
+def _paged_q4_plan(device_index, num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_shares):
+    """attn_fwd_paged_q4_plan on the current device, as ``_paged_plan``."""
+    rc, shares, need = attn_fwd_paged_q4_plan(num_seqs, Hq, Hkv, max_seqlen_q, max_seqlen_k, D, num_shares)
+    if rc != 0:
+        raise EtattnError(rc, "attn_fwd_paged_q4_plan")
     return shares, need
 
 
@@ -978,3 +1082,297 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
     if rc != 0:
         raise EtattnError(rc, "attn_fwd_paged")
     return out, lse
+
+
+# ---------------------------------------------------------------- the paged cache held in 4 bits, and its pages
+
+_Q4_SLOT_BYTES = {32: 20, 64: 36, 128: 72}
+
+
+def q4_pages(num_pages: int, Hkv: int, page_size: int, D: int, *, device=None):
+    """(k_pages, v_pages): an empty 4-bit cache, uint8 [num_pages, Hkv, block bytes]
+    each, with the keys and values of a page beside each other in one buffer."""
+    import torch
+    need = attn_paged_q4_block_bytes(page_size, D)
+    if need == 0:
+        raise ValueError(f"no 4-bit cache with pages of {page_size} and heads of {D}")
+    both = torch.zeros(num_pages, 2, Hkv, need, dtype=torch.uint8, device=torch.device("cuda") if device is None else device)
+    return both[:, 0], both[:, 1]
+
+
+def _q4_pages(torch, name, pages, D, device):
+    """(num_pages, Hkv, page_size) of a 4-bit cache, after checking it."""
+    shape = pages.shape
+    if len(shape) != 3 or pages.dtype != torch.uint8 or pages.device != device or pages.stride(2) != 1:
+        if len(shape) != 3:
+            raise ValueError(f"{name} must be [num_pages, Hkv, block bytes]")
+        _check(name, pages, shape, torch.uint8, device)
+        raise ValueError(f"{name}'s blocks must be contiguous")
+    slot = _Q4_SLOT_BYTES.get(D)
+    if slot is None or shape[2] % slot != 0:
+        raise ValueError(f"{name}: blocks of {shape[2]} bytes hold no rows of {D} elements")
+    return shape[0], shape[1], shape[2] // slot
+
+
+def paged_append_q4(k, v, k_pages, v_pages, slots, *, q=None, q_weight=None, k_weight=None, rope_cos=None,
+                    rope_sin=None, positions=None, interleaved: bool = False, eps: float = 1e-6, q_out=None,
+                    stream=None):
+    """Writes this step's keys and values k, v [T, Hkv, D] into the 4-bit cache, the
+    keys normed and rotated on the way (as ``qk_norm_rope``), and returns q
+    [T, Hq, D] normed and rotated (None without q).
+
+    k_pages, v_pages: uint8 [num_pages, Hkv, block bytes] (``q4_pages``); slots:
+    int64 [T], page * page_size + slot of every token, negative for none, and
+    positions: int32 [T], as ``paged_extend`` makes them."""
+    import torch
+    T, _, D = k.shape
+    dtype, device, code = k.dtype, k.device, _code_of(k)
+    num_pages, Hkv, page_size = _q4_pages(torch, "k_pages", k_pages, D, device)
+    if v_pages.shape != k_pages.shape or v_pages.dtype != torch.uint8 or v_pages.device != device or v_pages.stride(2) != 1:
+        _check("v_pages", v_pages, k_pages.shape, torch.uint8, device)
+        _q4_pages(torch, "v_pages", v_pages, D, device)
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or v.dtype != dtype or v.device != device:
+        _check("k", k, (T, Hkv, D), dtype, device)
+        _check("v", v, (T, Hkv, D), dtype, device)
+    if slots.shape != (T,) or slots.dtype != torch.int64 or slots.device != device or not slots.is_contiguous():
+        _check("slots", slots, (T,), torch.int64, device, True)
+    wq, wk, cos, sin, rope_dim, max_position = _rope_args(torch, D, dtype, device, q_weight, k_weight, rope_cos,
+                                                          rope_sin)
+    pos = _positions(torch, positions, T, rope_dim, device)
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[1]
+        if q.shape != (T, Hq, D) or q.dtype != dtype or q.device != device:
+            _check("q", q, (T, Hq, D), dtype, device)
+        if q_out is not None:
+            _check("q_out", q_out, (T, Hq, D), dtype, device)
+    there = _elsewhere(torch, device, stream)
+    if there is not None:
+        with there:
+            return paged_append_q4(k, v, k_pages, v_pages, slots, q=q, q_weight=q_weight, k_weight=k_weight,
+                                   rope_cos=rope_cos, rope_sin=rope_sin, positions=positions,
+                                   interleaved=interleaved, eps=eps, q_out=q_out)
+    if q is None:
+        q_out, qp, op, q_stride, o_stride = None, 0, 0, (0, 0, 1), (0, 0, 1)
+    else:
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        qp, op, q_stride, o_stride = q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
+    rc = (_lib or load_library()).attn_paged_append_q4(
+        qp, k.data_ptr(), v.data_ptr(), wq, wk, cos, sin, pos, slots.data_ptr(), op, k_pages.data_ptr(),
+        v_pages.data_ptr(), T, Hq, Hkv, D, code,
+        _STRIDES[16](*q_stride, *k.stride(), *v.stride(), *o_stride, *k_pages.stride()[:2], *v_pages.stride()[:2]),
+        page_size, num_pages, rope_dim, interleaved, max_position, eps,
+        torch._C._cuda_getCurrentRawStream(device.index))
+    if rc != 0:
+        raise EtattnError(rc, "attn_paged_append_q4")
+    return q_out
+
+
+def paged_unpack_q4(pages, D: int, dtype, *, out=None, stream=None):
+    """The values of a 4-bit cache's blocks (k_pages or v_pages), rounded to
+    ``dtype``, which they were stored from: [num_pages, Hkv, page_size, D], the
+    16-bit cache's layout."""
+    import torch
+    device = pages.device
+    num_pages, Hkv, page_size = _q4_pages(torch, "pages", pages, D, device)
+    shape = (num_pages, Hkv, page_size, D)
+    if out is not None:
+        _check("out", out, shape, dtype, device)
+    there = _elsewhere(torch, device, stream)
+    if there is not None:
+        with there:
+            return paged_unpack_q4(pages, D, dtype, out=out)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+    rc = (_lib or load_library()).attn_paged_unpack_q4(
+        pages.data_ptr(), out.data_ptr(), Hkv, D, _code_of(out),
+        _STRIDES[6](*pages.stride()[:2], *out.stride()), page_size, num_pages,
+        torch._C._cuda_getCurrentRawStream(device.index))
+    if rc != 0:
+        raise EtattnError(rc, "attn_paged_unpack_q4")
+    return out
+
+
+def attention_paged_q4(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q=None,
+                       max_seqlen_q: int | None = None, max_seqlen_k: int | None = None, causal: bool = True,
+                       scale: float | None = None, window_left: int = -1, window_right: int = -1,
+                       num_shares: int | None = None, workspace=None, out=None, lse=None, return_lse: bool = True,
+                       stream=None):
+    """``attention_paged`` over a 4-bit cache (k_pages, v_pages as for
+    ``paged_append_q4``, stored from q's dtype); the other arguments are as there,
+    the plan ``attn_fwd_paged_q4_plan``."""
+    import torch
+    T, Hq, D = q.shape
+    dtype, device, code = q.dtype, q.device, _code_of(q)
+    num_pages, Hkv, page_size = _q4_pages(torch, "k_pages", k_pages, D, device)
+    S, width = block_table.shape
+    row, col = block_table.stride()
+    if (v_pages.shape != k_pages.shape or v_pages.dtype != torch.uint8 or v_pages.device != device
+            or v_pages.stride(2) != 1 or block_table.dtype != torch.int32 or block_table.device != device
+            or seqlens_k.shape != (S,) or seqlens_k.dtype != torch.int32 or seqlens_k.device != device
+            or not seqlens_k.is_contiguous()):
+        _check("v_pages", v_pages, k_pages.shape, torch.uint8, device)
+        _q4_pages(torch, "v_pages", v_pages, D, device)
+        _check("block_table", block_table, (S, width), torch.int32, device)
+        _check("seqlens_k", seqlens_k, (S,), torch.int32, device, True)
+    if col != 1 and width > 1:
+        raise ValueError("block_table's rows must be contiguous")
+    cu = 0
+    if cu_seqlens_q is None:
+        max_seqlen_q = T // S if S > 0 else 0
+    else:
+        _check("cu_seqlens_q", cu_seqlens_q, (S + 1,), torch.int32, device, True)
+        cu = cu_seqlens_q.data_ptr()
+        if max_seqlen_q is None:
+            raise ValueError("max_seqlen_q is needed with cu_seqlens_q")
+    if out is not None:
+        _check("out", out, (T, Hq, D), dtype, device)
+    if lse is not None:
+        _check("lse", lse, (Hq, T), torch.float32, device, True)
+    there = _elsewhere(torch, device, stream)
+    if there is not None:
+        with there:
+            return attention_paged_q4(q, k_pages, v_pages, block_table, seqlens_k, cu_seqlens_q=cu_seqlens_q,
+                                      max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, causal=causal,
+                                      scale=scale, window_left=window_left, window_right=window_right,
+                                      num_shares=num_shares, workspace=workspace, out=out, lse=lse,
+                                      return_lse=return_lse)
+    lib = _lib or load_library()
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if lse is None and return_lse:
+        lse = torch.empty(Hq, T, dtype=torch.float32, device=device)
+    if num_shares is None or workspace is None:
+        if max_seqlen_k is None:
+            max_seqlen_k = min(width * page_size, 1 << 30)
+        num_shares, ws_bytes = _paged_q4_plan(device.index, S, Hq, Hkv, int(max_seqlen_q), int(max_seqlen_k), D,
+                                              int(num_shares or 0))
+    if workspace is not None:
+        ws_bytes = _workspace(workspace, device)
+    elif ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    rc = lib.attn_fwd_paged_q4(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        block_table.data_ptr(), seqlens_k.data_ptr(), cu, S, max_seqlen_q, T, Hq, Hkv, D, code,
+        _STRIDES[10](*q.stride(), *k_pages.stride()[:2], *v_pages.stride()[:2], *out.stride()), page_size, num_pages,
+        width, row, causal, window_left, window_right, D ** -0.5 if scale is None else scale, num_shares,
+        0 if workspace is None else workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
+    if rc != 0:
+        raise EtattnError(rc, "attn_fwd_paged_q4")
+    return out, lse
+
+
+def _table_args(torch, name, amount, seqlens_k, block_table, free_pages, free_count):
+    """(num_seqs, max_pages, table_stride, device), after checking the tensors."""
+    S, width = block_table.shape
+    row, col = block_table.stride()
+    device, i32 = block_table.device, torch.int32
+    if (block_table.dtype != i32 or amount.shape != (S,) or amount.dtype != i32 or amount.device != device
+            or not amount.is_contiguous() or seqlens_k.shape != (S,) or seqlens_k.dtype != i32
+            or seqlens_k.device != device or not seqlens_k.is_contiguous() or len(free_pages.shape) != 1
+            or free_pages.dtype != i32 or free_pages.device != device or not free_pages.is_contiguous()
+            or free_count.shape != (1,) or free_count.dtype != i32 or free_count.device != device):
+        _check("block_table", block_table, (S, width), i32, device)
+        _check(name, amount, (S,), i32, device, True)
+        _check("seqlens_k", seqlens_k, (S,), i32, device, True)
+        _check("free_pages", free_pages, (free_pages.numel(),), i32, device, True)
+        _check("free_count", free_count, (1,), i32, device)
+    if col != 1 and width > 1 and S > 0:
+        raise ValueError("block_table's rows must be contiguous")
+    return S, width, row, device
+
+
+def paged_extend(new_tokens, seqlens_k, block_table, free_pages, free_count, *, page_size: int, total_tokens: int,
+                 seqlens_out=None, cu_seqlens_q=None, positions=None, slots=None, free_count_out=None, workspace=None,
+                 stream=None):
+    """Pages for a step's new tokens, on the device: takes them from the stack
+    ``free_pages`` (int32, ``free_count`` [1] of them free), writes them into
+    ``block_table`` [S, max_pages] and returns (seqlens_out [S], cu_seqlens_q
+    [S + 1], positions [T], slots [T], free_count_out [1]), new tensors when not
+    given.
+
+    new_tokens, seqlens_k: int32 [S], each sequence's new tokens and its keys before
+    the step; ``total_tokens`` T: at least the sum of new_tokens (positions 0 and slots
+    -1 behind it).  ``seqlens_out`` may be seqlens_k and ``free_count_out`` free_count,
+    as in a captured loop.  A step that does not fit takes nothing and is recorded in the
+    device status (``etattn_read_device_status``)."""
+    import torch
+    S, width, row, device = _table_args(torch, "new_tokens", new_tokens, seqlens_k, block_table, free_pages,
+                                        free_count)
+    i32 = torch.int32
+    if seqlens_out is not None:
+        _check("seqlens_out", seqlens_out, (S,), i32, device, True)
+    if cu_seqlens_q is not None:
+        _check("cu_seqlens_q", cu_seqlens_q, (S + 1,), i32, device, True)
+    if positions is not None:
+        _check("positions", positions, (total_tokens,), i32, device, True)
+    if slots is not None:
+        _check("slots", slots, (total_tokens,), torch.int64, device, True)
+    if free_count_out is not None:
+        _check("free_count_out", free_count_out, (1,), i32, device)
+    there = _elsewhere(torch, device, stream)
+    if there is not None:
+        with there:
+            return paged_extend(new_tokens, seqlens_k, block_table, free_pages, free_count, page_size=page_size,
+                                total_tokens=total_tokens, seqlens_out=seqlens_out, cu_seqlens_q=cu_seqlens_q,
+                                positions=positions, slots=slots, free_count_out=free_count_out, workspace=workspace)
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens_k)
+    if cu_seqlens_q is None:  # (zeros: of no sequences no kernel writes the first offset)
+        cu_seqlens_q = (torch.empty if S else torch.zeros)(S + 1, dtype=i32, device=device)
+    if positions is None:
+        positions = torch.empty(total_tokens, dtype=i32, device=device)
+    if slots is None:
+        slots = torch.empty(total_tokens, dtype=torch.int64, device=device)
+    if free_count_out is None:
+        free_count_out = torch.empty_like(free_count) if S else free_count.clone()
+    if workspace is None:
+        ws_bytes = 4 * (S + 1)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    else:
+        ws_bytes = _workspace(workspace, device)
+    rc = (_lib or load_library()).attn_paged_extend(
+        new_tokens.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+        free_count.data_ptr(), seqlens_out.data_ptr(), free_count_out.data_ptr(), cu_seqlens_q.data_ptr(),
+        positions.data_ptr(), slots.data_ptr(), S, total_tokens, page_size, width, row, free_pages.shape[0],
+        workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
+    if rc != 0:
+        raise EtattnError(rc, "attn_paged_extend")
+    return seqlens_out, cu_seqlens_q, positions, slots, free_count_out
+
+
+def paged_truncate(keep, seqlens_k, block_table, free_pages, free_count, *, page_size: int, seqlens_out=None,
+                   free_count_out=None, workspace=None, stream=None):
+    """The way back from ``paged_extend``: of every sequence the first keep[s] keys
+    stay (0: it has ended; a few less than seqlens_k: rejected drafts), and the pages
+    past them go on the stack ``free_pages``.  Returns (seqlens_out [S],
+    free_count_out [1]), new tensors when not given; they may be seqlens_k and
+    free_count."""
+    import torch
+    S, width, row, device = _table_args(torch, "keep", keep, seqlens_k, block_table, free_pages, free_count)
+    if seqlens_out is not None:
+        _check("seqlens_out", seqlens_out, (S,), torch.int32, device, True)
+    if free_count_out is not None:
+        _check("free_count_out", free_count_out, (1,), torch.int32, device)
+    there = _elsewhere(torch, device, stream)
+    if there is not None:
+        with there:
+            return paged_truncate(keep, seqlens_k, block_table, free_pages, free_count, page_size=page_size,
+                                  seqlens_out=seqlens_out, free_count_out=free_count_out, workspace=workspace)
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(seqlens_k)
+    if free_count_out is None:
+        free_count_out = torch.empty_like(free_count) if S else free_count.clone()
+    if workspace is None:
+        ws_bytes = 4 * (S + 1)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    else:
+        ws_bytes = _workspace(workspace, device)
+    rc = (_lib or load_library()).attn_paged_truncate(
+        keep.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+        seqlens_out.data_ptr(), free_count_out.data_ptr(), S, page_size, width, row, free_pages.shape[0],
+        workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
+    if rc != 0:
+        raise EtattnError(rc, "attn_paged_truncate")
+    return seqlens_out, free_count_out

@@ -1373,11 +1373,12 @@ int encode_pages(CUtensorMap* map, int dtype, const void* ptr, int D, int page_s
   return r == CUDA_SUCCESS ? ETATTN_OK : fail_cuda(cudaErrorInvalidValue);
 }
 
-int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
-               const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
-               int max_seqlen_q, int total_q, int Hq, int Hkv, int D, int dtype, const int64_t* st, int page_size,
-               int num_pages, int max_pages, int64_t table_stride, int causal, int window_left, int window_right,
-               float scale, int num_shares, void* workspace, size_t workspace_bytes, void* stream) {
+// Sizes of a call of attention over a paged cache, 16-bit or 4-bit.  *nothing: the
+// call is a successful no-op.
+int paged_sizes_ok(const int32_t* cu_seqlens_q, int num_seqs, int max_seqlen_q, int total_q, int Hq, int Hkv, int D,
+                   int dtype, const int64_t* st, int page_size, int num_pages, int max_pages, int64_t table_stride,
+                   float scale, int num_shares, bool* nothing) {
+  *nothing = false;
   if (dtype != ETATTN_F16 && dtype != ETATTN_BF16) return ETATTN_ERR_BAD_DTYPE;
   if (max_seqlen_q < 0 || max_seqlen_q > kMaxTokens || total_q < 0 || total_q > kMaxTokens || Hq < 0 ||
       Hq > kMaxGridYZ || !head_dim_ok(D))
@@ -1387,14 +1388,74 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
   if (!std::isfinite(scale) || !(scale > 0.f)) return ETATTN_ERR_BAD_SCALE;
   if (st == nullptr) return ETATTN_ERR_NULL_PTR;
   if (num_shares < 1 || num_shares > kMaxShares) return ETATTN_ERR_BAD_SHAPE;
-  if (Hq == 0 || total_q == 0) return ETATTN_OK;
+  if (Hq == 0 || total_q == 0) {
+    *nothing = true;
+    return ETATTN_OK;
+  }
   // Without offsets every row belongs to a sequence and has to be written.
   if (cu_seqlens_q == nullptr && (int64_t)num_seqs * max_seqlen_q != total_q) return ETATTN_ERR_BAD_SHAPE;
-  if (num_seqs == 0) return ETATTN_OK;
-  // A bound of 0 new tokens leaves nothing to share; whether the offsets keep it shows on the device.
-  if (max_seqlen_q == 0) num_shares = 1;
+  if (num_seqs == 0) {
+    *nothing = true;
+    return ETATTN_OK;
+  }
   if (num_pages < 1 || max_pages < 1) return ETATTN_ERR_BAD_SHAPE;
   if ((int64_t)max_seqlen_q * Hq > kMaxTokens) return ETATTN_ERR_BAD_SHAPE;  // a sequence's rows
+  return ETATTN_OK;
+}
+
+// What the kernels take of such a call beside the cache itself; the workspace's
+// parts when there are several shares.
+void paged_params(PagedParams& p, const void* q, void* o, float* lse, const int32_t* block_table,
+                  const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs, int max_seqlen_q, int total_q,
+                  int Hkv, int group, const int64_t* sq, const int64_t* so, int page_size, int num_pages, int max_pages,
+                  int64_t table_stride, int causal, int window_left, int window_right, float scale, int row_tile,
+                  int num_shares, void* workspace, const PagedLayout& L, int* status) {
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.q_st = sq[0];
+  p.q_sh = sq[1];
+  p.o_st = so[0];
+  p.o_sh = so[1];
+  p.block_table = block_table;
+  p.seqlens_k = seqlens_k;
+  p.cu_seqlens_q = cu_seqlens_q;
+  p.table_stride = table_stride;
+  p.num_seqs = num_seqs;
+  p.tokens_per_seq = max_seqlen_q;
+  p.max_seqlen_q = max_seqlen_q;
+  p.total_q = total_q;
+  p.Hkv = Hkv;
+  p.group = group;
+  p.max_keys = (int)std::min<int64_t>((int64_t)max_pages * page_size, kMaxTokens);
+  p.num_pages = num_pages;
+  p.page_shift = log2_of(page_size);
+  p.win_left = window_left_of(window_left);
+  p.win_right = window_right_of(window_right, causal);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.row_tile = row_tile;
+  p.shares = num_shares;
+  if (num_shares > 1) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.desc = reinterpret_cast<PagedShare*>(ws);
+    p.part_lse = reinterpret_cast<float*>(ws + L.lse_off);
+    p.part_o = reinterpret_cast<float*>(ws + L.o_off);
+  }
+  p.status = status;
+}
+
+int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+               const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
+               int max_seqlen_q, int total_q, int Hq, int Hkv, int D, int dtype, const int64_t* st, int page_size,
+               int num_pages, int max_pages, int64_t table_stride, int causal, int window_left, int window_right,
+               float scale, int num_shares, void* workspace, size_t workspace_bytes, void* stream) {
+  bool nothing = false;
+  if (int rc = paged_sizes_ok(cu_seqlens_q, num_seqs, max_seqlen_q, total_q, Hq, Hkv, D, dtype, st, page_size,
+                              num_pages, max_pages, table_stride, scale, num_shares, &nothing))
+    return rc;
+  if (nothing) return ETATTN_OK;
+  // A bound of 0 new tokens leaves nothing to share; whether the offsets keep it shows on the device.
+  if (max_seqlen_q == 0) num_shares = 1;
   if (!q || !o || !k_pages || !v_pages || !block_table || !seqlens_k) return ETATTN_ERR_NULL_PTR;
   const View vq = view3(q, total_q, Hq, D, st), vo = view3(o, total_q, Hq, D, st + 11);
   const View pk = view_pages(k_pages, num_pages, Hkv, page_size, D, st + 3);
@@ -1435,38 +1496,9 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
   if (int rc = encode_pages(&mk, dtype, k_pages, D, page_size, Hkv, num_pages, st + 3, box)) return rc;
   if (int rc = encode_pages(&mv, dtype, v_pages, D, page_size, Hkv, num_pages, st + 7, box)) return rc;
   PagedParams p{};
-  p.q = q;
-  p.o = o;
-  p.lse = lse;
-  p.q_st = st[0];
-  p.q_sh = st[1];
-  p.o_st = st[11];
-  p.o_sh = st[12];
-  p.block_table = block_table;
-  p.seqlens_k = seqlens_k;
-  p.cu_seqlens_q = cu_seqlens_q;
-  p.table_stride = table_stride;
-  p.num_seqs = num_seqs;
-  p.tokens_per_seq = max_seqlen_q;
-  p.max_seqlen_q = max_seqlen_q;
-  p.total_q = total_q;
-  p.Hkv = Hkv;
-  p.group = group;
-  p.max_keys = (int)std::min<int64_t>((int64_t)max_pages * page_size, kMaxTokens);
-  p.num_pages = num_pages;
-  p.page_shift = log2_of(page_size);
-  p.win_left = window_left_of(window_left);
-  p.win_right = window_right_of(window_right, causal);
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.row_tile = row_tile;
-  p.shares = num_shares;
-  if (num_shares > 1) {
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.desc = reinterpret_cast<PagedShare*>(ws);
-    p.part_lse = reinterpret_cast<float*>(ws + L.lse_off);
-    p.part_o = reinterpret_cast<float*>(ws + L.o_off);
-  }
-  p.status = status;
+  paged_params(p, q, o, lse, block_table, seqlens_k, cu_seqlens_q, num_seqs, max_seqlen_q, total_q, Hkv, group, st,
+               st + 11, page_size, num_pages, max_pages, table_stride, causal, window_left, window_right, scale,
+               row_tile, num_shares, workspace, L, status);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == ETATTN_BF16;
   cudaError_t e;
@@ -1475,6 +1507,284 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
     case 64: e = bf ? launch_paged_d64_1(mk, mv, p, s) : launch_paged_d64_0(mk, mv, p, s); break;
     default: e = bf ? launch_paged_d128_1(mk, mv, p, s) : launch_paged_d128_0(mk, mv, p, s);
   }
+  return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
+}
+
+// ---------------------------------------------------------------- the paged cache held in 4 bits
+// Bytes of a slot in a block: the codes and every group's scale and minimum (the
+// kernels' PagedQ4Cfg::ROW_BYTES).
+int64_t q4_slot_bytes(int D) { return D / 2 + 4 * (D / std::min(D, 64)); }
+
+// A cache [num_pages, Hkv, block bytes], with (page, head) strides in bytes; and the
+// same for pages_overlap, which counts in 16 bits.
+View view_blocks(const void* ptr, int num_pages, int Hkv, int64_t block, const int64_t* st) {
+  return View{ptr, 3, {num_pages, Hkv, block, 0}, {st[0], st[1], 1, 0}};
+}
+View halves_of(const View& v) {
+  return View{v.ptr, 4, {v.size[0], v.size[1], 1, v.size[2] / 2}, {v.stride[0] / 2, v.stride[1] / 2, v.size[2] / 2, 1}};
+}
+// Strides as everywhere, and blocks that do not run into one another.
+bool blocks_ok(const View& v) {
+  if (!strides_ok(v, 1)) return false;
+  const bool pages = v.size[0] > 1, heads = v.size[1] > 1;
+  if ((pages && v.stride[0] < v.size[2]) || (heads && v.stride[1] < v.size[2])) return false;
+  if (!pages || !heads) return true;
+  return v.stride[0] >= v.stride[1] ? v.stride[0] >= (v.size[1] - 1) * v.stride[1] + v.size[2]
+                                    : v.stride[1] >= (v.size[0] - 1) * v.stride[0] + v.size[2];
+}
+
+int append_q4_impl(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                   const float* cos, const float* sin, const int32_t* positions, const int64_t* slots, void* q_out,
+                   void* k_pages, void* v_pages, int total_tokens, int Hq, int Hkv, int D, int dtype, const int64_t* st,
+                   int page_size, int num_pages, int rope_dim, int interleaved, int max_position, float eps,
+                   void* stream) {
+  if (dtype != ETATTN_F16 && dtype != ETATTN_BF16) return ETATTN_ERR_BAD_DTYPE;
+  if (total_tokens < 0 || total_tokens > kMaxTokens || Hq < 0 || Hq > kMaxGridYZ || Hkv > kMaxGridYZ ||
+      !head_dim_ok(D) || !rope_dim_ok(rope_dim, D) || !page_size_ok(page_size) || num_pages < 0)
+    return ETATTN_ERR_BAD_SHAPE;
+  if (Hkv <= 0) return ETATTN_ERR_BAD_HEADS;
+  if (st == nullptr) return ETATTN_ERR_NULL_PTR;
+  if (total_tokens == 0) return ETATTN_OK;
+  if (num_pages < 1) return ETATTN_ERR_BAD_SHAPE;
+  if (int rc = tables_ok(cos, sin, rope_dim, max_position, q_weight, k_weight, eps)) return rc;
+  if (!k || !v || !k_pages || !v_pages || !slots || (rope_dim > 0 && !positions) || (Hq > 0 && (!q || !q_out)))
+    return ETATTN_ERR_NULL_PTR;
+  const View vq = view3(q, total_tokens, Hq, D, st), vk = view3(k, total_tokens, Hkv, D, st + 3);
+  const View vv = view3(v, total_tokens, Hkv, D, st + 6), oq = view3(q_out, total_tokens, Hq, D, st + 9);
+  const int64_t block = page_size * q4_slot_bytes(D);
+  const View pk = view_blocks(k_pages, num_pages, Hkv, block, st + 12);
+  const View pv = view_blocks(v_pages, num_pages, Hkv, block, st + 14);
+  for (const View* t : {&vq, &vk, &vv, &oq})
+    if (!strides_ok(*t, 2)) return ETATTN_ERR_BAD_STRIDE;
+  if (!blocks_ok(pk) || !blocks_ok(pv)) return ETATTN_ERR_BAD_STRIDE;
+  for (const View* t : {&vk, &vv, &pk, &pv})
+    if (!aligned16(t->ptr)) return ETATTN_ERR_BAD_ALIGN;
+  if (Hq > 0 && (!aligned16(q) || !aligned16(q_out))) return ETATTN_ERR_BAD_ALIGN;
+  if (!aligned4(positions) || (reinterpret_cast<uintptr_t>(slots) & 7u)) return ETATTN_ERR_BAD_ALIGN;
+  for (const View* t : {&vq, &vk, &vv})
+    if (overlaps3(oq, *t) || overlaps(pk, 1, *t, 2) || overlaps(pv, 1, *t, 2)) return ETATTN_ERR_ALIAS;
+  // The pages of keys and values may interleave in one buffer.
+  if (overlaps(oq, 2, pk, 1) || overlaps(oq, 2, pv, 1) || pages_overlap(halves_of(pk), halves_of(pv)))
+    return ETATTN_ERR_ALIAS;
+  const int64_t table = rope_dim > 0 ? 2LL * max_position * rope_dim : 0;
+  const Flat reads[] = {{q_weight, 2 * D}, {k_weight, 2 * D}, {cos, table}, {sin, table},
+                        {positions, rope_dim > 0 ? 4LL * total_tokens : 0}, {slots, 8LL * total_tokens}};
+  if (overlaps_any(oq, 2, reads) || overlaps_any(pk, 1, reads) || overlaps_any(pv, 1, reads)) return ETATTN_ERR_ALIAS;
+
+  int dev = 0;
+  int* status = nullptr;
+  if (int rc = current_device(&dev, &status)) return rc;
+  AppendQ4Params p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.cos = cos;
+  p.sin = sin;
+  p.positions = rope_dim > 0 ? positions : nullptr;
+  p.slots = slots;
+  p.q_out = q_out;
+  p.k_pages = static_cast<uint8_t*>(k_pages);
+  p.v_pages = static_cast<uint8_t*>(v_pages);
+  int64_t* dst[] = {&p.q_st, &p.q_sh, &p.k_st, &p.k_sh, &p.v_st, &p.v_sh, &p.qo_st, &p.qo_sh};
+  for (int i = 0; i < 8; ++i) *dst[i] = st[3 * (i / 2) + i % 2];
+  p.kp_sp = st[12];
+  p.kp_sh = st[13];
+  p.vp_sp = st[14];
+  p.vp_sh = st[15];
+  p.total_tokens = total_tokens;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.rope_dim = rope_dim;
+  p.interleaved = interleaved != 0;
+  p.max_position = max_position;
+  p.eps = eps;
+  p.num_pages = num_pages;
+  p.page_shift = log2_of(page_size);
+  p.status = status;
+  const cudaError_t e = launch_append_q4(D, dtype == ETATTN_BF16, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
+}
+
+int unpack_q4_impl(const void* pages, void* out, int Hkv, int D, int dtype, const int64_t* st, int page_size,
+                   int num_pages, void* stream) {
+  if (dtype != ETATTN_F16 && dtype != ETATTN_BF16) return ETATTN_ERR_BAD_DTYPE;
+  if (Hkv > kMaxGridYZ || !head_dim_ok(D) || !page_size_ok(page_size) || num_pages < 0) return ETATTN_ERR_BAD_SHAPE;
+  if (Hkv <= 0) return ETATTN_ERR_BAD_HEADS;
+  if (st == nullptr) return ETATTN_ERR_NULL_PTR;
+  if (num_pages == 0) return ETATTN_OK;
+  if (!pages || !out) return ETATTN_ERR_NULL_PTR;
+  const View pv = view_blocks(pages, num_pages, Hkv, page_size * q4_slot_bytes(D), st);
+  const View vo = view_pages(out, num_pages, Hkv, page_size, D, st + 2);
+  if (!blocks_ok(pv) || !strides_ok(vo, 2)) return ETATTN_ERR_BAD_STRIDE;
+  if (!aligned16(pages) || !aligned16(out)) return ETATTN_ERR_BAD_ALIGN;
+  if (overlaps(pv, 1, vo, 2)) return ETATTN_ERR_ALIAS;
+  int dev = 0;
+  int* status = nullptr;
+  if (int rc = current_device(&dev, &status)) return rc;
+  UnpackQ4Params p{};
+  p.pages = static_cast<const uint8_t*>(pages);
+  p.out = out;
+  p.p_sp = st[0];
+  p.p_sh = st[1];
+  p.o_sp = st[2];
+  p.o_sh = st[3];
+  p.o_st = st[4];
+  p.num_pages = num_pages;
+  p.Hkv = Hkv;
+  p.page_shift = log2_of(page_size);
+  const cudaError_t e = launch_unpack_q4(D, dtype == ETATTN_BF16, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
+}
+
+// Rows of a unit: 8 (three CTAs on an SM), 16 (two) or 32 (one CTA of eight warps).
+int paged_q4_row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+int paged_q4_tile_keys(int D) { return D == 128 ? 128 : 256; }  // the kernel's PagedQ4Cfg::TK
+
+int paged_q4_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                  const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
+                  int max_seqlen_q, int total_q, int Hq, int Hkv, int D, int dtype, const int64_t* st, int page_size,
+                  int num_pages, int max_pages, int64_t table_stride, int causal, int window_left, int window_right,
+                  float scale, int num_shares, void* workspace, size_t workspace_bytes, void* stream) {
+  bool nothing = false;
+  if (int rc = paged_sizes_ok(cu_seqlens_q, num_seqs, max_seqlen_q, total_q, Hq, Hkv, D, dtype, st, page_size,
+                              num_pages, max_pages, table_stride, scale, num_shares, &nothing))
+    return rc;
+  if (nothing) return ETATTN_OK;
+  if (max_seqlen_q == 0) num_shares = 1;  // as in paged_impl
+  if (!q || !o || !k_pages || !v_pages || !block_table || !seqlens_k) return ETATTN_ERR_NULL_PTR;
+  const View vq = view3(q, total_q, Hq, D, st), vo = view3(o, total_q, Hq, D, st + 7);
+  const int64_t block = page_size * q4_slot_bytes(D);
+  const View pk = view_blocks(k_pages, num_pages, Hkv, block, st + 3);
+  const View pv = view_blocks(v_pages, num_pages, Hkv, block, st + 5);
+  const View vl{lse, 2, {Hq, total_q, 0, 0}, {total_q, 1, 0, 0}};
+  if (!strides_ok(vq, 2) || !strides_ok(vo, 2) || !blocks_ok(pk) || !blocks_ok(pv)) return ETATTN_ERR_BAD_STRIDE;
+  for (const View* t : {&vq, &vo, &pk, &pv})
+    if (!aligned16(t->ptr)) return ETATTN_ERR_BAD_ALIGN;
+  if (!aligned4(lse) || !aligned4(block_table) || !aligned4(seqlens_k) || !aligned4(cu_seqlens_q))
+    return ETATTN_ERR_BAD_ALIGN;
+  const Flat reads[] = {{block_table, table_bytes(num_seqs, max_pages, table_stride)},
+                        {seqlens_k, 4LL * num_seqs},
+                        {cu_seqlens_q, 4LL * (num_seqs + 1)}};
+  const int group = Hq / Hkv;
+  const int row_tile = paged_q4_row_tile((int64_t)max_seqlen_q * group);
+  const PagedLayout L = paged_layout(num_shares, row_tile, D);
+  View vw{};
+  if (num_shares > 1) {
+    if (workspace == nullptr) return ETATTN_ERR_NULL_PTR;
+    if (reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign) return ETATTN_ERR_BAD_ALIGN;
+    if (workspace_bytes < L.total) return ETATTN_ERR_BAD_SHAPE;
+    vw = View{workspace, 1, {(int64_t)L.total, 0, 0, 0}, {1, 0, 0, 0}};
+  }
+  struct Sized {
+    const View* view;
+    size_t esz;
+  };
+  const Sized writes[] = {{&vo, 2}, {lse ? &vl : nullptr, 4}, {num_shares > 1 ? &vw : nullptr, 1}};
+  const Sized inputs[] = {{&vq, 2}, {&pk, 1}, {&pv, 1}};
+  for (int i = 0; i < 3; ++i) {
+    if (writes[i].view == nullptr) continue;
+    for (const Sized& in : inputs)
+      if (overlaps(*writes[i].view, writes[i].esz, *in.view, in.esz)) return ETATTN_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (writes[j].view && overlaps(*writes[i].view, writes[i].esz, *writes[j].view, writes[j].esz))
+        return ETATTN_ERR_ALIAS;
+    if (overlaps_any(*writes[i].view, writes[i].esz, reads)) return ETATTN_ERR_ALIAS;
+  }
+
+  int dev = 0;
+  int* status = nullptr;
+  if (int rc = current_device(&dev, &status)) return rc;
+  PagedQ4Params p{};
+  paged_params(p, q, o, lse, block_table, seqlens_k, cu_seqlens_q, num_seqs, max_seqlen_q, total_q, Hkv, group, st,
+               st + 7, page_size, num_pages, max_pages, table_stride, causal, window_left, window_right, scale,
+               row_tile, num_shares, workspace, L, status);
+  p.k_pages = static_cast<const uint8_t*>(k_pages);
+  p.v_pages = static_cast<const uint8_t*>(v_pages);
+  p.kp_sp = st[3];
+  p.kp_sh = st[4];
+  p.vp_sp = st[5];
+  p.vp_sh = st[6];
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf = dtype == ETATTN_BF16;
+  cudaError_t e;
+  switch (D) {
+    case 32: e = bf ? launch_paged_q4_d32_1(p, s) : launch_paged_q4_d32_0(p, s); break;
+    case 64: e = bf ? launch_paged_q4_d64_1(p, s) : launch_paged_q4_d64_0(p, s); break;
+    default: e = bf ? launch_paged_q4_d128_1(p, s) : launch_paged_q4_d128_0(p, s);
+  }
+  return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
+}
+
+// ---------------------------------------------------------------- pages handed out and taken back
+size_t tables_bytes(int num_seqs) { return num_seqs > 0 ? 4 * ((size_t)num_seqs + 1) : 0; }
+
+// Both directions.  seqlens_out and free_count_out may be seqlens_k and free_count
+// themselves; nothing else may overlap.
+int tables_impl(const int32_t* amount, const int32_t* seqlens_k, int32_t* block_table, int32_t* free_pages,
+                const int32_t* free_count, int32_t* seqlens_out, int32_t* free_count_out, int32_t* cu_seqlens,
+                int32_t* positions, int64_t* slots, int num_seqs, int total_tokens, int page_size, int max_pages,
+                int64_t table_stride, int capacity, bool extend, void* workspace, size_t workspace_bytes, void* stream) {
+  if (total_tokens < 0 || total_tokens > kMaxTokens || capacity < 0 || capacity > kMaxTokens)
+    return ETATTN_ERR_BAD_SHAPE;
+  if (int rc = pages_ok(num_seqs, page_size, capacity, max_pages, table_stride)) return rc;
+  if (num_seqs == 0) return total_tokens == 0 ? ETATTN_OK : ETATTN_ERR_BAD_SHAPE;
+  if (!amount || !seqlens_k || !free_count || !seqlens_out || !free_count_out || !workspace ||
+      (max_pages > 0 && !block_table) || (capacity > 0 && !free_pages))
+    return ETATTN_ERR_NULL_PTR;
+  if (extend && (!cu_seqlens || (total_tokens > 0 && (!positions || !slots)))) return ETATTN_ERR_NULL_PTR;
+  const size_t need = tables_bytes(num_seqs);
+  if (workspace_bytes < need) return ETATTN_ERR_BAD_SHAPE;
+  if (reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign) return ETATTN_ERR_BAD_ALIGN;
+  const Flat all[] = {{amount, 4LL * num_seqs},                                                          // read
+                      {seqlens_k, 4LL * num_seqs},
+                      {free_count, 4},
+                      {block_table, max_pages > 0 ? table_bytes(num_seqs, max_pages, table_stride) : 0},  // read or written
+                      {free_pages, 4LL * capacity},
+                      {seqlens_out, 4LL * num_seqs},                                                     // written
+                      {free_count_out, 4},
+                      {extend ? cu_seqlens : nullptr, 4LL * (num_seqs + 1)},
+                      {extend ? positions : nullptr, 4LL * total_tokens},
+                      {extend ? slots : nullptr, 8LL * total_tokens},
+                      {workspace, (int64_t)need}};
+  for (const Flat& a : all)
+    if (!aligned4(a.ptr)) return ETATTN_ERR_BAD_ALIGN;
+  if (extend && (reinterpret_cast<uintptr_t>(slots) & 7u)) return ETATTN_ERR_BAD_ALIGN;
+  for (int i = 3; i < 11; ++i) {
+    if (all[i].ptr == nullptr) continue;
+    for (int j = 0; j < i; ++j) {
+      if (all[j].ptr == nullptr) continue;
+      if ((i == 5 && j == 1 || i == 6 && j == 2) && all[i].ptr == all[j].ptr) continue;  // in place
+      const View a{all[i].ptr, 1, {all[i].bytes, 0, 0, 0}, {1, 0, 0, 0}}, b{all[j].ptr, 1, {all[j].bytes, 0, 0, 0}, {1, 0, 0, 0}};
+      if (overlaps(a, 1, b, 1)) return ETATTN_ERR_ALIAS;
+    }
+  }
+
+  int dev = 0;
+  int* status = nullptr;
+  if (int rc = current_device(&dev, &status)) return rc;
+  TablesParams p{};
+  p.amount = amount;
+  p.seqlens = seqlens_k;
+  p.table = block_table;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.seqlens_out = seqlens_out;
+  p.free_count_out = free_count_out;
+  p.cu_seqlens = cu_seqlens;
+  p.positions = positions;
+  p.slots = slots;
+  p.first = static_cast<int*>(workspace);
+  p.table_stride = table_stride;
+  p.num_seqs = num_seqs;
+  p.max_pages = max_pages;
+  p.capacity = capacity;
+  p.total_tokens = total_tokens;
+  p.page_shift = log2_of(page_size);
+  p.extend = extend;
+  p.status = status;
+  const cudaError_t e = launch_tables(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
 }
 
@@ -1789,6 +2099,88 @@ int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max
   return ETATTN_OK;
 }
 
+int attn_paged_append_q4(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                         const float* rope_cos, const float* rope_sin, const int32_t* positions, const int64_t* slots,
+                         void* q_out, void* k_pages, void* v_pages, int total_tokens, int Hq, int Hkv, int D, int dtype,
+                         const int64_t* strides, int page_size, int num_pages, int rope_dim, int interleaved,
+                         int max_position, float eps, void* stream) {
+  return append_q4_impl(q, k, v, q_weight, k_weight, rope_cos, rope_sin, positions, slots, q_out, k_pages, v_pages,
+                        total_tokens, Hq, Hkv, D, dtype, strides, page_size, num_pages, rope_dim, interleaved,
+                        max_position, eps, stream);
+}
+
+int attn_paged_unpack_q4(const void* pages, void* out, int Hkv, int D, int dtype, const int64_t* strides, int page_size,
+                         int num_pages, void* stream) {
+  return unpack_q4_impl(pages, out, Hkv, D, dtype, strides, page_size, num_pages, stream);
+}
+
+size_t attn_paged_q4_block_bytes(int page_size, int D) {
+  return page_size_ok(page_size) && head_dim_ok(D) ? (size_t)(page_size * q4_slot_bytes(D)) : 0;
+}
+
+int attn_fwd_paged_q4(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                      const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
+                      int max_seqlen_q, int total_q, int Hq, int Hkv, int D, int dtype, const int64_t* strides,
+                      int page_size, int num_pages, int max_pages, int64_t table_stride, int causal, int window_left,
+                      int window_right, float scale, int num_shares, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  return paged_q4_impl(q, k_pages, v_pages, o, lse, block_table, seqlens_k, cu_seqlens_q, num_seqs, max_seqlen_q,
+                       total_q, Hq, Hkv, D, dtype, strides, page_size, num_pages, max_pages, table_stride, causal,
+                       window_left, window_right, scale, num_shares, workspace, workspace_bytes, stream);
+}
+
+size_t attn_fwd_paged_q4_workspace_size(int Hq, int Hkv, int max_seqlen_q, int D, int num_shares) {
+  if (Hq < 0 || Hkv <= 0 || Hq % Hkv != 0 || max_seqlen_q < 0 || !head_dim_ok(D) || num_shares < 1 ||
+      num_shares > kMaxShares)
+    return 0;
+  if (num_shares == 1 || Hq == 0 || max_seqlen_q == 0) return 0;
+  return paged_layout(num_shares, paged_q4_row_tile((int64_t)max_seqlen_q * (Hq / Hkv)), D).total;
+}
+
+int attn_fwd_paged_q4_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int D, int* num_shares,
+                           size_t* workspace_bytes) {
+  if (num_shares == nullptr) return ETATTN_ERR_NULL_PTR;
+  if (num_seqs < 0 || Hq < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || !head_dim_ok(D) || *num_shares < 0 ||
+      *num_shares > kMaxShares)
+    return ETATTN_ERR_BAD_SHAPE;
+  if (Hkv <= 0 || Hq % Hkv != 0) return ETATTN_ERR_BAD_HEADS;
+  if (*num_shares == 0) {
+    int dev = 0, num_sms = 0;
+    int* status = nullptr;
+    if (int rc = current_device(&dev, &status, &num_sms)) return rc;
+    // What the GPU runs at once, and no more shares than key tiles.
+    const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_q4_row_tile(rows), tk = paged_q4_tile_keys(D);
+    const double tiles = (double)num_seqs * Hkv * (double)((rows + mt - 1) / mt) *
+                         (double)std::max<int64_t>(1, (max_seqlen_k + tk - 1) / tk);
+    *num_shares = (int)std::max(1.0, std::min(tiles, (mt == 8 ? 3.0 : mt == 16 ? 2.0 : 1.0) * num_sms));
+  }
+  if (workspace_bytes) *workspace_bytes = attn_fwd_paged_q4_workspace_size(Hq, Hkv, max_seqlen_q, D, *num_shares);
+  return ETATTN_OK;
+}
+
+int attn_paged_extend(const int32_t* new_tokens, const int32_t* seqlens_k, int32_t* block_table,
+                      const int32_t* free_pages, const int32_t* free_count, int32_t* seqlens_out,
+                      int32_t* free_count_out, int32_t* cu_seqlens_q, int32_t* positions, int64_t* slots, int num_seqs,
+                      int total_tokens, int page_size, int max_pages, int64_t table_stride, int capacity,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  return tables_impl(new_tokens, seqlens_k, block_table, const_cast<int32_t*>(free_pages), free_count, seqlens_out,
+                     free_count_out, cu_seqlens_q, positions, slots, num_seqs, total_tokens, page_size, max_pages,
+                     table_stride, capacity, true, workspace, workspace_bytes, stream);
+}
+
+int attn_paged_truncate(const int32_t* keep, const int32_t* seqlens_k, const int32_t* block_table, int32_t* free_pages,
+                        const int32_t* free_count, int32_t* seqlens_out, int32_t* free_count_out, int num_seqs,
+                        int page_size, int max_pages, int64_t table_stride, int capacity, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  return tables_impl(keep, seqlens_k, const_cast<int32_t*>(block_table), free_pages, free_count, seqlens_out,
+                     free_count_out, nullptr, nullptr, nullptr, num_seqs, 0, page_size, max_pages, table_stride,
+                     capacity, false, workspace, workspace_bytes, stream);
+}
+
+size_t attn_paged_tables_workspace_size(int num_seqs) {
+  return num_seqs <= kMaxGridYZ ? tables_bytes(num_seqs) : 0;
+}
+
 int attn_fwd_varlen_host_plan(const int32_t* cu_seqlens_host, int num_seqs, int max_chunks,
                                          int32_t* seq_bounds) {
   if (cu_seqlens_host == nullptr || seq_bounds == nullptr) return -ETATTN_ERR_NULL_PTR;
@@ -1979,7 +2371,8 @@ const char* etattn_status_string(int code) {
     case ETATTN_ERR_LAUNCH: return "a CUDA runtime call failed";
     case ETATTN_ERR_DEVICE: return "the device reported a failure (a bounded wait ran out)";
     case ETATTN_ERR_NO_DEVICE: return "no sm_103 CUDA device is current";
-    case ETATTN_ERR_BAD_INDEX: return "a position or a page of the block table is out of range";
+    case ETATTN_ERR_BAD_INDEX: return "a position, a slot or a page of the block table is out of range";
+    case ETATTN_ERR_NO_PAGES: return "a step needs more pages than are free, or gives back more than there is room for";
     default: return "unknown status";
   }
 }
@@ -2003,7 +2396,7 @@ int etattn_read_device_status(int* out, int clear, void* stream) {
     if (e != cudaSuccess) return fail_cuda(e);
   }
   *out = word == kDevOk ? ETATTN_OK : word == kDevBadSeqlens ? ETATTN_ERR_BAD_SEQLENS
-         : word == kDevBadIndex ? ETATTN_ERR_BAD_INDEX : ETATTN_ERR_DEVICE;
+         : word == kDevBadIndex ? ETATTN_ERR_BAD_INDEX : word == kDevNoPages ? ETATTN_ERR_NO_PAGES : ETATTN_ERR_DEVICE;
   return ETATTN_OK;
 }
 

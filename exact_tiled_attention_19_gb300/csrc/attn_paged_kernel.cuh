@@ -63,9 +63,14 @@
 
 namespace etattn {
 
+// Tiles that entering a unit costs.  8 KV heads of 128, us with 1 / 2 / 3 / 4: 64
+// ragged sequences of up to 16384 keys 86.6 / 79.6 / 79.4 / 79.9, 512 of up to
+// 2048 keys 121 / 103 / 108 / 115.
+constexpr int kUnitCost = 2;
+
 template <int D_, int MT_>
 struct PagedCfg {
-  static constexpr int D = D_, MT = MT_;
+  static constexpr int D = D_, MT = MT_, UNIT_COST = kUnitCost;
   static constexpr int GROUPS = MT / 16;              // of four consumer warps, 16 rows each
   static constexpr int TK = 8192 / D;                 // keys per tile: 16 KB each of K and V
   static constexpr int WK = TK / 4;                   // keys per consumer warp
@@ -88,11 +93,6 @@ struct PagedCfg {
   static_assert(GROUPS == 1 ? SMEM_BYTES <= 115712 : SMEM_BYTES <= 232448, "two CTAs per SM, or one");
   static constexpr int CONSUMER_WARPS = 4 * GROUPS, THREADS = 32 * (CONSUMER_WARPS + 1);
 };
-
-// Tiles that entering a unit costs.  8 KV heads of 128, us with 1 / 2 / 3 / 4: 64
-// ragged sequences of up to 16384 keys 86.6 / 79.6 / 79.4 / 79.9, 512 of up to
-// 2048 keys 121 / 103 / 108 / 115.
-constexpr int kUnitCost = 2;
 
 // What FP16 weights, and the accumulators with them, are multiplied by.
 constexpr float kF16Weight = 32768.f;
@@ -279,10 +279,28 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* s
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status)) != 0;
 }
 
-// The producer warp's walk along its piece of the line.  False: a wait ran out.
+// How a box, the keys of a tile that lie in one page, comes into a stage: K and
+// V each by one TMA copy; `page` may be num_pages, past the map, and then the box is
+// filled with zeros.
 template <class C>
-__device__ __forceinline__ bool paged_walk(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedParams& p,
-                                           uint8_t* smem, int lane, PagedRing& ring) {
+struct PagedTmaBoxes {
+  const CUtensorMap &kmap, &vmap;
+  uint64_t policy;
+  uint32_t bytes;  // of a box of K, or of V
+  __device__ __forceinline__ PagedTmaBoxes(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p)
+      : kmap(k), vmap(v), policy(l2_policy_evict_first()), bytes((uint32_t)min(1 << p.page_shift, C::TK) * 2 * C::D) {}
+  __device__ __forceinline__ void load(uint8_t* stage, int box, int slot, int head, int page, uint64_t* bar) const {
+    uint8_t* dst = stage + box * bytes;
+    tma_load_5d_hint(dst, &kmap, bar, 0, slot, 0, head, page, policy);
+    tma_load_5d_hint(dst + C::TILE_BYTES, &vmap, bar, 0, slot, 0, head, page, policy);
+  }
+  __device__ __forceinline__ int bad_page(const PagedParams& p) const { return p.num_pages; }
+};
+
+// The producer warp's walk along its piece of the line.  False: a wait ran out.
+template <class C, class Boxes>
+__device__ __forceinline__ bool paged_walk(const Boxes& from, const PagedParams& p, uint8_t* smem, int lane,
+                                           PagedRing& ring) {
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
   uint64_t* empty = full + C::STAGES;
   uint64_t* ufull = empty + C::STAGES;
@@ -303,7 +321,7 @@ __device__ __forceinline__ bool paged_walk(const CUtensorMap& kmap, const CUtens
   const bool one_each = p.num_seqs <= 32;
   const int per = (p.num_seqs + 31) / 32;
   const int s_begin = min(p.num_seqs, lane * per), s_end = min(p.num_seqs, s_begin + per);
-  auto length = [](const PagedSeq& q) { return (int64_t)q.units * (q.tiles + kUnitCost); };
+  auto length = [](const PagedSeq& q) { return (int64_t)q.units * (q.tiles + C::UNIT_COST); };
   int64_t mine = 0;
   if (one_each) mine = length(win.mine);
   else
@@ -342,9 +360,9 @@ __device__ __forceinline__ bool paged_walk(const CUtensorMap& kmap, const CUtens
   at = __shfl_sync(0xffffffffu, at, holder);
   if (!one_each) win.load(p, s, lane);
   PagedSeq q = win.at(s);
-  int unit = (int)div_pos(begin - at, q.tiles + kUnitCost);
-  int64_t u0 = at + (int64_t)unit * (q.tiles + kUnitCost);  // where the unit lies on the line
-  int tile = max(0, (int)(begin - u0) - kUnitCost);
+  int unit = (int)div_pos(begin - at, q.tiles + C::UNIT_COST);
+  int64_t u0 = at + (int64_t)unit * (q.tiles + C::UNIT_COST);  // where the unit lies on the line
+  int tile = max(0, (int)(begin - u0) - C::UNIT_COST);
 
   PagedShare mark{};  // for the join, written at the end
   int64_t mark_u0 = 0;
@@ -354,19 +372,17 @@ __device__ __forceinline__ bool paged_walk(const CUtensorMap& kmap, const CUtens
     mark.n = q.n;
     mark.head0 = (unit / q.nrt) * p.group;
     mark.row0 = (unit % q.nrt) * C::MT;
-    mark_u0 = u0 + kUnitCost;
+    mark_u0 = u0 + C::UNIT_COST;
     mark_tiles = q.tiles;
   }
 
   const int page_keys = 1 << p.page_shift;
   const int box_keys = min(page_keys, C::TK);
   const int boxes = C::TK / box_keys;  // pages of a tile (1 when a page holds whole tiles); at most 32
-  const uint32_t box_bytes = (uint32_t)box_keys * 2 * C::D;
-  const uint64_t policy = l2_policy_evict_first();
 
   // Unit by unit; `stop` is the end of this share's tiles in the unit.
   while (true) {
-    const int stop = (int)max((int64_t)0, min((int64_t)q.tiles, end - u0 - kUnitCost));
+    const int stop = (int)max((int64_t)0, min((int64_t)q.tiles, end - u0 - C::UNIT_COST));
     if (tile < stop) {
       const int head = unit / q.nrt;
       const int row0 = (unit - head * q.nrt) * C::MT, rows = min(C::MT, q.n * p.group - row0);
@@ -405,17 +421,14 @@ __device__ __forceinline__ bool paged_walk(const CUtensorMap& kmap, const CUtens
         const uint32_t loads = __popc(__ballot_sync(0xffffffffu, on));
         if (!warp_wait(empty + ring.stage, ring.phase, p.status)) return false;
         uint8_t* base = smem + ring.stage * C::STAGE_BYTES;
-        if (lane == 0) mbar_arrive_expect_tx(full + ring.stage, loads * 2 * box_bytes);
+        if (lane == 0) mbar_arrive_expect_tx(full + ring.stage, loads * 2 * from.bytes);
         __syncwarp();
         if (on) {
           if (pg < 0 || pg >= p.num_pages) {
             atomicCAS(p.status, 0, kDevBadIndex);
-            pg = p.num_pages;  // past the map: the box is filled with zeros
+            pg = from.bad_page(p);
           }
-          const int slot = k0 & (page_keys - 1);
-          uint8_t* dst = base + lane * box_bytes;
-          tma_load_5d_hint(dst, &kmap, full + ring.stage, 0, slot, 0, head, pg, policy);
-          tma_load_5d_hint(dst + C::TILE_BYTES, &vmap, full + ring.stage, 0, slot, 0, head, pg, policy);
+          from.load(base, lane, k0 & (page_keys - 1), head, pg, full + ring.stage);
         }
         __syncwarp();
         if (++ring.stage == C::STAGES) {
@@ -425,7 +438,7 @@ __device__ __forceinline__ bool paged_walk(const CUtensorMap& kmap, const CUtens
       }
     }
     // The next unit of the line.
-    u0 += q.tiles + kUnitCost;
+    u0 += q.tiles + C::UNIT_COST;
     if (u0 >= end) break;
     tile = 0;
     if (++unit == q.units) {
@@ -447,14 +460,13 @@ __device__ __forceinline__ bool paged_walk(const CUtensorMap& kmap, const CUtens
 }
 
 // The producer warp: the walk, the end of the line, and its copies seen home.
-template <class C>
-__device__ __forceinline__ void paged_producer(const CUtensorMap& kmap, const CUtensorMap& vmap, const PagedParams& p,
-                                               uint8_t* smem, int lane) {
+template <class C, class Boxes>
+__device__ __forceinline__ void paged_producer(const Boxes& from, const PagedParams& p, uint8_t* smem, int lane) {
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
   uint64_t* ufull = full + 2 * C::STAGES;
   uint64_t* uempty = ufull + 1;
   PagedRing ring;
-  const bool ended = paged_walk<C>(kmap, vmap, p, smem, lane, ring) && warp_wait(uempty, ring.uphase, p.status);
+  const bool ended = paged_walk<C>(from, p, smem, lane, ring) && warp_wait(uempty, ring.uphase, p.status);
   if (ended && lane == 0) {
     reinterpret_cast<PagedUnit*>(smem + C::OFF_UNIT)->tiles = 0;
     mbar_arrive(ufull);
@@ -565,7 +577,7 @@ __global__ void __launch_bounds__(PagedCfg<D, MT>::THREADS, MT == 16 ? 2 : 1)
   __syncthreads();
   pdl_wait();
   if (warp == C::CONSUMER_WARPS) {
-    paged_producer<C>(kmap, vmap, p, smem, lane);
+    paged_producer<C>(PagedTmaBoxes<C>(kmap, vmap, p), p, smem, lane);
     return;
   }
 

@@ -1,0 +1,744 @@
+// Attention of a few new query rows per sequence over a paged key-value cache
+// held in 4 bits, exact over the values that the cache stands for and in one
+// pass over it.  Work line, producer and joined partial states are those of
+// attn_paged_kernel.cuh; the consumers compute on the codes.
+//
+// Mathematics.  Element d of key j, in group h of G = min(D, 64) elements, is
+//     k_jd = s_jh c_jd + m_jh,   c_jd in 0 .. 15,
+// with scale s and minimum m in the type of q, and values likewise.  So
+//     <q_i, k_j>      = sum_h ( s_jh <q_ih, c_jh> + m_jh sum_d q_id ),
+//     sum_j P_ij v_jd = sum_j (P_ij s_jh) c_jd + sum_j P_ij m_jh,
+// products of small whole numbers on the tensor core, with a scale and a minimum
+// per key and group applied to their FP32 results (keys) or to the weights in FP32
+// (values).  The cache's codes are never turned into 16-bit numbers in memory.
+//
+// Codes as operands.  The bits of a code in the low bits of a half make the
+// denormal c 2^-24, which the tensor core multiplies exactly; one position higher
+// (bits 4 to 7) they make c 2^-20.  So a word of eight codes becomes four operand
+// registers by four ANDs and one shift, with no conversion and no offset to take
+// away: the minimum goes into a term of its own.  The order of the elements within
+// a product does not matter as long as q has the same one; q's elements that meet
+// codes at the higher position are divided by 16, as are the outputs at them.
+//   Both products have the codes as their left operand (m16n8k16), so that 8 rows
+// fill the right one: S^T = K Q^T with 16 keys, O^T = V^T P^T with 16 elements.  A lane has
+// the scores of one key in the former, and of one row in P^T: an 8 x 8 transpose of the
+// weights, already scaled and rounded, lies between.  A register of V^T holds two keys
+// of one element: byte permutes bring the halves of two keys' words together first.
+//
+// Precision.  q's rows are scaled by powers of two so that their largest element
+// is within 2^14 .. 2^15, and held as FP16: exact for both input types (elements below
+// 2^-29 of the largest lose bits).  Scores, maxima, sums, minima terms and accumulators are
+// FP32.  Weights times scales, P s, are scaled by a power of two per group, which
+// follows the largest scale that the warp has seen, and rounded to FP16: in two
+// parts of together 2^-21 for FP16 outputs, in one for BF16 ones, whose 2^-12 is an
+// eighth of the output's own rounding.  The tensor core cuts off what falls below an
+// accumulator's last bit, always downwards, and codes are never negative, so a
+// running sum would drift: a tile's products with V start from 0 and are added to the
+// running sums in FP32 (without it one sequence of 524288 keys was 1.6 times as far
+// from 64 bits as a rounding).
+#pragma once
+
+#include <cstdint>
+#include <type_traits>
+
+#include "attn_paged_kernel.cuh"
+
+namespace etattn {
+
+template <int D_, int MT_>
+struct PagedQ4Cfg {
+  static constexpr int D = D_, MT = MT_;
+  static constexpr int UNIT_COST = 3;
+  static constexpr int GROUPS = MT / 16 > 1 ? 2 : 1;  // of four consumer warps
+  static constexpr int ROWS = MT < 16 ? 8 : 16;       // of a group
+  static constexpr int G = D < 64 ? D : 64, H = D / G;
+  static constexpr int TK = D == 128 ? 128 : 256;     // keys per tile
+  static constexpr int WK = TK / 4, NT = WK / 8;      // per consumer warp, and in blocks of 8
+  static constexpr int SPREAD = 32;                   // keys of the largest box whose blocks different warps take
+  static constexpr int PANEL = G / 2 + 4;             // bytes of a key's group: codes, scale and minimum
+  static constexpr int ROW_BYTES = H * PANEL;
+  static constexpr int TILE_BYTES = TK * ROW_BYTES;
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V: 18 KB, or 10 KB for D = 32
+  // Three CTAs of 8 rows share an SM, two of 16, or one of 32.
+  static constexpr int CTAS = MT == 8 ? 3 : MT == 16 ? 2 : 1;
+  static constexpr int BUDGET = MT == 8 ? 76800 : MT == 16 ? 115712 : 232448;
+  static constexpr int MERGE_BYTES = 4 * ROWS * G * 4;  // a group's: four warps' rows, one group of elements
+  static constexpr int Q_PITCH = 2 * D + 16;            // padded: no bank conflicts
+  static constexpr int STATE_BYTES = (2 + H) * 4 * 16 * 4;  // a group's m, l and minima's terms: 4 warps x 16 each
+  static constexpr int FIXED = GROUPS * MERGE_BYTES + MT * Q_PITCH + GROUPS * STATE_BYTES + 48;
+  static constexpr int FIT = (BUDGET - FIXED - 192) / STAGE_BYTES;
+  static constexpr int STAGES = FIT < 11 ? FIT : 11;
+  static constexpr int OFF_MERGE = STAGES * STAGE_BYTES;
+  static constexpr int OFF_Q = OFF_MERGE + GROUPS * MERGE_BYTES;
+  static constexpr int OFF_STATE = OFF_Q + MT * Q_PITCH;
+  static constexpr int OFF_UNIT = OFF_STATE + GROUPS * STATE_BYTES;
+  static constexpr int OFF_BARS = OFF_UNIT + 48;
+  static constexpr int SMEM_BYTES = OFF_BARS + 2 * (STAGES + 1) * 8;
+  static_assert(STAGES >= 3 && SMEM_BYTES <= BUDGET, "");
+  static constexpr int CONSUMER_WARPS = 4 * GROUPS, THREADS = 32 * (CONSUMER_WARPS + 1);
+};
+
+// A box: a block of the cache (one page and head: for every group the codes of its
+// slots, then their scales and minima) in one copy, or, where a page holds more than
+// a tile, the tile's slots of every part.
+template <class C>
+struct PagedQ4Boxes {
+  const PagedQ4Params& p;
+  uint64_t policy;
+  uint32_t bytes;  // of a box of K, or of V
+  __device__ __forceinline__ explicit PagedQ4Boxes(const PagedQ4Params& p_)
+      : p(p_), policy(l2_policy_evict_first()), bytes((uint32_t)min(1 << p_.page_shift, C::TK) * C::ROW_BYTES) {}
+  // Large boxes one after the other; small ones so that those of a warp, NT in a
+  // row, lie SPREAD keys apart, with those of the other warps between them.
+  __device__ __forceinline__ void load(uint8_t* stage, int box, int slot, int head, int page, uint64_t* bar) const {
+    const uint8_t* src[2] = {p.k_pages + page * p.kp_sp + head * p.kp_sh, p.v_pages + page * p.vp_sp + head * p.vp_sh};
+    uint8_t* dst = stage + ((1 << p.page_shift) <= C::SPREAD
+                                ? (box % C::NT) * (C::SPREAD * C::ROW_BYTES) + (box / C::NT) * bytes
+                                : box * bytes);
+#pragma unroll
+    for (int i = 0; i < 2; ++i, dst += C::TILE_BYTES) {
+      if ((1 << p.page_shift) <= C::TK) {
+        bulk_load_hint(dst, src[i], bytes, bar, policy);
+      } else {
+        const int64_t page_keys = 1 << p.page_shift;
+#pragma unroll
+        for (int h = 0; h < C::H; ++h) {
+          const uint8_t* from = src[i] + h * page_keys * C::PANEL;
+          uint8_t* to = dst + h * C::TK * C::PANEL;
+          bulk_load_hint(to, from + slot * (C::G / 2), C::TK * (C::G / 2), bar, policy);
+          bulk_load_hint(to + C::TK * (C::G / 2), from + page_keys * (C::G / 2) + slot * 4, C::TK * 4, bar, policy);
+        }
+      }
+    }
+  }
+  // (Recorded; the rows of that sequence mean nothing.)
+  __device__ __forceinline__ int bad_page(const PagedParams&) const { return 0; }
+};
+
+// d = A B
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// x, y as hi + lo, two pairs of halves: hi by cutting bits off, lo the rest, rounded.
+__device__ __forceinline__ void split_halves(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const float hx = __uint_as_float(__float_as_uint(x) & 0xffffe000u), hy = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
+  hi = pack_f16x2(hx, hy);
+  lo = pack_f16x2(x - hx, y - hy);
+}
+
+// Pairs of FP32 numbers in one 64-bit register, for paired arithmetic.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ float2 parts_of(uint64_t x) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// A scale (low half) and a minimum.
+template <bool BF16>
+__device__ __forceinline__ void scale_and_min(uint32_t w, float& s, float& m) {
+  if (BF16) unpack_bf16x2(w, s, m);
+  else unpack_f16x2(w, s, m);
+}
+
+// The 8 x 8 matrix of halves that the warp holds, a row of four registers each, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+constexpr uint32_t kLowCodes = 0x000f000fu, kHighCodes = 0x00f000f0u;
+
+// Adds up a group's four warps' scaled rows, one group of elements at a time, and
+// writes them: the output, or the unit's partial rows.  A lane holds elements
+// G/8 g .. of rows 2 t4 and 2 t4 + 1 (and of those 8 further down).
+template <class C, bool BF16>
+__device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const PagedUnit& w, int grp, int rows, float* merge,
+                                               const float (&o)[C::H][C::ROWS / 8][2][C::G / 8], bool whole,
+                                               int64_t part_row) {
+  constexpr int G = C::G, RUN = G / 8;
+  const int tid = C::GROUPS == 1 ? threadIdx.x : threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3, row0 = w.row0 + 16 * grp;
+  // Where a row's four elements x4 lie: eight lanes that store together hit eight
+  // different quarters of the banks.
+  auto place = [](int r, int x4) {
+    return (x4 ^ (G == 64 ? (r & 4) | ((r >> 1) & 1) : (r & 6))) * 4;
+  };
+#pragma unroll
+  for (int h = 0; h < C::H; ++h) {
+#pragma unroll
+    for (int hr = 0; hr < C::ROWS / 8; ++hr)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * hr + 2 * t4 + j;
+        float* dst = merge + (warp * C::ROWS + r) * G;
+        const float(&v)[RUN] = o[h][hr][j];
+#pragma unroll
+        for (int i = 0; i < RUN; i += 4)
+          *reinterpret_cast<float4*>(dst + place(r, (g * RUN + i) / 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+    group_barrier<C>(grp);
+    for (int x = tid; x < rows * (G / 8); x += 128) {
+      const int r = x / (G / 8), c = (x % (G / 8)) * 8;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float* src = merge + (y * C::ROWS + r) * G;
+        const float4 u0 = *reinterpret_cast<const float4*>(src + place(r, c / 4));
+        const float4 u1 = *reinterpret_cast<const float4*>(src + place(r, c / 4 + 1));
+        v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
+        v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
+      }
+      if (whole) {
+        const int rr = row0 + r, i = rr / p.group;
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          u[k] = BF16 ? pack_bf16x2(v[2 * k], v[2 * k + 1]) : pack_f16x2(v[2 * k], v[2 * k + 1]);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (int64_t)(w.t0 + i) * p.o_st +
+                                  (int64_t)(w.head0 + rr - i * p.group) * p.o_sh + h * G + c) =
+            make_uint4(u[0], u[1], u[2], u[3]);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + (part_row + r) * C::D + h * G + c);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+    // The next group, or the next unit's (whose state the warps write first, and
+    // meet, before they come here again).
+    if (h + 1 < C::H) group_barrier<C>(grp);
+  }
+}
+
+template <int D, int MT, bool BF16, bool SPREAD>
+__global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>::CTAS)
+    attn_paged_q4_kernel(const __grid_constant__ PagedQ4Params p) {
+  using C = PagedQ4Cfg<D, MT>;
+  constexpr int G = C::G, H = C::H, NT = C::NT, RH = C::ROWS / 8;
+  constexpr int KW = G / 32, ON = G / 16;      // words of a key's group that a lane reads; blocks of 16 elements
+  constexpr bool TWO = !BF16;                  // weights in two parts
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* ufull = empty + C::STAGES;
+  uint64_t* uempty = ufull + 1;
+
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, C::CONSUMER_WARPS);
+    }
+    mbar_init(ufull, 1);
+    mbar_init(uempty, C::CONSUMER_WARPS);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  if (warp == C::CONSUMER_WARPS) {
+    paged_producer<C>(PagedQ4Boxes<C>(p), p, smem, lane);
+    return;
+  }
+
+  // ------------------------------------------------ consumers
+  // The warp's rows, and its quarter of a tile's keys.
+  const int grp = C::GROUPS == 1 ? 0 : warp >> 2, quarter = C::GROUPS == 1 ? warp : warp & 3;
+  const int g = lane >> 2, t4 = lane & 3;
+  float* st_m = reinterpret_cast<float*>(smem + C::OFF_STATE + grp * C::STATE_BYTES);
+  float* st_l = st_m + 64;
+  float* st_low = st_l + 64;
+  float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE + grp * C::MERGE_BYTES);
+  // Q's operands, which the warp reads again for every tile (the registers are needed
+  // for the values): where the rows are merged, which happens after the last tile.
+  uint4* q_ops = reinterpret_cast<uint4*>(merge) + quarter * (H * KW * RH * 32) + lane;
+  static_assert(4 * H * KW * RH * 32 * 16 <= C::MERGE_BYTES, "");
+  const int share = blockIdx.x;
+  // Blocks of 8 keys lie in one box each.  The warp takes NT of them: neighbours in a
+  // large box, or the same place of NT boxes (SPREAD), which lie a constant step apart
+  // either way.  Its first one, key `key_at` of the tile, starts `first` bytes (its
+  // scales `first_scale` bytes) into the tile; groups are `panel` apart.
+  constexpr uint32_t kCodeStep = SPREAD ? C::SPREAD * C::ROW_BYTES : 8 * (G / 2);
+  constexpr uint32_t kScaleStep = SPREAD ? C::SPREAD * C::ROW_BYTES : 8 * 4;
+  const int box_keys = min(1 << p.page_shift, C::TK);
+  const uint32_t panel = (uint32_t)box_keys * C::PANEL;
+  const int key_step = SPREAD ? box_keys : 8;
+  int key_at, box_at, in_box;  // the latter two: where the box starts, and the block's first key in it
+  if (SPREAD) {
+    const int per_box = box_keys >> 3, row = quarter / per_box;  // blocks of a box; the warp's row of NT boxes
+    in_box = (quarter - row * per_box) * 8;
+    key_at = row * NT * box_keys + in_box;
+    box_at = row * box_keys * C::ROW_BYTES;
+  } else {
+    key_at = quarter * C::WK;
+    in_box = key_at & (box_keys - 1);
+    box_at = (key_at - in_box) * C::ROW_BYTES;
+  }
+  const uint32_t first = box_at + in_box * (G / 2), first_scale = box_at + box_keys * (G / 2) + in_box * 4;
+  // The lane's part of a block: elements G/4 t4 .. of key g, with its scales, and of
+  // values, elements G/8 g .. of keys 2 t4 and 2 t4 + 1.  The second two of four lanes
+  // read the latter in the other order, which keeps a warp's reads on different banks.
+  const uint32_t k_at = first + g * (G / 2) + t4 * (G / 8), s_at = first_scale + g * 4;
+  const uint32_t v_first = C::TILE_BYTES + first + (2 * t4 + (t4 >> 1)) * (G / 2) + g * (G / 16);
+  const uint32_t v_second = C::TILE_BYTES + first + (2 * t4 + 1 - (t4 >> 1)) * (G / 2) + g * (G / 16);
+  const uint32_t low_halves = t4 < 2 ? 0x5410u : 0x1054u, high_halves = t4 < 2 ? 0x7632u : 0x3276u;
+
+  uint32_t phase = 0, uphase = 0;
+  int stage = 0;
+  bool alive = true;
+  while (true) {
+    // A wait that ran out in one warp ends its group, here, where none of them
+    // waits in a barrier for another.
+    alive = alive && mbar_wait(ufull, uphase, p.status);
+    uphase ^= 1;
+    if (group_any<C>(grp, !alive)) return;
+    __syncwarp();
+    const PagedUnit w = *reinterpret_cast<const PagedUnit*>(smem + C::OFF_UNIT);
+    if (w.tiles == 0) return;
+    const int row0 = w.row0 + 16 * grp;
+    const int rows = min(C::ROWS, w.n * p.group - row0);  // none (or fewer) for the second group of a short unit
+    const int delta = w.Lk - w.n;
+    // The tokens of the group's rows and the key ranges of rows 2 t4 and 2 t4 + 1 (and
+    // of those 8 further down).
+    const int tok_first = row0 / p.group, tok_last = (row0 + max(rows, 1) - 1) / p.group;
+    int row_lo[RH][2], row_hi[RH][2];
+#pragma unroll
+    for (int r = 0; r < RH; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = min((row0 + 2 * t4 + i + 8 * r) / p.group, tok_last) + delta;
+        row_lo[r][i] = max(0, c - p.win_left);
+        row_hi[r][i] = (int)min((int64_t)w.Lk - 1, (int64_t)c + p.win_right);
+      }
+    // Keys in [in_lo, in_hi] are read by every row of the group, those outside
+    // [any_lo, any_hi] by none.
+    const int in_lo = max(0, tok_last + delta - p.win_left);
+    const int in_hi = (int)min((int64_t)w.Lk - 1, (int64_t)tok_first + delta + p.win_right);
+    const int any_lo = max(0, tok_first + delta - p.win_left);
+    const int any_hi = (int)min((int64_t)w.Lk - 1, (int64_t)tok_last + delta + p.win_right);
+
+    // Q's operands: rows scaled by 2^up; their groups' sums (in units of 2^-24), and
+    // what brings a score back.  Rows past the last hold anything, and nothing of
+    // them is written.
+    uint64_t qsum[RH][H], back[RH];  // of rows 2 t4 and 2 t4 + 1
+    auto of_rows = [&](float x) { return pair_of(__shfl_sync(0xffffffffu, x, 8 * t4), __shfl_sync(0xffffffffu, x, 8 * t4 + 4)); };
+    uint32_t qseen = (uint32_t)(w.t0 | w.n | w.Lk | w.head0 | w.row0 | w.tile | w.tiles | w.from_start | w.to_end);
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      float x[H][KW][8];
+      float big = 0.f;
+      const uint8_t* src = smem + C::OFF_Q + (16 * grp + g + 8 * r) * C::Q_PITCH + t4 * (G / 2);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int y = 0; y < KW; ++y) {
+          const uint4 u = *reinterpret_cast<const uint4*>(src + h * 2 * G + y * 16);
+          qseen |= u.x | u.y | u.z | u.w;
+          const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            scale_and_min<BF16>(v[i], x[h][y][2 * i], x[h][y][2 * i + 1]);
+            big = fmaxf(big, fmaxf(fabsf(x[h][y][2 * i]), fabsf(x[h][y][2 * i + 1])));
+          }
+        }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // (big = 1.x 2^e: 2^(14 - e), within what FP32 holds.)
+      const int e = max(-90, min(110, (int)(__float_as_uint(big) >> 23) - 127));
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      const float down = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 + e + 10) << 23), 0x1p-126f);
+      back[r] = of_rows(down);
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float sum = 0.f;
+#pragma unroll
+        for (int y = 0; y < KW; ++y) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[h][y][i] *= up;
+            sum += x[h][y][i];
+          }
+          q_ops[((h * KW + y) * RH + r) * 32] =
+              make_uint4(pack_f16x2(x[h][y][0], x[h][y][4]), pack_f16x2(x[h][y][1] * 0.0625f, x[h][y][5] * 0.0625f),
+                         pack_f16x2(x[h][y][2], x[h][y][6]), pack_f16x2(x[h][y][3] * 0.0625f, x[h][y][7] * 0.0625f));
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qsum[r][h] = of_rows(sum * 0x1p-24f);
+      }
+    }
+    release_after(uempty, qseen, p.zero, lane == 0);
+    __syncwarp();
+
+    float m[RH][2];
+    uint64_t l[RH], low[RH][H], o[RH][H][ON][2];
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      m[r][0] = m[r][1] = -INFINITY;
+      l[r] = 0;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        low[r][h] = 0;
+#pragma unroll
+        for (int n = 0; n < ON; ++n) o[r][h][n][0] = o[r][h][n][1] = 0;
+      }
+    }
+    // The largest exponent of a value's scale so far, per group, and the power of two
+    // that takes scales below it to 2^15.
+    constexpr int kExpShift = BF16 ? 7 : 10, kExpMax = BF16 ? 255 : 31, kExpBias = BF16 ? 127 : 15;
+    constexpr int kExpMin = BF16 ? 14 : 0;  // (so that the power of two is one in FP32)
+    int top[H];
+    float lift[H];
+    auto lift_of = [](int x) { return __uint_as_float((uint32_t)(127 + 14 + kExpBias - x) << 23); };
+#pragma unroll
+    for (int h = 0; h < H; ++h) top[h] = kExpMin, lift[h] = lift_of(kExpMin);
+
+    for (int x = 0; x < w.tiles; ++x) {
+      const int tile0 = (w.tile + x) * C::TK, key0 = tile0 + key_at;
+      alive = alive && mbar_wait(full + stage, phase, p.status);
+      alive = __all_sync(0xffffffffu, alive);  // and the lanes, which leave the wait one by one, are together
+      uint32_t seen = 0;  // of everything read of V (what is read of K goes into the maxima)
+      if (alive && rows > 0) {
+        const uint8_t* tile = smem + stage * C::STAGE_BYTES;
+        const bool edge = tile0 < in_lo || tile0 + C::TK - 1 > in_hi;
+        // Scores of the warp's keys, in units of 1 / back, 16 keys at a time: of key g of
+        // two blocks.
+        uint64_t sc[NT][RH];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          uint4 q[KW][RH];
+#pragma unroll
+          for (int y = 0; y < KW; ++y)
+#pragma unroll
+            for (int r = 0; r < RH; ++r) q[y][r] = q_ops[((h * KW + y) * RH + r) * 32];
+#pragma unroll
+          for (int kb = 0; kb < NT / 2; ++kb) {
+            uint32_t c[2][KW], sm[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int n = 2 * kb + u;
+              if constexpr (KW == 2) {
+                const uint2 x = *reinterpret_cast<const uint2*>(tile + k_at + n * kCodeStep + h * panel);
+                c[u][0] = x.x, c[u][KW - 1] = x.y;
+              } else {
+                c[u][0] = *reinterpret_cast<const uint32_t*>(tile + k_at + n * kCodeStep + h * panel);
+              }
+              sm[u] = *reinterpret_cast<const uint32_t*>(tile + s_at + n * kScaleStep + h * panel);
+            }
+            float part[RH][4];
+#pragma unroll
+            for (int y = 0; y < KW; ++y)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t c0 = j == 0 ? c[0][y] : c[0][y] >> 8, c1 = j == 0 ? c[1][y] : c[1][y] >> 8;
+                const uint32_t a[4] = {c0 & kLowCodes, c1 & kLowCodes, c0 & kHighCodes, c1 & kHighCodes};
+#pragma unroll
+                for (int r = 0; r < RH; ++r) {
+                  const uint4 b = q[y][r];
+                  if (y == 0 && j == 0) mma16816_first(part[r], a, b.x, b.y);
+                  else mma16816<false>(part[r], a, j == 0 ? b.x : b.z, j == 0 ? b.y : b.w);
+                }
+              }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float s, mn;
+              scale_and_min<BF16>(sm[u], s, mn);
+              const uint64_t s2 = pair_of(s, s), mn2 = pair_of(mn, mn);
+#pragma unroll
+              for (int r = 0; r < RH; ++r) {
+                uint64_t& x = sc[2 * kb + u][r];
+                x = h == 0 ? mul_pair(mn2, qsum[r][h]) : fma_pair(mn2, qsum[r][h], x);
+                x = fma_pair(s2, pair_of(part[r][2 * u], part[r][2 * u + 1]), x);
+              }
+            }
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int key = key0 + n * key_step + g;
+#pragma unroll
+            for (int r = 0; r < RH; ++r) {
+              float2 x = parts_of(sc[n][r]);
+              if (key < row_lo[r][0] || key > row_hi[r][0]) x.x = -INFINITY;
+              if (key < row_lo[r][1] || key > row_hi[r][1]) x.y = -INFINITY;
+              sc[n][r] = pair_of(x.x, x.y);
+            }
+          }
+        }
+        float mx[RH][2];
+        bool grew = false;
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+          mx[r][0] = mx[r][1] = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < NT; n += 2) {
+            const float2 x = parts_of(sc[n][r]), y = parts_of(sc[n + 1][r]);
+            mx[r][0] = max3(mx[r][0], x.x, y.x);
+            mx[r][1] = max3(mx[r][1], x.y, y.y);
+          }
+          const float2 f = parts_of(back[r]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float& x = mx[r][i];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * (i == 0 ? f.x : f.y);
+            grew = grew || (2 * t4 + i + 8 * r < rows && x > m[r][i]);
+          }
+        }
+        // The values' scales and minima, and the largest bits of a scale (they order like
+        // the numbers, none of which is negative; the minima beside them are cut off).
+        uint32_t sm[NT][H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          uint32_t most = 0u;
+#pragma unroll
+          for (int n = 0; n < NT; n += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              sm[n + u][h] = *reinterpret_cast<const uint32_t*>(tile + C::TILE_BYTES + s_at + (n + u) * kScaleStep + h * panel);
+            most = __vimax3_u16x2(most, sm[n][h], sm[n + 1][h]);
+          }
+          grew = grew || (int)((most & 0xffffu) >> kExpShift) > top[h];
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+          float f[RH][2];
+#pragma unroll
+          for (int r = 0; r < RH; ++r) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float mn = fmaxf(m[r][i], mx[r][i]);
+              f[r][i] = mn == -INFINITY ? 1.f : ex2_approx(m[r][i] - mn);
+              m[r][i] = mn;
+            }
+            const uint64_t f2 = pair_of(f[r][0], f[r][1]);
+            l[r] = mul_pair(l[r], f2);
+#pragma unroll
+            for (int h = 0; h < H; ++h) low[r][h] = mul_pair(low[r][h], f2);
+          }
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            // Of keys that some row reads, and of finite scales alone: others (of unused
+            // slots, say) would leave no bits to the rest.
+            int now = top[h];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const int key = key0 + n * key_step + g, ex = (int)((sm[n][h] & 0xffffu) >> kExpShift);
+              if (ex < kExpMax && key >= any_lo && key <= any_hi) now = max(now, ex);
+            }
+            now = __reduce_max_sync(0xffffffffu, now);
+            const float down = now - top[h] > 126 ? 0.f : __uint_as_float((uint32_t)(127 - (now - top[h])) << 23);
+            top[h] = now;
+            lift[h] = lift_of(now);
+#pragma unroll
+            for (int r = 0; r < RH; ++r) {
+              const uint64_t f2 = pair_of(f[r][0] * down, f[r][1] * down);
+#pragma unroll
+              for (int n = 0; n < ON; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) o[r][h][n][i] = mul_pair(o[r][h][n][i], f2);
+            }
+          }
+        }
+        // P = 2^(S - m).
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+          const uint64_t ref = pair_of(m[r][0] == -INFINITY ? 0.f : -m[r][0], m[r][1] == -INFINITY ? 0.f : -m[r][1]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float2 e = parts_of(fma_pair(sc[n][r], back[r], ref));
+            sc[n][r] = pair_of(ex2_approx(e.x), ex2_approx(e.y));
+            l[r] = add_pair(l[r], sc[n][r]);
+          }
+        }
+        // O^T += codes^T (P s)^T, and P m, group by group.  EDGE: a key that the row does
+        // not read may have any scale.
+        auto values = [&](auto EDGE) {
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            float part[RH][ON][4];
+#pragma unroll
+            for (int kb = 0; kb < NT / 2; ++kb) {
+              uint32_t hi[RH][2], lo[RH][2];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int n = 2 * kb + u;
+                float s, mn;
+                scale_and_min<BF16>(sm[n][h], s, mn);
+                s *= lift[h];
+                const uint64_t s2 = pair_of(s, s), mn2 = pair_of(mn, mn);
+#pragma unroll
+                for (int r = 0; r < RH; ++r) {
+                  float2 ws = parts_of(mul_pair(sc[n][r], s2));
+                  if constexpr (decltype(EDGE)::value) {
+                    const float2 e = parts_of(sc[n][r]);
+                    float2 wm = parts_of(mul_pair(sc[n][r], mn2));
+                    if (e.x == 0.f) ws.x = wm.x = 0.f;
+                    if (e.y == 0.f) ws.y = wm.y = 0.f;
+                    low[r][h] = add_pair(low[r][h], pair_of(wm.x, wm.y));
+                  } else {
+                    low[r][h] = fma_pair(sc[n][r], mn2, low[r][h]);
+                  }
+                  if (TWO) {
+                    split_halves(ws.x, ws.y, hi[r][u], lo[r][u]);
+                    lo[r][u] = transposed(lo[r][u]);
+                  } else {
+                    hi[r][u] = pack_f16x2(ws.x, ws.y);
+                  }
+                  hi[r][u] = transposed(hi[r][u]);
+                }
+              }
+              // Two keys' words, 8 elements each, to pairs of halves of one element.
+              auto products = [&](int n, uint32_t b0, uint32_t b1) {
+                const uint32_t v[4] = {b0 & kLowCodes, b0 & kHighCodes, b1 & kLowCodes, b1 & kHighCodes};
+#pragma unroll
+                for (int r = 0; r < RH; ++r) {
+                  if (kb == 0) mma16816_first(part[r][n], v, hi[r][0], hi[r][1]);
+                  else mma16816<false>(part[r][n], v, hi[r][0], hi[r][1]);
+                  if (TWO) mma16816<false>(part[r][n], v, lo[r][0], lo[r][1]);
+                }
+              };
+              uint32_t a[2], b[2];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t far = (2 * kb + u) * kCodeStep + h * panel;
+                if constexpr (G == 64) {
+                  a[u] = *reinterpret_cast<const uint32_t*>(tile + v_first + far);
+                  b[u] = *reinterpret_cast<const uint32_t*>(tile + v_second + far);
+                } else {
+                  a[u] = *reinterpret_cast<const uint16_t*>(tile + v_first + far);
+                  b[u] = *reinterpret_cast<const uint16_t*>(tile + v_second + far);
+                }
+              }
+              const uint32_t x0 = __byte_perm(a[0], b[0], low_halves), x1 = __byte_perm(a[1], b[1], low_halves);
+              products(0, x0, x1);
+              products(1, x0 >> 8, x1 >> 8);
+              if constexpr (G == 64) {
+                const uint32_t y0 = __byte_perm(a[0], b[0], high_halves), y1 = __byte_perm(a[1], b[1], high_halves);
+                products(ON - 2, y0, y1);
+                products(ON - 1, y0 >> 8, y1 >> 8);
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < RH; ++r)
+#pragma unroll
+              for (int n = 0; n < ON; ++n) {
+                o[r][h][n][0] = add_pair(o[r][h][n][0], pair_of(part[r][n][0], part[r][n][1]));
+                o[r][h][n][1] = add_pair(o[r][h][n][1], pair_of(part[r][n][2], part[r][n][3]));
+              }
+            // (Each of the group's words and scales has gone into these products.)
+            seen |= __float_as_uint(part[0][0][0]) | __float_as_uint(part[0][ON - 1][0]);
+          }
+        };
+        if (edge) values(std::true_type{});
+        else values(std::false_type{});
+      }
+      // (Without having waited the warp gives nothing back: the stage's load may be on its way.)
+      release_after(empty + stage, seen, p.zero, lane == 0 && alive);
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (rows <= 0) continue;  // (the whole group)
+
+    // Merge the four warps' states.
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      // (of the keys of all lanes that have the row)
+      auto put_total = [&](uint64_t x, float* to) {
+        float2 f = parts_of(x);
+#pragma unroll
+        for (int by = 4; by < 32; by <<= 1) {
+          f.x += __shfl_xor_sync(0xffffffffu, f.x, by);
+          f.y += __shfl_xor_sync(0xffffffffu, f.y, by);
+        }
+        if (g == 0) to[0] = f.x, to[1] = f.y;
+      };
+      const int at = quarter * 16 + 8 * r + 2 * t4;
+      if (g == 0) st_m[at] = m[r][0], st_m[at + 1] = m[r][1];
+      put_total(l[r], st_l + at);
+#pragma unroll
+      for (int h = 0; h < H; ++h) put_total(low[r][h], st_low + h * 64 + at);
+    }
+    group_barrier<C>(grp);
+    // Row r's largest maximum (0 for none) and its sum.
+    auto state_of = [&](int r, float& ref, float& sum) {
+      float mm = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mm = fmaxf(mm, st_m[x * 16 + r]);
+      ref = mm == -INFINITY ? 0.f : mm;
+      sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sum += st_l[x * 16 + r] * ex2_approx(st_m[x * 16 + r] - ref);
+    };
+    // The warp's rows in full: powers of two taken back, minima added.
+    float full_o[H][RH][2][2 * ON];
+#pragma unroll
+    for (int r = 0; r < RH; ++r)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = 8 * r + 2 * t4 + j;
+        float ref, sum;
+        state_of(row, ref, sum);
+        const float inv = sum == 0.f ? 0.f : ex2_approx(st_m[quarter * 16 + row] - ref) / sum;  // no key: 0; a NaN sum stays one
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const float unit = 0x1p24f / lift[h], add = st_low[h * 64 + quarter * 16 + row];
+#pragma unroll
+          for (int n = 0; n < ON; ++n) {
+            const float2 even = parts_of(o[r][h][n][0]), odd = parts_of(o[r][h][n][1]);
+            full_o[h][r][j][2 * n] = ((j == 0 ? even.x : even.y) * unit + add) * inv;
+            full_o[h][r][j][2 * n + 1] = ((j == 0 ? odd.x : odd.y) * (unit * 0.0625f) + add) * inv;
+          }
+        }
+      }
+    const bool whole = w.from_start && w.to_end;
+    // Where this piece of the unit goes: the output, or the workspace (slot 0
+    // for a unit that began earlier, slot 1 for one that begins here).
+    const int64_t part_row = ((int64_t)share * 2 + (w.from_start ? 1 : 0)) * MT + 16 * grp;
+    const int r = C::GROUPS == 1 ? tid : tid & 127;
+    if (r < rows) {
+      float ref, sum;
+      state_of(r, ref, sum);
+      const float lse = sum == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(sum);
+      if (!whole) {
+        p.part_lse[part_row + r] = lse;
+      } else if (p.lse != nullptr) {
+        const int rr = row0 + r, i = rr / p.group;
+        p.lse[(int64_t)(w.head0 + rr - i * p.group) * p.total_q + w.t0 + i] = lse;
+      }
+    }
+    __syncwarp();
+    paged_q4_merge<C, BF16>(p, w, grp, rows, merge, full_o, whole, part_row);
+  }
+}
+
+}  // namespace etattn

@@ -2,6 +2,7 @@
 // and element type), implemented in attn_fwd_inst.cu.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -103,6 +104,20 @@ cudaError_t launch_pdl(void (*kern)(A...), dim3 grid, int threads, int smem, cud
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// The dynamic shared-memory opt-in is per device; set once per device.
+template <typename P>
+cudaError_t opt_in(void (*kern)(P), int smem, std::atomic<unsigned long long>& configured) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) configured.fetch_or(bit);
+  }
+  return e;
+}
+
 // Query/key norm and rotation, plain or into a paged cache (attn_rope.cu).
 // Strides in elements: token, head (pages: page, head, token); d-stride 1.
 struct RopeParams {
@@ -145,6 +160,54 @@ constexpr int kRopeBwdHeads = 2;   // heads a group of threads takes at a time
 cudaError_t launch_rope(int D, bool bf16, const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_rope_bwd(int D, bool bf16, const RopeBwdParams& p, cudaStream_t stream);
 
+// Norm, rotation and the append to a cache held in 4 bits (attn_append_q4.cu).
+struct AppendQ4Params {
+  const void *q, *k, *v;           // [T, Hq, D], [T, Hkv, D]
+  const void *q_weight, *k_weight; // [D] in the input type, or nullptr: no norm
+  const float *cos, *sin;          // [max_position, rope_dim / 2]
+  const int* positions;            // [T], or nullptr when rope_dim is 0
+  const int64_t* slots;            // [T]: page * page_size + slot; negative: no place
+  void* q_out;                     // [T, Hq, D]
+  uint8_t *k_pages, *v_pages;      // blocks of one page and head, byte strides
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, qo_st, qo_sh;
+  int64_t kp_sp, kp_sh, vp_sp, vp_sh;
+  int total_tokens, Hq, Hkv;
+  int rope_dim, interleaved, max_position;
+  float eps;
+  int num_pages, page_shift;
+  int q_blocks, kv_blocks;         // of the launch: q's rows, then k's, then v's
+  int* status;
+};
+cudaError_t launch_append_q4(int D, bool bf16, const AppendQ4Params& p, cudaStream_t stream);
+
+// The way back: 16-bit values of a cache's blocks.
+struct UnpackQ4Params {
+  const uint8_t* pages;
+  void* out;                       // [num_pages, Hkv, page_size, D]
+  int64_t p_sp, p_sh;              // bytes
+  int64_t o_sp, o_sh, o_st;        // elements
+  int num_pages, Hkv, page_shift;
+};
+cudaError_t launch_unpack_q4(int D, bool bf16, const UnpackQ4Params& p, cudaStream_t stream);
+
+// Pages handed out for a step's tokens and taken back (attn_tables.cu).
+struct TablesParams {
+  const int *amount, *seqlens;     // [S]: new tokens, or keys that stay; keys before
+  int* table;                      // [S, max_pages] (truncate only reads it)
+  int* free_pages;                 // [capacity] (extend only reads it)
+  const int* free_count;
+  int *seqlens_out, *free_count_out;
+  int *cu_seqlens, *positions;     // extend: [S + 1], [total_tokens]
+  int64_t* slots;                  // extend: [total_tokens]
+  int* first;                      // scratch [S + 1]: pages before each sequence's
+  int64_t table_stride;
+  int num_seqs, max_pages, capacity, total_tokens, page_shift;
+  int extend;
+  int fill;                        // whether the first launch fills in the pages and tokens, too
+  int* status;
+};
+cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream);
+
 // Attention over a paged cache (attn_paged_inst.cu).
 // What a CTA whose piece begins inside a unit leaves for the join.
 struct PagedShare {
@@ -184,5 +247,23 @@ ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d128_0)
 ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d128_1)
 
 #undef ETATTN_DECLARE_PAGED_LAUNCHER
+
+// The same over a cache held in 4 bits (attn_paged_q4_inst.cu): blocks of one
+// page and head, with byte strides.
+struct PagedQ4Params : PagedParams {
+  const uint8_t *k_pages, *v_pages;
+  int64_t kp_sp, kp_sh, vp_sp, vp_sh;
+};
+
+#define ETATTN_DECLARE_PAGED_Q4_LAUNCHER(name) cudaError_t name(const PagedQ4Params& p, cudaStream_t stream);
+
+ETATTN_DECLARE_PAGED_Q4_LAUNCHER(launch_paged_q4_d32_0)
+ETATTN_DECLARE_PAGED_Q4_LAUNCHER(launch_paged_q4_d32_1)
+ETATTN_DECLARE_PAGED_Q4_LAUNCHER(launch_paged_q4_d64_0)
+ETATTN_DECLARE_PAGED_Q4_LAUNCHER(launch_paged_q4_d64_1)
+ETATTN_DECLARE_PAGED_Q4_LAUNCHER(launch_paged_q4_d128_0)
+ETATTN_DECLARE_PAGED_Q4_LAUNCHER(launch_paged_q4_d128_1)
+
+#undef ETATTN_DECLARE_PAGED_Q4_LAUNCHER
 
 }  // namespace etattn

@@ -81,7 +81,8 @@ enum etattn_status {
   ETATTN_ERR_LAUNCH = 10,      /* a CUDA runtime call failed (the CUDA error is in etattn_last_cuda_error) */
   ETATTN_ERR_DEVICE = 11,      /* the device reported a failure (see etattn_read_device_status) */
   ETATTN_ERR_NO_DEVICE = 12,   /* no sm_103 device is current */
-  ETATTN_ERR_BAD_INDEX = 13,   /* a position or a page of the block table is out of range (found on the device) */
+  ETATTN_ERR_BAD_INDEX = 13,   /* a position, a slot or a page of the block table is out of range (found on the device) */
+  ETATTN_ERR_NO_PAGES = 14,    /* more pages asked for than are free, or given back than there is room for (found on the device) */
 };
 
 /*
@@ -498,6 +499,142 @@ int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max
                         size_t* workspace_bytes);
 
 /*
+ * ---- The paged cache held in 4 bits, and its pages ----
+ *
+ * Format.  A row of D elements is cut into groups of G = min(D, 64).  A group with
+ * minimum m and maximum M, both of the input type, has the scale s, the smallest
+ * number of that type with 15 s >= M - m, and the codes
+ *     c_d = round((x_d - m) / s), ties to even (0 when s is 0), 0 .. 15;
+ * it stands for the values s c_d + m, at most s/2 from x_d.  A group with an element
+ * that is not finite, or with M - m past FP32, has the scale and the minimum NaN
+ * and stands for NaN.
+ * A block holds one page and head: for every group, one after the other, the codes
+ * [page_size, G/2 bytes] (element e of the group in half e % 2 of byte e / 2, the low
+ * half first) and then [page_size, 2] scales and minima in the input type:
+ * attn_paged_q4_block_bytes(page_size, D) = page_size * (72, 36 or 20) bytes for D =
+ * 128, 64 or 32, 9/32 of the 16-bit cache (5/16 for D = 32).  k_pages and v_pages are [num_pages,
+ * Hkv] blocks with strides (page, head) in BYTES, multiples of 16; blocks do not run
+ * into one another, and those of keys and values may interleave in one buffer.
+ * page_size, block tables, lengths and offsets are those of the 16-bit cache.
+ */
+
+/* Bytes of a block (0 for invalid sizes). */
+size_t attn_paged_q4_block_bytes(int page_size, int D);
+
+/*
+ * attn_paged_append_q4: this step's keys and values into the 4-bit cache, keys (and
+ * queries) normed and rotated on the way.
+ *
+ *   q, q_out: [total_tokens, Hq, D]; Hq = 0 leaves them out (NULL)
+ *   k, v    : [total_tokens, Hkv, D]
+ *   weights, tables, eps, positions: as for attn_qk_norm_rope
+ *   slots   : DEVICE int64 [total_tokens], page * page_size + slot of the page
+ *             (attn_paged_extend makes them).  A token with a negative one has no
+ *             place: nothing of it is written, its q_out row neither.  One past
+ *             num_pages, or with a position out of range, is skipped and recorded
+ *             (ETATTN_ERR_BAD_INDEX).
+ *   strides : 16 int64 values, (t, h, d) for q, k, v, q_out in elements, then (page,
+ *             head) for k_pages and v_pages in bytes.
+ * A key is what norm and rotation leave, computed to about 2^-46 and rounded once to
+ * the input type, so that its codes are those of exact arithmetic and do not depend
+ * on the way it came.  k_pages, v_pages and q_out must not overlap anything that the
+ * call reads, or each other (ETATTN_ERR_ALIAS).  Two tokens must not be given the same slot.
+ */
+int attn_paged_append_q4(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                         const float* rope_cos, const float* rope_sin, const int32_t* positions, const int64_t* slots,
+                         void* q_out, void* k_pages, void* v_pages, int total_tokens, int Hq, int Hkv, int D, int dtype,
+                         const int64_t* strides, int page_size, int num_pages, int rope_dim, int interleaved,
+                         int max_position, float eps, void* stream);
+
+/*
+ * attn_paged_unpack_q4: the values of a cache's blocks, rounded to the input type.
+ *   pages: k_pages or v_pages;  out: logical [num_pages, Hkv, page_size, D]
+ *   strides: 6 int64 values, (page, head) of pages in bytes, (page, head, slot, d) of
+ *            out in elements.
+ * out has the 16-bit cache's layout, so that attn_fwd_paged can read it.
+ */
+int attn_paged_unpack_q4(const void* pages, void* out, int Hkv, int D, int dtype, const int64_t* strides, int page_size,
+                         int num_pages, void* stream);
+
+/*
+ * attn_fwd_paged_q4: attn_fwd_paged over the 4-bit cache, exact attention over the
+ * (unrounded) values that it stands for.
+ *   strides: 10 int64 values, (t, h, d) for q, (page, head) for k_pages and v_pages
+ *            in bytes, (t, h, d) for o.
+ * Everything else is as there, with attn_fwd_paged_q4_workspace_size and
+ * attn_fwd_paged_q4_plan for workspace and num_shares.  A page out of range is
+ * recorded, and the rows of that sequence mean nothing.  Elements of q above 2^110
+ * in size give no meaningful row.  A key whose weight is below 2^-126 may count as
+ * one that is not read.
+ */
+int attn_fwd_paged_q4(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                      const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
+                      int max_seqlen_q, int total_q, int Hq, int Hkv, int D, int dtype, const int64_t* strides,
+                      int page_size, int num_pages, int max_pages, int64_t table_stride, int causal, int window_left,
+                      int window_right, float scale, int num_shares, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* Bytes of workspace attn_fwd_paged_q4 needs (0 for one share, or for empty or
+ * invalid sizes); a unit has 8, 16 or 32 rows. */
+size_t attn_fwd_paged_q4_workspace_size(int Hq, int Hkv, int max_seqlen_q, int D, int num_shares);
+
+/* attn_fwd_paged_plan for attn_fwd_paged_q4. */
+int attn_fwd_paged_q4_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int D, int* num_shares,
+                           size_t* workspace_bytes);
+
+/*
+ * attn_paged_extend: pages for a step's new tokens, with everything the step's
+ * other calls read, made on the device from the sequences' lengths.
+ *
+ *   new_tokens : DEVICE int32 [num_seqs], n_s >= 0 new tokens of every sequence
+ *   seqlens_k  : DEVICE int32 [num_seqs], L_s keys before the step
+ *   block_table: DEVICE int32 [num_seqs, max_pages], row stride table_stride; its first
+ *                ceil(L_s / page_size) entries are held and only read, those of the
+ *                next ones up to ceil((L_s + n_s) / page_size) are written
+ *   free_pages : DEVICE int32 [capacity], a stack of free pages, free_count[0] of them;
+ *                new page i, counted sequence by sequence and column by column, is
+ *                free_pages[free_count[0] - 1 - i]
+ *   seqlens_out: int32 [num_seqs], L_s + n_s (may be seqlens_k itself)
+ *   free_count_out: int32 [1], the pages left (may be free_count itself)
+ *   cu_seqlens_q: int32 [num_seqs + 1], the sums of n_s
+ *   positions, slots: int32 and int64 [total_tokens], every new token's position and
+ *                page * page_size + slot.  total_tokens is the arrays' size, at least
+ *                the sum of n_s; behind it positions are 0 and slots -1.
+ *   workspace  : caller-owned DEVICE scratch, 256-byte aligned, at least
+ *                attn_paged_tables_workspace_size bytes, private to the call
+ * A step that does not fit is refused as a whole, and recorded: a negative length or
+ * count, a sequence past max_pages, more tokens than total_tokens, or a free count outside
+ * 0 .. capacity (ETATTN_ERR_BAD_SEQLENS), too few free pages (ETATTN_ERR_NO_PAGES).
+ * Then no page is taken, seqlens_out is seqlens_k, cu_seqlens_q is 0 throughout and every
+ * slot is -1, so that the step's other calls do nothing.  Page numbers are not
+ * looked into.  num_seqs <= 65535 and capacity <= 2^30.  Nothing but the two named pairs
+ * may overlap (ETATTN_ERR_ALIAS).
+ */
+int attn_paged_extend(const int32_t* new_tokens, const int32_t* seqlens_k, int32_t* block_table,
+                      const int32_t* free_pages, const int32_t* free_count, int32_t* seqlens_out,
+                      int32_t* free_count_out, int32_t* cu_seqlens_q, int32_t* positions, int64_t* slots, int num_seqs,
+                      int total_tokens, int page_size, int max_pages, int64_t table_stride, int capacity,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_paged_truncate: the way back.  Of sequence s the first keep[s] keys stay (0 <=
+ * keep[s] <= L_s: 0 for a request that ended, a few less than L_s where drafted tokens
+ * were rejected) and the pages past them go back: page i, counted as above from column
+ * ceil(keep[s] / page_size) to ceil(L_s / page_size) - 1, to free_pages[free_count[0] + i].
+ *   seqlens_out: keep;  free_count_out: the pages free then.
+ * Other arguments as above; the block table is only read.  A step that does not fit is refused as a
+ * whole, and recorded: lengths out of range (ETATTN_ERR_BAD_SEQLENS), or more pages
+ * than free_pages has room for (ETATTN_ERR_NO_PAGES).
+ */
+int attn_paged_truncate(const int32_t* keep, const int32_t* seqlens_k, const int32_t* block_table, int32_t* free_pages,
+                        const int32_t* free_count, int32_t* seqlens_out, int32_t* free_count_out, int num_seqs,
+                        int page_size, int max_pages, int64_t table_stride, int capacity, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attn_paged_extend and attn_paged_truncate need. */
+size_t attn_paged_tables_workspace_size(int num_seqs);
+
+/*
  * attn_fwd_host: attn_fwd for callers whose q, k, v live in HOST memory and
  * who want O (and lse) back in host memory, all in one call.
  *
@@ -566,7 +703,7 @@ int etattn_last_cuda_error(void);
 /*
  * Read the device status word of the current device that kernels set on a
  * failure they detect themselves (a bounded wait that ran out, a bad cu_seqlens
- * entry, or a position or page out of range).  Synchronises `stream`.  *out receives ETATTN_OK or the
+ * entry, a position or page out of range, or pages that ran out).  Synchronises `stream`.  *out receives ETATTN_OK or the
  * ETATTN_ERR_* code; when clear != 0 the word is reset to 0 afterwards.
  * Returns ETATTN_OK or ETATTN_ERR_LAUNCH.
  */

@@ -19,6 +19,9 @@ Modules
 ``cache``        norm and rotation of queries and keys with their gradients, the
                  append to a paged cache and attention over one (pinned in
                  ``tests/test_oracle_cache.py``).
+``quantised``    the paged cache held in 4 bits (rounding, codes, blocks) and pages
+                 handed out and taken back (pinned in
+                 ``tests/test_oracle_quantised.py``).
 
 Sources (web pages, cited by title and section):
   * "Intermediate and advanced extension" (triton-cuda-lab), workshop table row
