@@ -1327,16 +1327,18 @@ def paged_extend(new_tokens, seqlens_k, block_table, free_pages, free_count, *, 
         slots = torch.empty(total_tokens, dtype=torch.int64, device=device)
     if free_count_out is None:
         free_count_out = torch.empty_like(free_count) if S else free_count.clone()
-    if workspace is None:
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), _workspace(workspace, device)
+    elif S > 4096:  # (attn_paged_tables_workspace_size)
         ws_bytes = 4 * (S + 1)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-    else:
-        ws_bytes = _workspace(workspace, device)
+        ws = workspace.data_ptr()
     rc = (_lib or load_library()).attn_paged_extend(
         new_tokens.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
         free_count.data_ptr(), seqlens_out.data_ptr(), free_count_out.data_ptr(), cu_seqlens_q.data_ptr(),
-        positions.data_ptr(), slots.data_ptr(), S, total_tokens, page_size, width, row, free_pages.shape[0],
-        workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
+        positions.data_ptr(), slots.data_ptr(), S, total_tokens, page_size, width, row, free_pages.shape[0], ws,
+        ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
     if rc != 0:
         raise EtattnError(rc, "attn_paged_extend")
     return seqlens_out, cu_seqlens_q, positions, slots, free_count_out
@@ -1364,15 +1366,17 @@ def paged_truncate(keep, seqlens_k, block_table, free_pages, free_count, *, page
         seqlens_out = torch.empty_like(seqlens_k)
     if free_count_out is None:
         free_count_out = torch.empty_like(free_count) if S else free_count.clone()
-    if workspace is None:
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), _workspace(workspace, device)
+    elif S > 4096:  # (attn_paged_tables_workspace_size)
         ws_bytes = 4 * (S + 1)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-    else:
-        ws_bytes = _workspace(workspace, device)
+        ws = workspace.data_ptr()
     rc = (_lib or load_library()).attn_paged_truncate(
         keep.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
         seqlens_out.data_ptr(), free_count_out.data_ptr(), S, page_size, width, row, free_pages.shape[0],
-        workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
+        ws, ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
     if rc != 0:
         raise EtattnError(rc, "attn_paged_truncate")
     return seqlens_out, free_count_out

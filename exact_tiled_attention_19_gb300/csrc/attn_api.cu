@@ -1718,7 +1718,7 @@ int paged_q4_impl(const void* q, const void* k_pages, const void* v_pages, void*
 }
 
 // ---------------------------------------------------------------- pages handed out and taken back
-size_t tables_bytes(int num_seqs) { return num_seqs > 0 ? 4 * ((size_t)num_seqs + 1) : 0; }
+size_t tables_bytes(int num_seqs) { return num_seqs > kTablesNoScratch ? 4 * ((size_t)num_seqs + 1) : 0; }
 
 // Both directions.  seqlens_out and free_count_out may be seqlens_k and free_count
 // themselves; nothing else may overlap.
@@ -1730,13 +1730,13 @@ int tables_impl(const int32_t* amount, const int32_t* seqlens_k, int32_t* block_
     return ETATTN_ERR_BAD_SHAPE;
   if (int rc = pages_ok(num_seqs, page_size, capacity, max_pages, table_stride)) return rc;
   if (num_seqs == 0) return total_tokens == 0 ? ETATTN_OK : ETATTN_ERR_BAD_SHAPE;
-  if (!amount || !seqlens_k || !free_count || !seqlens_out || !free_count_out || !workspace ||
+  const size_t need = tables_bytes(num_seqs);
+  if (!amount || !seqlens_k || !free_count || !seqlens_out || !free_count_out || (need > 0 && !workspace) ||
       (max_pages > 0 && !block_table) || (capacity > 0 && !free_pages))
     return ETATTN_ERR_NULL_PTR;
   if (extend && (!cu_seqlens || (total_tokens > 0 && (!positions || !slots)))) return ETATTN_ERR_NULL_PTR;
-  const size_t need = tables_bytes(num_seqs);
   if (workspace_bytes < need) return ETATTN_ERR_BAD_SHAPE;
-  if (reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign) return ETATTN_ERR_BAD_ALIGN;
+  if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign) return ETATTN_ERR_BAD_ALIGN;
   const Flat all[] = {{amount, 4LL * num_seqs},                                                          // read
                       {seqlens_k, 4LL * num_seqs},
                       {free_count, 4},
@@ -1747,7 +1747,7 @@ int tables_impl(const int32_t* amount, const int32_t* seqlens_k, int32_t* block_
                       {extend ? cu_seqlens : nullptr, 4LL * (num_seqs + 1)},
                       {extend ? positions : nullptr, 4LL * total_tokens},
                       {extend ? slots : nullptr, 8LL * total_tokens},
-                      {workspace, (int64_t)need}};
+                      {need > 0 ? workspace : nullptr, (int64_t)need}};
   for (const Flat& a : all)
     if (!aligned4(a.ptr)) return ETATTN_ERR_BAD_ALIGN;
   if (extend && (reinterpret_cast<uintptr_t>(slots) & 7u)) return ETATTN_ERR_BAD_ALIGN;

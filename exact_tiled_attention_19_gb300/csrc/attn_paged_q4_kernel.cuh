@@ -130,33 +130,6 @@ __device__ __forceinline__ void split_halves(float x, float y, uint32_t& hi, uin
   lo = pack_f16x2(x - hx, y - hy);
 }
 
-// Pairs of FP32 numbers in one 64-bit register, for paired arithmetic.
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-  uint64_t x;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
-  return x;
-}
-__device__ __forceinline__ float2 parts_of(uint64_t x) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
-  return f;
-}
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // A scale (low half) and a minimum.
 template <bool BF16>
 __device__ __forceinline__ void scale_and_min(uint32_t w, float& s, float& m) {
@@ -347,7 +320,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     // what brings a score back.  Rows past the last hold anything, and nothing of
     // them is written.
     uint64_t qsum[RH][H], back[RH];  // of rows 2 t4 and 2 t4 + 1
-    auto of_rows = [&](float x) { return pair_of(__shfl_sync(0xffffffffu, x, 8 * t4), __shfl_sync(0xffffffffu, x, 8 * t4 + 4)); };
+    auto of_rows = [&](float x) { return packed_pair(__shfl_sync(0xffffffffu, x, 8 * t4), __shfl_sync(0xffffffffu, x, 8 * t4 + 4)); };
     uint32_t qseen = (uint32_t)(w.t0 | w.n | w.Lk | w.head0 | w.row0 | w.tile | w.tiles | w.from_start | w.to_end);
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
@@ -469,12 +442,12 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             for (int u = 0; u < 2; ++u) {
               float s, mn;
               scale_and_min<BF16>(sm[u], s, mn);
-              const uint64_t s2 = pair_of(s, s), mn2 = pair_of(mn, mn);
+              const uint64_t s2 = packed_pair(s, s), mn2 = packed_pair(mn, mn);
 #pragma unroll
               for (int r = 0; r < RH; ++r) {
                 uint64_t& x = sc[2 * kb + u][r];
                 x = h == 0 ? mul_pair(mn2, qsum[r][h]) : fma_pair(mn2, qsum[r][h], x);
-                x = fma_pair(s2, pair_of(part[r][2 * u], part[r][2 * u + 1]), x);
+                x = fma_pair(s2, packed_pair(part[r][2 * u], part[r][2 * u + 1]), x);
               }
             }
           }
@@ -488,7 +461,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
               float2 x = parts_of(sc[n][r]);
               if (key < row_lo[r][0] || key > row_hi[r][0]) x.x = -INFINITY;
               if (key < row_lo[r][1] || key > row_hi[r][1]) x.y = -INFINITY;
-              sc[n][r] = pair_of(x.x, x.y);
+              sc[n][r] = packed_pair(x.x, x.y);
             }
           }
         }
@@ -538,7 +511,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
               f[r][i] = mn == -INFINITY ? 1.f : ex2_approx(m[r][i] - mn);
               m[r][i] = mn;
             }
-            const uint64_t f2 = pair_of(f[r][0], f[r][1]);
+            const uint64_t f2 = packed_pair(f[r][0], f[r][1]);
             l[r] = mul_pair(l[r], f2);
 #pragma unroll
             for (int h = 0; h < H; ++h) low[r][h] = mul_pair(low[r][h], f2);
@@ -559,7 +532,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             lift[h] = lift_of(now);
 #pragma unroll
             for (int r = 0; r < RH; ++r) {
-              const uint64_t f2 = pair_of(f[r][0] * down, f[r][1] * down);
+              const uint64_t f2 = packed_pair(f[r][0] * down, f[r][1] * down);
 #pragma unroll
               for (int n = 0; n < ON; ++n)
 #pragma unroll
@@ -570,11 +543,11 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         // P = 2^(S - m).
 #pragma unroll
         for (int r = 0; r < RH; ++r) {
-          const uint64_t ref = pair_of(m[r][0] == -INFINITY ? 0.f : -m[r][0], m[r][1] == -INFINITY ? 0.f : -m[r][1]);
+          const uint64_t ref = packed_pair(m[r][0] == -INFINITY ? 0.f : -m[r][0], m[r][1] == -INFINITY ? 0.f : -m[r][1]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const float2 e = parts_of(fma_pair(sc[n][r], back[r], ref));
-            sc[n][r] = pair_of(ex2_approx(e.x), ex2_approx(e.y));
+            sc[n][r] = packed_pair(ex2_approx(e.x), ex2_approx(e.y));
             l[r] = add_pair(l[r], sc[n][r]);
           }
         }
@@ -593,7 +566,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
                 float s, mn;
                 scale_and_min<BF16>(sm[n][h], s, mn);
                 s *= lift[h];
-                const uint64_t s2 = pair_of(s, s), mn2 = pair_of(mn, mn);
+                const uint64_t s2 = packed_pair(s, s), mn2 = packed_pair(mn, mn);
 #pragma unroll
                 for (int r = 0; r < RH; ++r) {
                   float2 ws = parts_of(mul_pair(sc[n][r], s2));
@@ -602,7 +575,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
                     float2 wm = parts_of(mul_pair(sc[n][r], mn2));
                     if (e.x == 0.f) ws.x = wm.x = 0.f;
                     if (e.y == 0.f) ws.y = wm.y = 0.f;
-                    low[r][h] = add_pair(low[r][h], pair_of(wm.x, wm.y));
+                    low[r][h] = add_pair(low[r][h], packed_pair(wm.x, wm.y));
                   } else {
                     low[r][h] = fma_pair(sc[n][r], mn2, low[r][h]);
                   }
@@ -650,8 +623,8 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             for (int r = 0; r < RH; ++r)
 #pragma unroll
               for (int n = 0; n < ON; ++n) {
-                o[r][h][n][0] = add_pair(o[r][h][n][0], pair_of(part[r][n][0], part[r][n][1]));
-                o[r][h][n][1] = add_pair(o[r][h][n][1], pair_of(part[r][n][2], part[r][n][3]));
+                o[r][h][n][0] = add_pair(o[r][h][n][0], packed_pair(part[r][n][0], part[r][n][1]));
+                o[r][h][n][1] = add_pair(o[r][h][n][1], packed_pair(part[r][n][2], part[r][n][3]));
               }
             // (Each of the group's words and scales has gone into these products.)
             seen |= __float_as_uint(part[0][0][0]) | __float_as_uint(part[0][ON - 1][0]);

@@ -175,7 +175,7 @@ struct AppendQ4Params {
   int rope_dim, interleaved, max_position;
   float eps;
   int num_pages, page_shift;
-  int q_blocks, kv_blocks;         // of the launch: q's rows, then k's, then v's
+  int kv_blocks;                   // of the launch: as many for k as for v, the others for q
   int* status;
 };
 cudaError_t launch_append_q4(int D, bool bf16, const AppendQ4Params& p, cudaStream_t stream);
@@ -191,6 +191,7 @@ struct UnpackQ4Params {
 cudaError_t launch_unpack_q4(int D, bool bf16, const UnpackQ4Params& p, cudaStream_t stream);
 
 // Pages handed out for a step's tokens and taken back (attn_tables.cu).
+constexpr int kTablesNoScratch = 4096;  // sequences whose sums are in shared memory
 struct TablesParams {
   const int *amount, *seqlens;     // [S]: new tokens, or keys that stay; keys before
   int* table;                      // [S, max_pages] (truncate only reads it)
@@ -199,7 +200,7 @@ struct TablesParams {
   int *seqlens_out, *free_count_out;
   int *cu_seqlens, *positions;     // extend: [S + 1], [total_tokens]
   int64_t* slots;                  // extend: [total_tokens]
-  int* first;                      // scratch [S + 1]: pages before each sequence's
+  int* first;                      // scratch [S + 1] past kTablesNoScratch sequences: pages before each
   int64_t table_stride;
   int num_seqs, max_pages, capacity, total_tokens, page_shift;
   int extend;

@@ -601,7 +601,8 @@ int attn_fwd_paged_q4_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int 
  *                page * page_size + slot.  total_tokens is the arrays' size, at least
  *                the sum of n_s; behind it positions are 0 and slots -1.
  *   workspace  : caller-owned DEVICE scratch, 256-byte aligned, at least
- *                attn_paged_tables_workspace_size bytes, private to the call
+ *                attn_paged_tables_workspace_size bytes (none, and NULL, up to 4096
+ *                sequences), private to the call until its last launch has run
  * A step that does not fit is refused as a whole, and recorded: a negative length or
  * count, a sequence past max_pages, more tokens than total_tokens, or a free count outside
  * 0 .. capacity (ETATTN_ERR_BAD_SEQLENS), too few free pages (ETATTN_ERR_NO_PAGES).
@@ -631,7 +632,8 @@ int attn_paged_truncate(const int32_t* keep, const int32_t* seqlens_k, const int
                         int page_size, int max_pages, int64_t table_stride, int capacity, void* workspace,
                         size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace attn_paged_extend and attn_paged_truncate need. */
+/* Bytes of workspace attn_paged_extend and attn_paged_truncate need (0 up to 4096
+ * sequences, or past the limit). */
 size_t attn_paged_tables_workspace_size(int num_seqs);
 
 /*

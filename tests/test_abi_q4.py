@@ -156,9 +156,9 @@ def truncate_call(**kw):
 COMMON = [
     (dict(S=-1), 3), (dict(S=65536), 3), (dict(page=4), 3), (dict(page=24), 3), (dict(width=-1), 3), (dict(ts=5), 3),
     (dict(cap=-1), 3), (dict(cap=2 ** 30 + 1), 3), (dict(n=0), 1), (dict(L=0), 1), (dict(bt=0), 1), (dict(free=0), 1),
-    (dict(count=0), 1), (dict(Lo=0), 1), (dict(co=0), 1), (dict(ws=0), 1), (dict(ws=P[10] + 64), 6), (dict(wsb=20), 3),
+    (dict(count=0), 1), (dict(Lo=0), 1), (dict(co=0), 1), (dict(S=4097, ws=0), 1), (dict(S=4097, ws=P[10] + 64), 6), (dict(S=4097, wsb=16388), 3),
     (dict(L=P[1] + 2), 6), (dict(free=P[3] + 1), 6), (dict(Lo=P[0]), 7), (dict(Lo=P[1] + 4), 7), (dict(co=P[1]), 7),
-    (dict(bt=P[3] + 8), 7), (dict(free=P[0]), 7), (dict(ws=P[2]), 7), (dict(co=P[5] + 8), 7), (dict(Lo=P[4]), 7),
+    (dict(bt=P[3] + 8), 7), (dict(free=P[0]), 7), (dict(S=4097, ws=P[2]), 7), (dict(co=P[5] + 8), 7), (dict(Lo=P[4]), 7),
 ]
 
 
@@ -176,11 +176,12 @@ def test_truncate_refusals(kw, code):
 
 
 def test_tables_empty_work_and_in_place():
-    assert B.attn_paged_tables_workspace_size(5) == 24 and B.attn_paged_tables_workspace_size(0) == 0
+    size = B.attn_paged_tables_workspace_size
+    assert size(0) == size(5) == size(4096) == size(65536) == 0 and size(4097) == 4 * 4098
     assert extend_call(S=0, T=0) == 0 and truncate_call(S=0) == 0
     if NO_GPU:
         for call in (extend_call, truncate_call):
-            assert call() == call(wsb=24) == 12
+            assert call() == call(ws=0, wsb=0) == call(S=4097, wsb=16392) == 12
             assert call(Lo=P[1], co=P[4]) == 12            # in place
             assert call(width=0, ts=0, bt=0) == 12         # no pages to hold
             assert call(cap=0, free=0) == 12

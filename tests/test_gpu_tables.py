@@ -65,7 +65,7 @@ def check_extend(S, longest, page, seed, most, padding=0, in_place=False, wide=0
         assert dl.tolist() == list(lens) and count.tolist() == [len(free)]
 
 
-@pytest.mark.parametrize("S", [1, 2, 31, 33, 257, 1000, 1024, 1025, 3000, 9000])
+@pytest.mark.parametrize("S", [1, 2, 31, 33, 257, 1000, 1024, 1025, 3000, 4096, 4097, 9000])
 @pytest.mark.parametrize("page", [8, 16, 4096])
 def test_extend_decode_steps(S, page):
     check_extend(S, 3 * page, page, S + page, 1)
@@ -73,7 +73,7 @@ def test_extend_decode_steps(S, page):
 
 @pytest.mark.parametrize("S,longest,page,most", [(1, 0, 8, 1), (3, 100, 16, 700), (40, 50, 8, 60), (500, 30, 16, 90),
                                                  (1500, 64, 32, 31), (6, 9000, 64, 9000), (2000, 10, 8, 40),
-                                                 (1, 5, 16, 50000)])
+                                                 (1, 5, 16, 50000), (5000, 9, 8, 7), (4500, 12, 8, 20)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_extend_prompts(S, longest, page, most, in_place):
     check_extend(S, max(longest, most), page, S, most, in_place=in_place)
@@ -108,7 +108,8 @@ def check_truncate(S, longest, page, seed, how, in_place=False):
 
 
 @pytest.mark.parametrize("S,longest,page", [(1, 100, 8), (1, 0, 16), (50, 300, 16), (1024, 40, 8), (1025, 40, 8),
-                                            (3000, 200, 64), (20000, 9, 8)])
+                                            (3000, 200, 64), (4097, 30, 8),
+                                            (20000, 9, 8)])
 @pytest.mark.parametrize("how", ["ended", "drafts", "any"])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_truncate(S, longest, page, how, in_place):
@@ -127,7 +128,7 @@ REFUSED = {
 
 
 @pytest.mark.parametrize("what", REFUSED)
-@pytest.mark.parametrize("S", [3, 1500])
+@pytest.mark.parametrize("S", [3, 1500, 4500])
 def test_a_step_that_does_not_fit_takes_nothing(what, S):
     code, bad = REFUSED[what]
     lens, new = np.full(S, 7), np.zeros(S, int)
@@ -168,7 +169,7 @@ def test_no_sequences():
     assert [x.tolist() for x in got] == [[], [3]]
 
 
-@pytest.mark.parametrize("S", [5, 2000])
+@pytest.mark.parametrize("S", [5, 2000, 5000])
 def test_a_captured_loop_hands_out_and_takes_back(S):
     """One graph with an extension and a truncation, both in place, replayed over
     changing amounts; the same by the definition, step by step."""
