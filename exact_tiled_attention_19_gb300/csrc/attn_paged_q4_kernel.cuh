@@ -369,11 +369,19 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     release_after(uempty, qseen, p.zero, lane == 0);
     __syncwarp();
 
-    float m[RH][2];
+    // m: a reference for the row's weights, its largest score when it was last set.  Later
+    // ones may pass it by kSlack (in powers of two) before it is set again, which spares
+    // most tiles the maximum over their keys; weights are 2^kSlack at most.
+    constexpr float kSlack = 6.f;
+    float m[RH][2], bound[RH][2];
     uint64_t l[RH], low[RH][H], o[RH][H][ON][2];
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
-      m[r][0] = m[r][1] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[r][i] = -INFINITY;
+        bound[r][i] = 2 * t4 + i + 8 * r < rows ? -INFINITY : INFINITY;  // (a row that is nobody's never grows)
+      }
       l[r] = 0;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
@@ -383,12 +391,12 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
       }
     }
     // The largest exponent of a value's scale so far, per group, and the power of two
-    // that takes scales below it to 2^15.
+    // that takes scales below it, times the largest weight, to 2^15.
     constexpr int kExpShift = BF16 ? 7 : 10, kExpMax = BF16 ? 255 : 31, kExpBias = BF16 ? 127 : 15;
     constexpr int kExpMin = BF16 ? 14 : 0;  // (so that the power of two is one in FP32)
     int top[H];
     float lift[H];
-    auto lift_of = [](int x) { return __uint_as_float((uint32_t)(127 + 14 + kExpBias - x) << 23); };
+    auto lift_of = [](int x) { return __uint_as_float((uint32_t)(127 + 14 - (int)kSlack + kExpBias - x) << 23); };
 #pragma unroll
     for (int h = 0; h < H; ++h) top[h] = kExpMin, lift[h] = lift_of(kExpMin);
 
@@ -465,6 +473,8 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             }
           }
         }
+        // Whether some score passes the reference that weights are taken against by more
+        // than 2^kSlack allows.
         float mx[RH][2];
         bool grew = false;
 #pragma unroll
@@ -477,14 +487,9 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             mx[r][1] = max3(mx[r][1], x.y, y.y);
           }
           const float2 f = parts_of(back[r]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float& x = mx[r][i];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * (i == 0 ? f.x : f.y);
-            grew = grew || (2 * t4 + i + 8 * r < rows && x > m[r][i]);
-          }
+          mx[r][0] *= f.x;
+          mx[r][1] *= f.y;
+          grew = grew || mx[r][0] > bound[r][0] || mx[r][1] > bound[r][1];
         }
         // The values' scales and minima, and the largest bits of a scale (they order like
         // the numbers, none of which is negative; the minima beside them are cut off).
@@ -507,9 +512,12 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
           for (int r = 0; r < RH; ++r) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float mn = fmaxf(m[r][i], mx[r][i]);
+              float mn = fmaxf(m[r][i], mx[r][i]);
+#pragma unroll
+              for (int by = 4; by < 32; by <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, by));
               f[r][i] = mn == -INFINITY ? 1.f : ex2_approx(m[r][i] - mn);
               m[r][i] = mn;
+              bound[r][i] = 2 * t4 + i + 8 * r < rows ? mn + kSlack : INFINITY;
             }
             const uint64_t f2 = packed_pair(f[r][0], f[r][1]);
             l[r] = mul_pair(l[r], f2);
