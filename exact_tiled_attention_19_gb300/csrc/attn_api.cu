@@ -1638,8 +1638,10 @@ int unpack_q4_impl(const void* pages, void* out, int Hkv, int D, int dtype, cons
   return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
 }
 
-// Rows of a unit: 8 (three CTAs on an SM), 16 (two) or 32 (one CTA of eight warps).
-int paged_q4_row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// Rows of a unit: 8 (three CTAs on an SM) or 16 (two); more rows are several units.
+// (One of 32 rows, a CTA of eight consumer warps an SM, took 195 us for 8 x 32768 keys
+// and 8 new tokens where two of 16 take 180, heads of 64 98 against 89, of 32 79 against 72.)
+int paged_q4_row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
 int paged_q4_tile_keys(int D) { return D == 128 ? 128 : 256; }  // the kernel's PagedQ4Cfg::TK
 
 int paged_q4_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
@@ -2152,7 +2154,7 @@ int attn_fwd_paged_q4_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int 
     const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_q4_row_tile(rows), tk = paged_q4_tile_keys(D);
     const double tiles = (double)num_seqs * Hkv * (double)((rows + mt - 1) / mt) *
                          (double)std::max<int64_t>(1, (max_seqlen_k + tk - 1) / tk);
-    *num_shares = (int)std::max(1.0, std::min(tiles, (mt == 8 ? 3.0 : mt == 16 ? 2.0 : 1.0) * num_sms));
+    *num_shares = (int)std::max(1.0, std::min(tiles, (mt == 8 ? 3.0 : 2.0) * num_sms));
   }
   if (workspace_bytes) *workspace_bytes = attn_fwd_paged_q4_workspace_size(Hq, Hkv, max_seqlen_q, D, *num_shares);
   return ETATTN_OK;

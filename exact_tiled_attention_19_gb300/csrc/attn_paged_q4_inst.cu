@@ -53,8 +53,7 @@ cudaError_t launch_rows(const PagedQ4Params& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t ETATTN_PAGED_Q4_LAUNCHER(const PagedQ4Params& p, cudaStream_t stream) {
-  return p.row_tile == 8 ? launch_rows<8>(p, stream)
-                         : p.row_tile == 16 ? launch_rows<16>(p, stream) : launch_rows<32>(p, stream);
+  return p.row_tile == 8 ? launch_rows<8>(p, stream) : launch_rows<16>(p, stream);
 }
 
 }  // namespace etattn

@@ -49,8 +49,7 @@ template <int D_, int MT_>
 struct PagedQ4Cfg {
   static constexpr int D = D_, MT = MT_;
   static constexpr int UNIT_COST = 3;
-  static constexpr int GROUPS = MT / 16 > 1 ? 2 : 1;  // of four consumer warps
-  static constexpr int ROWS = MT < 16 ? 8 : 16;       // of a group
+  static constexpr int GROUPS = 1;                    // of four consumer warps
   static constexpr int G = D < 64 ? D : 64, H = D / G;
   static constexpr int TK = D == 128 ? 128 : 256;     // keys per tile
   static constexpr int WK = TK / 4, NT = WK / 8;      // per consumer warp, and in blocks of 8
@@ -59,23 +58,24 @@ struct PagedQ4Cfg {
   static constexpr int ROW_BYTES = H * PANEL;
   static constexpr int TILE_BYTES = TK * ROW_BYTES;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V: 18 KB, or 10 KB for D = 32
-  // Three CTAs of 8 rows share an SM, two of 16, or one of 32.
-  static constexpr int CTAS = MT == 8 ? 3 : MT == 16 ? 2 : 1;
-  static constexpr int BUDGET = MT == 8 ? 76800 : MT == 16 ? 115712 : 232448;
-  static constexpr int MERGE_BYTES = 4 * ROWS * G * 4;  // a group's: four warps' rows, one group of elements
+  // Three CTAs of 8 rows share an SM, or two of 16.
+  static_assert(MT == 8 || MT == 16, "");
+  static constexpr int CTAS = MT == 8 ? 3 : 2;
+  static constexpr int BUDGET = MT == 8 ? 76800 : 115712;
+  static constexpr int MERGE_BYTES = 4 * MT * G * 4;  // four warps' rows, one group of elements
   static constexpr int Q_PITCH = 2 * D + 16;            // padded: no bank conflicts
-  static constexpr int STATE_BYTES = (2 + H) * 4 * 16 * 4;  // a group's m, l and minima's terms: 4 warps x 16 each
-  static constexpr int FIXED = GROUPS * MERGE_BYTES + MT * Q_PITCH + GROUPS * STATE_BYTES + 48;
+  static constexpr int STATE_BYTES = (2 + H) * 4 * 16 * 4;  // m, l and minima's terms: 4 warps x 16 each
+  static constexpr int FIXED = MERGE_BYTES + MT * Q_PITCH + STATE_BYTES + 48;
   static constexpr int FIT = (BUDGET - FIXED - 192) / STAGE_BYTES;
   static constexpr int STAGES = FIT < 11 ? FIT : 11;
   static constexpr int OFF_MERGE = STAGES * STAGE_BYTES;
-  static constexpr int OFF_Q = OFF_MERGE + GROUPS * MERGE_BYTES;
+  static constexpr int OFF_Q = OFF_MERGE + MERGE_BYTES;
   static constexpr int OFF_STATE = OFF_Q + MT * Q_PITCH;
-  static constexpr int OFF_UNIT = OFF_STATE + GROUPS * STATE_BYTES;
+  static constexpr int OFF_UNIT = OFF_STATE + STATE_BYTES;
   static constexpr int OFF_BARS = OFF_UNIT + 48;
   static constexpr int SMEM_BYTES = OFF_BARS + 2 * (STAGES + 1) * 8;
   static_assert(STAGES >= 3 && SMEM_BYTES <= BUDGET, "");
-  static constexpr int CONSUMER_WARPS = 4 * GROUPS, THREADS = 32 * (CONSUMER_WARPS + 1);
+  static constexpr int CONSUMER_WARPS = 4, THREADS = 32 * (CONSUMER_WARPS + 1);
 };
 
 // A box: a block of the cache (one page and head: for every group the codes of its
@@ -123,6 +123,15 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// d = A B + c
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                              const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
 // x, y as hi + lo, two pairs of halves: hi by cutting bits off, lo the rest, rounded.
 __device__ __forceinline__ void split_halves(float x, float y, uint32_t& hi, uint32_t& lo) {
   const float hx = __uint_as_float(__float_as_uint(x) & 0xffffe000u), hy = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
@@ -146,16 +155,16 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 
 constexpr uint32_t kLowCodes = 0x000f000fu, kHighCodes = 0x00f000f0u;
 
-// Adds up a group's four warps' scaled rows, one group of elements at a time, and
+// Adds up the four warps' scaled rows, one group of elements at a time, and
 // writes them: the output, or the unit's partial rows.  A lane holds elements
 // G/8 g .. of rows 2 t4 and 2 t4 + 1 (and of those 8 further down).
 template <class C, bool BF16>
-__device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const PagedUnit& w, int grp, int rows, float* merge,
-                                               const float (&o)[C::H][C::ROWS / 8][2][C::G / 8], bool whole,
+__device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const PagedUnit& w, int rows, float* merge,
+                                               const float (&o)[C::H][C::MT / 8][2][C::G / 8], bool whole,
                                                int64_t part_row) {
   constexpr int G = C::G, RUN = G / 8;
-  const int tid = C::GROUPS == 1 ? threadIdx.x : threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t4 = lane & 3, row0 = w.row0 + 16 * grp;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3, row0 = w.row0;
   // Where a row's four elements x4 lie: eight lanes that store together hit eight
   // different quarters of the banks.
   auto place = [](int r, int x4) {
@@ -164,17 +173,17 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
 #pragma unroll
   for (int h = 0; h < C::H; ++h) {
 #pragma unroll
-    for (int hr = 0; hr < C::ROWS / 8; ++hr)
+    for (int hr = 0; hr < C::MT / 8; ++hr)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = 8 * hr + 2 * t4 + j;
-        float* dst = merge + (warp * C::ROWS + r) * G;
+        float* dst = merge + (warp * C::MT + r) * G;
         const float(&v)[RUN] = o[h][hr][j];
 #pragma unroll
         for (int i = 0; i < RUN; i += 4)
           *reinterpret_cast<float4*>(dst + place(r, (g * RUN + i) / 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
-    group_barrier<C>(grp);
+    group_barrier<C>(0);
     for (int x = tid; x < rows * (G / 8); x += 128) {
       const int r = x / (G / 8), c = (x % (G / 8)) * 8;
       float v[8];
@@ -182,7 +191,7 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
       for (int i = 0; i < 8; ++i) v[i] = 0.f;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const float* src = merge + (y * C::ROWS + r) * G;
+        const float* src = merge + (y * C::MT + r) * G;
         const float4 u0 = *reinterpret_cast<const float4*>(src + place(r, c / 4));
         const float4 u1 = *reinterpret_cast<const float4*>(src + place(r, c / 4 + 1));
         v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
@@ -205,7 +214,7 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
     }
     // The next group, or the next unit's (whose state the warps write first, and
     // meet, before they come here again).
-    if (h + 1 < C::H) group_barrier<C>(grp);
+    if (h + 1 < C::H) group_barrier<C>(0);
   }
 }
 
@@ -213,7 +222,7 @@ template <int D, int MT, bool BF16, bool SPREAD>
 __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>::CTAS)
     attn_paged_q4_kernel(const __grid_constant__ PagedQ4Params p) {
   using C = PagedQ4Cfg<D, MT>;
-  constexpr int G = C::G, H = C::H, NT = C::NT, RH = C::ROWS / 8;
+  constexpr int G = C::G, H = C::H, NT = C::NT, RH = MT / 8;
   constexpr int KW = G / 32, ON = G / 16;      // words of a key's group that a lane reads; blocks of 16 elements
   constexpr bool TWO = !BF16;                  // weights in two parts
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -241,13 +250,11 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
   }
 
   // ------------------------------------------------ consumers
-  // The warp's rows, and its quarter of a tile's keys.
-  const int grp = C::GROUPS == 1 ? 0 : warp >> 2, quarter = C::GROUPS == 1 ? warp : warp & 3;
-  const int g = lane >> 2, t4 = lane & 3;
-  float* st_m = reinterpret_cast<float*>(smem + C::OFF_STATE + grp * C::STATE_BYTES);
+  const int quarter = warp, g = lane >> 2, t4 = lane & 3;
+  float* st_m = reinterpret_cast<float*>(smem + C::OFF_STATE);
   float* st_l = st_m + 64;
   float* st_low = st_l + 64;
-  float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE + grp * C::MERGE_BYTES);
+  float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
   // Q's operands, which the warp reads again for every tile (the registers are needed
   // for the values): where the rows are merged, which happens after the last tile.
   uint4* q_ops = reinterpret_cast<uint4*>(merge) + quarter * (H * KW * RH * 32) + lane;
@@ -286,20 +293,19 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
   int stage = 0;
   bool alive = true;
   while (true) {
-    // A wait that ran out in one warp ends its group, here, where none of them
-    // waits in a barrier for another.
+    // A wait that ran out in one warp ends them all, here, where none of them waits
+    // in a barrier for another.
     alive = alive && mbar_wait(ufull, uphase, p.status);
     uphase ^= 1;
-    if (group_any<C>(grp, !alive)) return;
+    if (group_any<C>(0, !alive)) return;
     __syncwarp();
     const PagedUnit w = *reinterpret_cast<const PagedUnit*>(smem + C::OFF_UNIT);
     if (w.tiles == 0) return;
-    const int row0 = w.row0 + 16 * grp;
-    const int rows = min(C::ROWS, w.n * p.group - row0);  // none (or fewer) for the second group of a short unit
+    const int row0 = w.row0, rows = min(MT, w.n * p.group - row0);
     const int delta = w.Lk - w.n;
-    // The tokens of the group's rows and the key ranges of rows 2 t4 and 2 t4 + 1 (and
+    // The tokens of the rows and the key ranges of rows 2 t4 and 2 t4 + 1 (and
     // of those 8 further down).
-    const int tok_first = row0 / p.group, tok_last = (row0 + max(rows, 1) - 1) / p.group;
+    const int tok_first = row0 / p.group, tok_last = (row0 + rows - 1) / p.group;
     int row_lo[RH][2], row_hi[RH][2];
 #pragma unroll
     for (int r = 0; r < RH; ++r)
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         row_lo[r][i] = max(0, c - p.win_left);
         row_hi[r][i] = (int)min((int64_t)w.Lk - 1, (int64_t)c + p.win_right);
       }
-    // Keys in [in_lo, in_hi] are read by every row of the group, those outside
+    // Keys in [in_lo, in_hi] are read by every row, those outside
     // [any_lo, any_hi] by none.
     const int in_lo = max(0, tok_last + delta - p.win_left);
     const int in_hi = (int)min((int64_t)w.Lk - 1, (int64_t)tok_first + delta + p.win_right);
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     for (int r = 0; r < RH; ++r) {
       float x[H][KW][8];
       float big = 0.f;
-      const uint8_t* src = smem + C::OFF_Q + (16 * grp + g + 8 * r) * C::Q_PITCH + t4 * (G / 2);
+      const uint8_t* src = smem + C::OFF_Q + (g + 8 * r) * C::Q_PITCH + t4 * (G / 2);
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -373,15 +379,12 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     // ones may pass it by kSlack (in powers of two) before it is set again, which spares
     // most tiles the maximum over their keys; weights are 2^kSlack at most.
     constexpr float kSlack = 6.f;
-    float m[RH][2], bound[RH][2];
+    float m[RH][2];
     uint64_t l[RH], low[RH][H], o[RH][H][ON][2];
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        m[r][i] = -INFINITY;
-        bound[r][i] = 2 * t4 + i + 8 * r < rows ? -INFINITY : INFINITY;  // (a row that is nobody's never grows)
-      }
+      for (int i = 0; i < 2; ++i) m[r][i] = 2 * t4 + i + 8 * r < rows ? -INFINITY : INFINITY;  // (a row that is nobody's never grows)
       l[r] = 0;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
@@ -394,18 +397,19 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     // that takes scales below it, times the largest weight, to 2^15.
     constexpr int kExpShift = BF16 ? 7 : 10, kExpMax = BF16 ? 255 : 31, kExpBias = BF16 ? 127 : 15;
     constexpr int kExpMin = BF16 ? 14 : 0;  // (so that the power of two is one in FP32)
-    int top[H];
+    constexpr int kLift = 127 + 14 - (int)kSlack + kExpBias;
     float lift[H];
-    auto lift_of = [](int x) { return __uint_as_float((uint32_t)(127 + 14 - (int)kSlack + kExpBias - x) << 23); };
+    auto lift_of = [](int x) { return __uint_as_float((uint32_t)(kLift - x) << 23); };
+    auto top_of = [](float f) { return kLift - (int)(__float_as_uint(f) >> 23); };
 #pragma unroll
-    for (int h = 0; h < H; ++h) top[h] = kExpMin, lift[h] = lift_of(kExpMin);
+    for (int h = 0; h < H; ++h) lift[h] = lift_of(kExpMin);
 
     for (int x = 0; x < w.tiles; ++x) {
       const int tile0 = (w.tile + x) * C::TK, key0 = tile0 + key_at;
       alive = alive && mbar_wait(full + stage, phase, p.status);
       alive = __all_sync(0xffffffffu, alive);  // and the lanes, which leave the wait one by one, are together
-      uint32_t seen = 0;  // of everything read of V (what is read of K goes into the maxima)
-      if (alive && rows > 0) {
+      uint32_t seen = 0;  // of products that everything read of V has gone into (what is read of K goes into the maxima)
+      if (alive) {
         const uint8_t* tile = smem + stage * C::STAGE_BYTES;
         const bool edge = tile0 < in_lo || tile0 + C::TK - 1 > in_hi;
         // Scores of the warp's keys, in units of 1 / back, 16 keys at a time: of key g of
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
           const float2 f = parts_of(back[r]);
           mx[r][0] *= f.x;
           mx[r][1] *= f.y;
-          grew = grew || mx[r][0] > bound[r][0] || mx[r][1] > bound[r][1];
+          grew = grew || mx[r][0] > m[r][0] + kSlack || mx[r][1] > m[r][1] + kSlack;
         }
         // The values' scales and minima, and the largest bits of a scale (they order like
         // the numbers, none of which is negative; the minima beside them are cut off).
@@ -504,7 +508,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
               sm[n + u][h] = *reinterpret_cast<const uint32_t*>(tile + C::TILE_BYTES + s_at + (n + u) * kScaleStep + h * panel);
             most = __vimax3_u16x2(most, sm[n][h], sm[n + 1][h]);
           }
-          grew = grew || (int)((most & 0xffffu) >> kExpShift) > top[h];
+          grew = grew || (int)((most & 0xffffu) >> kExpShift) > top_of(lift[h]);
         }
         if (__any_sync(0xffffffffu, grew)) {
           float f[RH][2];
@@ -517,7 +521,6 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
               for (int by = 4; by < 32; by <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, by));
               f[r][i] = mn == -INFINITY ? 1.f : ex2_approx(m[r][i] - mn);
               m[r][i] = mn;
-              bound[r][i] = 2 * t4 + i + 8 * r < rows ? mn + kSlack : INFINITY;
             }
             const uint64_t f2 = packed_pair(f[r][0], f[r][1]);
             l[r] = mul_pair(l[r], f2);
@@ -528,15 +531,15 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
           for (int h = 0; h < H; ++h) {
             // Of keys that some row reads, and of finite scales alone: others (of unused
             // slots, say) would leave no bits to the rest.
-            int now = top[h];
+            const int top = top_of(lift[h]);
+            int now = top;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const int key = key0 + n * key_step + g, ex = (int)((sm[n][h] & 0xffffu) >> kExpShift);
               if (ex < kExpMax && key >= any_lo && key <= any_hi) now = max(now, ex);
             }
             now = __reduce_max_sync(0xffffffffu, now);
-            const float down = now - top[h] > 126 ? 0.f : __uint_as_float((uint32_t)(127 - (now - top[h])) << 23);
-            top[h] = now;
+            const float down = now - top > 126 ? 0.f : __uint_as_float((uint32_t)(127 - (now - top)) << 23);
             lift[h] = lift_of(now);
 #pragma unroll
             for (int r = 0; r < RH; ++r) {
@@ -564,46 +567,57 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         auto values = [&](auto EDGE) {
 #pragma unroll
           for (int h = 0; h < H; ++h) {
+            uint32_t hi[RH][NT], lo[RH][NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float s, mn;
+              scale_and_min<BF16>(sm[n][h], s, mn);
+              mn = fmaf(s, 8.f, mn);  // what code 8 stands for
+              s *= lift[h];
+              const uint64_t s2 = packed_pair(s, s), mn2 = packed_pair(mn, mn);
+#pragma unroll
+              for (int r = 0; r < RH; ++r) {
+                float2 ws = parts_of(mul_pair(sc[n][r], s2));
+                if constexpr (decltype(EDGE)::value) {
+                  const float2 e = parts_of(sc[n][r]);
+                  float2 wm = parts_of(mul_pair(sc[n][r], mn2));
+                  if (e.x == 0.f) ws.x = wm.x = 0.f;
+                  if (e.y == 0.f) ws.y = wm.y = 0.f;
+                  low[r][h] = add_pair(low[r][h], packed_pair(wm.x, wm.y));
+                } else {
+                  low[r][h] = fma_pair(sc[n][r], mn2, low[r][h]);
+                }
+                if (TWO) {
+                  split_halves(ws.x, ws.y, hi[r][n], lo[r][n]);
+                  lo[r][n] = transposed(lo[r][n]);
+                } else {
+                  hi[r][n] = pack_f16x2(ws.x, ws.y);
+                }
+                hi[r][n] = transposed(hi[r][n]);
+              }
+            }
+            // The sums start from -8 times the weights, which is the same for all elements.
+            float base[RH][4];
+            constexpr uint32_t kMinusEights[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
+#pragma unroll
+            for (int kb = 0; kb < NT / 2; ++kb)
+#pragma unroll
+              for (int r = 0; r < RH; ++r) {
+                if (kb == 0) mma16816_first(base[r], kMinusEights, hi[r][0], hi[r][1]);
+                else mma16816<false>(base[r], kMinusEights, hi[r][2 * kb], hi[r][2 * kb + 1]);
+                if (TWO) mma16816<false>(base[r], kMinusEights, lo[r][2 * kb], lo[r][2 * kb + 1]);
+              }
             float part[RH][ON][4];
 #pragma unroll
             for (int kb = 0; kb < NT / 2; ++kb) {
-              uint32_t hi[RH][2], lo[RH][2];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int n = 2 * kb + u;
-                float s, mn;
-                scale_and_min<BF16>(sm[n][h], s, mn);
-                s *= lift[h];
-                const uint64_t s2 = packed_pair(s, s), mn2 = packed_pair(mn, mn);
-#pragma unroll
-                for (int r = 0; r < RH; ++r) {
-                  float2 ws = parts_of(mul_pair(sc[n][r], s2));
-                  if constexpr (decltype(EDGE)::value) {
-                    const float2 e = parts_of(sc[n][r]);
-                    float2 wm = parts_of(mul_pair(sc[n][r], mn2));
-                    if (e.x == 0.f) ws.x = wm.x = 0.f;
-                    if (e.y == 0.f) ws.y = wm.y = 0.f;
-                    low[r][h] = add_pair(low[r][h], packed_pair(wm.x, wm.y));
-                  } else {
-                    low[r][h] = fma_pair(sc[n][r], mn2, low[r][h]);
-                  }
-                  if (TWO) {
-                    split_halves(ws.x, ws.y, hi[r][u], lo[r][u]);
-                    lo[r][u] = transposed(lo[r][u]);
-                  } else {
-                    hi[r][u] = pack_f16x2(ws.x, ws.y);
-                  }
-                  hi[r][u] = transposed(hi[r][u]);
-                }
-              }
               // Two keys' words, 8 elements each, to pairs of halves of one element.
               auto products = [&](int n, uint32_t b0, uint32_t b1) {
                 const uint32_t v[4] = {b0 & kLowCodes, b0 & kHighCodes, b1 & kLowCodes, b1 & kHighCodes};
 #pragma unroll
                 for (int r = 0; r < RH; ++r) {
-                  if (kb == 0) mma16816_first(part[r][n], v, hi[r][0], hi[r][1]);
-                  else mma16816<false>(part[r][n], v, hi[r][0], hi[r][1]);
-                  if (TWO) mma16816<false>(part[r][n], v, lo[r][0], lo[r][1]);
+                  if (kb == 0) mma16816_from(part[r][n], v, hi[r][0], hi[r][1], base[r]);
+                  else mma16816<false>(part[r][n], v, hi[r][2 * kb], hi[r][2 * kb + 1]);
+                  if (TWO) mma16816<false>(part[r][n], v, lo[r][2 * kb], lo[r][2 * kb + 1]);
                 }
               };
               uint32_t a[2], b[2];
@@ -634,7 +648,6 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
                 o[r][h][n][0] = add_pair(o[r][h][n][0], packed_pair(part[r][n][0], part[r][n][1]));
                 o[r][h][n][1] = add_pair(o[r][h][n][1], packed_pair(part[r][n][2], part[r][n][3]));
               }
-            // (Each of the group's words and scales has gone into these products.)
             seen |= __float_as_uint(part[0][0][0]) | __float_as_uint(part[0][ON - 1][0]);
           }
         };
@@ -648,7 +661,6 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         phase ^= 1;
       }
     }
-    if (rows <= 0) continue;  // (the whole group)
 
     // Merge the four warps' states.
 #pragma unroll
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
 #pragma unroll
       for (int h = 0; h < H; ++h) put_total(low[r][h], st_low + h * 64 + at);
     }
-    group_barrier<C>(grp);
+    group_barrier<C>(0);
     // Row r's largest maximum (0 for none) and its sum.
     auto state_of = [&](int r, float& ref, float& sum) {
       float mm = -INFINITY;
@@ -704,9 +716,9 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     const bool whole = w.from_start && w.to_end;
     // Where this piece of the unit goes: the output, or the workspace (slot 0
     // for a unit that began earlier, slot 1 for one that begins here).
-    const int64_t part_row = ((int64_t)share * 2 + (w.from_start ? 1 : 0)) * MT + 16 * grp;
-    const int r = C::GROUPS == 1 ? tid : tid & 127;
-    if (r < rows) {
+    const int64_t part_row = ((int64_t)share * 2 + (w.from_start ? 1 : 0)) * MT;
+    if (tid < rows) {
+      const int r = tid;
       float ref, sum;
       state_of(r, ref, sum);
       const float lse = sum == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(sum);
@@ -718,7 +730,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
       }
     }
     __syncwarp();
-    paged_q4_merge<C, BF16>(p, w, grp, rows, merge, full_o, whole, part_row);
+    paged_q4_merge<C, BF16>(p, w, rows, merge, full_o, whole, part_row);
   }
 }
 

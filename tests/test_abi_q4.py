@@ -124,7 +124,7 @@ def test_paged_refusals(kw, code):
 def test_paged_workspace_plan_and_empty_work():
     size = B.attn_fwd_paged_q4_workspace_size
     assert size(4, 2, 1, 64, 1) == 0 and size(4, 3, 1, 64, 8) == 0 and size(4, 2, 0, 64, 8) == 0
-    assert 0 < size(32, 8, 1, 128, 456) < size(32, 8, 4, 128, 456) < size(32, 8, 8, 128, 456)
+    assert 0 < size(32, 8, 1, 128, 456) < size(32, 8, 4, 128, 456) == size(32, 8, 8, 128, 456)
     assert paged_call(wsb=size(4, 2, 2, 64, 7) - 1) == 3
     assert paged_call(T=0, n=0) == 0 and paged_call(S=0, T=0, n=0) == 0
     assert B.attn_fwd_paged_q4_plan(1, 4, 3, 1, 100, 64)[0] == 4
