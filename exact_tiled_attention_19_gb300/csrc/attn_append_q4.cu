@@ -6,7 +6,8 @@
 // groups of G = min(D, 64).  With a group's minimum m and maximum M,
 //     s = the smallest number of the input type with 15 s >= M - m,
 //     c_d = round((x_d - m) / s), ties to even, 0 where s is 0;
-// the cache stands for s c_d + m, at most s / 2 from x_d.  A group with an element that is
+// the cache stands for s c_d + m, at most s / 2 from x_d.  (Where 15 s + m would pass the
+// type's largest number, s is the next one below.)  A group with an element that is
 // not finite, or whose spread passes FP32, gets the scale NaN and reads as NaN.
 //
 // Precision.  A code jumps where (x - m) / s passes a half, and a key's rounding to
@@ -122,6 +123,8 @@ __device__ __forceinline__ Quant quant_of(uint32_t extreme) {
   uint32_t b = (BF16 ? pack_bf16x2(span * (1.f / 15.f), 0.f) : pack_f16x2(span * (1.f / 15.f), 0.f)) & 0xffffu;
   if (15.f * from16<BF16>(b) < span) ++b;
   else if (b > 0 && 15.f * from16<BF16>(b - 1) >= span) --b;
+  // Code 15 must not stand for more than the type holds.
+  if (fmaf(15.f, from16<BF16>(b), mn) > (BF16 ? 0x1.fep127f : 65504.f)) --b;
   Quant z;
   z.word = __byte_perm(b, extreme, 0x5410);
   z.min = mn;

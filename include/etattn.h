@@ -505,9 +505,10 @@ int attn_fwd_paged_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max
  * minimum m and maximum M, both of the input type, has the scale s, the smallest
  * number of that type with 15 s >= M - m, and the codes
  *     c_d = round((x_d - m) / s), ties to even (0 when s is 0), 0 .. 15;
- * it stands for the values s c_d + m, at most s/2 from x_d.  A group with an element
- * that is not finite, or with M - m past FP32, has the scale and the minimum NaN
- * and stands for NaN.
+ * it stands for the values s c_d + m, at most s/2 from x_d.  (x_d - m and the quotient
+ * are rounded to FP32 on the way.  Where 15 s + m would pass the type's largest number,
+ * s is the next one below.)  A group with an element that is not finite, or with M - m
+ * past FP32, has the scale and the minimum NaN and stands for NaN.
  * A block holds one page and head: for every group, one after the other, the codes
  * [page_size, G/2 bytes] (element e of the group in half e % 2 of byte e / 2, the low
  * half first) and then [page_size, 2] scales and minima in the input type:

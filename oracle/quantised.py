@@ -55,8 +55,9 @@ def quantise(x, dtype):
         low = np.where(bad, 0.0, low)
         s = rounded(span / 15, dtype)
         s = np.where(15 * s < span, s + step(s, dtype), s)
-        # (the next number down may do, too, when span / 15 was rounded up to it)
-        assert np.all((s == 0) | (15 * (s - step(s * (1 - 2.0 ** -20), dtype)) < span))
+        below = s - step(s * (1 - 2.0 ** -20), dtype)
+        assert np.all((s == 0) | (15 * below < span))  # the smallest that does
+        s = np.where(15 * s + low > _MAX[dtype], below, s)
         c = np.where(s[..., None] > 0, np.round((np.where(bad[..., None], 0.0, x) - low[..., None]) /
                                                 np.where(s > 0, s, 1.0)[..., None]), 0.0)
     return c.astype(np.uint8), np.where(bad, np.nan, s), np.where(bad, np.nan, low)

@@ -205,6 +205,25 @@ def test_bad_slots_and_positions_are_skipped_and_recorded():
         assert binding.etattn_read_device_status(clear=True) == 13
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [32, 128])
+def test_the_types_largest_numbers_read_as_finite(dt, D):
+    big = torch.finfo(DT[dt]).max
+    x = torch.rand(8, 2, D, dtype=torch.float64)  # from 0 to the largest number: spreads within FP32
+    x[:, :, 1::9] = 1.0
+    x[0], x[1, :, 1:], x[2] = 1.0, 0.0, -1.0
+    x[3] -= 1.0
+    if dt == "f16":
+        x[4] = x[4] * 2 - 1
+    x = (x * big).to(DT[dt]).cuda()
+    k_pages, v_pages = binding.q4_pages(1, 2, 8, D)
+    binding.paged_append_q4(x, x, k_pages, v_pages, torch.arange(8).cuda())
+    for pages in (k_pages, v_pages):
+        got = f64(binding.paged_unpack_q4(pages, D, DT[dt])[0]).transpose(1, 0, 2)
+        assert np.array_equal(got, quantised.rounded(quantised.stored(f64(x), code_of(DT[dt])), code_of(DT[dt])))
+        assert np.all(np.isfinite(got)) and np.abs(got - f64(x)).max() <= 0.05 * big * (2 if dt == "f16" else 1)
+
+
 @pytest.mark.parametrize("D", [32, 64, 128])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("page,layout", [(8, "pair"), (16, "heads"), (256, "apart")])

@@ -77,3 +77,15 @@ def test_pages_by_hand():
     assert slots == [39, 24, 16, 12, 13, 14, 15, 8, 9, -1, -1]
     lens, free = Q.truncate([4, 0, 6], lens, t, left, 4)
     assert lens == [4, 0, 6] and free == [1, 6, 7, 5, 4]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_code_15_stands_for_no_more_than_the_type_holds(dt):
+    big = float(torch.finfo(DT[dt]).max)
+    for low in (-big if dt == "f16" else -big / 512, 0.0, big / 2):  # (spreads within FP32)
+        low = float(Q.rounded(low, dt))
+        x = np.full((1, 64), low)
+        x[0, ::3], x[0, 1] = big, Q.rounded(low / 2 + big / 4, dt)
+        c, s, m = Q.quantise(x, dt)
+        v = Q.values(c, s, m)
+        assert c.max() == 15 and np.all(np.abs(v) <= big) and np.all(np.abs(v - x) <= s[..., None] * 0.6)
