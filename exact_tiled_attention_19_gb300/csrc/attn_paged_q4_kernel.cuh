@@ -36,6 +36,13 @@
 // running sum would drift: a tile's products with V start from 0 and are added to the
 // running sums in FP32 (without it one sequence of 524288 keys was 1.6 times as far
 // from 64 bits as a rounding).
+//
+// Up to 4 rows of 128 elements (PAIRED; a decode step of four query heads a KV head).
+// The right operands' columns 4 .. 7 are the same rows again, for the second group of
+// elements: a lane applies the scales of one group, not of both.  Q's operands are 0
+// in the other group's columns, so that one accumulator takes the products of both groups
+// side by side, and the two parts of a score are in neighbouring lanes; the weights'
+// likewise.
 #pragma once
 
 #include <cstdint>
@@ -58,11 +65,13 @@ struct PagedQ4Cfg {
   static constexpr int ROW_BYTES = H * PANEL;
   static constexpr int TILE_BYTES = TK * ROW_BYTES;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V: 18 KB, or 10 KB for D = 32
-  // Three CTAs of 8 rows share an SM, or two of 16.
-  static_assert(MT == 8 || MT == 16, "");
-  static constexpr int CTAS = MT == 8 ? 3 : 2;
-  static constexpr int BUDGET = MT == 8 ? 76800 : 115712;
-  static constexpr int MERGE_BYTES = 4 * MT * G * 4;  // four warps' rows, one group of elements
+  // Three CTAs of up to 8 rows share an SM, or two of 16.
+  static constexpr bool PAIRED = MT == 4;
+  static_assert(MT == 8 || MT == 16 || (PAIRED && H == 2), "");
+  static constexpr int CTAS = MT <= 8 ? 3 : 2;
+  static constexpr int BUDGET = MT <= 8 ? 76800 : 115712;
+  static constexpr int COLS = PAIRED ? D : G;            // elements that are merged at a time
+  static constexpr int MERGE_BYTES = 4 * MT * COLS * 4;  // four warps' rows
   static constexpr int Q_PITCH = 2 * D + 16;            // padded: no bank conflicts
   static constexpr int STATE_BYTES = (2 + H) * 4 * 16 * 4;  // m, l and minima's terms: 4 warps x 16 each
   static constexpr int FIXED = MERGE_BYTES + MT * Q_PITCH + STATE_BYTES + 48;
@@ -155,43 +164,44 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 
 constexpr uint32_t kLowCodes = 0x000f000fu, kHighCodes = 0x00f000f0u;
 
-// Adds up the four warps' scaled rows, one group of elements at a time, and
-// writes them: the output, or the unit's partial rows.  A lane holds elements
-// G/8 g .. of rows 2 t4 and 2 t4 + 1 (and of those 8 further down).
+// Adds up the four warps' scaled rows, COLS elements at a time, and writes them: the
+// output, or the unit's partial rows.  A lane holds elements G/8 g .. of two rows (and
+// of those 8 further down) of every group, or of its own.
 template <class C, bool BF16>
 __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const PagedUnit& w, int rows, float* merge,
-                                               const float (&o)[C::H][C::MT / 8][2][C::G / 8], bool whole,
-                                               int64_t part_row) {
-  constexpr int G = C::G, RUN = G / 8;
+                                               const float (&o)[C::PAIRED ? 1 : C::H][(C::MT + 7) / 8][2][C::G / 8],
+                                               bool whole, int64_t part_row) {
+  constexpr int G = C::G, RUN = G / 8, COLS = C::COLS;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3, row0 = w.row0;
   // Where a row's four elements x4 lie: eight lanes that store together hit eight
   // different quarters of the banks.
   auto place = [](int r, int x4) {
+    if (C::PAIRED) return (x4 ^ ((r >> 1) & 1) ^ ((x4 >> 2) & 4)) * 4;
     return (x4 ^ (G == 64 ? (r & 4) | ((r >> 1) & 1) : (r & 6))) * 4;
   };
 #pragma unroll
-  for (int h = 0; h < C::H; ++h) {
+  for (int h = 0; h < C::D / COLS; ++h) {
 #pragma unroll
-    for (int hr = 0; hr < C::MT / 8; ++hr)
+    for (int hr = 0; hr < (C::MT + 7) / 8; ++hr)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int r = 8 * hr + 2 * t4 + j;
-        float* dst = merge + (warp * C::MT + r) * G;
+        const int r = C::PAIRED ? 2 * (t4 & 1) + j : 8 * hr + 2 * t4 + j, at = (C::PAIRED ? (t4 >> 1) * G : 0) + g * RUN;
+        float* dst = merge + (warp * C::MT + r) * COLS;
         const float(&v)[RUN] = o[h][hr][j];
 #pragma unroll
         for (int i = 0; i < RUN; i += 4)
-          *reinterpret_cast<float4*>(dst + place(r, (g * RUN + i) / 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          *reinterpret_cast<float4*>(dst + place(r, (at + i) / 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     group_barrier<C>(0);
-    for (int x = tid; x < rows * (G / 8); x += 128) {
-      const int r = x / (G / 8), c = (x % (G / 8)) * 8;
+    for (int x = tid; x < rows * (COLS / 8); x += 128) {
+      const int r = x / (COLS / 8), c = (x % (COLS / 8)) * 8;
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.f;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const float* src = merge + (y * C::MT + r) * G;
+        const float* src = merge + (y * C::MT + r) * COLS;
         const float4 u0 = *reinterpret_cast<const float4*>(src + place(r, c / 4));
         const float4 u1 = *reinterpret_cast<const float4*>(src + place(r, c / 4 + 1));
         v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
@@ -204,17 +214,17 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
         for (int k = 0; k < 4; ++k)
           u[k] = BF16 ? pack_bf16x2(v[2 * k], v[2 * k + 1]) : pack_f16x2(v[2 * k], v[2 * k + 1]);
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (int64_t)(w.t0 + i) * p.o_st +
-                                  (int64_t)(w.head0 + rr - i * p.group) * p.o_sh + h * G + c) =
+                                  (int64_t)(w.head0 + rr - i * p.group) * p.o_sh + h * COLS + c) =
             make_uint4(u[0], u[1], u[2], u[3]);
       } else {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + (part_row + r) * C::D + h * G + c);
+        float4* dst = reinterpret_cast<float4*>(p.part_o + (part_row + r) * C::D + h * COLS + c);
         dst[0] = make_float4(v[0], v[1], v[2], v[3]);
         dst[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
     }
-    // The next group, or the next unit's (whose state the warps write first, and
+    // The next elements, or the next unit's (whose state the warps write first, and
     // meet, before they come here again).
-    if (h + 1 < C::H) group_barrier<C>(0);
+    if (h + 1 < C::D / COLS) group_barrier<C>(0);
   }
 }
 
@@ -222,7 +232,9 @@ template <int D, int MT, bool BF16, bool SPREAD>
 __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>::CTAS)
     attn_paged_q4_kernel(const __grid_constant__ PagedQ4Params p) {
   using C = PagedQ4Cfg<D, MT>;
-  constexpr int G = C::G, H = C::H, NT = C::NT, RH = MT / 8;
+  constexpr int G = C::G, H = C::H, NT = C::NT, RH = (MT + 7) / 8;
+  constexpr bool PAIRED = C::PAIRED;
+  constexpr int HL = PAIRED ? 1 : H;           // groups whose scales a lane applies
   constexpr int KW = G / 32, ON = G / 16;      // words of a key's group that a lane reads; blocks of 16 elements
   constexpr bool TWO = !BF16;                  // weights in two parts
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -251,6 +263,8 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
 
   // ------------------------------------------------ consumers
   const int quarter = warp, g = lane >> 2, t4 = lane & 3;
+  // The first of the lane's rows (of the first 8), and its group where it has one.
+  const int row_at = PAIRED ? 2 * (t4 & 1) : 2 * t4, mine = PAIRED ? t4 >> 1 : 0;
   float* st_m = reinterpret_cast<float*>(smem + C::OFF_STATE);
   float* st_l = st_m + 64;
   float* st_low = st_l + 64;
@@ -284,7 +298,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
   // The lane's part of a block: elements G/4 t4 .. of key g, with its scales, and of
   // values, elements G/8 g .. of keys 2 t4 and 2 t4 + 1.  The second two of four lanes
   // read the latter in the other order, which keeps a warp's reads on different banks.
-  const uint32_t k_at = first + g * (G / 2) + t4 * (G / 8), s_at = first_scale + g * 4;
+  const uint32_t k_at = first + g * (G / 2) + t4 * (G / 8), s_at = first_scale + g * 4 + mine * panel;
   const uint32_t v_first = C::TILE_BYTES + first + (2 * t4 + (t4 >> 1)) * (G / 2) + g * (G / 16);
   const uint32_t v_second = C::TILE_BYTES + first + (2 * t4 + 1 - (t4 >> 1)) * (G / 2) + g * (G / 16);
   const uint32_t low_halves = t4 < 2 ? 0x5410u : 0x1054u, high_halves = t4 < 2 ? 0x7632u : 0x3276u;
@@ -303,15 +317,14 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     if (w.tiles == 0) return;
     const int row0 = w.row0, rows = min(MT, w.n * p.group - row0);
     const int delta = w.Lk - w.n;
-    // The tokens of the rows and the key ranges of rows 2 t4 and 2 t4 + 1 (and
-    // of those 8 further down).
+    // The tokens of the rows and the key ranges of the lane's.
     const int tok_first = row0 / p.group, tok_last = (row0 + rows - 1) / p.group;
     int row_lo[RH][2], row_hi[RH][2];
 #pragma unroll
     for (int r = 0; r < RH; ++r)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int c = min((row0 + 2 * t4 + i + 8 * r) / p.group, tok_last) + delta;
+        const int c = min((row0 + row_at + i + 8 * r) / p.group, tok_last) + delta;
         row_lo[r][i] = max(0, c - p.win_left);
         row_hi[r][i] = (int)min((int64_t)w.Lk - 1, (int64_t)c + p.win_right);
       }
@@ -325,14 +338,14 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     // Q's operands: rows scaled by 2^up; their groups' sums (in units of 2^-24), and
     // what brings a score back.  Rows past the last hold anything, and nothing of
     // them is written.
-    uint64_t qsum[RH][H], back[RH];  // of rows 2 t4 and 2 t4 + 1
+    uint64_t qsum[RH][HL], back[RH];  // of the lane's rows: columns 2 t4 and 2 t4 + 1
     auto of_rows = [&](float x) { return packed_pair(__shfl_sync(0xffffffffu, x, 8 * t4), __shfl_sync(0xffffffffu, x, 8 * t4 + 4)); };
     uint32_t qseen = (uint32_t)(w.t0 | w.n | w.Lk | w.head0 | w.row0 | w.tile | w.tiles | w.from_start | w.to_end);
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
       float x[H][KW][8];
       float big = 0.f;
-      const uint8_t* src = smem + C::OFF_Q + (g + 8 * r) * C::Q_PITCH + t4 * (G / 2);
+      const uint8_t* src = smem + C::OFF_Q + (PAIRED ? g & 3 : g + 8 * r) * C::Q_PITCH + t4 * (G / 2);
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -353,6 +366,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
       const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
       const float down = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 + e + 10) << 23), 0x1p-126f);
       back[r] = of_rows(down);
+      float total[HL];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         float sum = 0.f;
@@ -363,14 +377,18 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             x[h][y][i] *= up;
             sum += x[h][y][i];
           }
+          const bool own = !PAIRED || (g >> 2) == h;  // (the column's group)
           q_ops[((h * KW + y) * RH + r) * 32] =
-              make_uint4(pack_f16x2(x[h][y][0], x[h][y][4]), pack_f16x2(x[h][y][1] * 0.0625f, x[h][y][5] * 0.0625f),
-                         pack_f16x2(x[h][y][2], x[h][y][6]), pack_f16x2(x[h][y][3] * 0.0625f, x[h][y][7] * 0.0625f));
+              own ? make_uint4(pack_f16x2(x[h][y][0], x[h][y][4]), pack_f16x2(x[h][y][1] * 0.0625f, x[h][y][5] * 0.0625f),
+                               pack_f16x2(x[h][y][2], x[h][y][6]), pack_f16x2(x[h][y][3] * 0.0625f, x[h][y][7] * 0.0625f))
+                  : make_uint4(0, 0, 0, 0);
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qsum[r][h] = of_rows(sum * 0x1p-24f);
+        if (!PAIRED || (g >> 2) == h) total[PAIRED ? 0 : h] = sum * 0x1p-24f;
       }
+#pragma unroll
+      for (int h = 0; h < HL; ++h) qsum[r][h] = of_rows(total[h]);
     }
     release_after(uempty, qseen, p.zero, lane == 0);
     __syncwarp();
@@ -380,14 +398,14 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     // most tiles the maximum over their keys; weights are 2^kSlack at most.
     constexpr float kSlack = 6.f;
     float m[RH][2];
-    uint64_t l[RH], low[RH][H], o[RH][H][ON][2];
+    uint64_t l[RH], low[RH][HL], o[RH][HL][ON][2];
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[r][i] = 2 * t4 + i + 8 * r < rows ? -INFINITY : INFINITY;  // (a row that is nobody's never grows)
+      for (int i = 0; i < 2; ++i) m[r][i] = row_at + i + 8 * r < rows ? -INFINITY : INFINITY;  // (a row that is nobody's never grows)
       l[r] = 0;
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
+      for (int h = 0; h < HL; ++h) {
         low[r][h] = 0;
 #pragma unroll
         for (int n = 0; n < ON; ++n) o[r][h][n][0] = o[r][h][n][1] = 0;
@@ -398,11 +416,11 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     constexpr int kExpShift = BF16 ? 7 : 10, kExpMax = BF16 ? 255 : 31, kExpBias = BF16 ? 127 : 15;
     constexpr int kExpMin = BF16 ? 14 : 0;  // (so that the power of two is one in FP32)
     constexpr int kLift = 127 + 14 - (int)kSlack + kExpBias;
-    float lift[H];
+    float lift[HL];
     auto lift_of = [](int x) { return __uint_as_float((uint32_t)(kLift - x) << 23); };
     auto top_of = [](float f) { return kLift - (int)(__float_as_uint(f) >> 23); };
 #pragma unroll
-    for (int h = 0; h < H; ++h) lift[h] = lift_of(kExpMin);
+    for (int h = 0; h < HL; ++h) lift[h] = lift_of(kExpMin);
 
     for (int x = 0; x < w.tiles; ++x) {
       const int tile0 = (w.tile + x) * C::TK, key0 = tile0 + key_at;
@@ -415,52 +433,80 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         // Scores of the warp's keys, in units of 1 / back, 16 keys at a time: of key g of
         // two blocks.
         uint64_t sc[NT][RH];
+        // The products of one group's codes with q; `first`: from 0.
+        auto dots = [&](int h, int kb, const uint4(&q)[KW][RH], float(&part)[RH][4], bool first) {
+          uint32_t c[2][KW];
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-          uint4 q[KW][RH];
+          for (int u = 0; u < 2; ++u) {
+            const uint8_t* at = tile + k_at + (2 * kb + u) * kCodeStep + h * panel;
+            if constexpr (KW == 2) {
+              const uint2 x = *reinterpret_cast<const uint2*>(at);
+              c[u][0] = x.x, c[u][KW - 1] = x.y;
+            } else {
+              c[u][0] = *reinterpret_cast<const uint32_t*>(at);
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < KW; ++y)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t c0 = j == 0 ? c[0][y] : c[0][y] >> 8, c1 = j == 0 ? c[1][y] : c[1][y] >> 8;
+              const uint32_t a[4] = {c0 & kLowCodes, c1 & kLowCodes, c0 & kHighCodes, c1 & kHighCodes};
+#pragma unroll
+              for (int r = 0; r < RH; ++r) {
+                const uint4 b = q[y][r];
+                if (first && y == 0 && j == 0) mma16816_first(part[r], a, b.x, b.y);
+                else mma16816<false>(part[r], a, j == 0 ? b.x : b.z, j == 0 ? b.y : b.w);
+              }
+            }
+        };
+        // Their scales and minima; `h`: of the lane's groups.
+        auto scaled = [&](int h, int kb, const float(&part)[RH][4]) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float s, mn;
+            scale_and_min<BF16>(*reinterpret_cast<const uint32_t*>(tile + s_at + (2 * kb + u) * kScaleStep + h * panel), s, mn);
+            const uint64_t s2 = packed_pair(s, s), mn2 = packed_pair(mn, mn);
+#pragma unroll
+            for (int r = 0; r < RH; ++r) {
+              uint64_t& x = sc[2 * kb + u][r];
+              x = h == 0 ? mul_pair(mn2, qsum[r][h]) : fma_pair(mn2, qsum[r][h], x);
+              x = fma_pair(s2, packed_pair(part[r][2 * u], part[r][2 * u + 1]), x);
+            }
+          }
+        };
+        auto q_of = [&](int h, uint4(&q)[KW][RH]) {
 #pragma unroll
           for (int y = 0; y < KW; ++y)
 #pragma unroll
             for (int r = 0; r < RH; ++r) q[y][r] = q_ops[((h * KW + y) * RH + r) * 32];
+        };
+        if constexpr (PAIRED) {
+          uint4 q[H][KW][RH];
+#pragma unroll
+          for (int h = 0; h < H; ++h) q_of(h, q[h]);
 #pragma unroll
           for (int kb = 0; kb < NT / 2; ++kb) {
-            uint32_t c[2][KW], sm[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int n = 2 * kb + u;
-              if constexpr (KW == 2) {
-                const uint2 x = *reinterpret_cast<const uint2*>(tile + k_at + n * kCodeStep + h * panel);
-                c[u][0] = x.x, c[u][KW - 1] = x.y;
-              } else {
-                c[u][0] = *reinterpret_cast<const uint32_t*>(tile + k_at + n * kCodeStep + h * panel);
-              }
-              sm[u] = *reinterpret_cast<const uint32_t*>(tile + s_at + n * kScaleStep + h * panel);
-            }
             float part[RH][4];
 #pragma unroll
-            for (int y = 0; y < KW; ++y)
+            for (int h = 0; h < H; ++h) dots(h, kb, q[h], part, h == 0);
+            scaled(0, kb, part);
+          }
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t c0 = j == 0 ? c[0][y] : c[0][y] >> 8, c1 = j == 0 ? c[1][y] : c[1][y] >> 8;
-                const uint32_t a[4] = {c0 & kLowCodes, c1 & kLowCodes, c0 & kHighCodes, c1 & kHighCodes};
+          for (int n = 0; n < NT; ++n) {  // the other group's part
+            const float2 x = parts_of(sc[n][0]);
+            sc[n][0] = add_pair(sc[n][0], packed_pair(__shfl_xor_sync(0xffffffffu, x.x, 2), __shfl_xor_sync(0xffffffffu, x.y, 2)));
+          }
+        } else {
 #pragma unroll
-                for (int r = 0; r < RH; ++r) {
-                  const uint4 b = q[y][r];
-                  if (y == 0 && j == 0) mma16816_first(part[r], a, b.x, b.y);
-                  else mma16816<false>(part[r], a, j == 0 ? b.x : b.z, j == 0 ? b.y : b.w);
-                }
-              }
+          for (int h = 0; h < H; ++h) {
+            uint4 q[KW][RH];
+            q_of(h, q);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float s, mn;
-              scale_and_min<BF16>(sm[u], s, mn);
-              const uint64_t s2 = packed_pair(s, s), mn2 = packed_pair(mn, mn);
-#pragma unroll
-              for (int r = 0; r < RH; ++r) {
-                uint64_t& x = sc[2 * kb + u][r];
-                x = h == 0 ? mul_pair(mn2, qsum[r][h]) : fma_pair(mn2, qsum[r][h], x);
-                x = fma_pair(s2, packed_pair(part[r][2 * u], part[r][2 * u + 1]), x);
-              }
+            for (int kb = 0; kb < NT / 2; ++kb) {
+              float part[RH][4];
+              dots(h, kb, q, part, true);
+              scaled(h, kb, part);
             }
           }
         }
@@ -497,9 +543,9 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         }
         // The values' scales and minima, and the largest bits of a scale (they order like
         // the numbers, none of which is negative; the minima beside them are cut off).
-        uint32_t sm[NT][H];
+        uint32_t sm[NT][HL];
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
+        for (int h = 0; h < HL; ++h) {
           uint32_t most = 0u;
 #pragma unroll
           for (int n = 0; n < NT; n += 2) {
@@ -516,19 +562,21 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
           for (int r = 0; r < RH; ++r) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float mn = fmaxf(m[r][i], mx[r][i]);
+              // By this row's own scores alone: what brought the warp here may be another's.
+              float mn = mx[r][i];
 #pragma unroll
               for (int by = 4; by < 32; by <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, by));
-              f[r][i] = mn == -INFINITY ? 1.f : ex2_approx(m[r][i] - mn);
-              m[r][i] = mn;
+              const bool set = mn > m[r][i] + kSlack;
+              f[r][i] = set ? ex2_approx(m[r][i] - mn) : 1.f;
+              if (set) m[r][i] = mn;
             }
             const uint64_t f2 = packed_pair(f[r][0], f[r][1]);
             l[r] = mul_pair(l[r], f2);
 #pragma unroll
-            for (int h = 0; h < H; ++h) low[r][h] = mul_pair(low[r][h], f2);
+            for (int h = 0; h < HL; ++h) low[r][h] = mul_pair(low[r][h], f2);
           }
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
+          for (int h = 0; h < HL; ++h) {
             // Of keys that some row reads, and of finite scales alone: others (of unused
             // slots, say) would leave no bits to the rest.
             const int top = top_of(lift[h]);
@@ -538,7 +586,12 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
               const int key = key0 + n * key_step + g, ex = (int)((sm[n][h] & 0xffffu) >> kExpShift);
               if (ex < kExpMax && key >= any_lo && key <= any_hi) now = max(now, ex);
             }
-            now = __reduce_max_sync(0xffffffffu, now);
+            if constexpr (PAIRED) {  // over the lanes of the same group
+#pragma unroll
+              for (int by = 1; by < 32; by = by == 1 ? 4 : 2 * by) now = max(now, __shfl_xor_sync(0xffffffffu, now, by));
+            } else {
+              now = __reduce_max_sync(0xffffffffu, now);
+            }
             const float down = now - top > 126 ? 0.f : __uint_as_float((uint32_t)(127 - (now - top)) << 23);
             lift[h] = lift_of(now);
 #pragma unroll
@@ -565,9 +618,43 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         // O^T += codes^T (P s)^T, and P m, group by group.  EDGE: a key that the row does
         // not read may have any scale.
         auto values = [&](auto EDGE) {
+          float part[RH][ON][4], base[RH][4];
+          // Codes of one group and 16 keys with the weights; `first`: from `base`.
+          auto products = [&](int h, int kb, const uint32_t(&hi)[RH][2], const uint32_t(&lo)[RH][2], bool first) {
+            // Two keys' words, 8 elements each, to pairs of halves of one element.
+            auto block = [&](int n, uint32_t b0, uint32_t b1) {
+              const uint32_t v[4] = {b0 & kLowCodes, b0 & kHighCodes, b1 & kLowCodes, b1 & kHighCodes};
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
-            uint32_t hi[RH][NT], lo[RH][NT];
+              for (int r = 0; r < RH; ++r) {
+                if (first) mma16816_from(part[r][n], v, hi[r][0], hi[r][1], base[r]);
+                else mma16816<false>(part[r][n], v, hi[r][0], hi[r][1]);
+                if (TWO) mma16816<false>(part[r][n], v, lo[r][0], lo[r][1]);
+              }
+            };
+            uint32_t a[2], b[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t far = (2 * kb + u) * kCodeStep + h * panel;
+              if constexpr (G == 64) {
+                a[u] = *reinterpret_cast<const uint32_t*>(tile + v_first + far);
+                b[u] = *reinterpret_cast<const uint32_t*>(tile + v_second + far);
+              } else {
+                a[u] = *reinterpret_cast<const uint16_t*>(tile + v_first + far);
+                b[u] = *reinterpret_cast<const uint16_t*>(tile + v_second + far);
+              }
+            }
+            const uint32_t x0 = __byte_perm(a[0], b[0], low_halves), x1 = __byte_perm(a[1], b[1], low_halves);
+            block(0, x0, x1);
+            block(1, x0 >> 8, x1 >> 8);
+            if constexpr (G == 64) {
+              const uint32_t y0 = __byte_perm(a[0], b[0], high_halves), y1 = __byte_perm(a[1], b[1], high_halves);
+              block(ON - 2, y0, y1);
+              block(ON - 1, y0 >> 8, y1 >> 8);
+            }
+          };
+#pragma unroll
+          for (int h = 0; h < HL; ++h) {
+            uint32_t hi[NT / 2][RH][2], lo[NT / 2][RH][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               float s, mn;
@@ -587,59 +674,36 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
                 } else {
                   low[r][h] = fma_pair(sc[n][r], mn2, low[r][h]);
                 }
-                if (TWO) {
-                  split_halves(ws.x, ws.y, hi[r][n], lo[r][n]);
-                  lo[r][n] = transposed(lo[r][n]);
-                } else {
-                  hi[r][n] = pack_f16x2(ws.x, ws.y);
-                }
-                hi[r][n] = transposed(hi[r][n]);
+                uint32_t &a = hi[n / 2][r][n % 2], &b = lo[n / 2][r][n % 2];
+                if (TWO) split_halves(ws.x, ws.y, a, b), b = transposed(b);
+                else a = pack_f16x2(ws.x, ws.y);
+                a = transposed(a);
               }
             }
             // The sums start from -8 times the weights, which is the same for all elements.
-            float base[RH][4];
             constexpr uint32_t kMinusEights[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
 #pragma unroll
             for (int kb = 0; kb < NT / 2; ++kb)
 #pragma unroll
               for (int r = 0; r < RH; ++r) {
-                if (kb == 0) mma16816_first(base[r], kMinusEights, hi[r][0], hi[r][1]);
-                else mma16816<false>(base[r], kMinusEights, hi[r][2 * kb], hi[r][2 * kb + 1]);
-                if (TWO) mma16816<false>(base[r], kMinusEights, lo[r][2 * kb], lo[r][2 * kb + 1]);
+                if (kb == 0) mma16816_first(base[r], kMinusEights, hi[0][r][0], hi[0][r][1]);
+                else mma16816<false>(base[r], kMinusEights, hi[kb][r][0], hi[kb][r][1]);
+                if (TWO) mma16816<false>(base[r], kMinusEights, lo[kb][r][0], lo[kb][r][1]);
               }
-            float part[RH][ON][4];
+            if constexpr (PAIRED) {
 #pragma unroll
-            for (int kb = 0; kb < NT / 2; ++kb) {
-              // Two keys' words, 8 elements each, to pairs of halves of one element.
-              auto products = [&](int n, uint32_t b0, uint32_t b1) {
-                const uint32_t v[4] = {b0 & kLowCodes, b0 & kHighCodes, b1 & kLowCodes, b1 & kHighCodes};
+              for (int x = 0; x < H; ++x) {
+                const uint32_t own = (g >> 2) == x ? ~0u : 0u;  // the columns of this group
 #pragma unroll
-                for (int r = 0; r < RH; ++r) {
-                  if (kb == 0) mma16816_from(part[r][n], v, hi[r][0], hi[r][1], base[r]);
-                  else mma16816<false>(part[r][n], v, hi[r][2 * kb], hi[r][2 * kb + 1]);
-                  if (TWO) mma16816<false>(part[r][n], v, lo[r][2 * kb], lo[r][2 * kb + 1]);
-                }
-              };
-              uint32_t a[2], b[2];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const uint32_t far = (2 * kb + u) * kCodeStep + h * panel;
-                if constexpr (G == 64) {
-                  a[u] = *reinterpret_cast<const uint32_t*>(tile + v_first + far);
-                  b[u] = *reinterpret_cast<const uint32_t*>(tile + v_second + far);
-                } else {
-                  a[u] = *reinterpret_cast<const uint16_t*>(tile + v_first + far);
-                  b[u] = *reinterpret_cast<const uint16_t*>(tile + v_second + far);
+                for (int kb = 0; kb < NT / 2; ++kb) {
+                  const uint32_t a[RH][2] = {{hi[kb][0][0] & own, hi[kb][0][1] & own}};
+                  const uint32_t b[RH][2] = {{TWO ? lo[kb][0][0] & own : 0u, TWO ? lo[kb][0][1] & own : 0u}};
+                  products(x, kb, a, b, x == 0 && kb == 0);
                 }
               }
-              const uint32_t x0 = __byte_perm(a[0], b[0], low_halves), x1 = __byte_perm(a[1], b[1], low_halves);
-              products(0, x0, x1);
-              products(1, x0 >> 8, x1 >> 8);
-              if constexpr (G == 64) {
-                const uint32_t y0 = __byte_perm(a[0], b[0], high_halves), y1 = __byte_perm(a[1], b[1], high_halves);
-                products(ON - 2, y0, y1);
-                products(ON - 1, y0 >> 8, y1 >> 8);
-              }
+            } else {
+#pragma unroll
+              for (int kb = 0; kb < NT / 2; ++kb) products(h, kb, hi[kb], lo[kb], kb == 0);
             }
 #pragma unroll
             for (int r = 0; r < RH; ++r)
@@ -675,11 +739,12 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         }
         if (g == 0) to[0] = f.x, to[1] = f.y;
       };
-      const int at = quarter * 16 + 8 * r + 2 * t4;
+      // (Two lanes have a row where it is there for both groups, and write the same.)
+      const int at = quarter * 16 + 8 * r + row_at;
       if (g == 0) st_m[at] = m[r][0], st_m[at + 1] = m[r][1];
       put_total(l[r], st_l + at);
 #pragma unroll
-      for (int h = 0; h < H; ++h) put_total(low[r][h], st_low + h * 64 + at);
+      for (int h = 0; h < HL; ++h) put_total(low[r][h], st_low + (h + mine) * 64 + at);
     }
     group_barrier<C>(0);
     // Row r's largest maximum (0 for none) and its sum.
@@ -693,18 +758,18 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
       for (int x = 0; x < 4; ++x) sum += st_l[x * 16 + r] * ex2_approx(st_m[x * 16 + r] - ref);
     };
     // The warp's rows in full: powers of two taken back, minima added.
-    float full_o[H][RH][2][2 * ON];
+    float full_o[HL][RH][2][2 * ON];
 #pragma unroll
     for (int r = 0; r < RH; ++r)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = 8 * r + 2 * t4 + j;
+        const int row = 8 * r + row_at + j;
         float ref, sum;
         state_of(row, ref, sum);
         const float inv = sum == 0.f ? 0.f : ex2_approx(st_m[quarter * 16 + row] - ref) / sum;  // no key: 0; a NaN sum stays one
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const float unit = 0x1p24f / lift[h], add = st_low[h * 64 + quarter * 16 + row];
+        for (int h = 0; h < HL; ++h) {
+          const float unit = 0x1p24f / lift[h], add = st_low[(h + mine) * 64 + quarter * 16 + row];
 #pragma unroll
           for (int n = 0; n < ON; ++n) {
             const float2 even = parts_of(o[r][h][n][0]), odd = parts_of(o[r][h][n][1]);

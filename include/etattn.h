@@ -576,7 +576,7 @@ int attn_fwd_paged_q4(const void* q, const void* k_pages, const void* v_pages, v
                       void* stream);
 
 /* Bytes of workspace attn_fwd_paged_q4 needs (0 for one share, or for empty or
- * invalid sizes); a unit has 8 or 16 rows. */
+ * invalid sizes); a unit has 4, 8 or 16 rows. */
 size_t attn_fwd_paged_q4_workspace_size(int Hq, int Hkv, int max_seqlen_q, int D, int num_shares);
 
 /* attn_fwd_paged_plan for attn_fwd_paged_q4. */
