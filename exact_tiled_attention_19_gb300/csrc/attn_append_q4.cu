@@ -21,7 +21,14 @@
 // Memory bounds it for prompts: q is read and written once, k and v are read once and leave
 // 9/32 of their bytes.  D/16 threads hold a row, as in attn_rope.cu, and a row's sums,
 // minima and maxima take log2(D/16) shuffles each.  Blocks of q, of k and of v are apart,
-// so that no warp does two kinds of work, and take turns.
+// so that no warp does two kinds of work, and take turns, so that the arithmetic of k runs
+// beside the traffic of q.
+//
+// Measured (GB300; BF16, 32 + 2 x 8 heads of 128, norm and rotation): 16 x 1000 tokens 79.4 us, of
+// which q alone is 28 and k's two-part arithmetic about 7 (floor 58 us at the measured
+// copy bandwidth; issue slots busy 61 %, the integer units 47 %); 999 tokens of 16 + 2 x 4 heads of
+// 64 5.2 us; 8 tokens 3.6 us, the launch and the chain slot -> page.  Unpacking the 16000 tokens'
+// keys takes 8.2 us (6.2 at the copy bandwidth).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>

@@ -33,16 +33,38 @@
 // parts of together 2^-21 for FP16 outputs, in one for BF16 ones, whose 2^-12 is an
 // eighth of the output's own rounding.  The tensor core cuts off what falls below an
 // accumulator's last bit, always downwards, and codes are never negative, so a
-// running sum would drift: a tile's products with V start from 0 and are added to the
-// running sums in FP32 (without it one sequence of 524288 keys was 1.6 times as far
-// from 64 bits as a rounding).
+// running sum would drift.  A tile's products with V therefore start anew and are added to
+// the running sums in FP32; and they start from -8 times the sum of the tile's weights, so
+// that what accumulates is sum (P s)(c - 8), of both signs and small, while the minima's
+// term takes m + 8 s instead of m.  One sequence of 524288 keys: outputs in BF16 were 1.6 times
+// as far from 64 bits as a rounding of the exact ones with one running sum; in FP16 2.9 times
+// with tiles that start from 0, 1.15 times now.
+//   A row's weights are taken against a reference m that is set again only when a score
+// passes it by 2^6 (kSlack), and by the row's own scores alone, so that no other row and
+// nothing outside the row's range changes a bit of its result.
 //
 // Up to 4 rows of 128 elements (PAIRED; a decode step of four query heads a KV head).
 // The right operands' columns 4 .. 7 are the same rows again, for the second group of
 // elements: a lane applies the scales of one group, not of both.  Q's operands are 0
 // in the other group's columns, so that one accumulator takes the products of both groups
 // side by side, and the two parts of a score are in neighbouring lanes; the weights'
-// likewise.
+// likewise.  (The kernel for 8 rows takes 62.7 us for 8 x 32768 keys, where this one takes 57.2; 92
+// against 77 for 512 sequences up to 2048.)  Heads of 64 or 32 have one group, and nothing to share.
+//
+// What bounds it.  A key and a value of D = 128 are 144 bytes, 3.6 times fewer than in 16
+// bits, and 16 of them cost a warp as many instructions as 16 bits would: the loads alone
+// take 50 us of the 57 for 8 x 32768 keys (44.6 at the copy bandwidth), the instructions of the
+// consumers half of all issue slots (2.0 of 4 a cycle), of which the integer units
+// take 52 %; the tensor pipe is busy 26 %.  So everything here saves instructions per key: no
+// conversions, scales on pairs, maxima looked at only when they matter.
+//   mma.sync and not tcgen05: a tile of 128 query rows would be 15/16 empty, and the codes would
+// have to be written to shared memory as numbers first.  Three CTAs of four consumer warps an
+// SM: two leave the loads uncovered, and four leave 96 registers a thread, which spill.
+//
+// Measured (GB300; BF16, 32 query and 8 KV heads of 128, one new token, unless said; device
+// time; % of the measured copy bandwidth): 8 x 32768 keys 57.2 us (78 %), in FP16 64.0; 1 x 524288
+// 111 us (80 %); 64 sequences of 1 to 16384 keys 38.2 us (52 %); 16 rows (4 tokens) 8 x 32768
+// 95.3 us.  The cache in 16 bits takes 164, 325 and 80 us for the first three.
 #pragma once
 
 #include <cstdint>
@@ -55,6 +77,8 @@ namespace etattn {
 template <int D_, int MT_>
 struct PagedQ4Cfg {
   static constexpr int D = D_, MT = MT_;
+  // What a unit costs next to a tile: 2, 3, 4 and 6 take 41.5, 40.2, 42.2 and 44.9 us for 64 ragged
+  // sequences, 92.7, 89.9, 94.6 and 103 for 512 short ones.
   static constexpr int UNIT_COST = 3;
   static constexpr int GROUPS = 1;                    // of four consumer warps
   static constexpr int G = D < 64 ? D : 64, H = D / G;
