@@ -23,7 +23,7 @@
 // fill the right one: S^T = K Q^T with 16 keys, O^T = V^T P^T with 16 elements.  A lane has
 // the scores of one key in the former, and of one row in P^T: an 8 x 8 transpose of the
 // weights, already scaled and rounded, lies between.  A register of V^T holds two keys
-// of one element: byte permutes bring the halves of two keys' words together first.
+// of one element: transposed loads bring 16 bits of two keys together.
 //
 // Precision.  q's rows are scaled by powers of two so that their largest element
 // is within 2^14 .. 2^15, and held as FP16: exact for both input types (elements below
@@ -179,6 +179,17 @@ __device__ __forceinline__ void scale_and_min(uint32_t w, float& s, float& m) {
   else unpack_f16x2(w, s, m);
 }
 
+// Four (or two) 8 x 8 matrices of 16-bit values, transposed; eight lanes each give their
+// rows.  (Volatile, so that it stays behind the wait, but free of the other loads.)
+__device__ __forceinline__ void codes_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void codes_trans(uint32_t (&r)[2], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+
 // The 8 x 8 matrix of halves that the warp holds, a row of four registers each, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
@@ -189,8 +200,8 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 constexpr uint32_t kLowCodes = 0x000f000fu, kHighCodes = 0x00f000f0u;
 
 // Adds up the four warps' scaled rows, COLS elements at a time, and writes them: the
-// output, or the unit's partial rows.  A lane holds elements G/8 g .. of two rows (and
-// of those 8 further down) of every group, or of its own.
+// output, or the unit's partial rows.  A lane holds elements 4 g .. and 32 + 4 g .. of
+// two rows (and of those 8 further down) of every group, or of its own.
 template <class C, bool BF16>
 __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const PagedUnit& w, int rows, float* merge,
                                                const float (&o)[C::PAIRED ? 1 : C::H][(C::MT + 7) / 8][2][C::G / 8],
@@ -201,8 +212,8 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
   // Where a row's four elements x4 lie: eight lanes that store together hit eight
   // different quarters of the banks.
   auto place = [](int r, int x4) {
-    if (C::PAIRED) return (x4 ^ ((r >> 1) & 1) ^ ((x4 >> 2) & 4)) * 4;
-    return (x4 ^ (G == 64 ? (r & 4) | ((r >> 1) & 1) : (r & 6))) * 4;
+    if (C::PAIRED) return (x4 ^ (r & 2) ^ ((x4 >> 2) & 4)) * 4;
+    return (x4 ^ (r & 6)) * 4;
   };
 #pragma unroll
   for (int h = 0; h < C::D / COLS; ++h) {
@@ -210,12 +221,12 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
     for (int hr = 0; hr < (C::MT + 7) / 8; ++hr)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int r = C::PAIRED ? 2 * (t4 & 1) + j : 8 * hr + 2 * t4 + j, at = (C::PAIRED ? (t4 >> 1) * G : 0) + g * RUN;
+        const int r = C::PAIRED ? 2 * (t4 & 1) + j : 8 * hr + 2 * t4 + j, at = (C::PAIRED ? (t4 >> 1) * G : 0) + g * 4;
         float* dst = merge + (warp * C::MT + r) * COLS;
         const float(&v)[RUN] = o[h][hr][j];
 #pragma unroll
         for (int i = 0; i < RUN; i += 4)
-          *reinterpret_cast<float4*>(dst + place(r, (at + i) / 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          *reinterpret_cast<float4*>(dst + place(r, at / 4 + 2 * i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     group_barrier<C>(0);
     for (int x = tid; x < rows * (COLS / 8); x += 128) {
@@ -319,13 +330,12 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     box_at = (key_at - in_box) * C::ROW_BYTES;
   }
   const uint32_t first = box_at + in_box * (G / 2), first_scale = box_at + box_keys * (G / 2) + in_box * 4;
-  // The lane's part of a block: elements G/4 t4 .. of key g, with its scales, and of
-  // values, elements G/8 g .. of keys 2 t4 and 2 t4 + 1.  The second two of four lanes
-  // read the latter in the other order, which keeps a warp's reads on different banks.
+  // The lane's part of a block: elements G/4 t4 .. of key g, with its scales.  Of values it
+  // gets elements 4 g .. (and 32 + 4 g ..) of keys 2 t4 and 2 t4 + 1 by transposed loads
+  // of 8 keys' 16 bytes, of which it gives one address: of two blocks, G / 32 loads each.
   const uint32_t k_at = first + g * (G / 2) + t4 * (G / 8), s_at = first_scale + g * 4 + mine * panel;
-  const uint32_t v_first = C::TILE_BYTES + first + (2 * t4 + (t4 >> 1)) * (G / 2) + g * (G / 16);
-  const uint32_t v_second = C::TILE_BYTES + first + (2 * t4 + 1 - (t4 >> 1)) * (G / 2) + g * (G / 16);
-  const uint32_t low_halves = t4 < 2 ? 0x5410u : 0x1054u, high_halves = t4 < 2 ? 0x7632u : 0x3276u;
+  const uint32_t v_at = C::TILE_BYTES + first + (lane & 7) * (G / 2) +
+                        (G == 64 ? (lane >> 4) * 16 + ((lane >> 3) & 1) * kCodeStep : ((lane >> 3) & 1) * kCodeStep);
 
   uint32_t phase = 0, uphase = 0;
   int stage = 0;
@@ -645,7 +655,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
           float part[RH][ON][4], base[RH][4];
           // Codes of one group and 16 keys with the weights; `first`: from `base`.
           auto products = [&](int h, int kb, const uint32_t(&hi)[RH][2], const uint32_t(&lo)[RH][2], bool first) {
-            // Two keys' words, 8 elements each, to pairs of halves of one element.
+            // Four elements of two keys, a key's in a half, of either block.
             auto block = [&](int n, uint32_t b0, uint32_t b1) {
               const uint32_t v[4] = {b0 & kLowCodes, b0 & kHighCodes, b1 & kLowCodes, b1 & kHighCodes};
 #pragma unroll
@@ -655,25 +665,17 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
                 if (TWO) mma16816<false>(part[r][n], v, lo[r][0], lo[r][1]);
               }
             };
-            uint32_t a[2], b[2];
+            const uint32_t from = smem_u32(tile) + v_at + 2 * kb * kCodeStep + h * panel;
+            constexpr int X = RH == 1 ? ON : 2;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t far = (2 * kb + u) * kCodeStep + h * panel;
-              if constexpr (G == 64) {
-                a[u] = *reinterpret_cast<const uint32_t*>(tile + v_first + far);
-                b[u] = *reinterpret_cast<const uint32_t*>(tile + v_second + far);
-              } else {
-                a[u] = *reinterpret_cast<const uint16_t*>(tile + v_first + far);
-                b[u] = *reinterpret_cast<const uint16_t*>(tile + v_second + far);
+            for (int n0 = 0; n0 < ON; n0 += X) {
+              uint32_t x[X];
+              codes_trans(x, from + 8 * n0);
+#pragma unroll
+              for (int n = 0; n < X; n += 2) {
+                block(n0 + n, x[n], x[n + 1]);
+                block(n0 + n + 1, x[n] >> 8, x[n + 1] >> 8);
               }
-            }
-            const uint32_t x0 = __byte_perm(a[0], b[0], low_halves), x1 = __byte_perm(a[1], b[1], low_halves);
-            block(0, x0, x1);
-            block(1, x0 >> 8, x1 >> 8);
-            if constexpr (G == 64) {
-              const uint32_t y0 = __byte_perm(a[0], b[0], high_halves), y1 = __byte_perm(a[1], b[1], high_halves);
-              block(ON - 2, y0, y1);
-              block(ON - 1, y0 >> 8, y1 >> 8);
             }
           };
 #pragma unroll
