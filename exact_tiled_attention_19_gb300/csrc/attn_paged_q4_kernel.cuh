@@ -48,23 +48,23 @@
 // elements: a lane applies the scales of one group, not of both.  Q's operands are 0
 // in the other group's columns, so that one accumulator takes the products of both groups
 // side by side, and the two parts of a score are in neighbouring lanes; the weights'
-// likewise.  (The kernel for 8 rows takes 62.7 us for 8 x 32768 keys, where this one takes 57.2; 92
-// against 77 for 512 sequences up to 2048.)  Heads of 64 or 32 have one group, and nothing to share.
+// likewise.  (8 x 32768 keys took 57.2 us instead of 62.7 with the kernel for 8 rows, 512 sequences
+// up to 2048 keys 77 instead of 92.)  Heads of 64 or 32 have one group, and nothing to share.
 //
 // What bounds it.  A key and a value of D = 128 are 144 bytes, 3.6 times fewer than in 16
 // bits, and 16 of them cost a warp as many instructions as 16 bits would: the loads alone
-// take 50 us of the 57 for 8 x 32768 keys (44.6 at the copy bandwidth), the instructions of the
+// take 50 us of the 55 for 8 x 32768 keys (44.6 at the copy bandwidth), the instructions of the
 // consumers half of all issue slots (2.0 of 4 a cycle), of which the integer units
 // take 52 %; the tensor pipe is busy 26 %.  So everything here saves instructions per key: no
 // conversions, scales on pairs, maxima looked at only when they matter.
 //   mma.sync and not tcgen05: a tile of 128 query rows would be 15/16 empty, and the codes would
 // have to be written to shared memory as numbers first.  Three CTAs of four consumer warps an
-// SM: two leave the loads uncovered, and four leave 96 registers a thread, which spill.
+// SM: two took 64.5 us where three took 62.7, four (96 registers a thread, two stages) 66.
 //
 // Measured (GB300; BF16, 32 query and 8 KV heads of 128, one new token, unless said; device
-// time; % of the measured copy bandwidth): 8 x 32768 keys 57.2 us (78 %), in FP16 64.0; 1 x 524288
-// 111 us (80 %); 64 sequences of 1 to 16384 keys 38.2 us (52 %); 16 rows (4 tokens) 8 x 32768
-// 95.3 us.  The cache in 16 bits takes 164, 325 and 80 us for the first three.
+// time; % of the measured copy bandwidth): 8 x 32768 keys 54.9 us (81 %; 57.2 before the values'
+// loads were transposed ones), in FP16 62.9; 1 x 524288 107 us (83 %); 64 sequences of 1 to 16384
+// keys 36.9 us (54 %); 16 rows (4 tokens) 8 x 32768 94 us.  The cache in 16 bits takes 164, 325 and 80 us for the first three.
 #pragma once
 
 #include <cstdint>
