@@ -178,12 +178,13 @@ __device__ __forceinline__ uint32_t codes8(const uint32_t* x, const Quant& z) {
 }
 
 // A row of 16-bit values, the chunks' four words each, into its block.
-template <int D, bool BF16>
+// APART: the chunks are one of either group.
+template <int D, bool BF16, bool APART>
 __device__ __forceinline__ void store_row(uint8_t* block, int slot, int page_keys, const uint32_t (&y)[8], const Chunks& ch,
                                           int lane, bool on) {
   constexpr int G = D < 64 ? D : 64, H = D / G, LANES = D / 16;
   constexpr uint32_t kNone = BF16 ? 0x7f807f80u : 0x7c007c00u;  // infinities
-  const int ga = H == 1 ? 0 : ch.first / G, gb = H == 1 ? 0 : ch.second / G;
+  const int ga = H == 1 || APART ? 0 : ch.first / G, gb = H == 1 ? 0 : APART ? 1 : ch.second / G;
   const uint32_t a = extremes<BF16>(y), b = extremes<BF16>(y + 4);
   Quant za, zb;  // of the two chunks
   uint32_t word;  // of group `lane`, in the lanes below H
@@ -197,8 +198,8 @@ __device__ __forceinline__ void store_row(uint8_t* block, int slot, int page_key
     // The lower lanes come to hold group 0 and the upper ones group 1: each makes one
     // quantiser and gets the other.
     const int mine = lane / (LANES / 2);
-    const uint32_t e0 = min_pair<BF16>(ga == 0 ? a : kNone, gb == 0 ? b : kNone);
-    const uint32_t e1 = min_pair<BF16>(ga == 1 ? a : kNone, gb == 1 ? b : kNone);
+    const uint32_t e0 = APART ? a : min_pair<BF16>(ga == 0 ? a : kNone, gb == 0 ? b : kNone);
+    const uint32_t e1 = APART ? b : min_pair<BF16>(ga == 1 ? a : kNone, gb == 1 ? b : kNone);
     uint32_t e = min_pair<BF16>(mine ? e1 : e0, __shfl_xor_sync(0xffffffffu, mine ? e0 : e1, LANES / 2));
 #pragma unroll
     for (int off = LANES / 4; off > 0; off >>= 1) e = min_pair<BF16>(e, __shfl_xor_sync(0xffffffffu, e, off));
@@ -310,15 +311,15 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_q4_kernel(const __gr
   const Chunks ch = chunks_of(D, lane, FULL ? D : p.rope_dim, INTER);
   // The block's kind of rows: those of k and v are spread evenly among those of q, so
   // that their arithmetic runs beside q's traffic.
-  const int others = 2 * p.kv_blocks;
-  const int before = (int)div_pos((int64_t)blockIdx.x * others, gridDim.x);  // blocks of k and v before this one
-  const bool is_q = (int)div_pos((int64_t)(blockIdx.x + 1) * others, gridDim.x) == before;
+  const int before = (int)(blockIdx.x * p.others_step >> 32);  // blocks of k and v before this one
+  const bool is_q = (int)((blockIdx.x + 1) * p.others_step >> 32) == before;
   const int kind = is_q ? 0 : 1 + (before & 1);
   const int block = is_q ? (int)blockIdx.x - before : before >> 1;
   const int heads = kind == 0 ? p.Hq : p.Hkv, step = kind == 0 ? HQ : HP, per_token = (heads + step - 1) / step;
   const int64_t item = (int64_t)block * GROUPS + threadIdx.x / LANES;
   const bool live = item < (int64_t)p.total_tokens * per_token;
-  const int t = live ? (int)div_pos(item, per_token) : 0;
+  const uint64_t groups = kind == 0 ? p.q_groups : p.kv_groups;
+  const int t = !live ? 0 : groups == 0 ? (int)item : (int)__umul64hi((uint64_t)item, groups);
   const int h0 = live ? (int)(item - (int64_t)t * per_token) * step : 0;
   const int64_t st = kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st;
   const int64_t sh = kind == 0 ? p.q_sh : kind == 1 ? p.k_sh : p.v_sh;
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_q4_kernel(const __gr
       }
       uint32_t y[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
       if (kind == 1) key_row<D, BF16, INTER, FULL>(w2, c2, s2, ch, weight != nullptr, p.eps, y);
-      store_row<D, BF16>(out + (h0 + i) * oh, slot, page_keys, y, ch, lane, ok && h0 + i < heads);
+      store_row<D, BF16, FULL || INTER>(out + (h0 + i) * oh, slot, page_keys, y, ch, lane, ok && h0 + i < heads);
     }
   }
 }
@@ -486,7 +487,15 @@ cudaError_t append(const AppendQ4Params& p0, cudaStream_t s) {
   int64_t kv;
   const int64_t blocks = append_blocks<D>(p, HQ, HP, &kv);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  p.kv_blocks = (int)kv;
+  // Rounded up: the product with all blocks is that of k and v's blocks and less than
+  // 2^32 more, and with an item (below 2^37) a quotient whose fraction stays below 1.
+  p.others_step = (((uint64_t)(2 * kv) << 32) + blocks - 1) / blocks;
+  auto one_over = [](int heads, int each) {
+    const uint64_t groups = (heads + each - 1) / each;
+    return groups <= 1 ? 0 : ~uint64_t{0} / groups + 1;
+  };
+  p.q_groups = one_over(p.Hq, HQ);
+  p.kv_groups = one_over(p.Hkv, HP);
   const bool full = p.rope_dim == D;
   if (p.interleaved)
     return full ? launch_append<D, BF16, HQ, HP, true, true>(p, (unsigned)blocks, s)

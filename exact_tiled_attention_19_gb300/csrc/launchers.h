@@ -175,7 +175,8 @@ struct AppendQ4Params {
   int rope_dim, interleaved, max_position;
   float eps;
   int num_pages, page_shift;
-  int kv_blocks;                   // of the launch: as many for k as for v, the others for q
+  uint64_t others_step;            // of the launch: blocks of k and v (as many each) per block, times 2^32
+  uint64_t q_groups, kv_groups;    // one over a token's groups of heads, times 2^64 (0: one group)
   int* status;
 };
 cudaError_t launch_append_q4(int D, bool bf16, const AppendQ4Params& p, cudaStream_t stream);
