@@ -24,14 +24,15 @@
 // so that no warp does two kinds of work, and take turns, so that the arithmetic of k runs
 // beside the traffic of q.
 //
-// Measured (GB300; BF16, 32 + 2 x 8 heads of 128, norm and rotation): 16 x 1000 tokens 79.4 us, of
-// which q alone is 28 and k's two-part arithmetic about 7 (floor 58 us at the measured
-// copy bandwidth; issue slots busy 61 %, the integer units 47 %); 999 tokens of 16 + 2 x 4 heads of
-// 64 5.2 us; 8 tokens 3.6 us, the launch and the chain slot -> page.  Unpacking the 16000 tokens'
-// keys takes 8.2 us (6.2 at the copy bandwidth).
+// Measured (GB300; BF16, 32 + 2 x 8 heads of 128, norm and rotation): 16 x 1000 tokens 68.4 us, of
+// which q is 22 and k's two-part arithmetic 10 (51 us at the measured copy bandwidth; the
+// issue slots bound it: 215 instructions for a warp's four rows of v, 585 for k, 148 for q); 999 tokens
+// of 16 + 2 x 4 heads of 64 4.3 us; 8 tokens 2.8 us, the launch and the chain slot -> page.
+// Unpacking the 16000 tokens' keys takes 8.2 us (6.2 at the copy bandwidth).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "launchers.h"
@@ -42,7 +43,7 @@ namespace etattn {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;  // (16000 tokens: 68.4 us; 256: 71.3, 64: 72.7)
 
 // hi + lo, |lo| at most half a step of hi.
 struct Two {
@@ -303,16 +304,16 @@ __device__ __forceinline__ void key_row(const uint64_t (&w)[8], const uint64_t (
 // A group of D/16 threads takes consecutive heads of one token, as in attn_rope.cu: HQ of
 // q or HP of k or v.
 template <int D, bool BF16, int HQ, int HP, bool INTER, bool FULL>
-__global__ void __launch_bounds__(kAppendThreads, 3) append_q4_kernel(const __grid_constant__ AppendQ4Params p) {
+__global__ void __launch_bounds__(kAppendThreads, 6) append_q4_kernel(const __grid_constant__ AppendQ4Params p) {
   constexpr int LANES = D / 16, GROUPS = kAppendThreads / LANES;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x % LANES;
   const Chunks ch = chunks_of(D, lane, FULL ? D : p.rope_dim, INTER);
-  // The block's kind of rows: those of k and v are spread evenly among those of q, so
-  // that their arithmetic runs beside q's traffic.
-  const int before = (int)(blockIdx.x * p.others_step >> 32);  // blocks of k and v before this one
-  const bool is_q = (int)((blockIdx.x + 1) * p.others_step >> 32) == before;
+  // The block's kind of rows: those of k and v are spread among those of q, so that
+  // their arithmetic runs beside q's traffic.
+  const int before = min(p.others, (int)(blockIdx.x * p.others_step >> 32));  // blocks of k and v before this one
+  const bool is_q = min(p.others, (int)((blockIdx.x + 1) * p.others_step >> 32)) == before;
   const int kind = is_q ? 0 : 1 + (before & 1);
   const int block = is_q ? (int)blockIdx.x - before : before >> 1;
   const int heads = kind == 0 ? p.Hq : p.Hkv, step = kind == 0 ? HQ : HP, per_token = (heads + step - 1) / step;
@@ -411,15 +412,21 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_q4_kernel(const __gr
       }
     }
     if constexpr (STAGED) copy_wait<0>();
-#pragma unroll 1
-    for (int i = 0; i < HP; ++i) {
+    auto row = [&](int i, auto KEY) {
       if constexpr (STAGED) {
         ra = cells[(2 * i) * kAppendThreads + threadIdx.x];
         rb = cells[(2 * i + 1) * kAppendThreads + threadIdx.x];
       }
       uint32_t y[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
-      if (kind == 1) key_row<D, BF16, INTER, FULL>(w2, c2, s2, ch, weight != nullptr, p.eps, y);
+      if constexpr (decltype(KEY)::value) key_row<D, BF16, INTER, FULL>(w2, c2, s2, ch, weight != nullptr, p.eps, y);
       store_row<D, BF16, FULL || INTER>(out + (h0 + i) * oh, slot, page_keys, y, ch, lane, ok && h0 + i < heads);
+    };
+    if (kind == 1) {
+#pragma unroll 1
+      for (int i = 0; i < HP; ++i) row(i, std::true_type{});
+    } else {  // (two at a time: 76.5 us for 16000 tokens, one 78.0)
+#pragma unroll 2
+      for (int i = 0; i < HP; ++i) row(i, std::false_type{});
     }
   }
 }
@@ -487,9 +494,14 @@ cudaError_t append(const AppendQ4Params& p0, cudaStream_t s) {
   int64_t kv;
   const int64_t blocks = append_blocks<D>(p, HQ, HP, &kv);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  // Rounded up: the product with all blocks is that of k and v's blocks and less than
-  // 2^32 more, and with an item (below 2^37) a quotient whose fraction stays below 1.
-  p.others_step = (((uint64_t)(2 * kv) << 32) + blocks - 1) / blocks;
+  // k and v's blocks come in the first 6/7 of the launch: theirs take longer, and at the
+  // end the GPU would wait for a few of them (16000 tokens: 73.6 us spread over all of it,
+  // 71.3, 69.1, 68.4 and 69.5 over 95, 90, 86 and 80 %).  The product with all blocks is no
+  // less than their number.
+  p.others = (int)(2 * kv);
+  const uint64_t even = (((uint64_t)p.others << 32) + blocks - 1) / blocks;
+  p.others_step = std::min(even + even / 6, uint64_t{1} << 32);
+  // Rounded up: with an item (below 2^37) a quotient whose fraction stays below 1.
   auto one_over = [](int heads, int each) {
     const uint64_t groups = (heads + each - 1) / each;
     return groups <= 1 ? 0 : ~uint64_t{0} / groups + 1;
@@ -504,13 +516,13 @@ cudaError_t append(const AppendQ4Params& p0, cudaStream_t s) {
               : launch_append<D, BF16, HQ, HP, false, false>(p, (unsigned)blocks, s);
 }
 
-// One head a group for small calls, else four (eight of q), which read a token's place, angles and
-// weights for all of them.  Measured, us with 1 / 2 / 4 / 8 heads a group (32 + 8 heads
-// of 128, and 48 of those in all a token): 3.9 / 5.3 / 7.8 / 13 at 64 tokens, 9.5 / 10 /
-// 13 / 15 at 800 (1200 blocks of one head), 25 / 21 / 22 / 29 at 2400, 61 / 46 / 41 / 46 at
-// 6400, 146 / 106 / 85 / 83 at 16000; heads of 64: 5.1 / 7.2 / 8.4 / 13 at 999 tokens (376
-// blocks), 17 / 15 / 17 / 27 at 6000 (2250), 74 / 55 / 48 / 51 at 16000.
-constexpr int kOneHeadBlocks = 1216;  // eight on each of a GB300's 152 SMs
+// One head a group for small calls, else four (eight of q), which read a token's place, angles
+// and weights for all of them.  Measured, us of either (BF16, 32 + 2 x 8 heads): of 128, 3.2 and 6.8 at 64
+// tokens, 7.2 and 10.7 at 800, 19.0 and 19.2 at 2400 (7200 blocks of one head), 36 and 28 at
+// 4800, 115 and 69 at 16000; of 64, 4.8 and 8.5 at 800, 18.9 and 18.8 at 4800 (7200), 58 and 39 at
+// 16000.  At 16000 tokens of the former two, four and eight heads of k and v beside eight of q
+// take 74.7, 68.4 and 73.8 us, four of all 70.1.
+constexpr int kOneHeadBlocks = 7296;  // 48 on each of a GB300's 152 SMs
 template <int D, bool BF16>
 cudaError_t append_any(const AppendQ4Params& p, cudaStream_t s) {
   int64_t kv;

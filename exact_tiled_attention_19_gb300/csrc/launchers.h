@@ -175,7 +175,8 @@ struct AppendQ4Params {
   int rope_dim, interleaved, max_position;
   float eps;
   int num_pages, page_shift;
-  uint64_t others_step;            // of the launch: blocks of k and v (as many each) per block, times 2^32
+  int others;                      // blocks of the launch that are of k or v, as many each
+  uint64_t others_step;            // how many of them come with every block, times 2^32
   uint64_t q_groups, kv_groups;    // one over a token's groups of heads, times 2^64 (0: one group)
   int* status;
 };

@@ -153,6 +153,16 @@ def test_append_heads(Hq, Hkv):
         check_append(T, Hq, Hkv, 64, torch.bfloat16, 32, seed=Hq)
 
 
+@pytest.mark.parametrize("D,dt,Hq,Hkv,T,rope_dim,interleaved", [
+    (128, "bf16", 35, 5, 2700, 128, False), (128, "f16", 16, 8, 4000, 96, True), (128, "bf16", 0, 4, 15000, 0, False),
+    (128, "f16", 8, 1, 12000, 128, True), (64, "bf16", 40, 5, 4800, 48, False), (64, "f16", 0, 17, 7000, 64, True),
+    (32, "bf16", 32, 8, 10000, 32, False), (32, "f16", 17, 17, 9300, 16, False)])
+def test_append_many_tokens(D, dt, Hq, Hkv, T, rope_dim, interleaved):
+    """More than 7296 blocks of one head each, where a thread takes several heads."""
+    assert T * (Hq + 2 * Hkv) > 7296 * 128 // (D // 16)
+    check_append(T, Hq, Hkv, D, DT[dt], 16, rope_dim=rope_dim, interleaved=interleaved, weighted=rope_dim > 0, seed=T)
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("D", [32, 64, 128])
 def test_append_values_where_rounding_decides(dt, D):
