@@ -77,9 +77,12 @@ namespace etattn {
 template <int D_, int MT_>
 struct PagedQ4Cfg {
   static constexpr int D = D_, MT = MT_;
-  // What a unit costs next to a tile: 2, 3, 4 and 6 take 41.5, 40.2, 42.2 and 44.9 us for 64 ragged
-  // sequences, 92.7, 89.9, 94.6 and 103 for 512 short ones.
-  static constexpr int UNIT_COST = 3;
+  // What a unit costs next to a tile (of twice the keys for the smaller heads).  1, 2, 3 and 4 take,
+  // us for 64 ragged sequences and for 512 short ones: 4 rows of 128 40.2, 35.7, 37.0, - and 74.2,
+  // 69.2, 74.6, -; 16 rows 96, 76.9, 66.6, 68.5 and 228, 209, 196, 198; heads of 64 28.9, 30.2, 31.9, -
+  // and 61.5, 65.7, 71.3, -, 16 rows of them 47.8, 43.0, 46.1, 48.2 and 122, 117, 120, 127; of 32 26.9,
+  // 28.1, 29.6, 31.3 and 56.0, 61.5, 66.4, 73.7.
+  static constexpr int UNIT_COST = (D == 128 ? 2 : 1) + (MT == 16 ? 1 : 0);
   static constexpr int GROUPS = 1;                    // of four consumer warps
   static constexpr int G = D < 64 ? D : 64, H = D / G;
   static constexpr int TK = D == 128 ? 128 : 256;     // keys per tile
