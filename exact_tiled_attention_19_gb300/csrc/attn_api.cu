@@ -1709,6 +1709,7 @@ int paged_q4_impl(const void* q, const void* k_pages, const void* v_pages, void*
   p.kp_sh = st[4];
   p.vp_sp = st[5];
   p.vp_sh = st[6];
+  p.one_over_group = 1.f / (float)group;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == ETATTN_BF16;
   cudaError_t e;

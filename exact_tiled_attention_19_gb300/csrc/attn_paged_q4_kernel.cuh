@@ -99,6 +99,8 @@ struct PagedQ4Cfg {
   static constexpr int BUDGET = MT <= 8 ? 76800 : 115712;
   static constexpr int COLS = PAIRED ? D : G;            // elements that are merged at a time
   static constexpr int MERGE_BYTES = 4 * MT * COLS * 4;  // four warps' rows
+  static constexpr int WIDE = MT * COLS > 4 * 128 ? 8 : 4, CHUNKS = COLS / WIDE;  // elements that a thread writes of them
+  static_assert(MT * CHUNKS <= 128, "");
   static constexpr int Q_PITCH = 2 * D + 16;            // padded: no bank conflicts
   static constexpr int STATE_BYTES = (2 + H) * 4 * 16 * 4;  // m, l and minima's terms: 4 warps x 16 each
   static constexpr int FIXED = MERGE_BYTES + MT * Q_PITCH + STATE_BYTES + 48;
@@ -202,16 +204,18 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 
 constexpr uint32_t kLowCodes = 0x000f000fu, kHighCodes = 0x00f000f0u;
 
-// Adds up the four warps' scaled rows, COLS elements at a time, and writes them: the
+// Adds up the four warps' rows, COLS elements at a time, normalises and writes them: the
 // output, or the unit's partial rows.  A lane holds elements 4 g .. and 32 + 4 g .. of
-// two rows (and of those 8 further down) of every group, or of its own.
+// two rows (and of those 8 further down) of every group, or of its own; a thread writes
+// WIDE elements of row `tid / CHUNKS`, of whose sum `inv` is the inverse.
 template <class C, bool BF16>
 __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const PagedUnit& w, int rows, float* merge,
                                                const float (&o)[C::PAIRED ? 1 : C::H][(C::MT + 7) / 8][2][C::G / 8],
-                                               bool whole, int64_t part_row) {
-  constexpr int G = C::G, RUN = G / 8, COLS = C::COLS;
+                                               float inv, bool whole, int64_t part_row) {
+  constexpr int G = C::G, RUN = G / 8, COLS = C::COLS, WIDE = C::WIDE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t4 = lane & 3, row0 = w.row0;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int row = tid / C::CHUNKS, c = (tid % C::CHUNKS) * WIDE;
   // Where a row's four elements x4 lie: eight lanes that store together hit eight
   // different quarters of the banks.
   auto place = [](int r, int x4) {
@@ -232,32 +236,35 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
           *reinterpret_cast<float4*>(dst + place(r, at / 4 + 2 * i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     group_barrier<C>(0);
-    for (int x = tid; x < rows * (COLS / 8); x += 128) {
-      const int r = x / (COLS / 8), c = (x % (COLS / 8)) * 8;
-      float v[8];
+    if (row < rows) {
+      float v[WIDE];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int i = 0; i < WIDE; ++i) v[i] = 0.f;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const float* src = merge + (y * C::MT + r) * COLS;
-        const float4 u0 = *reinterpret_cast<const float4*>(src + place(r, c / 4));
-        const float4 u1 = *reinterpret_cast<const float4*>(src + place(r, c / 4 + 1));
-        v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
-        v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
-      }
-      if (whole) {
-        const int rr = row0 + r, i = rr / p.group;
-        uint32_t u[4];
+        const float* src = merge + (y * C::MT + row) * COLS;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int i = 0; i < WIDE; i += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(src + place(row, (c + i) / 4));
+          v[i] += u.x, v[i + 1] += u.y, v[i + 2] += u.z, v[i + 3] += u.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < WIDE; ++i) v[i] *= inv;
+      if (whole) {
+        const int rr = w.row0 + row, i = rr / p.group;
+        uint32_t u[WIDE / 2];
+#pragma unroll
+        for (int k = 0; k < WIDE / 2; ++k)
           u[k] = BF16 ? pack_bf16x2(v[2 * k], v[2 * k + 1]) : pack_f16x2(v[2 * k], v[2 * k + 1]);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (int64_t)(w.t0 + i) * p.o_st +
-                                  (int64_t)(w.head0 + rr - i * p.group) * p.o_sh + h * COLS + c) =
-            make_uint4(u[0], u[1], u[2], u[3]);
+        uint16_t* dst = static_cast<uint16_t*>(p.o) + (int64_t)(w.t0 + i) * p.o_st +
+                        (int64_t)(w.head0 + rr - i * p.group) * p.o_sh + h * COLS + c;
+        if constexpr (WIDE == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
+        else *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
       } else {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + (part_row + r) * C::D + h * COLS + c);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        float* dst = p.part_o + (part_row + row) * C::D + h * COLS + c;
+#pragma unroll
+        for (int i = 0; i < WIDE; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
     // The next elements, or the next unit's (whose state the warps write first, and
@@ -355,13 +362,18 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     const int row0 = w.row0, rows = min(MT, w.n * p.group - row0);
     const int delta = w.Lk - w.n;
     // The tokens of the rows and the key ranges of the lane's.
-    const int tok_first = row0 / p.group, tok_last = (row0 + rows - 1) / p.group;
+    // (x beyond a token's first row is at least 1/2 / 2^16 of a token from the next one,
+    // the FP32 product less than 2^-18 of 16 off.)
+    const int tok_first = row0 / p.group;
+    const float in_token = (float)(row0 - tok_first * p.group) + 0.5f;
+    auto tok_of = [&](int x) { return tok_first + (int)((in_token + (float)x) * p.one_over_group); };
+    const int tok_last = tok_of(rows - 1);
     int row_lo[RH][2], row_hi[RH][2];
 #pragma unroll
     for (int r = 0; r < RH; ++r)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int c = min((row0 + row_at + i + 8 * r) / p.group, tok_last) + delta;
+        const int c = min(tok_of(row_at + i + 8 * r), tok_last) + delta;
         row_lo[r][i] = max(0, c - p.win_left);
         row_hi[r][i] = (int)min((int64_t)w.Lk - 1, (int64_t)c + p.win_right);
       }
@@ -776,55 +788,61 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
       for (int h = 0; h < HL; ++h) put_total(low[r][h], st_low + (h + mine) * 64 + at);
     }
     group_barrier<C>(0);
-    // Row r's largest maximum (0 for none) and its sum.
-    auto state_of = [&](int r, float& ref, float& sum) {
-      float mm = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) mm = fmaxf(mm, st_m[x * 16 + r]);
-      ref = mm == -INFINITY ? 0.f : mm;
-      sum = 0.f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) sum += st_l[x * 16 + r] * ex2_approx(st_m[x * 16 + r] - ref);
-    };
-    // The warp's rows in full: powers of two taken back, minima added.
+    // The warp's rows against the largest maximum of the four (0 for none): powers of
+    // two taken back (apart, as together they may pass FP32), minima added.
     float full_o[HL][RH][2][2 * ON];
 #pragma unroll
-    for (int r = 0; r < RH; ++r)
+    for (int r = 0; r < RH; ++r) {
+      float2 most = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 y = *reinterpret_cast<const float2*>(st_m + x * 16 + 8 * r + row_at);
+        most = make_float2(fmaxf(most.x, y.x), fmaxf(most.y, y.y));
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = 8 * r + row_at + j;
-        float ref, sum;
-        state_of(row, ref, sum);
-        const float inv = sum == 0.f ? 0.f : ex2_approx(st_m[quarter * 16 + row] - ref) / sum;  // no key: 0; a NaN sum stays one
+        const float ref = j == 0 ? most.x : most.y, f = ex2_approx(m[r][j] - (ref == -INFINITY ? 0.f : ref));
+        const float even = 0x1p24f * f, odd = 0x1p20f * f;
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
-          const float unit = 0x1p24f / lift[h], add = st_low[(h + mine) * 64 + quarter * 16 + row];
+          const float unit = __uint_as_float((254u << 23) - __float_as_uint(lift[h]));  // 1 / lift
+          const float add = st_low[(h + mine) * 64 + quarter * 16 + 8 * r + row_at + j] * f;
 #pragma unroll
           for (int n = 0; n < ON; ++n) {
-            const float2 even = parts_of(o[r][h][n][0]), odd = parts_of(o[r][h][n][1]);
-            full_o[h][r][j][2 * n] = ((j == 0 ? even.x : even.y) * unit + add) * inv;
-            full_o[h][r][j][2 * n + 1] = ((j == 0 ? odd.x : odd.y) * (unit * 0.0625f) + add) * inv;
+            const float2 x = parts_of(o[r][h][n][0]), y = parts_of(o[r][h][n][1]);
+            full_o[h][r][j][2 * n] = fmaf((j == 0 ? x.x : x.y) * even, unit, add);
+            full_o[h][r][j][2 * n + 1] = fmaf((j == 0 ? y.x : y.y) * odd, unit, add);
           }
         }
       }
+    }
     const bool whole = w.from_start && w.to_end;
     // Where this piece of the unit goes: the output, or the workspace (slot 0
     // for a unit that began earlier, slot 1 for one that begins here).
     const int64_t part_row = ((int64_t)share * 2 + (w.from_start ? 1 : 0)) * MT;
-    if (tid < rows) {
-      const int r = tid;
-      float ref, sum;
-      state_of(r, ref, sum);
-      const float lse = sum == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(sum);
-      if (!whole) {
-        p.part_lse[part_row + r] = lse;
-      } else if (p.lse != nullptr) {
-        const int rr = row0 + r, i = rr / p.group;
-        p.lse[(int64_t)(w.head0 + rr - i * p.group) * p.total_q + w.t0 + i] = lse;
+    // The sum of the row that the thread writes a part of.
+    float inv = 0.f;
+    if (tid < rows * C::CHUNKS) {
+      const int r = tid / C::CHUNKS;
+      float ref = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) ref = fmaxf(ref, st_m[x * 16 + r]);
+      if (ref == -INFINITY) ref = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sum += st_l[x * 16 + r] * ex2_approx(st_m[x * 16 + r] - ref);
+      inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: 0; a NaN sum stays one
+      if (tid % C::CHUNKS == 0) {
+        const float lse = sum == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(sum);
+        if (!whole) {
+          p.part_lse[part_row + r] = lse;
+        } else if (p.lse != nullptr) {
+          const int rr = row0 + r, i = rr / p.group;
+          p.lse[(int64_t)(w.head0 + rr - i * p.group) * p.total_q + w.t0 + i] = lse;
+        }
       }
     }
     __syncwarp();
-    paged_q4_merge<C, BF16>(p, w, rows, merge, full_o, whole, part_row);
+    paged_q4_merge<C, BF16>(p, w, rows, merge, full_o, inv, whole, part_row);
   }
 }
 

@@ -256,6 +256,7 @@ ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d128_1)
 struct PagedQ4Params : PagedParams {
   const uint8_t *k_pages, *v_pages;
   int64_t kp_sp, kp_sh, vp_sp, vp_sh;
+  float one_over_group;
 };
 
 #define ETATTN_DECLARE_PAGED_Q4_LAUNCHER(name) cudaError_t name(const PagedQ4Params& p, cudaStream_t stream);
