@@ -77,12 +77,12 @@ namespace etattn {
 template <int D_, int MT_>
 struct PagedQ4Cfg {
   static constexpr int D = D_, MT = MT_;
-  // What a unit costs next to a tile (of twice the keys for the smaller heads).  1, 2, 3 and 4 take,
-  // us for 64 ragged sequences and for 512 short ones: 4 rows of 128 40.2, 35.7, 37.0, - and 74.2,
-  // 69.2, 74.6, -; 16 rows 96, 76.9, 66.6, 68.5 and 228, 209, 196, 198; heads of 64 28.9, 30.2, 31.9, -
-  // and 61.5, 65.7, 71.3, -, 16 rows of them 47.8, 43.0, 46.1, 48.2 and 122, 117, 120, 127; of 32 26.9,
-  // 28.1, 29.6, 31.3 and 56.0, 61.5, 66.4, 73.7.
-  static constexpr int UNIT_COST = (D == 128 ? 2 : 1) + (MT == 16 ? 1 : 0);
+  // What a unit costs next to a tile (of twice the keys for the smaller heads).  1, 2 and 3 take, us for
+  // 64 ragged sequences and for 512 short ones: 4 rows of 128 38.0, 34.7, 36.0 and 69.0, 66.5, 72.8; 8
+  // rows 45.4, 39.8, 41.2 and 87.4, 79.6, 85.8; 16 rows 87.2, 71.1, 65.3 and 198, 178, 170; heads of 64
+  // 28.4, 29.8, 31.5 and 59.7, 65.0, 70.9, 16 rows of them 42.5, 42.2, 45.2 and 102, 99.2, 106; of 32
+  // 25.9, 27.2, 28.9 and 54.2, 59.4, 64.3, 16 rows 39.2, 40.8, 44.0 and 82.1, 91.9, 100.
+  static constexpr int UNIT_COST = (D == 128 ? 2 : 1) + (MT == 16 && D > 32 ? 1 : 0);
   static constexpr int GROUPS = 1;                    // of four consumer warps
   static constexpr int G = D < 64 ? D : 64, H = D / G;
   static constexpr int TK = D == 128 ? 128 : 256;     // keys per tile
