@@ -420,6 +420,28 @@ def test_scales_of_values_that_grow_and_shrink():
         assert np.all(np.abs(f64(o)[0] - ro) <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -9 * rb)
 
 
+@pytest.mark.parametrize("n,Hq,Hkv", [(3, 24, 2), (7, 5, 1), (50, 36, 3), (9, 48, 1), (130, 8, 8), (2, 2, 1)])
+@pytest.mark.parametrize("D,dt", [(32, "bf16"), (64, "f16"), (128, "bf16")])
+def test_row_tiles_across_tokens_of_any_group(n, Hq, Hkv, D, dt):
+    attend([n + 200, n, 301], n, Hq, Hkv, D, DT[dt], 16, seed=n + D)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("n", [1, 5])
+def test_values_whose_scales_are_near_the_types_largest(D, n):
+    """Scales of 2^112 and more: the power of two that takes them to FP16, times that
+    of the codes, passes FP32."""
+    lens, page = [100, 20], 16
+    k_pages, _, table, seqlens = make_cache(lens, page, 2, D, torch.bfloat16, seed=2)
+    _, v_pages, _, _ = make_cache(lens, page, 2, D, torch.bfloat16, seed=2, spread=4e34)
+    assert quantised.parts(blocks_of(v_pages), page, D, "bf16")[1].max() > 2.0 ** 113
+    q = torch.randn(2 * n, 8, D).bfloat16().cuda()
+    for shares in (1, 3):
+        o, lse = binding.attention_paged_q4(q, k_pages, v_pages, table, seqlens, num_shares=shares)
+        assert bool(o.isfinite().all())
+        check_attention(o, lse, q, k_pages, v_pages, page, table, lens, [0, n, 2 * n])
+
+
 @pytest.mark.parametrize("page", [8, 32, 128])
 @pytest.mark.parametrize("n", [1, 2, 6])
 def test_nothing_outside_a_rows_keys_reaches_it(page, n):

@@ -222,3 +222,36 @@ def test_another_stream_owns_what_it_allocates():
     stream.synchronize()
     want = quantised.extend(np.ones(9, int), lens, table, free, 8, 9)
     assert got[3].tolist() == want[4] and got[0].tolist() == want[1]
+
+
+def test_a_16_bit_cache_takes_its_pages_too():
+    """The table and lengths of an extension in the calls of the 16-bit cache: each new key
+    is where the slots say, and attention over the pages is that over the keys in a row."""
+    page, D, Hkv, S = 16, 64, 2, 3
+    table, lens = i32(np.full((S, 5), -1)), i32([0, 0, 0])
+    pages, count = stack(list(np.random.default_rng(1).permutation(15)), 15)
+    k_pages, v_pages = (torch.zeros(15, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g, rows = torch.Generator().manual_seed(0), [[[], []] for _ in range(S)]
+    for new in ([37, 5, 16], [1, 0, 1], [2, 12, 16]):
+        k, v, q = (torch.randn(sum(new), h, D, generator=g).bfloat16().cuda() for h in (Hkv, Hkv, 4))
+        _, cu, _, slots, _ = binding.paged_extend(i32(new), lens, table, pages, count, page_size=page,
+                                                  total_tokens=sum(new), seqlens_out=lens, free_count_out=count)
+        binding.paged_append(k, v, k_pages, v_pages, table, lens, cu_seqlens_q=cu)
+        for x, y in ((k, k_pages), (v, v_pages)):
+            assert torch.equal(y.transpose(1, 2).reshape(-1, Hkv, D)[slots], x)
+        o, lse = binding.attention_paged(q, k_pages, v_pages, table, lens, cu_seqlens_q=cu, max_seqlen_q=max(new))
+        at = cu.tolist()
+        for s in range(S):
+            for x, y in zip(rows[s], (k, v)):
+                x.append(y[at[s]:at[s + 1]])
+            if new[s] == 0:
+                continue
+            ks, vs = (torch.cat(x).double().repeat_interleave(2, 1) for x in rows[s])
+            sc = torch.einsum("nhd,lhd->hnl", q[at[s]:at[s + 1]].double(), ks) / 8
+            L, n = ks.shape[0], new[s]
+            seen = torch.arange(L, device="cuda") <= torch.arange(n, device="cuda")[:, None] + L - n
+            P = sc.masked_fill(~seen, -torch.inf).softmax(-1)
+            want = torch.einsum("hnl,lhd->nhd", P, vs)
+            # a rounding of the output, and one of 2^-16 of every weight (two parts)
+            bound = 2.0 ** -8 * want.abs() + 2.0 ** -14 * torch.einsum("hnl,lhd->nhd", P, vs.abs()) + 1e-6
+            assert bool(((o[at[s]:at[s + 1]].double() - want).abs() <= bound).all())
