@@ -1638,11 +1638,11 @@ int unpack_q4_impl(const void* pages, void* out, int Hkv, int D, int dtype, cons
   return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
 }
 
-// Rows of a unit: 4 (of 128 elements) or 8 (three CTAs on an SM) or 16 (two); more rows
-// are several units.
+// Rows of a unit: 4 or 8 (three CTAs on an SM) or 16 (two); more rows are several units.
+// (What 4 have of their own: the kernel's comment.)
 // (One of 32 rows, a CTA of eight consumer warps an SM, took 195 us for 8 x 32768 keys
 // and 8 new tokens where two of 16 take 180, heads of 64 98 against 89, of 32 79 against 72.)
-int paged_q4_row_tile(int64_t rows, int D) { return rows <= 4 && D == 128 ? 4 : rows <= 8 ? 8 : 16; }
+int paged_q4_row_tile(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 int paged_q4_tile_keys(int D) { return D == 128 ? 128 : 256; }  // the kernel's PagedQ4Cfg::TK
 
 int paged_q4_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
@@ -1671,7 +1671,7 @@ int paged_q4_impl(const void* q, const void* k_pages, const void* v_pages, void*
                         {seqlens_k, 4LL * num_seqs},
                         {cu_seqlens_q, 4LL * (num_seqs + 1)}};
   const int group = Hq / Hkv;
-  const int row_tile = paged_q4_row_tile((int64_t)max_seqlen_q * group, D);
+  const int row_tile = paged_q4_row_tile((int64_t)max_seqlen_q * group);
   const PagedLayout L = paged_layout(num_shares, row_tile, D);
   View vw{};
   if (num_shares > 1) {
@@ -2138,7 +2138,7 @@ size_t attn_fwd_paged_q4_workspace_size(int Hq, int Hkv, int max_seqlen_q, int D
       num_shares > kMaxShares)
     return 0;
   if (num_shares == 1 || Hq == 0 || max_seqlen_q == 0) return 0;
-  return paged_layout(num_shares, paged_q4_row_tile((int64_t)max_seqlen_q * (Hq / Hkv), D), D).total;
+  return paged_layout(num_shares, paged_q4_row_tile((int64_t)max_seqlen_q * (Hq / Hkv)), D).total;
 }
 
 int attn_fwd_paged_q4_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int max_seqlen_k, int D, int* num_shares,
@@ -2153,7 +2153,7 @@ int attn_fwd_paged_q4_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int 
     int* status = nullptr;
     if (int rc = current_device(&dev, &status, &num_sms)) return rc;
     // What the GPU runs at once, and no more shares than key tiles.
-    const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_q4_row_tile(rows, D), tk = paged_q4_tile_keys(D);
+    const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_q4_row_tile(rows), tk = paged_q4_tile_keys(D);
     const double tiles = (double)num_seqs * Hkv * (double)((rows + mt - 1) / mt) *
                          (double)std::max<int64_t>(1, (max_seqlen_k + tk - 1) / tk);
     *num_shares = (int)std::max(1.0, std::min(tiles, (mt <= 8 ? 3.0 : 2.0) * num_sms));

@@ -53,9 +53,7 @@ cudaError_t launch_rows(const PagedQ4Params& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t ETATTN_PAGED_Q4_LAUNCHER(const PagedQ4Params& p, cudaStream_t stream) {
-#if ETATTN_INST_D == 128
   if (p.row_tile == 4) return launch_rows<4>(p, stream);
-#endif
   return p.row_tile == 8 ? launch_rows<8>(p, stream) : launch_rows<16>(p, stream);
 }
 

@@ -43,13 +43,17 @@
 // passes it by 2^6 (kSlack), and by the row's own scores alone, so that no other row and
 // nothing outside the row's range changes a bit of its result.
 //
-// Up to 4 rows of 128 elements (PAIRED; a decode step of four query heads a KV head).
+// Up to 4 rows (PAIRED; a decode step of four query heads a KV head), 128 elements.
 // The right operands' columns 4 .. 7 are the same rows again, for the second group of
 // elements: a lane applies the scales of one group, not of both.  Q's operands are 0
 // in the other group's columns, so that one accumulator takes the products of both groups
 // side by side, and the two parts of a score are in neighbouring lanes; the weights'
 // likewise.  (8 x 32768 keys took 57.2 us instead of 62.7 with the kernel for 8 rows, 512 sequences
-// up to 2048 keys 77 instead of 92.)  Heads of 64 or 32 have one group, and nothing to share.
+// up to 2048 keys 77 instead of 92.)  Heads of 64 or 32 have one group: there the second columns are the
+// same rows for a warp's second half of keys (a second side, with a state of its own, as if
+// another warp had them), and every scale, exponential and transpose serves twice as many
+// keys (8 x 32768 keys, heads of 64, 34.8 to 32.0 us; of 32 27.3 to 24.8; 512 sequences 59.8 to 56.7 and 54.2
+// to 50.7).
 //
 // What bounds it.  A key and a value of D = 128 are 144 bytes, 3.6 times fewer than in 16
 // bits, and 16 of them cost a warp as many instructions as 16 bits would: the loads alone
@@ -94,11 +98,12 @@ struct PagedQ4Cfg {
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V: 18 KB, or 10 KB for D = 32
   // Three CTAs of up to 8 rows share an SM, or two of 16.
   static constexpr bool PAIRED = MT == 4;
-  static_assert(MT == 8 || MT == 16 || (PAIRED && H == 2), "");
+  static constexpr int SIDES = PAIRED && H == 1 ? 2 : 1;  // runs of keys with a state of their own in a warp
+  static_assert(MT == 8 || MT == 16 || PAIRED, "");
   static constexpr int CTAS = MT <= 8 ? 3 : 2;
   static constexpr int BUDGET = MT <= 8 ? 76800 : 115712;
   static constexpr int COLS = PAIRED ? D : G;            // elements that are merged at a time
-  static constexpr int MERGE_BYTES = 4 * MT * COLS * 4;  // four warps' rows
+  static constexpr int MERGE_BYTES = 4 * MT * SIDES * COLS * 4;  // four warps' rows
   static constexpr int WIDE = MT * COLS > 4 * 128 ? 8 : 4, CHUNKS = COLS / WIDE;  // elements that a thread writes of them
   static_assert(MT * CHUNKS <= 128, "");
   static constexpr int Q_PITCH = 2 * D + 16;            // padded: no bank conflicts
@@ -219,7 +224,7 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
   // Where a row's four elements x4 lie: eight lanes that store together hit eight
   // different quarters of the banks.
   auto place = [](int r, int x4) {
-    if (C::PAIRED) return (x4 ^ (r & 2) ^ ((x4 >> 2) & 4)) * 4;
+    if (C::PAIRED && C::H == 2) return (x4 ^ (r & 2) ^ ((x4 >> 2) & 4)) * 4;
     return (x4 ^ (r & 6)) * 4;
   };
 #pragma unroll
@@ -228,8 +233,9 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
     for (int hr = 0; hr < (C::MT + 7) / 8; ++hr)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int r = C::PAIRED ? 2 * (t4 & 1) + j : 8 * hr + 2 * t4 + j, at = (C::PAIRED ? (t4 >> 1) * G : 0) + g * 4;
-        float* dst = merge + (warp * C::MT + r) * COLS;
+        constexpr bool APART = C::PAIRED && C::H == 2;  // (its lanes have a group each; of two sides rows 4 .. are the second's)
+        const int r = APART ? 2 * (t4 & 1) + j : 8 * hr + 2 * t4 + j, at = (APART ? (t4 >> 1) * G : 0) + g * 4;
+        float* dst = merge + (warp * C::MT * C::SIDES + r) * COLS;
         const float(&v)[RUN] = o[h][hr][j];
 #pragma unroll
         for (int i = 0; i < RUN; i += 4)
@@ -241,11 +247,11 @@ __device__ __forceinline__ void paged_q4_merge(const PagedParams& p, const Paged
 #pragma unroll
       for (int i = 0; i < WIDE; ++i) v[i] = 0.f;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
+      for (int y = 0; y < 4 * C::SIDES; ++y) {
         const float* src = merge + (y * C::MT + row) * COLS;
 #pragma unroll
         for (int i = 0; i < WIDE; i += 4) {
-          const float4 u = *reinterpret_cast<const float4*>(src + place(row, (c + i) / 4));
+          const float4 u = *reinterpret_cast<const float4*>(src + place(y % C::SIDES * C::MT + row, (c + i) / 4));
           v[i] += u.x, v[i + 1] += u.y, v[i + 2] += u.z, v[i + 3] += u.w;
         }
       }
@@ -279,6 +285,8 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
   using C = PagedQ4Cfg<D, MT>;
   constexpr int G = C::G, H = C::H, NT = C::NT, RH = (MT + 7) / 8;
   constexpr bool PAIRED = C::PAIRED;
+  constexpr int SIDES = C::SIDES, NB = NT / SIDES;  // blocks of 8 keys of a side
+  constexpr int PARTS = PAIRED ? 2 : H;        // of the codes that have operands of Q of their own: groups, or sides
   constexpr int HL = PAIRED ? 1 : H;           // groups whose scales a lane applies
   constexpr int KW = G / 32, ON = G / 16;      // words of a key's group that a lane reads; blocks of 16 elements
   constexpr bool TWO = !BF16;                  // weights in two parts
@@ -308,16 +316,18 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
 
   // ------------------------------------------------ consumers
   const int quarter = warp, g = lane >> 2, t4 = lane & 3;
-  // The first of the lane's rows (of the first 8), and its group where it has one.
+  // The first of the lane's rows (of the first 8), its group or side where it has one, and
+  // the row of its state.
   const int row_at = PAIRED ? 2 * (t4 & 1) : 2 * t4, mine = PAIRED ? t4 >> 1 : 0;
+  const int mine_group = H == 2 ? mine : 0, state_at = SIDES == 2 ? 2 * t4 : row_at;
   float* st_m = reinterpret_cast<float*>(smem + C::OFF_STATE);
   float* st_l = st_m + 64;
   float* st_low = st_l + 64;
   float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
   // Q's operands, which the warp reads again for every tile (the registers are needed
   // for the values): where the rows are merged, which happens after the last tile.
-  uint4* q_ops = reinterpret_cast<uint4*>(merge) + quarter * (H * KW * RH * 32) + lane;
-  static_assert(4 * H * KW * RH * 32 * 16 <= C::MERGE_BYTES, "");
+  uint4* q_ops = reinterpret_cast<uint4*>(merge) + quarter * (PARTS * KW * RH * 32) + lane;
+  static_assert(4 * PARTS * KW * RH * 32 * 16 <= C::MERGE_BYTES, "");
   const int share = blockIdx.x;
   // Blocks of 8 keys lie in one box each.  The warp takes NT of them: neighbours in a
   // large box, or the same place of NT boxes (SPREAD), which lie a constant step apart
@@ -328,6 +338,9 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
   const int box_keys = min(1 << p.page_shift, C::TK);
   const uint32_t panel = (uint32_t)box_keys * C::PANEL;
   const int key_step = SPREAD ? box_keys : 8;
+  // Where the second part of the codes and scales lies: the other group, or the other side.
+  const uint32_t code_part = H == 2 ? panel : NB * kCodeStep, scale_part = H == 2 ? panel : NB * kScaleStep;
+  const int key_lane = g + (SIDES == 2 ? mine * NB * key_step : 0);
   int key_at, box_at, in_box;  // the latter two: where the box starts, and the block's first key in it
   if (SPREAD) {
     const int per_box = box_keys >> 3, row = quarter / per_box;  // blocks of a box; the warp's row of NT boxes
@@ -343,7 +356,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
   // The lane's part of a block: elements G/4 t4 .. of key g, with its scales.  Of values it
   // gets elements 4 g .. (and 32 + 4 g ..) of keys 2 t4 and 2 t4 + 1 by transposed loads
   // of 8 keys' 16 bytes, of which it gives one address: of two blocks, G / 32 loads each.
-  const uint32_t k_at = first + g * (G / 2) + t4 * (G / 8), s_at = first_scale + g * 4 + mine * panel;
+  const uint32_t k_at = first + g * (G / 2) + t4 * (G / 8), s_at = first_scale + g * 4 + mine * scale_part;
   const uint32_t v_at = C::TILE_BYTES + first + (lane & 7) * (G / 2) +
                         (G == 64 ? (lane >> 4) * 16 + ((lane >> 3) & 1) * kCodeStep : ((lane >> 3) & 1) * kCodeStep);
 
@@ -426,15 +439,15 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             x[h][y][i] *= up;
             sum += x[h][y][i];
           }
-          const bool own = !PAIRED || (g >> 2) == h;  // (the column's group)
-          q_ops[((h * KW + y) * RH + r) * 32] =
-              own ? make_uint4(pack_f16x2(x[h][y][0], x[h][y][4]), pack_f16x2(x[h][y][1] * 0.0625f, x[h][y][5] * 0.0625f),
-                               pack_f16x2(x[h][y][2], x[h][y][6]), pack_f16x2(x[h][y][3] * 0.0625f, x[h][y][7] * 0.0625f))
-                  : make_uint4(0, 0, 0, 0);
+          const uint4 v = make_uint4(pack_f16x2(x[h][y][0], x[h][y][4]), pack_f16x2(x[h][y][1] * 0.0625f, x[h][y][5] * 0.0625f),
+                                     pack_f16x2(x[h][y][2], x[h][y][6]), pack_f16x2(x[h][y][3] * 0.0625f, x[h][y][7] * 0.0625f));
+#pragma unroll
+          for (int part = h; part < PARTS; part += H)  // (0 in the columns of the other group, or side)
+            q_ops[((part * KW + y) * RH + r) * 32] = !PAIRED || (g >> 2) == part ? v : make_uint4(0, 0, 0, 0);
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (!PAIRED || (g >> 2) == h) total[PAIRED ? 0 : h] = sum * 0x1p-24f;
+        if (HL == H || (g >> 2) == h) total[HL == H ? h : 0] = sum * 0x1p-24f;
       }
 #pragma unroll
       for (int h = 0; h < HL; ++h) qsum[r][h] = of_rows(total[h]);
@@ -481,13 +494,13 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         const bool edge = tile0 < in_lo || tile0 + C::TK - 1 > in_hi;
         // Scores of the warp's keys, in units of 1 / back, 16 keys at a time: of key g of
         // two blocks.
-        uint64_t sc[NT][RH];
-        // The products of one group's codes with q; `first`: from 0.
+        uint64_t sc[NB][RH];
+        // The products of one part's codes with q; `first`: from 0.
         auto dots = [&](int h, int kb, const uint4(&q)[KW][RH], float(&part)[RH][4], bool first) {
           uint32_t c[2][KW];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint8_t* at = tile + k_at + (2 * kb + u) * kCodeStep + h * panel;
+            const uint8_t* at = tile + k_at + (2 * kb + u) * kCodeStep + h * code_part;
             if constexpr (KW == 2) {
               const uint2 x = *reinterpret_cast<const uint2*>(at);
               c[u][0] = x.x, c[u][KW - 1] = x.y;
@@ -514,7 +527,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             float s, mn;
-            scale_and_min<BF16>(*reinterpret_cast<const uint32_t*>(tile + s_at + (2 * kb + u) * kScaleStep + h * panel), s, mn);
+            scale_and_min<BF16>(*reinterpret_cast<const uint32_t*>(tile + s_at + (2 * kb + u) * kScaleStep + h * scale_part), s, mn);
             const uint64_t s2 = packed_pair(s, s), mn2 = packed_pair(mn, mn);
 #pragma unroll
             for (int r = 0; r < RH; ++r) {
@@ -531,18 +544,18 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             for (int r = 0; r < RH; ++r) q[y][r] = q_ops[((h * KW + y) * RH + r) * 32];
         };
         if constexpr (PAIRED) {
-          uint4 q[H][KW][RH];
+          uint4 q[PARTS][KW][RH];
 #pragma unroll
-          for (int h = 0; h < H; ++h) q_of(h, q[h]);
+          for (int h = 0; h < PARTS; ++h) q_of(h, q[h]);
 #pragma unroll
-          for (int kb = 0; kb < NT / 2; ++kb) {
+          for (int kb = 0; kb < NB / 2; ++kb) {
             float part[RH][4];
 #pragma unroll
-            for (int h = 0; h < H; ++h) dots(h, kb, q[h], part, h == 0);
+            for (int h = 0; h < PARTS; ++h) dots(h, kb, q[h], part, h == 0);
             scaled(0, kb, part);
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {  // the other group's part
+          for (int n = 0; H == 2 && n < NB; ++n) {  // the other group's part
             const float2 x = parts_of(sc[n][0]);
             sc[n][0] = add_pair(sc[n][0], packed_pair(__shfl_xor_sync(0xffffffffu, x.x, 2), __shfl_xor_sync(0xffffffffu, x.y, 2)));
           }
@@ -552,7 +565,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             uint4 q[KW][RH];
             q_of(h, q);
 #pragma unroll
-            for (int kb = 0; kb < NT / 2; ++kb) {
+            for (int kb = 0; kb < NB / 2; ++kb) {
               float part[RH][4];
               dots(h, kb, q, part, true);
               scaled(h, kb, part);
@@ -561,8 +574,8 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         }
         if (edge) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int key = key0 + n * key_step + g;
+          for (int n = 0; n < NB; ++n) {
+            const int key = key0 + n * key_step + key_lane;
 #pragma unroll
             for (int r = 0; r < RH; ++r) {
               float2 x = parts_of(sc[n][r]);
@@ -580,7 +593,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         for (int r = 0; r < RH; ++r) {
           mx[r][0] = mx[r][1] = -INFINITY;
 #pragma unroll
-          for (int n = 0; n < NT; n += 2) {
+          for (int n = 0; n < NB; n += 2) {
             const float2 x = parts_of(sc[n][r]), y = parts_of(sc[n + 1][r]);
             mx[r][0] = max3(mx[r][0], x.x, y.x);
             mx[r][1] = max3(mx[r][1], x.y, y.y);
@@ -592,15 +605,15 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         }
         // The values' scales and minima, and the largest bits of a scale (they order like
         // the numbers, none of which is negative; the minima beside them are cut off).
-        uint32_t sm[NT][HL];
+        uint32_t sm[NB][HL];
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
           uint32_t most = 0u;
 #pragma unroll
-          for (int n = 0; n < NT; n += 2) {
+          for (int n = 0; n < NB; n += 2) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-              sm[n + u][h] = *reinterpret_cast<const uint32_t*>(tile + C::TILE_BYTES + s_at + (n + u) * kScaleStep + h * panel);
+              sm[n + u][h] = *reinterpret_cast<const uint32_t*>(tile + C::TILE_BYTES + s_at + (n + u) * kScaleStep + h * scale_part);
             most = __vimax3_u16x2(most, sm[n][h], sm[n + 1][h]);
           }
           grew = grew || (int)((most & 0xffffu) >> kExpShift) > top_of(lift[h]);
@@ -631,11 +644,11 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             const int top = top_of(lift[h]);
             int now = top;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const int key = key0 + n * key_step + g, ex = (int)((sm[n][h] & 0xffffu) >> kExpShift);
+            for (int n = 0; n < NB; ++n) {
+              const int key = key0 + n * key_step + key_lane, ex = (int)((sm[n][h] & 0xffffu) >> kExpShift);
               if (ex < kExpMax && key >= any_lo && key <= any_hi) now = max(now, ex);
             }
-            if constexpr (PAIRED) {  // over the lanes of the same group
+            if constexpr (PAIRED && H == 2) {  // over the lanes of the same group
 #pragma unroll
               for (int by = 1; by < 32; by = by == 1 ? 4 : 2 * by) now = max(now, __shfl_xor_sync(0xffffffffu, now, by));
             } else {
@@ -658,7 +671,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         for (int r = 0; r < RH; ++r) {
           const uint64_t ref = packed_pair(m[r][0] == -INFINITY ? 0.f : -m[r][0], m[r][1] == -INFINITY ? 0.f : -m[r][1]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NB; ++n) {
             const float2 e = parts_of(fma_pair(sc[n][r], back[r], ref));
             sc[n][r] = packed_pair(ex2_approx(e.x), ex2_approx(e.y));
             l[r] = add_pair(l[r], sc[n][r]);
@@ -680,7 +693,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
                 if (TWO) mma16816<false>(part[r][n], v, lo[r][0], lo[r][1]);
               }
             };
-            const uint32_t from = smem_u32(tile) + v_at + 2 * kb * kCodeStep + h * panel;
+            const uint32_t from = smem_u32(tile) + v_at + 2 * kb * kCodeStep + h * code_part;
             constexpr int X = RH == 1 ? ON : 2;
 #pragma unroll
             for (int n0 = 0; n0 < ON; n0 += X) {
@@ -695,9 +708,9 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
           };
 #pragma unroll
           for (int h = 0; h < HL; ++h) {
-            uint32_t hi[NT / 2][RH][2], lo[NT / 2][RH][2];
+            uint32_t hi[NB / 2][RH][2], lo[NB / 2][RH][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NB; ++n) {
               float s, mn;
               scale_and_min<BF16>(sm[n][h], s, mn);
               mn = fmaf(s, 8.f, mn);  // what code 8 stands for
@@ -724,7 +737,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             // The sums start from -8 times the weights, which is the same for all elements.
             constexpr uint32_t kMinusEights[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
 #pragma unroll
-            for (int kb = 0; kb < NT / 2; ++kb)
+            for (int kb = 0; kb < NB / 2; ++kb)
 #pragma unroll
               for (int r = 0; r < RH; ++r) {
                 if (kb == 0) mma16816_first(base[r], kMinusEights, hi[0][r][0], hi[0][r][1]);
@@ -733,10 +746,10 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
               }
             if constexpr (PAIRED) {
 #pragma unroll
-              for (int x = 0; x < H; ++x) {
-                const uint32_t own = (g >> 2) == x ? ~0u : 0u;  // the columns of this group
+              for (int x = 0; x < PARTS; ++x) {
+                const uint32_t own = (g >> 2) == x ? ~0u : 0u;  // the columns of this group, or side
 #pragma unroll
-                for (int kb = 0; kb < NT / 2; ++kb) {
+                for (int kb = 0; kb < NB / 2; ++kb) {
                   const uint32_t a[RH][2] = {{hi[kb][0][0] & own, hi[kb][0][1] & own}};
                   const uint32_t b[RH][2] = {{TWO ? lo[kb][0][0] & own : 0u, TWO ? lo[kb][0][1] & own : 0u}};
                   products(x, kb, a, b, x == 0 && kb == 0);
@@ -744,7 +757,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
               }
             } else {
 #pragma unroll
-              for (int kb = 0; kb < NT / 2; ++kb) products(h, kb, hi[kb], lo[kb], kb == 0);
+              for (int kb = 0; kb < NB / 2; ++kb) products(h, kb, hi[kb], lo[kb], kb == 0);
             }
 #pragma unroll
             for (int r = 0; r < RH; ++r)
@@ -781,11 +794,11 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         if (g == 0) to[0] = f.x, to[1] = f.y;
       };
       // (Two lanes have a row where it is there for both groups, and write the same.)
-      const int at = quarter * 16 + 8 * r + row_at;
+      const int at = quarter * 16 + 8 * r + state_at;
       if (g == 0) st_m[at] = m[r][0], st_m[at + 1] = m[r][1];
       put_total(l[r], st_l + at);
 #pragma unroll
-      for (int h = 0; h < HL; ++h) put_total(low[r][h], st_low + (h + mine) * 64 + at);
+      for (int h = 0; h < HL; ++h) put_total(low[r][h], st_low + (h + mine_group) * 64 + at);
     }
     group_barrier<C>(0);
     // The warp's rows against the largest maximum of the four (0 for none): powers of
@@ -795,8 +808,8 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     for (int r = 0; r < RH; ++r) {
       float2 most = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float2 y = *reinterpret_cast<const float2*>(st_m + x * 16 + 8 * r + row_at);
+      for (int x = 0; x < 4 * SIDES; ++x) {
+        const float2 y = *reinterpret_cast<const float2*>(st_m + x / SIDES * 16 + x % SIDES * MT + 8 * r + row_at);
         most = make_float2(fmaxf(most.x, y.x), fmaxf(most.y, y.y));
       }
 #pragma unroll
@@ -806,7 +819,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
           const float unit = __uint_as_float((254u << 23) - __float_as_uint(lift[h]));  // 1 / lift
-          const float add = st_low[(h + mine) * 64 + quarter * 16 + 8 * r + row_at + j] * f;
+          const float add = st_low[(h + mine_group) * 64 + quarter * 16 + 8 * r + state_at + j] * f;
 #pragma unroll
           for (int n = 0; n < ON; ++n) {
             const float2 x = parts_of(o[r][h][n][0]), y = parts_of(o[r][h][n][1]);
@@ -826,10 +839,13 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
       const int r = tid / C::CHUNKS;
       float ref = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) ref = fmaxf(ref, st_m[x * 16 + r]);
+      for (int x = 0; x < 4 * SIDES; ++x) ref = fmaxf(ref, st_m[x / SIDES * 16 + x % SIDES * MT + r]);
       if (ref == -INFINITY) ref = 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) sum += st_l[x * 16 + r] * ex2_approx(st_m[x * 16 + r] - ref);
+      for (int x = 0; x < 4 * SIDES; ++x) {
+        const int at = x / SIDES * 16 + x % SIDES * MT + r;
+        sum += st_l[at] * ex2_approx(st_m[at] - ref);
+      }
       inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: 0; a NaN sum stays one
       if (tid % C::CHUNKS == 0) {
         const float lse = sum == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(sum);

@@ -38,9 +38,9 @@ def to_bits(x, dtype):
 
 def from_bits(b, dtype):
     b = np.asarray(b, np.uint16)
-    if dtype == "f16":
-        return b.view(np.float16).astype(np.float64)
-    return (b.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    with np.errstate(invalid="ignore"):  # (signalling NaN)
+        x = b.view(np.float16) if dtype == "f16" else (b.astype(np.uint32) << 16).view(np.float32)
+        return x.astype(np.float64)
 
 
 def quantise(x, dtype):

@@ -82,7 +82,7 @@ def check_append(T, Hq, Hkv, D, dtype, page, layout="pair", rope_dim=None, inter
     q, k, v = fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:]
     places = torch.randperm(num * page, generator=g)[:T]
     gone = torch.rand(T, generator=g) < 0.1
-    slots = torch.where(gone, torch.tensor(-1 - places), places).cuda()
+    slots = torch.where(gone, -1 - places, places).cuda()
     kw = {}
     if weighted:
         wq, wk = ((1 + 0.3 * torch.randn(D, generator=g)).to(dtype).cuda() for _ in range(2))
