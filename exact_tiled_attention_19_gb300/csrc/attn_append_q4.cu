@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_q4_kernel(const __gr
       pos = p.positions[t];
       ok = ok && pos >= 0 && pos < p.max_position;
     }
-    if (!ok) atomicCAS(p.status, 0, (int)kDevBadIndex);
+    if (!ok && lane == 0) atomicCAS(p.status, 0, (int)kDevBadIndex);
   }
   const int64_t page = ok ? place >> p.page_shift : 0;
   const int slot = ok ? (int)(place & (page_keys - 1)) : 0;
