@@ -22,7 +22,7 @@
 //
 // Measured (GB300, device time): 8 sequences, one token each, 3.6 us; 1000 sequences with prompts,
 // 7.0 us in one launch (11.8 by the cluster, whose barriers and exchange cost about 3 us);
-// 4000 sequences truncated 6.4 us (10.0 by the cluster); 20000 sequences, one token each, 23.2 us.
+// 4000 sequences truncated 6.4 us (10.0 by the cluster); 20000 sequences, one token each, 18.5 us.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -315,9 +315,12 @@ __global__ void __launch_bounds__(256) tables_fill_kernel(const __grid_constant_
 
 }  // namespace
 
-// Tokens and pages that one CTA takes; tokens that a cluster does before a wide launch
-// of their own is faster.
-constexpr int kOneCtaItems = 2048, kClusterTokens = 32768, kWideCtas = 304;
+// Tokens and pages that one CTA takes; tokens that a cluster does before a wide launch of
+// their own is faster: where the sums are in shared memory (in place; 4000 sequences with
+// 16000 tokens and their truncation 15.9 us by the cluster, 18.5 by two launches), and where they are
+// in memory, which eight CTAs bisect more slowly (5000 tokens 12.5 and 13.4, 16000 14.3 and 13.2,
+// 32000 18.6 and 12.8).
+constexpr int kOneCtaItems = 2048, kClusterTokens = 32768, kClusterTokensInMemory = 8192, kWideCtas = 304;
 
 cudaError_t launch_tables(const TablesParams& p0, cudaStream_t stream) {
   TablesParams p = p0;
@@ -369,7 +372,7 @@ cudaError_t launch_tables(const TablesParams& p0, cudaStream_t stream) {
     p.fill = 1;
     return small(wide, 1, 1);
   }
-  p.fill = !p.extend || p.total_tokens <= kClusterTokens;
+  p.fill = !p.extend || p.total_tokens <= kClusterTokensInMemory;
   const cudaError_t e = launch(tables_kernel, 0, kCtas, kCtas);
   if (e != cudaSuccess || p.fill) return e;
   const int64_t blocks = std::min<int64_t>((p.total_tokens + 255) / 256, 4 * kWideCtas);
