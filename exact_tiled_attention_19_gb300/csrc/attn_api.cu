@@ -1638,11 +1638,12 @@ int unpack_q4_impl(const void* pages, void* out, int Hkv, int D, int dtype, cons
   return e == cudaSuccess ? ETATTN_OK : fail_cuda(e);
 }
 
-// Rows of a unit: 4 or 8 (three CTAs on an SM) or 16 (two); more rows are several units.
+// Rows of a unit: 4, 8 or 16; more rows are several units.
 // (What 4 have of their own: the kernel's comment.)
 // (One of 32 rows, a CTA of eight consumer warps an SM, took 195 us for 8 x 32768 keys
 // and 8 new tokens where two of 16 take 180, heads of 64 98 against 89, of 32 79 against 72.)
 int paged_q4_row_tile(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+int paged_q4_ctas(int row_tile, int D) { return (row_tile == 16 ? 2 : 3) + (D == 32 ? 1 : 0); }  // PagedQ4Cfg::CTAS
 int paged_q4_tile_keys(int D) { return D == 128 ? 128 : 256; }  // the kernel's PagedQ4Cfg::TK
 
 int paged_q4_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
@@ -2156,7 +2157,7 @@ int attn_fwd_paged_q4_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int 
     const int64_t rows = (int64_t)max_seqlen_q * (Hq / Hkv), mt = paged_q4_row_tile(rows), tk = paged_q4_tile_keys(D);
     const double tiles = (double)num_seqs * Hkv * (double)((rows + mt - 1) / mt) *
                          (double)std::max<int64_t>(1, (max_seqlen_k + tk - 1) / tk);
-    *num_shares = (int)std::max(1.0, std::min(tiles, (mt <= 8 ? 3.0 : 2.0) * num_sms));
+    *num_shares = (int)std::max(1.0, std::min(tiles, paged_q4_ctas(mt, D) * (double)num_sms));
   }
   if (workspace_bytes) *workspace_bytes = attn_fwd_paged_q4_workspace_size(Hq, Hkv, max_seqlen_q, D, *num_shares);
   return ETATTN_OK;

@@ -63,12 +63,13 @@
 // conversions, scales on pairs, maxima looked at only when they matter.
 //   mma.sync and not tcgen05: a tile of 128 query rows would be 15/16 empty, and the codes would
 // have to be written to shared memory as numbers first.  Three CTAs of four consumer warps an
-// SM: two took 64.5 us where three took 62.7, four (96 registers a thread, two stages) 66.
+// SM: two took 64.5 us where three took 62.7; four (96 registers a thread, two stages) take 56.3
+// where three take 54.7.
 //
 // Measured (GB300; BF16, 32 query and 8 KV heads of 128, one new token, unless said; device
-// time; % of the measured copy bandwidth): 8 x 32768 keys 54.9 us (81 %; 57.2 before the values'
-// loads were transposed ones), in FP16 62.9; 1 x 524288 107 us (83 %); 64 sequences of 1 to 16384
-// keys 36.9 us (54 %); 16 rows (4 tokens) 8 x 32768 94 us.  The cache in 16 bits takes 164, 325 and 80 us for the first three.
+// time; % of the measured copy bandwidth): 8 x 32768 keys 54.7 us (82 %; 57.2 before the values'
+// loads were transposed ones), in FP16 61.3; 1 x 524288 104.9 us (85 %); 64 sequences of 1 to 16384
+// keys 34.9 us (57 %); 16 rows (4 tokens) 8 x 32768 93.8 us; heads of 64 31.9, of 32 24.6.  The cache in 16 bits takes 164, 325 and 80 us for the first three.
 #pragma once
 
 #include <cstdint>
@@ -85,8 +86,8 @@ struct PagedQ4Cfg {
   // 64 ragged sequences and for 512 short ones: 4 rows of 128 38.0, 34.7, 36.0 and 69.0, 66.5, 72.8; 8
   // rows 45.4, 39.8, 41.2 and 87.4, 79.6, 85.8; 16 rows 87.2, 71.1, 65.3 and 198, 178, 170; heads of 64
   // 28.4, 29.8, 31.5 and 59.7, 65.0, 70.9, 16 rows of them 42.5, 42.2, 45.2 and 102, 99.2, 106; of 32
-  // 25.9, 27.2, 28.9 and 54.2, 59.4, 64.3, 16 rows 39.2, 40.8, 44.0 and 82.1, 91.9, 100.
-  static constexpr int UNIT_COST = (D == 128 ? 2 : 1) + (MT == 16 && D > 32 ? 1 : 0);
+  // 23.2, 24.4, - and 47.0, 51.1, -, 16 rows 34.9, 34.0, - and 78.7, 76.6, -.
+  static constexpr int UNIT_COST = (D == 128 ? 2 : 1) + (MT == 16 ? 1 : 0);
   static constexpr int GROUPS = 1;                    // of four consumer warps
   static constexpr int G = D < 64 ? D : 64, H = D / G;
   static constexpr int TK = D == 128 ? 128 : 256;     // keys per tile
@@ -96,12 +97,15 @@ struct PagedQ4Cfg {
   static constexpr int ROW_BYTES = H * PANEL;
   static constexpr int TILE_BYTES = TK * ROW_BYTES;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V: 18 KB, or 10 KB for D = 32
-  // Three CTAs of up to 8 rows share an SM, or two of 16.
+  // Three CTAs of up to 8 rows share an SM, or two of 16; one more of heads of 32, whose stages are
+  // smaller (three or four, us: 64 ragged sequences 24.7 and 23.3, 512 short ones 50.9 and 47.1; 16
+  // rows, two or three, 39.2 and 34.4, 82.4 and 78.7).  With four of heads of 64 two stages are left
+  // (8 x 32768 keys 32.0 and 33.7), and three of 16 rows of them spill (FP16 58.8 and 60.5).
   static constexpr bool PAIRED = MT == 4;
   static constexpr int SIDES = PAIRED && H == 1 ? 2 : 1;  // runs of keys with a state of their own in a warp
   static_assert(MT == 8 || MT == 16 || PAIRED, "");
-  static constexpr int CTAS = MT <= 8 ? 3 : 2;
-  static constexpr int BUDGET = MT <= 8 ? 76800 : 115712;
+  static constexpr int CTAS = (MT == 16 ? 2 : 3) + (D == 32 ? 1 : 0);
+  static constexpr int BUDGET = CTAS == 4 ? 57344 : CTAS == 3 ? 76800 : 115712;
   static constexpr int COLS = PAIRED ? D : G;            // elements that are merged at a time
   static constexpr int MERGE_BYTES = 4 * MT * SIDES * COLS * 4;  // four warps' rows
   static constexpr int WIDE = MT * COLS > 4 * 128 ? 8 : 4, CHUNKS = COLS / WIDE;  // elements that a thread writes of them
