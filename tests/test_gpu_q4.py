@@ -380,6 +380,14 @@ def test_masks_and_scales(kw, n, page):
     attend([500, 64, 129, 31], n, 4, 2, 128, torch.bfloat16, page, seed=n, **kw)
 
 
+@pytest.mark.parametrize("kw", [dict(window_left=0), dict(window_left=17), dict(window_left=300),
+                                dict(causal=False, window_left=20, window_right=3), dict(causal=False)])
+@pytest.mark.parametrize("n,Hq,Hkv", [(1, 8, 2), (2, 4, 2), (4, 2, 2), (3, 1, 1)])
+@pytest.mark.parametrize("D,dt,page", [(32, "f16", 8), (64, "bf16", 64), (64, "f16", 16), (128, "f16", 16)])
+def test_masks_of_up_to_four_rows(kw, n, Hq, Hkv, D, dt, page):
+    attend([700, 64, 129, 260, n], n, Hq, Hkv, D, DT[dt], page, seed=n, **kw)
+
+
 def test_ragged_new_tokens_and_empty_rows():
     # No new token; more new tokens than keys (rows without a key); no keys at all.
     attend([40, 300, 3, 0, 150], None, 8, 2, 64, torch.float16, 16, cu=[0, 0, 3, 8, 9, 11], seed=3)
