@@ -69,7 +69,8 @@
 // Measured (GB300; BF16, 32 query and 8 KV heads of 128, one new token, unless said; device
 // time; % of the measured copy bandwidth): 8 x 32768 keys 54.7 us (82 %; 57.2 before the values'
 // loads were transposed ones), in FP16 61.3; 1 x 524288 104.9 us (85 %); 64 sequences of 1 to 16384
-// keys 34.9 us (57 %); 16 rows (4 tokens) 8 x 32768 93.8 us; heads of 64 31.9, of 32 24.6.  The cache in 16 bits takes 164, 325 and 80 us for the first three.
+// keys 34.9 us (57 %); 16 rows (4 tokens) 8 x 32768 93.8 us; heads of 64 31.9, of 32 24.6.  The
+// cache in 16 bits takes 164, 325 and 80 us for the first, the second and the 64 sequences.
 #pragma once
 
 #include <cstdint>
@@ -97,13 +98,13 @@ struct PagedQ4Cfg {
   static constexpr int ROW_BYTES = H * PANEL;
   static constexpr int TILE_BYTES = TK * ROW_BYTES;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V: 18 KB, or 10 KB for D = 32
+  static constexpr bool PAIRED = MT == 4;
+  static constexpr int SIDES = PAIRED && H == 1 ? 2 : 1;  // runs of keys with a state of their own in a warp
+  static_assert(MT == 8 || MT == 16 || PAIRED, "");
   // Three CTAs of up to 8 rows share an SM, or two of 16; one more of heads of 32, whose stages are
   // smaller (three or four, us: 64 ragged sequences 24.7 and 23.3, 512 short ones 50.9 and 47.1; 16
   // rows, two or three, 39.2 and 34.4, 82.4 and 78.7).  With four of heads of 64 two stages are left
   // (8 x 32768 keys 32.0 and 33.7), and three of 16 rows of them spill (FP16 58.8 and 60.5).
-  static constexpr bool PAIRED = MT == 4;
-  static constexpr int SIDES = PAIRED && H == 1 ? 2 : 1;  // runs of keys with a state of their own in a warp
-  static_assert(MT == 8 || MT == 16 || PAIRED, "");
   static constexpr int CTAS = (MT == 16 ? 2 : 3) + (D == 32 ? 1 : 0);
   static constexpr int BUDGET = CTAS == 4 ? 57344 : CTAS == 3 ? 76800 : 115712;
   static constexpr int COLS = PAIRED ? D : G;            // elements that are merged at a time
