@@ -28,10 +28,13 @@
 // Precision.  q's rows are scaled by powers of two so that their largest element
 // is within 2^14 .. 2^15, and held as FP16: exact for both input types (elements below
 // 2^-29 of the largest lose bits).  Scores, maxima, sums, minima terms and accumulators are
-// FP32.  Weights times scales, P s, are scaled by a power of two per group, which
-// follows the largest scale that the warp has seen, and rounded to FP16: in two
-// parts of together 2^-21 for FP16 outputs, in one for BF16 ones, whose 2^-12 is an
-// eighth of the output's own rounding.  The tensor core cuts off what falls below an
+// FP32.  Weights times scales, P s, are multiplied by a power of two per row and group, which
+// takes the largest P s that the row has seen in the warp to 2^5.5 or more (2^4.5 right after
+// larger scores), and rounded to FP16: in two parts of together 2^-21 for FP16 outputs, in one
+// for BF16 ones, whose 2^-11 is an eighth of the output's own rounding (two there take 62.5 us
+// where one takes 55.6 for 8 x 32768 keys, 128 and 98 with 16 rows; with one, outputs are up to 1.02 times
+// as far from 64 bits as those of FP32 weights).  A P s below 2^-19 of the row's largest loses bits, by
+// 2^-28 of that at most.  The tensor core cuts off what falls below an
 // accumulator's last bit, always downwards, and codes are never negative, so a
 // running sum would drift.  A tile's products with V therefore start anew and are added to
 // the running sums in FP32; and they start from -8 times the sum of the tile's weights, so
@@ -40,8 +43,12 @@
 // as far from 64 bits as a rounding of the exact ones with one running sum; in FP16 2.9 times
 // with tiles that start from 0, 1.15 times now.
 //   A row's weights are taken against a reference m that is set again only when a score
-// passes it by 2^6 (kSlack), and by the row's own scores alone, so that no other row and
-// nothing outside the row's range changes a bit of its result.
+// passes it by 2^6 (kSlack), and the power of two when a P s may pass what FP16 holds.  Both go by
+// the row's own scores, and by the scales of keys that it reads times their weights, so that no
+// other row and nothing outside the row's range changes a bit of its result, and a key of a large
+// scale that counts for nothing in a row takes nothing from its others.  (One power of two for all
+// rows of a warp, by the scales alone, lost the rows' other keys where one had values 2^30 times as
+// large; it took 54.7 us for 8 x 32768 keys where a row's own takes 55.6, 16 rows 93.6 and 97.8.)
 //
 // Up to 4 rows (PAIRED; a decode step of four query heads a KV head), 128 elements.
 // The right operands' columns 4 .. 7 are the same rows again, for the second group of
@@ -295,6 +302,9 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
   constexpr int HL = PAIRED ? 1 : H;           // groups whose scales a lane applies
   constexpr int KW = G / 32, ON = G / 16;      // words of a key's group that a lane reads; blocks of 16 elements
   constexpr bool TWO = !BF16;                  // weights in two parts
+  // Rows' key ranges are kept where there are registers for them, or made again at the edges (4
+  // rows 55.7 and 56.0 us, 8 rows 63.2 and 61.5, 16 rows 100.3 and 97.9).
+  constexpr bool RANGES = PAIRED;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
@@ -378,7 +388,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     const PagedUnit w = *reinterpret_cast<const PagedUnit*>(smem + C::OFF_UNIT);
     if (w.tiles == 0) return;
     const int row0 = w.row0, rows = min(MT, w.n * p.group - row0);
-    const int delta = w.Lk - w.n;
+    const int delta = w.Lk - w.n, Lk = w.Lk;
     // The tokens of the rows and the key ranges of the lane's.
     // (x beyond a token's first row is at least 1/2 / 2^16 of a token from the next one,
     // the FP32 product less than 2^-18 of 16 off.)
@@ -386,21 +396,20 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
     const float in_token = (float)(row0 - tok_first * p.group) + 0.5f;
     auto tok_of = [&](int x) { return tok_first + (int)((in_token + (float)x) * p.one_over_group); };
     const int tok_last = tok_of(rows - 1);
-    int row_lo[RH][2], row_hi[RH][2];
-#pragma unroll
-    for (int r = 0; r < RH; ++r)
+    int row_lo[RANGES ? RH : 1][2], row_hi[RANGES ? RH : 1][2];
+    auto ranges = [&](int r) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int c = min(tok_of(row_at + i + 8 * r), tok_last) + delta;
-        row_lo[r][i] = max(0, c - p.win_left);
-        row_hi[r][i] = (int)min((int64_t)w.Lk - 1, (int64_t)c + p.win_right);
+        row_lo[RANGES ? r : 0][i] = max(0, c - p.win_left);
+        row_hi[RANGES ? r : 0][i] = (int)min((int64_t)Lk - 1, (int64_t)c + p.win_right);
       }
-    // Keys in [in_lo, in_hi] are read by every row, those outside
-    // [any_lo, any_hi] by none.
+    };
+#pragma unroll
+    for (int r = 0; RANGES && r < RH; ++r) ranges(r);
+    // Keys in [in_lo, in_hi] are read by every row.
     const int in_lo = max(0, tok_last + delta - p.win_left);
     const int in_hi = (int)min((int64_t)w.Lk - 1, (int64_t)tok_first + delta + p.win_right);
-    const int any_lo = max(0, tok_first + delta - p.win_left);
-    const int any_hi = (int)min((int64_t)w.Lk - 1, (int64_t)tok_last + delta + p.win_right);
 
     // Q's operands: rows scaled by 2^up; their groups' sums (in units of 2^-24), and
     // what brings a score back.  Rows past the last hold anything, and nothing of
@@ -478,16 +487,25 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
         for (int n = 0; n < ON; ++n) o[r][h][n][0] = o[r][h][n][1] = 0;
       }
     }
-    // The largest exponent of a value's scale so far, per group, and the power of two
-    // that takes scales below it, times the largest weight, to 2^15.
-    constexpr int kExpShift = BF16 ? 7 : 10, kExpMax = BF16 ? 255 : 31, kExpBias = BF16 ? 127 : 15;
-    constexpr int kExpMin = BF16 ? 14 : 0;  // (so that the power of two is one in FP32)
-    constexpr int kLift = 127 + 14 - (int)kSlack + kExpBias;
-    float lift[HL];
-    auto lift_of = [](int x) { return __uint_as_float((uint32_t)(kLift - x) << 23); };
-    auto top_of = [](float f) { return kLift - (int)(__float_as_uint(f) >> 23); };
+    // What P s is multiplied by before it becomes FP16: a new one takes the row's largest so far to
+    // 2^5.5 .. 2^7.5, and it is set again when a P s may pass 2^15.5.  `lifts`: two rows' as BF16
+    // numbers, the first's in the low half.
+    constexpr float kPre = BF16 ? 0x1p-8f : 1.f;  // of scales beforehand, so that P s stays within FP32
+    constexpr int kExpShift = BF16 ? 7 : 10, kExpMax = BF16 ? 255 : 31;
+    // P = 2^x, a scale's exponent E and that of the power of two: x + E + lift - kBias is the product's.
+    constexpr int kBias = BF16 ? 127 + 127 + 8 : 15 + 127, kLiftTo = 6, kLiftPast = 14, kLiftMost = 247;
+    constexpr int kMagic = 0x4b000000;  // 2^23 as a number: whole numbers beside it are its lowest bits
+    uint32_t lifts[RH][HL];
+    int top[HL];  // the largest exponent of a scale that passes nothing in the lane's rows whatever its weight
 #pragma unroll
-    for (int h = 0; h < HL; ++h) lift[h] = lift_of(kExpMin);
+    for (int h = 0; h < HL; ++h) {
+      top[h] = -1;
+#pragma unroll
+      for (int r = 0; r < RH; ++r) lifts[r][h] = (uint32_t)kLiftMost << 23 | kLiftMost << 7;
+    }
+    auto lift_of = [&](int h, int r, int i) { return __uint_as_float(i == 0 ? lifts[r][h] << 16 : lifts[r][h] & 0xffff0000u); };
+    auto power = [](int biased) { return biased <= 0 ? 0.f : __uint_as_float((uint32_t)biased << 23); };
+    auto number = [](int x) { return __uint_as_float((uint32_t)(kMagic + x)); };
 
     for (int x = 0; x < w.tiles; ++x) {
       const int tile0 = (w.tile + x) * C::TK, key0 = tile0 + key_at;
@@ -577,21 +595,39 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             }
           }
         }
+        // Whether what code 8 of a key that not all rows read stands for is not finite: a weight of 0
+        // would not take it away.  (What lies in slots of nobody's may be anything.)
+        bool odd = false;
         if (edge) {
 #pragma unroll
           for (int n = 0; n < NB; ++n) {
             const int key = key0 + n * key_step + key_lane;
 #pragma unroll
-            for (int r = 0; r < RH; ++r) {
+            for (int h = 0; h < HL; ++h) {
+              float s, mn;
+              scale_and_min<BF16>(*reinterpret_cast<const uint32_t*>(tile + C::TILE_BYTES + s_at + n * kScaleStep + h * scale_part), s, mn);
+              odd = odd || (!(fabsf(fmaf(s, 8.f, mn)) < INFINITY) && (key < in_lo || key > in_hi));
+            }
+          }
+          odd = __any_sync(0xffffffffu, odd);
+#pragma unroll
+          for (int r = 0; r < RH; ++r) {
+            if constexpr (!RANGES) ranges(r);
+            const int(&lo)[2] = row_lo[RANGES ? r : 0], (&hi)[2] = row_hi[RANGES ? r : 0];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              const int key = key0 + n * key_step + key_lane;
               float2 x = parts_of(sc[n][r]);
-              if (key < row_lo[r][0] || key > row_hi[r][0]) x.x = -INFINITY;
-              if (key < row_lo[r][1] || key > row_hi[r][1]) x.y = -INFINITY;
+              if (key < lo[0] || key > hi[0]) x.x = -INFINITY;
+              if (key < lo[1] || key > hi[1]) x.y = -INFINITY;
               sc[n][r] = packed_pair(x.x, x.y);
             }
           }
         }
         // Whether some score passes the reference that weights are taken against by more
-        // than 2^kSlack allows.
+        // than 2^kSlack allows, or a scale is so large that with such a weight P s might pass what
+        // FP16 holds (scales' bits order like the numbers, none of which is negative; the minima
+        // beside them are cut off).
         float mx[RH][2];
         bool grew = false;
 #pragma unroll
@@ -603,71 +639,130 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             mx[r][0] = max3(mx[r][0], x.x, y.x);
             mx[r][1] = max3(mx[r][1], x.y, y.y);
           }
-          const float2 f = parts_of(back[r]);
-          mx[r][0] *= f.x;
-          mx[r][1] *= f.y;
-          grew = grew || mx[r][0] > m[r][0] + kSlack || mx[r][1] > m[r][1] + kSlack;
+          const float2 f = parts_of(back[r]);  // (NaN while there was no key: not larger)
+          grew = grew || fmaf(mx[r][0], f.x, -m[r][0]) > kSlack || fmaf(mx[r][1], f.y, -m[r][1]) > kSlack;
         }
-        // The values' scales and minima, and the largest bits of a scale (they order like
-        // the numbers, none of which is negative; the minima beside them are cut off).
-        uint32_t sm[NB][HL];
+        uint32_t sm[NB][HL];  // the values' scales and minima
+        int most[HL];
+        bool large = false;
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
-          uint32_t most = 0u;
+          uint32_t bits = 0u;
 #pragma unroll
           for (int n = 0; n < NB; n += 2) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
               sm[n + u][h] = *reinterpret_cast<const uint32_t*>(tile + C::TILE_BYTES + s_at + (n + u) * kScaleStep + h * scale_part);
-            most = __vimax3_u16x2(most, sm[n][h], sm[n + 1][h]);
+            bits = __vimax3_u16x2(bits, sm[n][h], sm[n + 1][h]);
           }
-          grew = grew || (int)((most & 0xffffu) >> kExpShift) > top_of(lift[h]);
+          most[h] = (int)((bits & 0xffffu) >> kExpShift);
+          large = large || most[h] > top[h];
         }
-        if (__any_sync(0xffffffffu, grew)) {
-          float f[RH][2];
-#pragma unroll
-          for (int r = 0; r < RH; ++r) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              // By this row's own scores alone: what brought the warp here may be another's.
-              float mn = mx[r][i];
-#pragma unroll
-              for (int by = 4; by < 32; by <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, by));
-              const bool set = mn > m[r][i] + kSlack;
-              f[r][i] = set ? ex2_approx(m[r][i] - mn) : 1.f;
-              if (set) m[r][i] = mn;
-            }
-            const uint64_t f2 = packed_pair(f[r][0], f[r][1]);
-            l[r] = mul_pair(l[r], f2);
-#pragma unroll
-            for (int h = 0; h < HL; ++h) low[r][h] = mul_pair(low[r][h], f2);
-          }
+        if (__any_sync(0xffffffffu, grew || large)) {
+          // With the weights that the lane has: its largest score of every row, its largest scale.
 #pragma unroll
           for (int h = 0; h < HL; ++h) {
-            // Of keys that some row reads, and of finite scales alone: others (of unused
-            // slots, say) would leave no bits to the rest.
-            const int top = top_of(lift[h]);
-            int now = top;
+            float past = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-              const int key = key0 + n * key_step + key_lane, ex = (int)((sm[n][h] & 0xffffu) >> kExpShift);
-              if (ex < kExpMax && key >= any_lo && key <= any_hi) now = max(now, ex);
-            }
-            if constexpr (PAIRED && H == 2) {  // over the lanes of the same group
+            for (int r = 0; r < RH; ++r)
 #pragma unroll
-              for (int by = 1; by < 32; by = by == 1 ? 4 : 2 * by) now = max(now, __shfl_xor_sync(0xffffffffu, now, by));
+              for (int i = 0; i < 2; ++i)
+                past = fmaxf(past, fmaf(mx[r][i], i == 0 ? parts_of(back[r]).x : parts_of(back[r]).y, -m[r][i]) +
+                                       number(__float_as_uint(lift_of(h, r, i)) >> 23));
+            grew = grew || __float_as_int(past) + most[h] >= kMagic + kLiftPast + kBias;
+          }
+          if (__any_sync(0xffffffffu, grew)) {
+            // Row by row, by its own scores and the scales of keys that it reads alone: what
+            // brought the warp here may be another's.
+            uint64_t exps[NB][HL];  // the scales' exponents (0 for NaN: such a row is NaN whatever its lift)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int h = 0; h < HL; ++h) {
+                const int ex = (int)((sm[n][h] & 0xffffu) >> kExpShift);
+                const float e = number(ex < kExpMax ? ex : 0);
+                exps[n][h] = packed_pair(e, e);
+              }
+#pragma unroll
+            for (int h = 0; h < HL; ++h) top[h] = kExpMax;
+            // The largest exponent of P s of either row, in a half each.
+            auto far_of = [&](int h, int r) {
+              float2 far = make_float2(0x1p23f, 0x1p23f);
+              const uint64_t ref = packed_pair(m[r][0] == -INFINITY ? 0.f : -m[r][0], m[r][1] == -INFINITY ? 0.f : -m[r][1]);
+#pragma unroll
+              for (int n = 0; n < NB; n += 2) {
+                const float2 e = parts_of(add_pair(fma_pair(sc[n][r], back[r], ref), exps[n][h]));
+                const float2 d = parts_of(add_pair(fma_pair(sc[n + 1][r], back[r], ref), exps[n + 1][h]));
+                far = make_float2(max3(far.x, e.x, d.x), max3(far.y, e.y, d.y));
+              }
+              uint32_t both = __byte_perm(__float_as_uint(far.x), __float_as_uint(far.y), 0x5410);
+#pragma unroll
+              for (int by = 4; by < 32; by <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, by));
+              return both;
+            };
+            auto set_lifts = [&](int h, int r, const int(&now)[2]) {
+              lifts[r][h] = (uint32_t)now[0] << 7 | (uint32_t)now[1] << 23;
+#pragma unroll
+              for (int i = 0; i < 2; ++i)  // (not for a row that is nobody's)
+                if (m[r][i] != INFINITY) top[h] = min(top[h], kLiftPast - (int)kSlack + kBias - now[i]);
+            };
+            if (x == 0) {  // nothing to scale yet
+#pragma unroll
+              for (int r = 0; r < RH; ++r) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  float mn = mx[r][i];
+#pragma unroll
+                  for (int by = 4; by < 32; by <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, by));
+                  m[r][i] = fmaxf(m[r][i], mn * (i == 0 ? parts_of(back[r]).x : parts_of(back[r]).y));
+                }
+#pragma unroll
+                for (int h = 0; h < HL; ++h) {
+                  const uint32_t far = far_of(h, r);
+                  set_lifts(h, r, {min(kLiftMost, kLiftTo + kBias - (int)(far & 0xffffu)), min(kLiftMost, kLiftTo + kBias - (int)(far >> 16))});
+                }
+              }
             } else {
-              now = __reduce_max_sync(0xffffffffu, now);
-            }
-            const float down = now - top > 126 ? 0.f : __uint_as_float((uint32_t)(127 - (now - top)) << 23);
-            lift[h] = lift_of(now);
 #pragma unroll
-            for (int r = 0; r < RH; ++r) {
-              const uint64_t f2 = packed_pair(f[r][0] * down, f[r][1] * down);
+              for (int r = 0; r < RH; ++r) {
+                float part[2];  // 2^(m - its new value) is part, 0.5 .. 1, times 2^-up
+                int up[2];
 #pragma unroll
-              for (int n = 0; n < ON; ++n)
+                for (int i = 0; i < 2; ++i) {
+                  float mn = mx[r][i];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) o[r][h][n][i] = mul_pair(o[r][h][n][i], f2);
+                  for (int by = 4; by < 32; by <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, by));
+                  const float f = i == 0 ? parts_of(back[r]).x : parts_of(back[r]).y;
+                  const bool set = fmaf(mn, f, -m[r][i]) > kSlack;
+                  mn *= f;
+                  up[i] = set ? (int)fminf(mn - m[r][i], 1000.f) : 0;
+                  part[i] = set ? ex2_approx(m[r][i] - mn + (float)up[i]) : 1.f;
+                  if (set) m[r][i] = mn;
+                }
+                const uint64_t f2 = packed_pair(part[0] * power(127 - up[0]), part[1] * power(127 - up[1]));
+                l[r] = mul_pair(l[r], f2);
+#pragma unroll
+                for (int h = 0; h < HL; ++h) {
+                  low[r][h] = mul_pair(low[r][h], f2);
+                  const uint32_t far = far_of(h, r);
+                  float by[2];
+                  int now[2];
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const int was = (int)(__float_as_uint(lift_of(h, r, i)) >> 23), e = (int)(i == 0 ? far & 0xffffu : far >> 16);
+                    // The largest P s so far fell by `up` powers of two, so that there is room above it.
+                    now[i] = min(was + up[i], kLiftMost);
+                    if (now[i] + e > kLiftPast + kBias) now[i] = kLiftTo + kBias - e;
+                    by[i] = part[i] * power(127 - up[i] + now[i] - was);
+                  }
+                  set_lifts(h, r, now);
+                  const uint64_t o2 = packed_pair(by[0], by[1]);
+#pragma unroll
+                  for (int n = 0; n < ON; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) o[r][h][n][i] = mul_pair(o[r][h][n][i], o2);
+                }
+              }
             }
           }
         }
@@ -682,9 +777,9 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             l[r] = add_pair(l[r], sc[n][r]);
           }
         }
-        // O^T += codes^T (P s)^T, and P m, group by group.  EDGE: a key that the row does
-        // not read may have any scale.
-        auto values = [&](auto EDGE) {
+        // O^T += codes^T (P s)^T, and P m, group by group.  ODD: a key that the row does
+        // not read may have any scale and minimum.
+        auto values = [&](auto ODD) {
           float part[RH][ON][4], base[RH][4];
           // Codes of one group and 16 keys with the weights; `first`: from `base`.
           auto products = [&](int h, int kb, const uint32_t(&hi)[RH][2], const uint32_t(&lo)[RH][2], bool first) {
@@ -714,22 +809,26 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
 #pragma unroll
           for (int h = 0; h < HL; ++h) {
             uint32_t hi[NB / 2][RH][2], lo[NB / 2][RH][2];
+            uint64_t lift[RH];
+#pragma unroll
+            for (int r = 0; r < RH; ++r) lift[r] = packed_pair(lift_of(h, r, 0), lift_of(h, r, 1));
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
               float s, mn;
               scale_and_min<BF16>(sm[n][h], s, mn);
               mn = fmaf(s, 8.f, mn);  // what code 8 stands for
-              s *= lift[h];
+              s *= kPre;
               const uint64_t s2 = packed_pair(s, s), mn2 = packed_pair(mn, mn);
 #pragma unroll
               for (int r = 0; r < RH; ++r) {
-                float2 ws = parts_of(mul_pair(sc[n][r], s2));
-                if constexpr (decltype(EDGE)::value) {
-                  const float2 e = parts_of(sc[n][r]);
-                  float2 wm = parts_of(mul_pair(sc[n][r], mn2));
-                  if (e.x == 0.f) ws.x = wm.x = 0.f;
-                  if (e.y == 0.f) ws.y = wm.y = 0.f;
-                  low[r][h] = add_pair(low[r][h], packed_pair(wm.x, wm.y));
+                // (In this order: a scale alone may be too large for the row's lift, where its weight is small.)
+                float2 ws = parts_of(mul_pair(mul_pair(sc[n][r], s2), lift[r]));
+                if constexpr (decltype(ODD)::value) {
+                  const float2 e = parts_of(sc[n][r]), was = parts_of(low[r][h]);
+                  float2 now = parts_of(fma_pair(sc[n][r], mn2, low[r][h]));
+                  if (e.x == 0.f) ws.x = 0.f, now.x = was.x;
+                  if (e.y == 0.f) ws.y = 0.f, now.y = was.y;
+                  low[r][h] = packed_pair(now.x, now.y);
                 } else {
                   low[r][h] = fma_pair(sc[n][r], mn2, low[r][h]);
                 }
@@ -774,7 +873,7 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
             seen |= __float_as_uint(part[0][0][0]) | __float_as_uint(part[0][ON - 1][0]);
           }
         };
-        if (edge) values(std::true_type{});
+        if (odd) values(std::true_type{});
         else values(std::false_type{});
       }
       // (Without having waited the warp gives nothing back: the stage's load may be on its way.)
@@ -820,10 +919,10 @@ __global__ void __launch_bounds__(PagedQ4Cfg<D, MT>::THREADS, PagedQ4Cfg<D, MT>:
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float ref = j == 0 ? most.x : most.y, f = ex2_approx(m[r][j] - (ref == -INFINITY ? 0.f : ref));
-        const float even = 0x1p24f * f, odd = 0x1p20f * f;
+        const float even = 0x1p24f / kPre * f, odd = 0x1p20f / kPre * f;
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
-          const float unit = __uint_as_float((254u << 23) - __float_as_uint(lift[h]));  // 1 / lift
+          const float unit = __uint_as_float((254u << 23) - __float_as_uint(lift_of(h, r, j)));  // 1 / its power of two
           const float add = st_low[(h + mine_group) * 64 + quarter * 16 + 8 * r + state_at + j] * f;
 #pragma unroll
           for (int n = 0; n < ON; ++n) {

@@ -566,7 +566,9 @@ int attn_paged_unpack_q4(const void* pages, void* out, int Hkv, int D, int dtype
  * attn_fwd_paged_q4_plan for workspace and num_shares.  A page out of range is
  * recorded, and the rows of that sequence mean nothing.  Elements of q above 2^110
  * in size give no meaningful row.  A key whose weight is below 2^-126 may count as
- * one that is not read.
+ * one that is not read.  Weights times values' scales are held to 2^-11 of themselves (BF16)
+ * or 2^-21 (FP16) or, where that is more, 2^-28 of the row's largest; a row's result does not
+ * depend on other rows, or on keys that it does not read.
  */
 int attn_fwd_paged_q4(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
                       const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,
