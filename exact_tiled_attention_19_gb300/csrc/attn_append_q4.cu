@@ -125,14 +125,18 @@ __device__ __forceinline__ Quant quant_of(uint32_t extreme) {
   float mn, mx;
   if (BF16) unpack_bf16x2(extreme, mn, mx);
   else unpack_f16x2(extreme, mn, mx);
-  const float span = -mx - mn;
+  // The spread, and whether it is above its rounding to FP32 (in FP16 it is exact, in BF16 a
+  // small minimum beside a large maximum may fall below it).
+  const float span = __fsub_rn(-mx, mn);
+  const bool above = BF16 && two_sum(-mx, -mn).lo > 0.f;
   // The product is off by a few 2^-24, so its rounding by a step of the 16-bit type at
   // most; 15 s is exact in FP32 and tells.
+  auto covers = [&](uint32_t scale) { return 15.f * from16<BF16>(scale) > span || (15.f * from16<BF16>(scale) == span && !above); };
   uint32_t b = (BF16 ? pack_bf16x2(span * (1.f / 15.f), 0.f) : pack_f16x2(span * (1.f / 15.f), 0.f)) & 0xffffu;
-  if (15.f * from16<BF16>(b) < span) ++b;
-  else if (b > 0 && 15.f * from16<BF16>(b - 1) >= span) --b;
-  // Code 15 must not stand for more than the type holds.
-  if (fmaf(15.f, from16<BF16>(b), mn) > (BF16 ? 0x1.fep127f : 65504.f)) --b;
+  if (!covers(b)) ++b;
+  else if (b > 0 && covers(b - 1)) --b;
+  // Code 15 must not stand for more than the type holds (the difference is exact where it decides).
+  if (mn > (BF16 ? 0x1.fep127f : 65504.f) - 15.f * from16<BF16>(b)) --b;
   Quant z;
   z.word = __byte_perm(b, extreme, 0x5410);
   z.min = mn;

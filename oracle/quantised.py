@@ -52,12 +52,16 @@ def quantise(x, dtype):
         span = high - low
         bad = ~np.isfinite(x).all(-1) | ~np.isfinite(np.where(np.isfinite(span), span, np.inf).astype(np.float32))
         span = np.where(bad, 0.0, span)
-        low = np.where(bad, 0.0, low)
+        low, high = np.where(bad, 0.0, low), np.where(bad, 0.0, high)
+        # The spread's own rounding to 64 bits (Knuth's error-free sum): 15 s is exact.
+        back = high - span
+        above = (high - (span + back)) + (back - low) > 0
+        covers = lambda s: (15 * s > span) | ((15 * s == span) & ~above)  # noqa: E731
         s = rounded(span / 15, dtype)
-        s = np.where(15 * s < span, s + step(s, dtype), s)
+        s = np.where(covers(s), s, s + step(s, dtype))
         below = s - step(s * (1 - 2.0 ** -20), dtype)
-        assert np.all((s == 0) | (15 * below < span))  # the smallest that does
-        s = np.where(15 * s + low > _MAX[dtype], below, s)
+        assert np.all((s == 0) | ~covers(below))  # the smallest that does
+        s = np.where(low > _MAX[dtype] - 15 * s, below, s)  # (the difference is exact where it decides)
         c = np.where(s[..., None] > 0, np.round((np.where(bad[..., None], 0.0, x) - low[..., None]) /
                                                 np.where(s > 0, s, 1.0)[..., None]), 0.0)
     return c.astype(np.uint8), np.where(bad, np.nan, s), np.where(bad, np.nan, low)
