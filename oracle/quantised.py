@@ -15,8 +15,9 @@ _MAX = {"f16": 65504.0, "bf16": float.fromhex("0x1.fep127")}
 def step(x, dtype):
     """The distance of neighbouring numbers of the type at x."""
     bits, least = _TYPES[dtype]
-    _, e = np.frexp(np.asarray(x, np.float64))
-    return np.ldexp(1.0, np.maximum(e - bits, least))
+    x = np.asarray(x, np.float64)
+    _, e = np.frexp(x)
+    return np.ldexp(1.0, np.where(x == 0, least, np.maximum(e - bits, least)))
 
 
 def rounded(x, dtype):

@@ -36,3 +36,15 @@ def test_scales_are_those_of_rational_arithmetic(dt):
         x[3] = high
         _, s, m = Q.quantise(x, dt)
         assert s == scale_of(low, high, dt) and m == low
+
+
+@pytest.mark.parametrize("dt,least", [("f16", 2.0 ** -24), ("bf16", 2.0 ** -133)])
+def test_groups_of_the_smallest_numbers(dt, least):
+    """Spreads below 15 of the smallest number have the smallest scale, not none."""
+    assert Q.step(0.0, dt) == least and Q.step(least, dt) == least
+    for high, low in ((1, 0), (1, -1), (15, 0), (16, 0), (3, -3), (0, 0)):
+        x = np.full(64, low * least)
+        x[5] = high * least
+        c, s, m = Q.quantise(x, dt)
+        assert s == -(-(high - low) // 15) * least and m == low * least
+        assert np.array_equal(Q.values(c[None], s[None], m[None])[0], x) or high - low > 15
