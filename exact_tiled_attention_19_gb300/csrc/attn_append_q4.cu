@@ -245,19 +245,49 @@ __device__ __forceinline__ void key_row(const uint64_t (&w)[8], const uint64_t (
   }
   Two r{1.f, 0.f};
   if (norm) {
-    uint64_t hi = mul_pair(x[0], x[0]), lo = 0;  // (squares of 16-bit numbers are exact)
+    Two ss;
+    bool zero = false;  // an infinite element: 1 / sqrt is 0
+#pragma unroll 1
+    for (bool again = false;; again = true) {
+      uint64_t hi = mul_pair(x[0], x[0]), lo = 0;  // (exact within FP32's range)
 #pragma unroll
-    for (int j = 1; j < 8; ++j) {
-      uint64_t e;
-      two_sum_pair(hi, mul_pair(x[j], x[j]), hi, e);
-      lo = add_pair(lo, e);
+      for (int j = 1; j < 8; ++j) {
+        uint64_t e;
+        two_sum_pair(hi, mul_pair(x[j], x[j]), hi, e);
+        lo = add_pair(lo, e);
+      }
+      const float2 h = parts_of(hi), l = parts_of(lo);
+      ss = Two{h.x, l.x} + Two{h.y, l.y};
+#pragma unroll
+      for (int off = D / 32; off > 0; off >>= 1)
+        ss = ss + Two{__shfl_xor_sync(0xffffffffu, ss.hi, off), __shfl_xor_sync(0xffffffffu, ss.lo, off)};
+      // Squares of BF16 numbers may leave FP32's range.  Rows of such are scaled by a power of two,
+      // eps by its square, so that the larger of both is near 1 (the norm takes it away again).
+      // (16000 tokens 68.9 us without the test, 69.3 with it.)
+      const bool far = !(ss.hi < 0x1p100f) || (ss.hi < 0x1p-60f && eps < 0x1p-60f);
+      if (again || !__any_sync(0xffffffffu, far)) break;
+      float big = 0.f;
+      int nan = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 v = parts_of(x[j]);
+        big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+        nan |= v.x != v.x || v.y != v.y;
+      }
+#pragma unroll
+      for (int off = D / 32; off > 0; off >>= 1) {
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+        nan |= __shfl_xor_sync(0xffffffffu, nan, off);
+      }
+      const int e = max((int)(__float_as_uint(big) >> 23) - 126, ((int)(__float_as_uint(eps) >> 23) - 127) / 2);
+      const float by = far ? __uint_as_float((uint32_t)(127 - max(-126, min(126, e))) << 23) : 1.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = mul_pair(x[j], packed_pair(by, by));
+      eps = eps * by * by;
+      zero = big == INFINITY && nan == 0;
     }
-    const float2 h = parts_of(hi), l = parts_of(lo);
-    Two ss = Two{h.x, l.x} + Two{h.y, l.y};
-#pragma unroll
-    for (int off = D / 32; off > 0; off >>= 1)
-      ss = ss + Two{__shfl_xor_sync(0xffffffffu, ss.hi, off), __shfl_xor_sync(0xffffffffu, ss.lo, off)};
     r = two_rsqrt(Two{ss.hi * (1.f / D), ss.lo * (1.f / D)} + Two{eps, 0.f});
+    if (zero) r = Two{0.f, 0.f};
   }
   const uint64_t rh = packed_pair(r.hi, r.hi), rl = packed_pair(r.lo, r.lo), minus_rh = packed_pair(-r.hi, -r.hi);
   float hi[16], lo[16];

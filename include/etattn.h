@@ -380,6 +380,8 @@ int attn_fwd_varlen_ex(const void* q, const void* k, const void* v, void* o, flo
  *           range is skipped and recorded (ETATTN_ERR_BAD_INDEX).
  *   strides: 12 int64 values, (t, h, d) for q, k, q_out, k_out.
  *   eps   : finite and > 0 when there is a weight (ETATTN_ERR_BAD_SCALE).
+ * The squares of a row are summed in FP32: a BF16 row with elements past 2^60, or one whose
+ * squares and eps are below 2^-126, is outside the norm's range.
  * Hq or Hk may be 0 (its pointers may then be NULL).  Outputs must not
  * overlap anything that the call reads (weights, tables and positions among
  * it) or each other (ETATTN_ERR_ALIAS); different heads of one fused buffer
@@ -536,9 +538,10 @@ size_t attn_paged_q4_block_bytes(int page_size, int D);
  *             (ETATTN_ERR_BAD_INDEX).
  *   strides : 16 int64 values, (t, h, d) for q, k, v, q_out in elements, then (page,
  *             head) for k_pages and v_pages in bytes.
- * A key is what norm and rotation leave, computed to about 2^-46 and rounded once to
- * the input type, so that its codes are those of exact arithmetic and do not depend
- * on the way it came.  k_pages, v_pages and q_out must not overlap anything that the
+ * A key is what norm and rotation leave, computed to about 2^-46 (or 2^-149, where that is
+ * more) and rounded once to the input type, so that its codes are those of exact arithmetic
+ * and do not depend on the way it came; for rows of any size, and norm weights below 2^76.
+ * (Queries are computed in FP32, as by attn_qk_norm_rope.)  k_pages, v_pages and q_out must not overlap anything that the
  * call reads, or each other (ETATTN_ERR_ALIAS).  Two tokens must not be given the same slot.
  */
 int attn_paged_append_q4(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
