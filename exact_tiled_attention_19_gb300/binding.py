@@ -1319,14 +1319,14 @@ def paged_extend(new_tokens, seqlens_k, block_table, free_pages, free_count, *, 
                                 positions=positions, slots=slots, free_count_out=free_count_out, workspace=workspace)
     if seqlens_out is None:
         seqlens_out = torch.empty_like(seqlens_k)
-    if cu_seqlens_q is None:  # (zeros: of no sequences no kernel writes the first offset)
-        cu_seqlens_q = (torch.empty if S else torch.zeros)(S + 1, dtype=i32, device=device)
+    if cu_seqlens_q is None:
+        cu_seqlens_q = torch.empty(S + 1, dtype=i32, device=device)
     if positions is None:
         positions = torch.empty(total_tokens, dtype=i32, device=device)
     if slots is None:
         slots = torch.empty(total_tokens, dtype=torch.int64, device=device)
     if free_count_out is None:
-        free_count_out = torch.empty_like(free_count) if S else free_count.clone()
+        free_count_out = torch.empty_like(free_count)
     ws, ws_bytes = 0, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), _workspace(workspace, device)
@@ -1337,10 +1337,16 @@ def paged_extend(new_tokens, seqlens_k, block_table, free_pages, free_count, *, 
     rc = (_lib or load_library()).attn_paged_extend(
         new_tokens.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
         free_count.data_ptr(), seqlens_out.data_ptr(), free_count_out.data_ptr(), cu_seqlens_q.data_ptr(),
-        positions.data_ptr(), slots.data_ptr(), S, total_tokens, page_size, width, row, free_pages.shape[0], ws,
-        ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
+        positions.data_ptr(), slots.data_ptr(), S, total_tokens if S else min(total_tokens, 0), page_size, width, row,
+        free_pages.shape[0], ws, ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
     if rc != 0:
         raise EtattnError(rc, "attn_paged_extend")
+    if S == 0:  # the C call does nothing then
+        cu_seqlens_q.zero_()
+        positions.zero_()
+        slots.fill_(-1)
+        if free_count_out is not free_count:
+            free_count_out.copy_(free_count)
     return seqlens_out, cu_seqlens_q, positions, slots, free_count_out
 
 
@@ -1365,7 +1371,7 @@ def paged_truncate(keep, seqlens_k, block_table, free_pages, free_count, *, page
     if seqlens_out is None:
         seqlens_out = torch.empty_like(seqlens_k)
     if free_count_out is None:
-        free_count_out = torch.empty_like(free_count) if S else free_count.clone()
+        free_count_out = torch.empty_like(free_count)
     ws, ws_bytes = 0, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), _workspace(workspace, device)
@@ -1379,4 +1385,6 @@ def paged_truncate(keep, seqlens_k, block_table, free_pages, free_count, *, page
         ws, ws_bytes, torch._C._cuda_getCurrentRawStream(device.index))
     if rc != 0:
         raise EtattnError(rc, "attn_paged_truncate")
+    if S == 0 and free_count_out is not free_count:  # the C call does nothing then
+        free_count_out.copy_(free_count)
     return seqlens_out, free_count_out

@@ -615,7 +615,8 @@ int attn_fwd_paged_q4_plan(int num_seqs, int Hq, int Hkv, int max_seqlen_q, int 
  * Then no page is taken, seqlens_out is seqlens_k, cu_seqlens_q is 0 throughout and every
  * slot is -1, so that the step's other calls do nothing.  Page numbers are not
  * looked into.  num_seqs <= 65535 and capacity <= 2^30.  Nothing but the two named pairs
- * may overlap (ETATTN_ERR_ALIAS).
+ * may overlap (ETATTN_ERR_ALIAS).  With num_seqs = 0 (and total_tokens = 0) nothing is read or
+ * written: cu_seqlens_q[0] and free_count_out are the caller's to set then.
  */
 int attn_paged_extend(const int32_t* new_tokens, const int32_t* seqlens_k, int32_t* block_table,
                       const int32_t* free_pages, const int32_t* free_count, int32_t* seqlens_out,
