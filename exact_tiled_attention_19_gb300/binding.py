@@ -1086,7 +1086,8 @@ def attention_paged(q, k_pages, v_pages, block_table, seqlens_k, *, cu_seqlens_q
 
 # ---------------------------------------------------------------- the paged cache held in 4 bits, and its pages
 
-_Q4_SLOT_BYTES = {32: 20, 64: 36, 128: 72}
+_Q4_SLOT_BYTES = {32: 20, 64: 36, 128: 72}  # attn_paged_q4_block_bytes of a page, per slot
+_TABLES_NO_SCRATCH = 4096                   # sequences up to which attn_paged_tables_workspace_size is 0
 
 
 def q4_pages(num_pages: int, Hkv: int, page_size: int, D: int, *, device=None):
@@ -1330,8 +1331,8 @@ def paged_extend(new_tokens, seqlens_k, block_table, free_pages, free_count, *, 
     ws, ws_bytes = 0, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), _workspace(workspace, device)
-    elif S > 4096:  # (attn_paged_tables_workspace_size)
-        ws_bytes = 4 * (S + 1)
+    elif S > _TABLES_NO_SCRATCH:
+        ws_bytes = attn_paged_tables_workspace_size(S)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         ws = workspace.data_ptr()
     rc = (_lib or load_library()).attn_paged_extend(
@@ -1375,8 +1376,8 @@ def paged_truncate(keep, seqlens_k, block_table, free_pages, free_count, *, page
     ws, ws_bytes = 0, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), _workspace(workspace, device)
-    elif S > 4096:  # (attn_paged_tables_workspace_size)
-        ws_bytes = 4 * (S + 1)
+    elif S > _TABLES_NO_SCRATCH:
+        ws_bytes = attn_paged_tables_workspace_size(S)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         ws = workspace.data_ptr()
     rc = (_lib or load_library()).attn_paged_truncate(

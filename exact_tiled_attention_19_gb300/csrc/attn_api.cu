@@ -1511,10 +1511,6 @@ int paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o,
 }
 
 // ---------------------------------------------------------------- the paged cache held in 4 bits
-// Bytes of a slot in a block: the codes and every group's scale and minimum (the
-// kernels' PagedQ4Cfg::ROW_BYTES).
-int64_t q4_slot_bytes(int D) { return D / 2 + 4 * (D / std::min(D, 64)); }
-
 // A cache [num_pages, Hkv, block bytes], with (page, head) strides in bytes; and the
 // same for pages_overlap, which counts in 16 bits.
 View view_blocks(const void* ptr, int num_pages, int Hkv, int64_t block, const int64_t* st) {
@@ -1643,8 +1639,6 @@ int unpack_q4_impl(const void* pages, void* out, int Hkv, int D, int dtype, cons
 // (One of 32 rows, a CTA of eight consumer warps an SM, took 195 us for 8 x 32768 keys
 // and 8 new tokens where two of 16 take 180, heads of 64 98 against 89, of 32 79 against 72.)
 int paged_q4_row_tile(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
-int paged_q4_ctas(int row_tile, int D) { return (row_tile == 16 ? 2 : 3) + (D == 32 ? 1 : 0); }  // PagedQ4Cfg::CTAS
-int paged_q4_tile_keys(int D) { return D == 128 ? 128 : 256; }  // the kernel's PagedQ4Cfg::TK
 
 int paged_q4_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
                   const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens_q, int num_seqs,

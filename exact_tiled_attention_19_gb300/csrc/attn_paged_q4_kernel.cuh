@@ -98,11 +98,12 @@ struct PagedQ4Cfg {
   static constexpr int UNIT_COST = (D == 128 ? 2 : 1) + (MT == 16 ? 1 : 0);
   static constexpr int GROUPS = 1;                    // of four consumer warps
   static constexpr int G = D < 64 ? D : 64, H = D / G;
-  static constexpr int TK = D == 128 ? 128 : 256;     // keys per tile
+  static constexpr int TK = paged_q4_tile_keys(D);    // keys per tile
   static constexpr int WK = TK / 4, NT = WK / 8;      // per consumer warp, and in blocks of 8
   static constexpr int SPREAD = 32;                   // keys of the largest box whose blocks different warps take
   static constexpr int PANEL = G / 2 + 4;             // bytes of a key's group: codes, scale and minimum
   static constexpr int ROW_BYTES = H * PANEL;
+  static_assert(ROW_BYTES == q4_slot_bytes(D), "");
   static constexpr int TILE_BYTES = TK * ROW_BYTES;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V: 18 KB, or 10 KB for D = 32
   static constexpr bool PAIRED = MT == 4;
@@ -112,7 +113,7 @@ struct PagedQ4Cfg {
   // smaller (three or four, us: 64 ragged sequences 24.7 and 23.3, 512 short ones 50.9 and 47.1; 16
   // rows, two or three, 39.2 and 34.4, 82.4 and 78.7).  With four of heads of 64 two stages are left
   // (8 x 32768 keys 32.0 and 33.7), and three of 16 rows of them spill (FP16 58.8 and 60.5).
-  static constexpr int CTAS = (MT == 16 ? 2 : 3) + (D == 32 ? 1 : 0);
+  static constexpr int CTAS = paged_q4_ctas(MT, D);
   static constexpr int BUDGET = CTAS == 4 ? 57344 : CTAS == 3 ? 76800 : 115712;
   static constexpr int COLS = PAIRED ? D : G;            // elements that are merged at a time
   static constexpr int MERGE_BYTES = 4 * MT * SIDES * COLS * 4;  // four warps' rows

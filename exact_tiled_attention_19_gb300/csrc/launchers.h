@@ -253,6 +253,12 @@ ETATTN_DECLARE_PAGED_LAUNCHER(launch_paged_d128_1)
 
 // The same over a cache held in 4 bits (attn_paged_q4_inst.cu): blocks of one
 // page and head, with byte strides.
+// What the host's plan and checks have in common with the kernels: bytes of a slot in a
+// block (the codes and every group's scale and minimum), keys of a tile, and CTAs an SM for
+// units of `rows` rows (4, 8 or 16).
+constexpr int q4_slot_bytes(int D) { return D / 2 + 4 * (D < 64 ? 1 : D / 64); }
+constexpr int paged_q4_tile_keys(int D) { return D == 128 ? 128 : 256; }
+constexpr int paged_q4_ctas(int rows, int D) { return (rows == 16 ? 2 : 3) + (D == 32 ? 1 : 0); }
 struct PagedQ4Params : PagedParams {
   const uint8_t *k_pages, *v_pages;
   int64_t kp_sp, kp_sh, vp_sp, vp_sh;
