@@ -1637,7 +1637,8 @@ int unpack_q4_impl(const void* pages, void* out, int Hkv, int D, int dtype, cons
 // Rows of a unit: 4, 8 or 16; more rows are several units.
 // (What 4 have of their own: the kernel's comment.)
 // (One of 32 rows, a CTA of eight consumer warps an SM, took 195 us for 8 x 32768 keys
-// and 8 new tokens where two of 16 take 180, heads of 64 98 against 89, of 32 79 against 72.)
+// and 8 new tokens where two of 16 took 180, heads of 64 98 against 89, of 32 79 against 72;
+// the kernels' later changes left two of 16 at 185, 93 and 70.)
 int paged_q4_row_tile(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 
 int paged_q4_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,

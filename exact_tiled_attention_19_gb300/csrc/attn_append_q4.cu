@@ -24,10 +24,11 @@
 // so that no warp does two kinds of work, and take turns, so that the arithmetic of k runs
 // beside the traffic of q.
 //
-// Measured (GB300; BF16, 32 + 2 x 8 heads of 128, norm and rotation): 16 x 1000 tokens 68.4 us, of
+// Measured (GB300; BF16, 32 + 2 x 8 heads of 128, norm and rotation): 16 x 1000 tokens 69.4 us, of
 // which q is 22 and k's two-part arithmetic 10 (51 us at the measured copy bandwidth; the
-// issue slots bound it: 215 instructions for a warp's four rows of v, 585 for k, 148 for q); 999 tokens
-// of 16 + 2 x 4 heads of 64 4.3 us; 8 tokens 2.8 us, the launch and the chain slot -> page.
+// issue slots bound it: some 230 instructions for a warp's four rows of v, 620 for k, 148 for q); 16000
+// tokens of 32 + 2 x 8 heads of 64 and of 32 39.5 and 26.5 us (26.2 and 13.2 at the copy bandwidth); 999
+// tokens of 16 + 2 x 4 heads of 64 4.3 us; 8 tokens 2.8 us, the launch and the chain slot -> page.
 // Unpacking the 16000 tokens' keys takes 8.2 us (6.2 at the copy bandwidth).
 #include <algorithm>
 #include <atomic>
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_q4_kernel(const __gr
     if (kind == 1) {
 #pragma unroll 1
       for (int i = 0; i < HP; ++i) row(i, std::true_type{});
-    } else {  // (two at a time: 76.5 us for 16000 tokens, one 78.0)
+    } else {  // (two at a time: 2 % faster for 16000 tokens than one)
 #pragma unroll 2
       for (int i = 0; i < HP; ++i) row(i, std::false_type{});
     }
@@ -530,8 +531,10 @@ cudaError_t append(const AppendQ4Params& p0, cudaStream_t s) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   // k and v's blocks come in the first 6/7 of the launch: theirs take longer, and at the
   // end the GPU would wait for a few of them (16000 tokens: 73.6 us spread over all of it,
-  // 71.3, 69.1, 68.4 and 69.5 over 95, 90, 86 and 80 %).  The product with all blocks is no
-  // less than their number.
+  // 71.3, 69.1, 68.4 and 69.5 over 95, 90, 86 and 80 %; all of it and 86 % with 8, 16, 40 and 64 heads
+  // of q 54.4 and 50.9, 60.8 and 56.7, 81.7 and 76.4, 105 and 99.3, with 32 of each at 8000 tokens 98.0 and 94.4,
+  // without q no difference, with heads of 64 42.6 and 39.5, of 32 27.9 and 26.4).  The product with all
+  // blocks is no less than their number.
   p.others = (int)(2 * kv);
   const uint64_t even = (((uint64_t)p.others << 32) + blocks - 1) / blocks;
   p.others_step = std::min(even + even / 6, uint64_t{1} << 32);

@@ -66,17 +66,20 @@
 // bits, and 16 of them cost a warp as many instructions as 16 bits would: the loads alone
 // take 50 us of the 55 for 8 x 32768 keys (44.6 at the copy bandwidth), the instructions of the
 // consumers half of all issue slots (2.0 of 4 a cycle), of which the integer units
-// take 52 %; the tensor pipe is busy 26 %.  So everything here saves instructions per key: no
-// conversions, scales on pairs, maxima looked at only when they matter.
+// take 51 %; the tensor pipe is busy 27 %.  (Heads of 64 and 32: 1.8 and 2.0, 46 %, 22 and 15 %;
+// 16 rows 1.7, 33 %, 30 %: no unit is full, fixed latencies and waits for tiles lie in between.)  So everything here saves instructions per key: no
+// conversions, scales on pairs, maxima looked at only when they matter.  And code: short sequences run
+// it through once a unit, so what a key that not all rows read may need (`values`, odd) is apart (512
+// short sequences of 16 rows 203 us with it in every edge tile, 181 without).
 //   mma.sync and not tcgen05: a tile of 128 query rows would be 15/16 empty, and the codes would
 // have to be written to shared memory as numbers first.  Three CTAs of four consumer warps an
 // SM: two took 64.5 us where three took 62.7; four (96 registers a thread, two stages) take 56.3
 // where three take 54.7.
 //
 // Measured (GB300; BF16, 32 query and 8 KV heads of 128, one new token, unless said; device
-// time; % of the measured copy bandwidth): 8 x 32768 keys 54.7 us (82 %; 57.2 before the values'
-// loads were transposed ones), in FP16 61.3; 1 x 524288 104.9 us (85 %); 64 sequences of 1 to 16384
-// keys 34.9 us (57 %); 16 rows (4 tokens) 8 x 32768 93.8 us; heads of 64 31.9, of 32 24.6.  The
+// time; % of the measured copy bandwidth): 8 x 32768 keys 55.5 us (80 %), in FP16 62.0; 1 x 524288
+// 107.5 us (83 %); 64 sequences of 1 to 16384 keys 35.4 us (56 %); 16 rows (4 tokens) 8 x 32768 97.7
+// us; heads of 64 32.0, of 32 24.6.  The
 // cache in 16 bits takes 164, 325 and 80 us for the first, the second and the 64 sequences.
 #pragma once
 
@@ -90,8 +93,8 @@ namespace etattn {
 template <int D_, int MT_>
 struct PagedQ4Cfg {
   static constexpr int D = D_, MT = MT_;
-  // What a unit costs next to a tile (of twice the keys for the smaller heads).  1, 2 and 3 take, us for
-  // 64 ragged sequences and for 512 short ones: 4 rows of 128 38.0, 34.7, 36.0 and 69.0, 66.5, 72.8; 8
+  // What a unit costs next to a tile (of twice the keys for the smaller heads).  1, 2 and 3 took (before a
+  // row had a power of two of its own), us for 64 ragged sequences and for 512 short ones: 4 rows of 128 38.0, 34.7, 36.0 and 69.0, 66.5, 72.8; 8
   // rows 45.4, 39.8, 41.2 and 87.4, 79.6, 85.8; 16 rows 87.2, 71.1, 65.3 and 198, 178, 170; heads of 64
   // 28.4, 29.8, 31.5 and 59.7, 65.0, 70.9, 16 rows of them 42.5, 42.2, 45.2 and 102, 99.2, 106; of 32
   // 23.2, 24.4, - and 47.0, 51.1, -, 16 rows 34.9, 34.0, - and 78.7, 76.6, -.

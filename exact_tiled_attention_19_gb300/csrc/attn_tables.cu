@@ -17,7 +17,9 @@
 //    launch of one CTA and a wide one after it.
 //  * More sequences are divided among a cluster of eight, which exchanges its sums, after
 //    which every CTA knows whether the step fits, before anything is written; the
-//    offsets go through memory.  A step of many tokens has them filled in by a second
+//    offsets go through memory.  (Eight, as a cluster is the widest group that may wait for its
+//    own in a launch; a wider sum would be three launches and a scratch that outlives them, for
+//    batches that are rare: 20000 sequences take 18.5 us, 14.9 to truncate.)  A step of many tokens has them filled in by a second
 //    launch as wide as the GPU.
 //
 // Measured (GB300, device time): 8 sequences, one token each, 3.6 us; 1000 sequences with prompts,

@@ -568,8 +568,8 @@ int attn_paged_unpack_q4(const void* pages, void* out, int Hkv, int D, int dtype
  * Everything else is as there, with attn_fwd_paged_q4_workspace_size and
  * attn_fwd_paged_q4_plan for workspace and num_shares.  A page out of range is
  * recorded, and the rows of that sequence mean nothing.  Elements of q above 2^110
- * in size give no meaningful row.  A key whose weight is below 2^-126 may count as
- * one that is not read.  Weights times values' scales are held to 2^-11 of themselves (BF16)
+ * in size give no meaningful row, nor do values whose size times 64 times the keys passes
+ * FP32.  A key whose weight is below 2^-126 may count as one that is not read.  Weights times values' scales are held to 2^-11 of themselves (BF16)
  * or 2^-21 (FP16) or, where that is more, 2^-28 of the row's largest; a row's result does not
  * depend on other rows, or on keys that it does not read.
  */
