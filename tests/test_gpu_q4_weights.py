@@ -7,13 +7,15 @@ Bounds.  For row i, key j and a group with scale s, minimum m and codes c, let p
 the weight.  The kernel adds p s (c - 8) and p (m + 8 s), so with
     B = sum_j p_j (s_j |c_jd - 8| + |m_j + 8 s_j|)
 the terms of tests/test_gpu_q4.py stand: ds_j for a key's score (and the sum's is their mean),
-w of p s for its rounding to FP16 (2^-11 in one part, for BF16 outputs; 2^-21 in two), 2^-20 for exponential and sum,
-(32 + keys / 16) 2^-24 for the sums.  P s is multiplied by a power of two for each row, warp
-and group, which takes the largest so far to 2^5.5 and more; a score that passes the row's
-reference may leave it a factor of two lower, and the tests here have at most one such time
-after the largest P s.  FP16's denormals lose 2^-25 a part, |c - 8| is 8 at most: 2^-24 8 / 2^4.5
-< 2^-25 of the row's largest p s a key, and
-    |dO| <= (w + 2^-20 + (32 + keys/16) 2^-24) B + B weighted by ds + u |O| + 2^-25 keys max_j p_j s_j,
+w of p s for its rounding to FP16 (2^-11 in one part, for BF16 outputs; 2^-21 in two), 2^-20
+for exponential and sum.  A tile's products with c are added to -8 times its weights, so
+partial sums reach 8 sum p s and more, whatever c is: the sums' (32 + keys / 16) 2^-24 are of
+    A = sum_j p_j (8 s_j + s_j |c_jd - 8| + |m_j + 8 s_j|).
+P s is multiplied by a power of two for each row, warp and group, which takes the largest
+so far to 2^5.5 and more; a score that passes the row's reference may leave it a factor of two
+lower, and the tests here have at most one such time after the largest P s.  FP16's denormals
+lose 2^-25 a part, |c - 8| is 8 at most: 2^-24 8 / 2^4.5 < 2^-25 of the row's largest p s a key, and
+    |dO| <= (w + 2^-20) B + (32 + keys/16) 2^-24 A + B weighted by ds + u |O| + 2^-25 keys max_j p_j s_j,
 with 2^-25 more for FP16 outputs.  max_j is over the keys that the row itself reads."""
 
 import math
@@ -68,7 +70,8 @@ def check_rows(o, q, k_pages, v_pages, page, table, L, scale=None):
             V = vc[hk, :keys] * wide(s) + wide(m)
             terms = wide(s) * np.abs(vc[hk, :keys] - 8) + np.abs(wide(m) + 8 * wide(s))
             want = p @ V
-            bound = ((w + 2.0 ** -20 + (32 + keys / 16) * 2.0 ** -24) * (p @ terms) + 1.1 * (p * (ds + p @ ds)) @ terms + u * np.abs(want)
+            bound = ((w + 2.0 ** -20) * (p @ terms) + (32 + keys / 16) * 2.0 ** -24 * (p @ (8 * wide(s) + terms))
+                     + 1.1 * (p * (ds + p @ ds)) @ terms + u * np.abs(want)
                      + 2.0 ** -25 * keys * wide((p[:, None] * s).max(0)) + least)
             x = np.abs(f64(o)[i, h] - want)
             assert np.all(x <= bound), f"row {i}, head {h}: {np.max(x / bound):.2f} of the bound"
